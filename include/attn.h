@@ -64,7 +64,7 @@
 extern "C" {
 #endif
 
-#define ATTN_ABI_VERSION 6
+#define ATTN_ABI_VERSION 7
 
 #if defined(__GNUC__)
 #define ATTN_API __attribute__((visibility("default")))
@@ -78,7 +78,8 @@ typedef enum attn_status {
     ATTN_EUNSUPPORTED = -2,  /* valid but not implemented (dtype, D, relation mix, GPU) */
     ATTN_ECUDA = -3,         /* a CUDA runtime call failed; see attn_last_error_string() */
     ATTN_ETIMEOUT = -4,      /* a kernel's bounded wait expired (device watchdog) */
-    ATTN_EWORKSPACE = -5     /* workspace missing or smaller than *_workspace_bytes() */
+    ATTN_EWORKSPACE = -5,    /* workspace missing or smaller than *_workspace_bytes() */
+    ATTN_ENOPAGES = -6       /* a cache has too few free pages (device status; nothing was changed) */
 } attn_status;
 
 typedef enum attn_dtype { ATTN_F16 = 0, ATTN_BF16 = 1, ATTN_F32 = 2 } attn_dtype;
@@ -140,7 +141,15 @@ typedef struct attn_fwd_args {
     uint64_t *pruned_tiles; /* optional device counter, or NULL: with pruning on, the
                                forward adds the number of pruned tiles to it */
     int32_t qk_fp8;       /* 0: q and k are `dtype`; 1: q and k are fp8 e4m3 (see below) */
+    int32_t H_kv;         /* heads of k and v: 0 = H; else a divisor of H (grouped heads, below) */
 } attn_fwd_args;
+
+/* Grouped heads (H_kv in the forward and the backward; no counterpart on the
+ * pages): k and v hold H_kv heads, each shared by a group of G = H / H_kv
+ * query heads: query head h attends to key / value head h / G (integer
+ * division).  In the backward dk and dv hold H_kv heads too, each the sum over
+ * its group's query heads, added in f32 in a fixed order and rounded once.
+ * H_kv must divide H (ATTN_EINVAL). */
 
 /* fp8 queries and keys (qk_fp8 = 1; no counterpart on the pages, a use of the
  * sm_103a tensor cores' 8-bit score contraction): q and k hold e4m3 values,
@@ -188,6 +197,7 @@ typedef struct attn_bwd_args {
     float prune_threshold; /* must be 0: the backward of a tile-pruned forward is not
                               defined, and a non-zero value returns ATTN_EUNSUPPORTED */
     int32_t dq_mode;      /* attn_dq_mode */
+    int32_t H_kv;         /* heads of k, v, dk and dv: 0 = H; else a divisor of H */
 } attn_bwd_args;
 
 /* Partial attention results over disjoint key sets, to be merged
@@ -242,6 +252,77 @@ typedef struct attn_csr_args {
     const int32_t *row_order;
 } attn_csr_args;
 
+/* A paged key / value cache (no counterpart on the pages; what serving needs
+ * next to the forward).  All arrays are the caller's device memory.
+ *
+ * Token t of sequence s, layer y, head h lives in row t % page_size of page
+ * table[s * table_stride + t / page_size]; k and v are (n_layers, n_pages,
+ * page_size, H_kv, D) with one set of element strides for both, D contiguous,
+ * rows 16-byte aligned (strides multiples of 8 elements for 16-bit types, 4
+ * for f32).  refs[p] counts the sequences that hold page p (and any references
+ * the caller adds); a page with refs[p] == 0 is free, so the counts are the
+ * allocator's whole state.  Pages are allocated lowest index first, in list
+ * order: the same calls give the same tables.
+ *
+ * The operations below run on `stream`, read and write only device memory and
+ * do not synchronise, so a captured loop can hold them.  They validate on the
+ * device: a list with an entry out of range, a sequence listed twice (except in
+ * attn_cache_free), or lengths that do not fit leaves the whole cache as it
+ * was, and attn_device_status() reports ATTN_EINVAL (ATTN_ENOPAGES when the
+ * free pages do not suffice).  Operations on one cache must be ordered by the
+ * caller (one stream); reads of it may overlap. */
+typedef struct attn_cache {
+    void *k, *v;              /* (n_layers, n_pages, page_size, H_kv, D) dtype */
+    int64_t stride_layer, stride_page, stride_tok, stride_head; /* elements, of both k and v */
+    int32_t *table;           /* (max_seqs, max_pages) page indices */
+    int32_t *lens;            /* (max_seqs) tokens of each sequence; 0 = empty */
+    int32_t *refs;            /* (n_pages) reference counts; 0 = free */
+    int64_t table_stride;     /* elements between the table's rows, >= max_pages */
+    int32_t n_layers, n_pages;
+    int32_t page_size;        /* a power of two, 1..1024 */
+    int32_t H_kv, D;          /* heads; head dim (64 or 128) */
+    int32_t dtype;            /* attn_dtype */
+    int32_t max_seqs;         /* rows of table, 1..ATTN_CACHE_MAX_SEQS */
+    int32_t max_pages;        /* pages a sequence can hold */
+} attn_cache;
+
+#define ATTN_CACHE_MAX_SEQS 262144
+
+/* Attention of new tokens over the cache: one token (decoding), a chunk, or a
+ * tree of drafted tokens per sequence, grouped heads, in one call.
+ *
+ * Entry i is sequence seqs[i] with L = lens[seqs[i]] cached tokens, whose last
+ * T = cu[i + 1] - cu[i] are the query tokens themselves (their rows are in the
+ * cache: attn_cache_extend, attn_cache_write).  Query token t of the entry is row
+ * cu[i] + t of q, o and lse.  It sees every token before the T new ones, and new
+ * token u if bit u % 64 of mask[(cu[i] + t) * mask_words + u / 64] is set, or
+ * without a mask if u <= t.  A query that sees nothing gets O = 0, lse = -inf.
+ *     o = sum_j softmax_j(scale <q, k_j>) v_j, query head h over cache head h / (H / H_kv)
+ * Rows of q from cu[n] on are not read, and their o and lse rows are left as
+ * they were; so are those of an entry that does not fit (sequence out of range,
+ * T > L, offsets that decrease or leave [0, n_q], more new tokens than the mask
+ * has bits), which attn_device_status() reports as ATTN_EINVAL.  Cache slots
+ * from token L on are never used, whatever they hold; cached rows below L and q
+ * must be finite. */
+typedef struct attn_tree_args {
+    attn_cache cache;     /* H_kv divides H; dtype also of q */
+    int32_t layer;
+    int32_t H;            /* query heads */
+    attn_tensor q;        /* in:  (n_q, H, D) */
+    attn_tensor o;        /* out: (n_q, H, D), o_dtype */
+    float *lse;           /* out: (H, n_q) f32, natural log; may be NULL */
+    const int32_t *seqs;  /* device, n sequences */
+    const int32_t *cu;    /* device, n + 1 offsets from 0 */
+    const uint64_t *mask; /* device, (n_q, mask_words), or NULL: new tokens see those up to themselves */
+    int32_t n;            /* entries */
+    int32_t n_q;          /* query rows */
+    int32_t mask_words;   /* 64-bit words of a mask row: new tokens of an entry <= 64 * mask_words */
+    float scale;          /* any finite value */
+    int32_t o_dtype;      /* the cache's dtype or ATTN_F32 */
+    void *workspace;      /* attn_tree_workspace_bytes() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} attn_tree_args;
+
 /* Library ABI version (ATTN_ABI_VERSION) and struct sizes, for bindings to
  * check their mirrors of the structs above. */
 ATTN_API int attn_abi_version(void);
@@ -249,6 +330,8 @@ ATTN_API size_t attn_fwd_args_size(void);
 ATTN_API size_t attn_bwd_args_size(void);
 ATTN_API size_t attn_merge_args_size(void);
 ATTN_API size_t attn_csr_args_size(void);
+ATTN_API size_t attn_cache_size(void);
+ATTN_API size_t attn_tree_args_size(void);
 
 /* Bytes of device workspace the call needs (depends on n_seq, H, n_q, and
  * for the forward on the number of key splits: n_splits > 1 adds the partial
@@ -339,6 +422,62 @@ ATTN_API int attn_bwd_selected_dq_mode(const attn_bwd_args *a);
 
 /* Attention over the CSR relation of `a` (see attn_csr_args). */
 ATTN_API int attn_csr_fwd(const attn_csr_args *a, void *stream);
+
+/* Attention of new tokens over the cache (see attn_tree_args): an attention
+ * kernel over equal shares of all (sequence, head, keys) work, and a kernel that
+ * merges the shares of a split sequence.  The workspace depends on sizes only
+ * (not on lengths); calls that may overlap need one each. */
+ATTN_API int attn_tree_fwd(const attn_tree_args *a, void *stream);
+ATTN_API size_t attn_tree_workspace_bytes(const attn_tree_args *a);
+
+/* Bytes of workspace attn_cache_extend, _fork, _keep and _compact need for
+ * lists of n entries (256-byte aligned device memory); 0 for bad arguments. */
+ATTN_API size_t attn_cache_workspace_bytes(const attn_cache *c, int32_t n);
+
+/* Room for counts[i] >= 0 more tokens of sequence seqs[i]: allocates the pages
+ * they need and adds counts[i] to lens.  The new rows hold whatever the pages
+ * held until attn_cache_write fills them.  A partial last page that other
+ * sequences hold too is replaced by a copy first (all layers). */
+ATTN_API int attn_cache_extend(const attn_cache *c, const int32_t *seqs, const int32_t *counts,
+                               int32_t n, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Writes new k and v rows (n_rows, H_kv, D) of one layer: rows
+ * [cu[i], cu[i + 1]) become the last cu[i + 1] - cu[i] tokens of sequence
+ * seqs[i] (cu: n + 1 offsets from 0; rows from cu[n] on are not read).  An
+ * entry that does not fit, that repeats an earlier entry's sequence, or a row
+ * whose page other sequences hold too is skipped and reported as ATTN_EINVAL;
+ * the others are written. */
+ATTN_API int attn_cache_write(const attn_cache *c, int32_t layer, const int32_t *seqs,
+                              const int32_t *cu, int32_t n, const attn_tensor *k, const attn_tensor *v,
+                              int32_t n_rows, void *stream);
+
+/* children[i] becomes a copy of parents[i]: it shares the parent's full pages
+ * and gets a page of its own for the rows of a partial last one (all layers;
+ * the rest of that page is left as it was).  Children must be empty and
+ * listed once; a parent may be listed many times. */
+ATTN_API int attn_cache_fork(const attn_cache *c, const int32_t *parents, const int32_t *children,
+                             int32_t n, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Of the last n_draft[i] tokens of sequence seqs[i] keeps the n_keep[i] whose
+ * offsets (in [0, n_draft[i]), strictly ascending) stand at
+ * keep[i * keep_stride]: their rows move down, in all layers, to follow the
+ * tokens before the drafts; the sequence ends behind them and the pages it no
+ * longer needs are released.  Rows behind the new end keep what they hold.  A
+ * row that would move into a page that other sequences hold too: ATTN_EINVAL. */
+ATTN_API int attn_cache_keep(const attn_cache *c, const int32_t *seqs, const int32_t *n_draft,
+                             const int32_t *keep, int64_t keep_stride, const int32_t *n_keep, int32_t n,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Releases the pages of the sequences and empties them.  A sequence listed
+ * twice is released once; entries out of range are skipped and reported. */
+ATTN_API int attn_cache_free(const attn_cache *c, const int32_t *seqs, int32_t n, void *stream);
+
+/* Moves the live pages to the front: with L live pages, those at or above L
+ * move, in ascending order, to the free pages below L (all layers, k and v);
+ * the tables and counts follow.  remap (n_pages entries, or NULL) gets every
+ * page's new index, for references that the caller holds. */
+ATTN_API int attn_cache_compact(const attn_cache *c, int32_t *remap, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 /* Forward for callers that cannot allocate device memory (no counterpart on
  * the pages; a deployment convenience).  Same arguments and results as

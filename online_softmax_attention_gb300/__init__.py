@@ -11,12 +11,18 @@ argument structs:
   disjoint key sets from each set's result (the split-K merge)
 * ``csr_fwd(row_ptr, col, v, scores=... | q=..., k=...)`` -> ``(o, lse)``:
   attention over a general CSR relation (softmax over each row's edges)
-* ``FwdCall`` / ``BwdCall`` hold prepared argument structs for repeated
+* ``Cache``: a paged key / value cache -- ``extend``, ``write``, ``fork``,
+  ``keep``, ``free``, ``compact``
+* ``tree_fwd(q, cache, seqs, cu_seqlens_q, mask=...)`` -> ``(o, lse)``:
+  attention of new tokens (one, a chunk, a tree of drafts) over the cache
+* ``FwdCall`` / ``BwdCall`` / ``TreeCall`` hold prepared argument structs for repeated
   launches (the benchmark and CUDA-graph capture use them).
 
 Tensors are (tokens, heads, D) with the D axis contiguous; any token / head
 strides whose rows stay 16-byte aligned are accepted (for example an (H, N, D)
-tensor viewed as (N, H, D)).  ``cu_seqlens`` follow flash-attn's varlen
+tensor viewed as (N, H, D)).  k and v may have fewer heads than q, each shared
+by a group of query heads (query head h reads head h // (H / H_kv)); dk and dv
+then have their heads.  ``cu_seqlens`` follow flash-attn's varlen
 convention ``[0, L1, L1+L2, ...]`` as int32.
 """
 from __future__ import annotations
@@ -26,11 +32,12 @@ import ctypes
 import torch
 
 from . import _abi
+from .cache import Cache, TreeCall, tree_fwd
 from ._abi import (ATTN_BF16, ATTN_CAUSAL, ATTN_F16, ATTN_F32, ATTN_FULL, ATTN_KERNEL_AUTO,
                    ATTN_KERNEL_SIMT, ATTN_KERNEL_TC, AttnError, check)
 
 __all__ = ["fwd", "bwd", "merge", "csr_fwd", "FwdCall", "BwdCall", "MergeCall", "CsrCall",
-           "device_status", "launch_count", "AttnError", "library_path"]
+           "Cache", "TreeCall", "tree_fwd", "device_status", "launch_count", "AttnError", "library_path"]
 
 _DT = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}
 _E4M3 = getattr(torch, "float8_e4m3fn", None)
@@ -81,6 +88,14 @@ def _view(t: torch.Tensor | None, name: str) -> _abi.AttnTensor:
     return _abi.AttnTensor(t.data_ptr() if t.numel() else None, st, sh)
 
 
+def _kv_shape(k: torch.Tensor, v: torch.Tensor, D: int):
+    """(tokens, heads) of k and v, which share one shape and q's D.  Fewer heads
+    than q has are grouped heads: the library checks that they divide q's."""
+    if k.dim() != 3 or tuple(v.shape) != tuple(k.shape) or k.shape[2] != D or k.shape[1] < 1:
+        raise ValueError(f"k and v must both be (tokens, heads, {D}), got {tuple(k.shape)} and {tuple(v.shape)}")
+    return k.shape[0], k.shape[1]
+
+
 def _cu(cu, device) -> torch.Tensor | None:
     if cu is None:
         return None
@@ -119,7 +134,7 @@ class FwdCall:
             raise TypeError("q, k, v must share one dtype")
         dev = q.device
         Tq, H, D = q.shape
-        Tk = k.shape[0]
+        Tk, H_kv = _kv_shape(k, v, D)
         out_dtype = out_dtype or v.dtype
         self.cu_q = _cu(cu_seqlens_q, dev)
         self.cu_k = _cu(cu_seqlens_k if cu_seqlens_k is not None else cu_seqlens_q, dev)
@@ -134,6 +149,7 @@ class FwdCall:
         a.relation = ATTN_CAUSAL if causal else ATTN_FULL
         a.dtype, a.o_dtype = _dtype_code(v.dtype), _dtype_code(self.o.dtype)
         a.qk_fp8 = 1 if qk_fp8 else 0
+        a.H_kv = H_kv
         a.n_seq = (self.cu_q.numel() - 1) if self.cu_q is not None else 1
         a.cu_seqlens_q = self.cu_q.data_ptr() if self.cu_q is not None else None
         a.cu_seqlens_k = self.cu_k.data_ptr() if self.cu_k is not None else None
@@ -221,13 +237,13 @@ class BwdCall:
                  dq_mode: str = "auto"):
         dev = q.device
         Tq, H, D = q.shape
-        Tk = k.shape[0]
+        Tk, H_kv = _kv_shape(k, v, D)
         gdt = grad_dtype or q.dtype
         self.cu_q = _cu(cu_seqlens_q, dev)
         self.cu_k = _cu(cu_seqlens_k if cu_seqlens_k is not None else cu_seqlens_q, dev)
         self.dq = dq if dq is not None else torch.empty((Tq, H, D), dtype=gdt, device=dev)
-        self.dk = dk if dk is not None else torch.empty((Tk, H, D), dtype=gdt, device=dev)
-        self.dv = dv if dv is not None else torch.empty((Tk, H, D), dtype=gdt, device=dev)
+        self.dk = dk if dk is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
+        self.dv = dv if dv is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
         self.inputs = (q, k, v, o, lse, dout)
         a = _abi.BwdArgs()
         a.q, a.k, a.v = _view(q, "q"), _view(k, "k"), _view(v, "v")
@@ -246,6 +262,7 @@ class BwdCall:
         a.num_ctas = int(num_ctas)
         a.prune_threshold = float(prune_threshold)  # non-zero: the library refuses (fails closed)
         a.dq_mode = _DQ_MODES[dq_mode]
+        a.H_kv = H_kv
         lib = _abi.load()
         need = lib.attn_bwd_workspace_bytes(ctypes.byref(a))
         self.workspace = workspace if workspace is not None else _workspace(need, dev)

@@ -12,9 +12,10 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libattn_gb300.so")
 
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED, ATTN_ECUDA, ATTN_ETIMEOUT, ATTN_EWORKSPACE = 0, -1, -2, -3, -4, -5
+ATTN_ENOPAGES = -6
 ATTN_F16, ATTN_BF16, ATTN_F32 = 0, 1, 2
 ATTN_FULL, ATTN_CAUSAL = 0, 1
 ATTN_KERNEL_AUTO, ATTN_KERNEL_SIMT, ATTN_KERNEL_TC = 0, 1, 2
@@ -32,6 +33,9 @@ EXPORTS = (
     "attn_selftest_exp2", "attn_set_watchdog_cycles", "attn_merge_args_size",
     "attn_fwd_num_splits", "attn_merge", "attn_csr_args_size", "attn_csr_fwd",
     "attn_bwd_selected_dq_mode", "attn_fwd_simple_workspace_bytes",
+    "attn_cache_size", "attn_tree_args_size", "attn_tree_fwd", "attn_tree_workspace_bytes",
+    "attn_cache_workspace_bytes", "attn_cache_extend", "attn_cache_write", "attn_cache_fork",
+    "attn_cache_keep", "attn_cache_free", "attn_cache_compact",
 )
 
 
@@ -51,7 +55,7 @@ class FwdArgs(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("kernel", ctypes.c_int32), ("num_ctas", ctypes.c_int32), ("num_splits", ctypes.c_int32),
         ("prune_threshold", ctypes.c_float), ("pruned_tiles", ctypes.c_void_p),
-        ("qk_fp8", ctypes.c_int32),
+        ("qk_fp8", ctypes.c_int32), ("H_kv", ctypes.c_int32),
     ]
 
 
@@ -74,6 +78,28 @@ class CsrArgs(ctypes.Structure):
     ]
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("stride_layer", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+        ("stride_tok", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+        ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64), ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", Cache), ("layer", ctypes.c_int32), ("H", ctypes.c_int32), ("q", AttnTensor),
+        ("o", AttnTensor), ("lse", ctypes.c_void_p), ("seqs", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p), ("n", ctypes.c_int32), ("n_q", ctypes.c_int32),
+        ("mask_words", ctypes.c_int32), ("scale", ctypes.c_float), ("o_dtype", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class BwdArgs(ctypes.Structure):
     _fields_ = [
         ("q", AttnTensor), ("k", AttnTensor), ("v", AttnTensor), ("o", AttnTensor),
@@ -85,7 +111,7 @@ class BwdArgs(ctypes.Structure):
         ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("kernel", ctypes.c_int32), ("num_ctas", ctypes.c_int32),
-        ("prune_threshold", ctypes.c_float), ("dq_mode", ctypes.c_int32),
+        ("prune_threshold", ctypes.c_float), ("dq_mode", ctypes.c_int32), ("H_kv", ctypes.c_int32),
     ]
 
 
@@ -105,7 +131,8 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     fa, ba, ma = ctypes.POINTER(FwdArgs), ctypes.POINTER(BwdArgs), ctypes.POINTER(MergeArgs)
-    ca = ctypes.POINTER(CsrArgs)
+    ca, cc, ta = ctypes.POINTER(CsrArgs), ctypes.POINTER(Cache), ctypes.POINTER(TreeArgs)
+    at = ctypes.POINTER(AttnTensor)
     sigs = {
         "attn_abi_version": (ctypes.c_int, []),
         "attn_fwd_args_size": (sz, []),
@@ -132,6 +159,17 @@ def load() -> ctypes.CDLL:
         "attn_set_watchdog_cycles": (ctypes.c_longlong, [ctypes.c_longlong]),
         "attn_bwd_selected_kernel": (ctypes.c_int, [ba]),
         "attn_bwd_selected_dq_mode": (ctypes.c_int, [ba]),
+        "attn_cache_size": (sz, []),
+        "attn_tree_args_size": (sz, []),
+        "attn_tree_fwd": (ctypes.c_int, [ta, vp]),
+        "attn_tree_workspace_bytes": (sz, [ta]),
+        "attn_cache_workspace_bytes": (sz, [cc, i32]),
+        "attn_cache_extend": (ctypes.c_int, [cc, vp, vp, i32, vp, sz, vp]),
+        "attn_cache_write": (ctypes.c_int, [cc, i32, vp, vp, i32, at, at, i32, vp]),
+        "attn_cache_fork": (ctypes.c_int, [cc, vp, vp, i32, vp, sz, vp]),
+        "attn_cache_keep": (ctypes.c_int, [cc, vp, vp, vp, ctypes.c_int64, vp, i32, vp, sz, vp]),
+        "attn_cache_free": (ctypes.c_int, [cc, vp, i32, vp]),
+        "attn_cache_compact": (ctypes.c_int, [cc, vp, vp, sz, vp]),
         "attn_launch_count": (ctypes.c_uint64, []),
         "attn_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "attn_last_error_string": (ctypes.c_char_p, []),
@@ -145,7 +183,9 @@ def load() -> ctypes.CDLL:
     if lib.attn_fwd_args_size() != ctypes.sizeof(FwdArgs) or \
             lib.attn_bwd_args_size() != ctypes.sizeof(BwdArgs) or \
             lib.attn_merge_args_size() != ctypes.sizeof(MergeArgs) or \
-            lib.attn_csr_args_size() != ctypes.sizeof(CsrArgs):
+            lib.attn_csr_args_size() != ctypes.sizeof(CsrArgs) or \
+            lib.attn_cache_size() != ctypes.sizeof(Cache) or \
+            lib.attn_tree_args_size() != ctypes.sizeof(TreeArgs):
         raise ImportError("libattn_gb300 struct layout does not match the binding")
     _lib = lib
     return lib

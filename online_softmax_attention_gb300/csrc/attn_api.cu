@@ -111,7 +111,7 @@ int choose_tc(int kernel, bool tc_ok, bool &use_tc) {
     return ATTN_OK;
 }
 
-int check_common(int n_q, int n_k, int H, int D, int relation, int dtype, int n_seq,
+int check_common(int n_q, int n_k, int H, int H_kv, int D, int relation, int dtype, int n_seq,
                  const int32_t *cu_q, const int32_t *cu_k, float scale) {
     if (n_q < 0 || n_k < 0 || H < 1 || n_seq < 1) return ATTN_EINVAL;
     if (!valid_dtype(dtype)) return ATTN_EINVAL;
@@ -121,6 +121,7 @@ int check_common(int n_q, int n_k, int H, int D, int relation, int dtype, int n_
     if (!cu_q && n_seq != 1) return ATTN_EINVAL;
     if (!cu_q && relation == ATTN_CAUSAL && n_q != n_k) return ATTN_EUNSUPPORTED;
     if (D != 64 && D != 128) return ATTN_EUNSUPPORTED;
+    if (H_kv < 0 || (H_kv > 0 && H % H_kv != 0)) return ATTN_EINVAL;
     // work-item numbering is int32: H * (tiles + sequences) must fit
     const int64_t items = (int64_t)H * ((int64_t)(n_q > n_k ? n_q : n_k) / kSimtBlock + n_seq + 1);
     if (items >= (int64_t)1 << 31 || (int64_t)n_q * H >= (int64_t)1 << 31) return ATTN_EUNSUPPORTED;
@@ -180,7 +181,7 @@ FwdLayout fwd_layout(int n_seq, int n_q, int H, int D, int splits, size_t op_byt
 // Bytes of the bf16 operand parts a forward with these parameters keeps in the
 // workspace (f32 inputs on the tensor cores only).
 size_t split_op_bytes(const FwdParams &p, bool use_tc) {
-    return use_tc && p.dtype == ATTN_F32 ? x3_split_bytes(p.n_q, p.n_k, p.H) : 0;
+    return use_tc && p.dtype == ATTN_F32 ? x3_split_bytes(p.n_q, p.n_k, p.H, p.Hkv) : 0;
 }
 
 FwdLayout fwd_layout_of(const FwdParams &p, bool use_tc) {
@@ -194,7 +195,7 @@ FwdLayout fwd_layout_of(const FwdParams &p, bool use_tc) {
 // tensors exist).
 int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_views = true) {
     if (!a) return ATTN_EINVAL;
-    int rc = check_common(a->n_q, a->n_k, a->H, a->D, a->relation, a->dtype, a->n_seq,
+    int rc = check_common(a->n_q, a->n_k, a->H, a->H_kv, a->D, a->relation, a->dtype, a->n_seq,
                           a->cu_seqlens_q, a->cu_seqlens_k, a->scale);
     if (rc) return rc;
     if (a->o_dtype != a->dtype && a->o_dtype != ATTN_F32) return ATTN_EINVAL;
@@ -223,6 +224,8 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     p.v_st = a->v.stride_tok; p.v_sh = a->v.stride_head;
     p.o_st = a->o.stride_tok; p.o_sh = a->o.stride_head;
     p.n_q = a->n_q; p.n_k = a->n_k; p.H = a->H; p.D = a->D;
+    p.Hkv = a->H_kv > 0 ? a->H_kv : a->H;
+    p.group = p.H / p.Hkv;
     p.scale = a->scale;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.causal = a->relation == ATTN_CAUSAL;
@@ -325,7 +328,7 @@ bool bwd_fused(const attn_bwd_args *a) {
 
 int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     if (!a) return ATTN_EINVAL;
-    int rc = check_common(a->n_q, a->n_k, a->H, a->D, a->relation, a->dtype, a->n_seq,
+    int rc = check_common(a->n_q, a->n_k, a->H, a->H_kv, a->D, a->relation, a->dtype, a->n_seq,
                           a->cu_seqlens_q, a->cu_seqlens_k, a->scale);
     if (rc) return rc;
     if (a->o_dtype != a->dtype && a->o_dtype != ATTN_F32) return ATTN_EINVAL;
@@ -355,6 +358,8 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     p.dk_st = a->dk.stride_tok; p.dk_sh = a->dk.stride_head;
     p.dv_st = a->dv.stride_tok; p.dv_sh = a->dv.stride_head;
     p.n_q = a->n_q; p.n_k = a->n_k; p.H = a->H; p.D = a->D;
+    p.Hkv = a->H_kv > 0 ? a->H_kv : a->H;
+    p.group = p.H / p.Hkv;
     p.scale = a->scale;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.causal = a->relation == ATTN_CAUSAL;
@@ -375,6 +380,115 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     rc = choose_tc(a->kernel, tc_bwd_supported(p), use_tc);
     if (rc) return rc;
     if (a->dq_mode == ATTN_DQ_FUSED && !use_tc) return ATTN_EUNSUPPORTED;
+    return ATTN_OK;
+}
+
+// ---- cache -----------------------------------------------------------------
+
+bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// Validates the cache's description and fills the kernels' view of it.
+int plan_cache(const attn_cache *c, CacheParams &p) {
+    if (!c || !valid_dtype(c->dtype)) return ATTN_EINVAL;
+    if (c->n_layers < 1 || c->n_pages < 1 || c->H_kv < 1 || c->max_seqs < 1 || c->max_pages < 1 ||
+        c->table_stride < c->max_pages)
+        return ATTN_EINVAL;
+    if (c->D != 64 && c->D != 128) return ATTN_EUNSUPPORTED;
+    if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) ||
+        c->max_seqs > ATTN_CACHE_MAX_SEQS || c->H_kv > 4096 || c->n_layers > 32767)
+        return ATTN_EUNSUPPORTED;
+    // token positions are int32
+    if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31 || c->n_pages > (1 << 30)) return ATTN_EUNSUPPORTED;
+    const int64_t es = (int64_t)elem_size(c->dtype);
+    if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return ATTN_EINVAL;
+    for (int64_t st : {c->stride_layer, c->stride_page, c->stride_tok, c->stride_head})
+        if (st <= 0 || (st * es) % 16 != 0) return ATTN_EINVAL;
+    if (!aligned4(c->table) || !aligned4(c->lens) || !aligned4(c->refs)) return ATTN_EINVAL;
+    std::memset(&p, 0, sizeof(p));
+    p.k = static_cast<char *>(c->k);
+    p.v = static_cast<char *>(c->v);
+    p.b_layer = c->stride_layer * es;
+    p.b_page = c->stride_page * es;
+    p.b_tok = c->stride_tok * es;
+    p.b_head = c->stride_head * es;
+    p.table = c->table;
+    p.lens = c->lens;
+    p.refs = c->refs;
+    p.table_stride = c->table_stride;
+    p.n_layers = c->n_layers;
+    p.n_pages = c->n_pages;
+    while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+    p.H = c->H_kv;
+    p.row_bytes = (int)(c->D * es);
+    p.max_seqs = c->max_seqs;
+    p.max_pages = c->max_pages;
+    return ATTN_OK;
+}
+
+// Lays the plan out in the workspace; returns its bytes.
+size_t cache_plan(const CacheParams &p, int n, void *workspace, CachePlan &w) {
+    const size_t list = align256(sizeof(int) * ((size_t)n + 1)), pages = align256(sizeof(int) * (size_t)p.n_pages);
+    char *at = static_cast<char *>(workspace);
+    auto take = [&](size_t bytes) {
+        int *r = reinterpret_cast<int *>(at);
+        at += bytes;
+        return r;
+    };
+    w.hdr = take(align256(sizeof(int) * kPlanHdr));
+    w.first = take(list);
+    w.len = take(list);
+    w.src = take(list);
+    w.pages = take(pages);
+    w.from = take(pages);
+    w.remap = take(pages);
+    return align256(sizeof(int) * kPlanHdr) + 3 * list + 3 * pages;
+}
+
+// Validates the arguments of the cached attention but for the workspace.
+int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
+    if (!a) return ATTN_EINVAL;
+    std::memset(&p, 0, sizeof(p));
+    const int rc = plan_cache(&a->cache, p.c);
+    if (rc) return rc;
+    if (a->layer < 0 || a->layer >= a->cache.n_layers || a->H < 1 || a->H % a->cache.H_kv != 0 || a->n < 0 ||
+        a->n_q < 0 || a->mask_words < 0)
+        return ATTN_EINVAL;
+    if (a->o_dtype != a->cache.dtype && a->o_dtype != ATTN_F32) return ATTN_EINVAL;
+    if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return ATTN_EINVAL;
+    if ((int64_t)a->n_q * a->H >= (int64_t)1 << 31) return ATTN_EUNSUPPORTED;
+    const bool any = a->n_q > 0 && a->n > 0;
+    if (check_views && any &&
+        (!valid_view(a->q, a->cache.dtype, true) || !valid_view(a->o, a->o_dtype, true) || !aligned4(a->seqs) ||
+         !aligned4(a->cu) || (reinterpret_cast<uintptr_t>(a->lse) & 3) || (reinterpret_cast<uintptr_t>(a->mask) & 7) ||
+         (a->mask && a->mask_words < 1)))
+        return ATTN_EINVAL;
+    p.c.k += a->layer * p.c.b_layer;
+    p.c.v += a->layer * p.c.b_layer;
+    p.q = a->q.ptr; p.o = a->o.ptr; p.lse = a->lse;
+    p.q_st = a->q.stride_tok; p.q_sh = a->q.stride_head;
+    p.o_st = a->o.stride_tok; p.o_sh = a->o.stride_head;
+    p.seqs = a->seqs; p.cu = a->cu;
+    p.mask = reinterpret_cast<const unsigned long long *>(a->mask);
+    p.n = a->n; p.n_q = a->n_q; p.mask_words = a->mask_words;
+    p.H = a->H; p.group = a->H / a->cache.H_kv; p.D = a->cache.D;
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.dtype = a->cache.dtype; p.o_dtype = a->o_dtype;
+    return ATTN_OK;
+}
+
+size_t tree_layout(const TreeParams &p, size_t &ml) {
+    const size_t rows = 2 * (size_t)tree_blocks() * (size_t)tree_rows(p);
+    ml = align256(sizeof(float) * rows * (size_t)p.D);
+    return ml + align256(sizeof(float2) * rows);
+}
+
+int build_cache(const attn_cache *c, int n, void *workspace, size_t workspace_bytes, CacheParams &p, CachePlan &w) {
+    const int rc = plan_cache(c, p);
+    if (rc) return rc;
+    if (n < 0) return ATTN_EINVAL;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+        workspace_bytes < cache_plan(p, n, workspace, w))
+        return ATTN_EWORKSPACE;
     return ATTN_OK;
 }
 
@@ -428,9 +542,9 @@ int attn_fwd(const attn_fwd_args *a, void *stream) {
     if (a->n_q == 0) return ATTN_OK;
     if (log_on())
         std::fprintf(stderr,
-                     "[attn] fwd n_q=%d n_k=%d H=%d D=%d n_seq=%d relation=%s dtype=%s%s o_dtype=%s "
+                     "[attn] fwd n_q=%d n_k=%d H=%d H_kv=%d D=%d n_seq=%d relation=%s dtype=%s%s o_dtype=%s "
                      "kernel=%s splits=%d prune=%g\n",
-                     a->n_q, a->n_k, a->H, a->D, a->n_seq, p.causal ? "causal" : "full",
+                     a->n_q, a->n_k, a->H, p.Hkv, a->D, a->n_seq, p.causal ? "causal" : "full",
                      p.qk_fp8 ? "e4m3+" : "", dtype_name(a->dtype), dtype_name(a->o_dtype),
                      use_tc ? "tc" : "simt", p.n_splits, (double)a->prune_threshold);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -504,7 +618,7 @@ int attn_bwd_preprocess(const attn_bwd_args *a, void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int kv_block = use_tc ? tc_bwd_kv_block(p) : kSimtBlock;
     const int q_block = use_tc ? tc_bwd_q_block(p) : kSimtBlock;
-    cudaError_t e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.H, kv_block, p.causal, 1,
+    cudaError_t e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.Hkv, kv_block, p.causal, 1,
                                 1, p.sched_kv, p.status, s);
     if (e == cudaSuccess && !p.dq_accum)  // the fused dq needs no query-block schedule
         e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.H, q_block, p.causal, 0,
@@ -548,9 +662,9 @@ int attn_bwd(const attn_bwd_args *a, void *stream) {
         bool use_tc = false;
         if (build_bwd(a, p, use_tc) == ATTN_OK)
             std::fprintf(stderr,
-                         "[attn] bwd n_q=%d n_k=%d H=%d D=%d n_seq=%d relation=%s dtype=%s "
+                         "[attn] bwd n_q=%d n_k=%d H=%d H_kv=%d D=%d n_seq=%d relation=%s dtype=%s "
                          "grad_dtype=%s kernel=%s dq=%s\n",
-                         a->n_q, a->n_k, a->H, a->D, a->n_seq, p.causal ? "causal" : "full",
+                         a->n_q, a->n_k, a->H, p.Hkv, a->D, a->n_seq, p.causal ? "causal" : "full",
                          dtype_name(a->dtype), dtype_name(a->grad_dtype), use_tc ? "tc" : "simt",
                          p.dq_accum ? "fused" : "separate");
     }
@@ -705,6 +819,122 @@ int attn_csr_fwd(const attn_csr_args *a, void *stream) {
     return ATTN_OK;
 }
 
+size_t attn_tree_args_size(void) { return sizeof(attn_tree_args); }
+
+size_t attn_tree_workspace_bytes(const attn_tree_args *a) {
+    TreeParams p;
+    size_t ml;
+    return plan_tree(a, p, false) == ATTN_OK ? tree_layout(p, ml) : 0;
+}
+
+int attn_tree_fwd(const attn_tree_args *a, void *stream) {
+    TreeParams p;
+    const int rc = plan_tree(a, p);
+    if (rc) return rc;
+    if (p.n == 0 || p.n_q == 0) return ATTN_OK;
+    size_t ml;
+    if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255) || a->workspace_bytes < tree_layout(p, ml))
+        return ATTN_EWORKSPACE;
+    p.part_o = static_cast<float *>(a->workspace);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(a->workspace) + ml);
+    if (!(p.c.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e = launch_tree_fwd(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+size_t attn_cache_size(void) { return sizeof(attn_cache); }
+
+size_t attn_cache_workspace_bytes(const attn_cache *c, int32_t n) {
+    CacheParams p;
+    if (plan_cache(c, p) != ATTN_OK || n < 0) return 0;
+    CachePlan w;
+    return cache_plan(p, n, nullptr, w);
+}
+
+int attn_cache_extend(const attn_cache *c, const int32_t *seqs, const int32_t *counts, int32_t n, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    CacheParams p;
+    CachePlan w;
+    const int rc = build_cache(c, n, workspace, workspace_bytes, p, w);
+    if (rc || n == 0) return rc;
+    if (!aligned4(seqs) || !aligned4(counts)) return ATTN_EINVAL;
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e = launch_cache_extend(p, w, seqs, counts, n, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+int attn_cache_fork(const attn_cache *c, const int32_t *parents, const int32_t *children, int32_t n, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+    CacheParams p;
+    CachePlan w;
+    const int rc = build_cache(c, n, workspace, workspace_bytes, p, w);
+    if (rc || n == 0) return rc;
+    if (!aligned4(parents) || !aligned4(children)) return ATTN_EINVAL;
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e = launch_cache_fork(p, w, parents, children, n, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+int attn_cache_keep(const attn_cache *c, const int32_t *seqs, const int32_t *n_draft, const int32_t *keep,
+                    int64_t keep_stride, const int32_t *n_keep, int32_t n, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+    CacheParams p;
+    CachePlan w;
+    const int rc = build_cache(c, n, workspace, workspace_bytes, p, w);
+    if (rc || n == 0) return rc;
+    // without columns (keep_stride 0) nothing can be kept, and keep is not read
+    if (!aligned4(seqs) || !aligned4(n_draft) || !aligned4(n_keep) || keep_stride < 0 ||
+        (keep_stride > 0 && !aligned4(keep)))
+        return ATTN_EINVAL;
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e =
+        launch_cache_keep(p, w, seqs, n_draft, keep, keep_stride, n_keep, n, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+int attn_cache_free(const attn_cache *c, const int32_t *seqs, int32_t n, void *stream) {
+    CacheParams p;
+    const int rc = plan_cache(c, p);
+    if (rc) return rc;
+    if (n < 0) return ATTN_EINVAL;
+    if (n == 0) return ATTN_OK;
+    if (!aligned4(seqs)) return ATTN_EINVAL;
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e = launch_cache_free(p, seqs, n, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+int attn_cache_compact(const attn_cache *c, int32_t *remap, void *workspace, size_t workspace_bytes, void *stream) {
+    CacheParams p;
+    CachePlan w;
+    const int rc = build_cache(c, 0, workspace, workspace_bytes, p, w);
+    if (rc) return rc;
+    if (remap) {
+        if (!aligned4(remap)) return ATTN_EINVAL;
+        w.remap = remap;
+    }
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e = launch_cache_compact(p, w, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+int attn_cache_write(const attn_cache *c, int32_t layer, const int32_t *seqs, const int32_t *cu, int32_t n,
+                     const attn_tensor *k, const attn_tensor *v, int32_t n_rows, void *stream) {
+    CacheParams p;
+    const int rc = plan_cache(c, p);
+    if (rc) return rc;
+    if (layer < 0 || layer >= c->n_layers || n < 0 || n_rows < 0 || !k || !v) return ATTN_EINVAL;
+    if (n == 0 || n_rows == 0) return ATTN_OK;
+    if (!aligned4(seqs) || !aligned4(cu) || !valid_view(*k, c->dtype, true) || !valid_view(*v, c->dtype, true))
+        return ATTN_EINVAL;
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    const int64_t es = (int64_t)elem_size(c->dtype);
+    const cudaError_t e = launch_cache_write(
+        p, layer, seqs, cu, n, static_cast<const char *>(k->ptr), static_cast<const char *>(v->ptr), k->stride_tok * es,
+        k->stride_head * es, v->stride_tok * es, v->stride_head * es, n_rows, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
 const char *attn_strerror(int code) {
     switch (code) {
     case ATTN_OK: return "success";
@@ -713,6 +943,7 @@ const char *attn_strerror(int code) {
     case ATTN_ECUDA: return "CUDA runtime error";
     case ATTN_ETIMEOUT: return "device watchdog timeout";
     case ATTN_EWORKSPACE: return "workspace missing, too small or misaligned";
+    case ATTN_ENOPAGES: return "too few free cache pages";
     default: return "unknown status";
     }
 }

@@ -8,8 +8,8 @@
 // query rows accumulating dq, each owning what it writes.  Here:
 //   preprocess  Dr_i = <dO_i, O_i> (f32) and lse2_i = lse_i * log2(e), one warp
 //               per (row, head);
-//   dkdv        one work item per (sequence, head, 64-key block): loop over the
-//               64-row query blocks that can see the block, recompute
+//   dkdv        one work item per (sequence, key head, 64-key block): loop over the
+//               64-row query blocks of the head's group that can see the block, recompute
 //               P = 2^(s*scale*log2e - lse*log2e), dV += P^T dO, dP = dO V^T,
 //               dS = P (dP - Dr), dK += dS^T Q; write dK * scale and dV once;
 //   dq          one work item per (sequence, head, 64-row query block): loop
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
         __syncthreads();
         if (w >= total) break;
         // causal: earlier key blocks are seen by more query blocks, so run them first
-        const WorkItem it = map_item(w, p.sched_kv.prefix, p.n_seq, p.H, false);
+        const WorkItem it = map_item(w, p.sched_kv.prefix, p.n_seq, p.Hkv, false);
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);
@@ -200,12 +200,15 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
 
         const int qb_first = p.causal ? key0 / B : 0;
         const int qb_end = (Lq + B - 1) / B;
-        const Tin *qbase = gq + (int64_t)q_start * p.q_st + (int64_t)h * p.q_sh;
-        const Tin *dobase = gdo + (int64_t)q_start * p.do_st + (int64_t)h * p.do_sh;
-        const int64_t stat_base = (int64_t)h * p.n_q + q_start;
+        const int per_head = max(0, qb_end - qb_first);
 
-        for (int qb = qb_first; qb < qb_end; ++qb) {
-            const int row0 = qb * B;
+        // the query blocks of every query head that shares this key / value head
+        for (int x = 0; x < per_head * p.group; ++x) {
+            const int g = x / per_head, hq = h * p.group + g;
+            const int row0 = (qb_first + x - g * per_head) * B;
+            const Tin *qbase = gq + (int64_t)q_start * p.q_st + (int64_t)hq * p.q_sh;
+            const Tin *dobase = gdo + (int64_t)q_start * p.do_st + (int64_t)hq * p.do_sh;
+            const int64_t stat_base = (int64_t)hq * p.n_q + q_start;
             __syncthreads();
             stage_tile<Tin, D>(sQ, qbase, p.q_st, row0, Lq);
             stage_tile<Tin, D>(sdO, dobase, p.do_st, row0, Lq);
@@ -332,8 +335,8 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
 
         const int n_keys = p.causal ? min(Lk, row0 + B) : Lk;
         const int n_tiles = (n_keys + B - 1) / B;
-        const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)h * p.k_sh;
-        const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)h * p.v_sh;
+        const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)(h / p.group) * p.k_sh;
+        const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)(h / p.group) * p.v_sh;
 
         for (int kt = 0; kt < n_tiles; ++kt) {
             const int key0 = kt * B;

@@ -7,8 +7,10 @@
 // accumulating dk and dv, one over the query rows accumulating dq, each owning
 // what it writes (no atomics; results are run-to-run deterministic).
 //
-// dkdv kernel -- work item = 128 keys of one (sequence, head); loop over the
-// 128-row query blocks that can see them.  Per block, with the key tile as the
+// dkdv kernel -- work item = 128 keys of one (sequence, key head); loop over the
+// 128-row query blocks that can see them, of every query head that shares the
+// key head (its group), so that dK and dV sum over the group in the same
+// accumulators, in a fixed order.  Per block, with the key tile as the
 // MMA's M dimension (TMEM lane = key):
 //   S^T  = K Q^T          (smem x smem)            -> TMEM [0, 128)
 //   dP^T = V dO^T         (smem x smem)            -> TMEM [128, 256)
@@ -153,11 +155,13 @@ __device__ __forceinline__ void zero_cols(T *dst, int n) {
 // =============================== dK, dV =======================================
 
 struct DkdvInfo {
-    int q_start, Lq, k_start, Lk, h, key0, qb0, nq, t;
+    int q_start, Lq, k_start, Lk, h, key0, qb0, t;
+    int nqh;  // query blocks of one query head that can see the keys
+    int nq;   // query blocks of the item: nqh of each query head that shares key head h, head by head
 };
 
 __device__ __forceinline__ DkdvInfo dkdv_info(const BwdParams &p, int w) {
-    const WorkItem it = map_item(w, p.sched_kv.prefix, p.n_seq, p.H, false);
+    const WorkItem it = map_item(w, p.sched_kv.prefix, p.n_seq, p.Hkv, false);
     DkdvInfo f;
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
@@ -165,7 +169,8 @@ __device__ __forceinline__ DkdvInfo dkdv_info(const BwdParams &p, int w) {
     f.t = it.t;
     f.key0 = it.t * BT;
     f.qb0 = p.causal ? it.t : 0;
-    f.nq = max(0, cdiv(f.Lq, BT) - f.qb0);
+    f.nqh = max(0, cdiv(f.Lq, BT) - f.qb0);
+    f.nq = f.nqh * p.group;
     return f;
 }
 
@@ -223,12 +228,13 @@ __device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, u
         if (f.nq == 0) continue;
         bool ok = true;
         if (dout_role) {
-            for (int qb = 0; qb < f.nq; ++qb) {
-                ok = load_row(bars.q_full, bars.do_empty, dr.slot(), dr.phase(), sDO, &a.tdo,
-                              f.q_start + BT * (f.qb0 + qb), f.h);
-                if (!ok) break;
-                ++dr.i;
-            }
+            for (int g = 0; g < p.group && ok; ++g)
+                for (int qb = 0; qb < f.nqh; ++qb) {
+                    ok = load_row(bars.q_full, bars.do_empty, dr.slot(), dr.phase(), sDO, &a.tdo,
+                                  f.q_start + BT * (f.qb0 + qb), f.h * p.group + g);
+                    if (!ok) break;
+                    ++dr.i;
+                }
             if (!ok) break;
             continue;
         }
@@ -245,12 +251,13 @@ __device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, u
         __syncwarp();
         ++kv_uses;
         kv_pending = true;
-        for (int qb = 0; qb < f.nq; ++qb) {
-            ok = load_row(bars.q_full, bars.q_empty, qr.slot(), qr.phase(), sQ, &a.tq,
-                          f.q_start + BT * (f.qb0 + qb), f.h);
-            if (!ok) break;
-            ++qr.i;
-        }
+        for (int g = 0; g < p.group && ok; ++g)
+            for (int qb = 0; qb < f.nqh; ++qb) {
+                ok = load_row(bars.q_full, bars.q_empty, qr.slot(), qr.phase(), sQ, &a.tq,
+                              f.q_start + BT * (f.qb0 + qb), f.h * p.group + g);
+                if (!ok) break;
+                ++qr.i;
+            }
         if (!ok) break;
     }
     if (aborting(wd) && (threadIdx.x & 31) == 0) {
@@ -551,7 +558,7 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
         // threads fetches one value one block ahead of its use, from an address
         // clamped into the sequence so that the load needs no predicate and no
         // arithmetic waits on it before the value is staged.
-        const float *stat_src = (e < BT ? p.lse2 : p.dr) + (int64_t)f.h * p.n_q + f.q_start;
+        const float *stat_src = (e < BT ? p.lse2 : p.dr) + (int64_t)(f.h * p.group) * p.n_q + f.q_start;
         auto fetch_stat = [&](int qb, bool &valid) -> float {
             const int qr = BT * (f.qb0 + qb) + (e & (BT - 1));
             valid = qr < f.Lq;
@@ -559,14 +566,20 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
         };
         bool stat_valid;
         float stat_next = fetch_stat(0, stat_valid);
-        for (int qb = 0; qb < f.nq; ++qb) {
+        int qh = 0;  // block x of the item is block qh of its query head
+        for (int x = 0; x < f.nq; ++x) {
+            const bool diag = p.causal && (f.qb0 + qh == f.t);  // query block == key block
+            if (++qh == f.nqh) {  // the next block is the first of the group's next query head
+                qh = 0;
+                stat_src += p.n_q;
+            }
             float *sb = stats + (stat_i & 1) * 2 * BT;
             sb[e] = stat_valid ? -stat_next : (e < BT ? -INFINITY : 0.f);
             mbar_arrive_warp(smem_u32(&bars.stats_ready[stat_i & 1]));
             bool ok = mbar_wait(smem_u32(&bars.stats_ready[stat_i & 1]), (stat_i >> 1) & 1, wd);
             if (!__all_sync(0xffffffffu, ok)) return;
             ++stat_i;
-            if (qb + 1 < f.nq) stat_next = fetch_stat(qb + 1, stat_valid);  // in flight during this block
+            if (x + 1 < f.nq) stat_next = fetch_stat(qh, stat_valid);  // in flight during this block
             const float2 *nlse2 = reinterpret_cast<const float2 *>(sb + 64 * wg);
             const float2 *ndr = reinterpret_cast<const float2 *>(sb + BT + 64 * wg);
 
@@ -580,7 +593,6 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
             tmem_ld_wait(r[0]);
             tmem_ld_wait(r[1]);
             float2 pr[32];
-            const bool diag = p.causal && (f.qb0 + qb == f.t);  // query block == key block
             const float2 sc2 = make_float2(sl2, sl2);
             uint32_t pk[32];
 #pragma unroll
@@ -681,8 +693,9 @@ __device__ void dkdvq_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *sta
         ++dqf_cnt;
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
-        const int row = BT * (f.qb0 + j) + kl;
-        float *dst = p.dq_accum + (((int64_t)f.h * (D / 4) + wg * (D / 8)) * p.n_q + f.q_start + row) * 4;
+        const int g = j / f.nqh;  // block j of the item: block j - g nqh of the group's query head g
+        const int row = BT * (f.qb0 + j - g * f.nqh) + kl;
+        float *dst = p.dq_accum + (((int64_t)(f.h * p.group + g) * (D / 4) + wg * (D / 8)) * p.n_q + f.q_start + row) * 4;
         // 32 columns at a time (8 groups of 4); TMEM is released after the last load
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -717,11 +730,12 @@ __device__ void dkdvq_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *sta
             if (live) zero_cols(dst, D);
             continue;
         }
-        const float *stat_src = (e < BT ? p.lse2 : p.dr) + (int64_t)f.h * p.n_q + f.q_start;
+        const float *stat_src = (e < BT ? p.lse2 : p.dr) + (int64_t)(f.h * p.group) * p.n_q + f.q_start;
         auto fetch_stat = [&](int qb, bool &valid) -> float {
-            const int qr = BT * (f.qb0 + qb) + (e & (BT - 1));
+            const int g = qb / f.nqh;
+            const int qr = BT * (f.qb0 + qb - g * f.nqh) + (e & (BT - 1));
             valid = qr < f.Lq;
-            return __ldg(stat_src + min(qr, f.Lq - 1));
+            return __ldg(stat_src + (int64_t)g * p.n_q + min(qr, f.Lq - 1));
         };
         bool stat_valid;
         float stat_next = fetch_stat(0, stat_valid);
@@ -746,7 +760,7 @@ __device__ void dkdvq_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *sta
             tmem_ld_wait(r[0]);
             tmem_ld_wait(r[1]);
             float2 pr[32];
-            const bool diag = p.causal && (f.qb0 + qb == f.t);
+            const bool diag = p.causal && (f.qb0 + qb % f.nqh == f.t);
             const float2 sc2 = make_float2(sl2, sl2);
             uint32_t pk[32];
 #pragma unroll
@@ -916,6 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
 
 struct DqInfo {
     int q_start, Lq, k_start, Lk, h, row0, nk;
+    int hk;  // key / value head of query head h (grouped heads)
 };
 
 __device__ __forceinline__ DqInfo dq_info(const BwdParams &p, int w) {
@@ -924,6 +939,7 @@ __device__ __forceinline__ DqInfo dq_info(const BwdParams &p, int w) {
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
     f.h = it.h;
+    f.hk = it.h / p.group;
     f.row0 = it.t * BT;
     f.nk = p.causal ? cdiv(min(f.Lk, f.row0 + BT), BT) : cdiv(f.Lk, BT);
     return f;
@@ -965,8 +981,8 @@ __device__ void dq_producer(const TcBwdArgs &a, DqBars &bars, uint32_t sQ, uint3
         mbar_expect_tx(bar, 2 * C::kTileBytes);
 #pragma unroll
         for (int g = 0; g < C::kBoxes; ++g) {
-            tma_load_3d(sK + ks * C::kTileBytes + g * C::kBoxBytes, &a.tk, 64 * g, f.k_start + BT * j, f.h, bar);
-            tma_load_3d(sV + vs * C::kTileBytes + g * C::kBoxBytes, &a.tv, 64 * g, f.k_start + BT * j, f.h, bar);
+            tma_load_3d(sK + ks * C::kTileBytes + g * C::kBoxBytes, &a.tk, 64 * g, f.k_start + BT * j, f.hk, bar);
+            tma_load_3d(sV + vs * C::kTileBytes + g * C::kBoxBytes, &a.tv, 64 * g, f.k_start + BT * j, f.hk, bar);
         }
         ++kr.i;
         ++vr.i;
@@ -1321,8 +1337,8 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
 bool make_maps(const BwdParams &p, TcBwdArgs &a) {
     a.p = p;
     return make_tile_map(&a.tq, p.q, p.dtype, p.D, p.n_q, p.H, p.q_st, p.q_sh) &&
-           make_tile_map(&a.tk, p.k, p.dtype, p.D, p.n_k, p.H, p.k_st, p.k_sh) &&
-           make_tile_map(&a.tv, p.v, p.dtype, p.D, p.n_k, p.H, p.v_st, p.v_sh) &&
+           make_tile_map(&a.tk, p.k, p.dtype, p.D, p.n_k, p.Hkv, p.k_st, p.k_sh) &&
+           make_tile_map(&a.tv, p.v, p.dtype, p.D, p.n_k, p.Hkv, p.v_st, p.v_sh) &&
            make_tile_map(&a.tdo, p.dout, p.dtype, p.D, p.n_q, p.H, p.do_st, p.do_sh);
 }
 

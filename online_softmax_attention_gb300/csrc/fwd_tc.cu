@@ -132,6 +132,7 @@ struct PruneShared {
 
 struct ItemInfo {
     int q_start, Lq, k_start, Lk, h, row0;
+    int hk;      // key / value head of the item's query head (grouped heads)
     int c;       // key split (split-K chunk) of this item
     int j0;      // first key tile of the chunk
     int n[NQT];  // key tiles each query tile scans, from j0 on
@@ -153,6 +154,7 @@ __device__ __forceinline__ ItemInfo item_info(const FwdParams &p, int w) {
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
     f.h = it.h;
+    f.hk = it.h / p.group;
     f.c = it.c;
     f.row0 = it.t * kItemRows;
     int full[NQT], most = 0;
@@ -255,7 +257,7 @@ __device__ void producer(const TcFwdArgs &a, FwdBars &bars, int *sched_item, uin
             q_pending[t] = true;
         }
         if (!ok) break;
-        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), f.h);
+        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), f.hk);
         if (!ok) break;
     }
     if (aborting(wd) && (threadIdx.x & 31) == 0) {
@@ -700,8 +702,8 @@ cudaError_t launch_fwd_tc(const FwdParams &p, int num_ctas, cudaStream_t s) {
     args.p = p;
     const int qk_dtype = p.qk_fp8 ? kDtypeE4M3 : p.dtype;
     if (!make_tile_map(&args.tq, p.q, qk_dtype, p.D, p.n_q, p.H, p.q_st, p.q_sh) ||
-        !make_tile_map(&args.tk, p.k, qk_dtype, p.D, p.n_k, p.H, p.k_st, p.k_sh) ||
-        !make_tile_map(&args.tv, p.v, p.dtype, p.D, p.n_k, p.H, p.v_st, p.v_sh))
+        !make_tile_map(&args.tk, p.k, qk_dtype, p.D, p.n_k, p.Hkv, p.k_st, p.k_sh) ||
+        !make_tile_map(&args.tv, p.v, p.dtype, p.D, p.n_k, p.Hkv, p.v_st, p.v_sh))
         return cudaErrorInvalidValue;
     if (p.qk_fp8) return p.D == 128 ? launch_d<128, true>(args, num_ctas, s) : cudaErrorInvalidValue;
     return p.D == 64 ? launch_d<64, false>(args, num_ctas, s) : launch_d<128, false>(args, num_ctas, s);

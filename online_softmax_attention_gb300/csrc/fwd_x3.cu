@@ -164,13 +164,12 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8
 struct SplitJob {
     const float *x;
     int64_t st, sh;
-    int tokens, parts;
+    int tokens, H, parts;
     __nv_bfloat16 *out;  // parts arrays of tokens * H * 64
 };
 
 struct SplitParams {
     SplitJob job[3];
-    int H;
 };
 
 __global__ void __launch_bounds__(256) split_parts_kernel(const SplitParams sp) {
@@ -180,13 +179,13 @@ __global__ void __launch_bounds__(256) split_parts_kernel(const SplitParams sp) 
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     for (int j = 0; j < 3; ++j) {
         const SplitJob &jb = sp.job[j];
-        const int64_t n4 = (int64_t)jb.tokens * sp.H * C4;
-        const int64_t part_elems = (int64_t)jb.tokens * sp.H * D;
+        const int64_t n4 = (int64_t)jb.tokens * jb.H * C4;
+        const int64_t part_elems = (int64_t)jb.tokens * jb.H * D;
         for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += stride) {
             const int64_t row = i / C4;
             const int c4 = (int)(i - row * C4);
-            const int64_t t = row / sp.H;
-            const int h = (int)(row - t * sp.H);
+            const int64_t t = row / jb.H;
+            const int h = (int)(row - t * jb.H);
             float4 r = load4(jb.x + t * jb.st + h * jb.sh + 4 * c4);
             __nv_bfloat16 *dst = jb.out + row * D + 4 * c4;
             for (int k = 0; k < jb.parts; ++k) {
@@ -250,7 +249,7 @@ __device__ void producer(const X3Args &a, X3Bars &bars, int *sched_item, uint32_
             q_pending[t] = true;
         }
         if (!ok) break;
-        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), f.h);
+        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), f.h / p.group);
         if (!ok) break;
     }
     if (aborting(wd)) {
@@ -625,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_x3_kernel(const __grid_consta
 
 }  // namespace
 
-size_t x3_split_bytes(int n_q, int n_k, int H) {
-    return (size_t)kParts * ((int64_t)n_q + 2 * (int64_t)n_k) * H * D * 2;
+size_t x3_split_bytes(int n_q, int n_k, int H, int Hkv) {
+    return (size_t)kParts * ((int64_t)n_q * H + 2 * (int64_t)n_k * Hkv) * D * 2;
 }
 
 bool x3_fwd_supported(const FwdParams &p) {
@@ -638,13 +637,12 @@ cudaError_t launch_fwd_x3(const FwdParams &p, int num_ctas, cudaStream_t s) {
     if (!p.split_ws) return cudaErrorInvalidValue;
     // the bf16 parts, each a contiguous (tokens, heads, 64) array
     __nv_bfloat16 *base = static_cast<__nv_bfloat16 *>(p.split_ws);
-    const int64_t qn = (int64_t)p.n_q * p.H * D, kn = (int64_t)p.n_k * p.H * D;
+    const int64_t qn = (int64_t)p.n_q * p.H * D, kn = (int64_t)p.n_k * p.Hkv * D;
     __nv_bfloat16 *q_parts = base, *k_parts = q_parts + kParts * qn, *v_parts = k_parts + kParts * kn;
     SplitParams sp;
-    sp.H = p.H;
-    sp.job[0] = SplitJob{static_cast<const float *>(p.q), p.q_st, p.q_sh, p.n_q, kParts, q_parts};
-    sp.job[1] = SplitJob{static_cast<const float *>(p.k), p.k_st, p.k_sh, p.n_k, kParts, k_parts};
-    sp.job[2] = SplitJob{static_cast<const float *>(p.v), p.v_st, p.v_sh, p.n_k, kParts, v_parts};
+    sp.job[0] = SplitJob{static_cast<const float *>(p.q), p.q_st, p.q_sh, p.n_q, p.H, kParts, q_parts};
+    sp.job[1] = SplitJob{static_cast<const float *>(p.k), p.k_st, p.k_sh, p.n_k, p.Hkv, kParts, k_parts};
+    sp.job[2] = SplitJob{static_cast<const float *>(p.v), p.v_st, p.v_sh, p.n_k, p.Hkv, kParts, v_parts};
     const int64_t n4 = (qn + kn) / 4;
     const int blocks = (int)std::min<int64_t>((n4 + 255) / 256, (int64_t)sm_count() * 8);
     cudaError_t e = launch_pdl(split_parts_kernel, dim3(blocks), dim3(256), 0, s, sp);
@@ -654,11 +652,11 @@ cudaError_t launch_fwd_x3(const FwdParams &p, int num_ctas, cudaStream_t s) {
 
     X3Args args;
     args.p = p;
-    const int64_t st = (int64_t)p.H * D;
+    const int64_t st = (int64_t)p.H * D, kv_st = (int64_t)p.Hkv * D;
     for (int g = 0; g < kParts; ++g)
         if (!make_tile_map(&args.tq[g], q_parts + g * qn, ATTN_BF16, D, p.n_q, p.H, st, D, BM) ||
-            !make_tile_map(&args.tk[g], k_parts + g * kn, ATTN_BF16, D, p.n_k, p.H, st, D, BN) ||
-            !make_tile_map(&args.tv[g], v_parts + g * kn, ATTN_BF16, D, p.n_k, p.H, st, D, BN))
+            !make_tile_map(&args.tk[g], k_parts + g * kn, ATTN_BF16, D, p.n_k, p.Hkv, kv_st, D, BN) ||
+            !make_tile_map(&args.tv[g], v_parts + g * kn, ATTN_BF16, D, p.n_k, p.Hkv, kv_st, D, BN))
             return cudaErrorInvalidValue;
     if (p.o_dtype != ATTN_F32) return cudaErrorInvalidValue;
     auto kern = fwd_x3_kernel;

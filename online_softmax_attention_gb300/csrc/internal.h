@@ -24,6 +24,7 @@ struct FwdParams {
     float *lse;
     int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;
     int n_q, n_k, H, D;
+    int Hkv, group;    // key / value heads; query heads that share one (H = Hkv * group)
     float scale;       // score scale
     float scale_log2;  // scale * log2(e)
     int causal;
@@ -97,6 +98,67 @@ struct CsrParams {
 
 cudaError_t launch_csr_fwd(const CsrParams &p, cudaStream_t s);
 
+// A paged key / value cache (attn_cache with byte strides and its page size as
+// a shift), and the list arguments of its operations.
+struct CacheParams {
+    char *k, *v;
+    int64_t b_layer, b_page, b_tok, b_head;  // byte strides
+    int *table, *lens, *refs;
+    int64_t table_stride;
+    int n_layers, n_pages, page_shift, H, row_bytes;
+    int max_seqs, max_pages;
+    int *status;
+};
+
+// Workspace of the cache operations: what the one-block plan kernels hand to
+// the kernels that carry the plan out.
+struct CachePlan {
+    int *hdr;    // [0] 1: carry out, 0: refused; [1] compact: live pages; [2] compact: moves
+    int *first;  // n + 1: prefix of the entries' new pages
+    int *len;    // n: extend, keep: length before the call (keep: before the drafts); fork: the parent's
+    int *src;    // n: page whose rows are copied to the entry's first new page, or -1
+    int *pages;  // n_pages: the new pages in order; compact: the pages moved to
+    int *from;   // n_pages: compact: the pages moved from
+    int *remap;  // n_pages: compact: every page's new index
+};
+constexpr int kPlanHdr = 64;
+
+// Attention of new tokens over the cache (attn_tree_args).
+struct TreeParams {
+    CacheParams c;          // k, v: the layer's
+    const void *q;
+    void *o;
+    float *lse;
+    int64_t q_st, q_sh, o_st, o_sh;  // elements
+    const int *seqs, *cu;
+    const unsigned long long *mask;
+    int n, n_q, mask_words;
+    int H, group, D;
+    float scale_log2;
+    int dtype, o_dtype;
+    // partial results of split units: two slots for each block of the grid, rows
+    // (f32 sums relative to the row's max; max in log2 units, sum) in row order
+    float *part_o;          // (2 blocks, tree_rows, D)
+    float2 *part_ml;        // (2 blocks, tree_rows)
+};
+// Query rows (token, head of the group) of a work unit, and the grid.
+int tree_rows(const TreeParams &p);
+int tree_blocks();
+cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s);
+
+cudaError_t launch_cache_extend(const CacheParams &c, const CachePlan &w, const int *seqs, const int *counts, int n,
+                                cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheParams &c, const CachePlan &w, const int *parents, const int *children, int n,
+                              cudaStream_t s);
+cudaError_t launch_cache_keep(const CacheParams &c, const CachePlan &w, const int *seqs, const int *n_draft,
+                              const int *keep, int64_t keep_stride, const int *n_keep, int n, cudaStream_t s);
+cudaError_t launch_cache_free(const CacheParams &c, const int *seqs, int n, cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheParams &c, const CachePlan &w, cudaStream_t s);
+// kb / vb, ks_* / vs_*: the new rows and their byte strides (token, head)
+cudaError_t launch_cache_write(const CacheParams &c, int layer, const int *seqs, const int *cu, int n, const char *kb,
+                               const char *vb, int64_t ks_tok, int64_t ks_head, int64_t vs_tok, int64_t vs_head,
+                               int n_rows, cudaStream_t s);
+
 struct BwdParams {
     const void *q, *k, *v, *o, *dout;
     const float *lse;
@@ -104,6 +166,7 @@ struct BwdParams {
     int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh, do_st, do_sh;
     int64_t dq_st, dq_sh, dk_st, dk_sh, dv_st, dv_sh;
     int n_q, n_k, H, D;
+    int Hkv, group;     // key / value heads; query heads that share one (H = Hkv * group)
     float scale, scale_log2;
     int causal;
     int dtype, o_dtype, grad_dtype;

@@ -34,7 +34,7 @@ cudaError_t launch_fwd_tc(const FwdParams &p, int num_ctas, cudaStream_t s);
 // whether it covers the arguments, the workspace bytes of the operand parts,
 // and the launch (the split prepass, then the attention kernel).
 bool x3_fwd_supported(const FwdParams &p);
-size_t x3_split_bytes(int n_q, int n_k, int H);
+size_t x3_split_bytes(int n_q, int n_k, int H, int Hkv);
 cudaError_t launch_fwd_x3(const FwdParams &p, int num_ctas, cudaStream_t s);
 cudaError_t launch_bwd_dkdv_tc(const BwdParams &p, int num_ctas, cudaStream_t s);
 cudaError_t launch_bwd_dq_tc(const BwdParams &p, int num_ctas, cudaStream_t s);
