@@ -31,7 +31,7 @@ import ctypes
 
 import torch
 
-from . import _abi
+from . import _abi, _host
 from .cache import Cache, TreeCall, tree_fwd
 from ._abi import (ATTN_BF16, ATTN_CAUSAL, ATTN_F16, ATTN_F32, ATTN_FULL, ATTN_KERNEL_AUTO,
                    ATTN_KERNEL_SIMT, ATTN_KERNEL_TC, AttnError, check)
@@ -73,19 +73,26 @@ def _dtype_code(dt: torch.dtype) -> int:
     return _DT[dt]
 
 
-def _view(t: torch.Tensor | None, name: str) -> _abi.AttnTensor:
-    if t is None:
-        return _abi.AttnTensor(None, 0, 0)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be (tokens, heads, D), got {tuple(t.shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+def _fields(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """Address, token stride and head stride of a (tokens, heads, D) tensor."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be (tokens, heads, D), got {tuple(shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the D axis must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     # a size-1 axis is never stepped along, so any aligned stride describes it
-    st = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    sh = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return _abi.AttnTensor(t.data_ptr() if t.numel() else None, st, sh)
+    if shape[0] <= 1:
+        st = shape[1] * shape[2]
+        if shape[0] == 0:
+            return 0, st, sh if shape[1] > 1 else shape[2]
+    return t.data_ptr(), st, sh if shape[1] > 1 else shape[2]
+
+
+def _view(t: torch.Tensor | None, name: str) -> _abi.AttnTensor:
+    return _abi.AttnTensor(None, 0, 0) if t is None else _abi.AttnTensor(*_fields(t, name))
 
 
 def _kv_shape(k: torch.Tensor, v: torch.Tensor, D: int):
@@ -99,6 +106,8 @@ def _kv_shape(k: torch.Tensor, v: torch.Tensor, D: int):
 def _cu(cu, device) -> torch.Tensor | None:
     if cu is None:
         return None
+    if isinstance(cu, torch.Tensor) and cu.dtype == torch.int32 and cu.device == device and cu.is_contiguous():
+        return cu
     cu = torch.as_tensor(cu)
     if cu.dtype != torch.int32:
         cu = cu.to(torch.int32)
@@ -141,36 +150,29 @@ class FwdCall:
         self.o = out if out is not None else torch.empty((Tq, H, D), dtype=out_dtype, device=dev)
         self.lse = lse if lse is not None else torch.empty((H, Tq), dtype=torch.float32, device=dev)
         self.inputs = (q, k, v)
-        a = _abi.FwdArgs()
-        a.q, a.k, a.v, a.o = _view(q, "q"), _view(k, "k"), _view(v, "v"), _view(self.o, "out")
-        a.lse = self.lse.data_ptr() if self.lse.numel() else None
-        a.n_q, a.n_k, a.H, a.D = Tq, Tk, H, D
-        a.scale = float(scale) if scale is not None else D ** -0.5
-        a.relation = ATTN_CAUSAL if causal else ATTN_FULL
-        a.dtype, a.o_dtype = _dtype_code(v.dtype), _dtype_code(self.o.dtype)
-        a.qk_fp8 = 1 if qk_fp8 else 0
-        a.H_kv = H_kv
-        a.n_seq = (self.cu_q.numel() - 1) if self.cu_q is not None else 1
-        a.cu_seqlens_q = self.cu_q.data_ptr() if self.cu_q is not None else None
-        a.cu_seqlens_k = self.cu_k.data_ptr() if self.cu_k is not None else None
-        a.kernel = _KERNELS[kernel]
-        a.num_ctas = int(num_ctas)
-        a.num_splits = int(num_splits)
-        a.prune_threshold = float(prune_threshold)
         # pruned-tile counter (device, int64 storage of the library's uint64)
         self.pruned_tiles = torch.zeros(1, dtype=torch.int64, device=dev) if prune_threshold else None
-        a.pruned_tiles = self.pruned_tiles.data_ptr() if self.pruned_tiles is not None else None
-        lib = _abi.load()
-        need = lib.attn_fwd_workspace_bytes(ctypes.byref(a))
-        self.workspace = workspace if workspace is not None else _workspace(need, dev)
-        a.workspace = self.workspace.data_ptr()
-        a.workspace_bytes = self.workspace.numel() * self.workspace.element_size()
-        self.args = a
-        self._fn = lib.attn_fwd
+        cu_q, cu_k = self.cu_q, self.cu_k
+        self.args = _abi.FwdArgs.from_buffer_copy(_host.FWD.pack(
+            *_fields(q, "q"), *_fields(k, "k"), *_fields(v, "v"), *_fields(self.o, "out"),
+            self.lse.data_ptr(), Tq, Tk, H, D, _host.f32(scale) if scale is not None else D ** -0.5,
+            ATTN_CAUSAL if causal else ATTN_FULL, _dtype_code(v.dtype), _dtype_code(self.o.dtype),
+            (cu_q.numel() - 1) if cu_q is not None else 1, cu_q.data_ptr() if cu_q is not None else 0,
+            cu_k.data_ptr() if cu_k is not None else 0, 0, 0, _KERNELS[kernel], int(num_ctas), int(num_splits),
+            _host.f32(prune_threshold), self.pruned_tiles.data_ptr() if self.pruned_tiles is not None else 0,
+            1 if qk_fp8 else 0, H_kv))
+        self._index = dev.index
+        self._at = ctypes.addressof(self.args)
+        if workspace is None:
+            workspace = _workspace(_host.entry("attn_fwd_workspace_bytes")(self._at), dev)
+        self.workspace = workspace
+        self.args.workspace = workspace.data_ptr()
+        self.args.workspace_bytes = workspace.numel() * workspace.element_size()
+        self._fn = _host.entry("attn_fwd")
 
     def run(self, stream: torch.cuda.Stream | None = None):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        check(self._fn(ctypes.byref(self.args), ctypes.c_void_p(s.cuda_stream)), "attn_fwd")
+        s = _host.raw_stream(self._index) if stream is None else stream.cuda_stream
+        _host.call(self._index, self._fn, "attn_fwd", self._at, s)
         return self.o, self.lse
 
     def selected_kernel(self) -> str:
@@ -245,47 +247,40 @@ class BwdCall:
         self.dk = dk if dk is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
         self.dv = dv if dv is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
         self.inputs = (q, k, v, o, lse, dout)
-        a = _abi.BwdArgs()
-        a.q, a.k, a.v = _view(q, "q"), _view(k, "k"), _view(v, "v")
-        a.o, a.dout = _view(o, "o"), _view(dout, "dout")
-        a.lse = lse.data_ptr() if lse.numel() else None
-        a.dq, a.dk, a.dv = _view(self.dq, "dq"), _view(self.dk, "dk"), _view(self.dv, "dv")
-        a.n_q, a.n_k, a.H, a.D = Tq, Tk, H, D
-        a.scale = float(scale) if scale is not None else D ** -0.5
-        a.relation = ATTN_CAUSAL if causal else ATTN_FULL
-        a.dtype, a.o_dtype = _dtype_code(q.dtype), _dtype_code(o.dtype)
-        a.grad_dtype = _dtype_code(gdt)
-        a.n_seq = (self.cu_q.numel() - 1) if self.cu_q is not None else 1
-        a.cu_seqlens_q = self.cu_q.data_ptr() if self.cu_q is not None else None
-        a.cu_seqlens_k = self.cu_k.data_ptr() if self.cu_k is not None else None
-        a.kernel = _KERNELS[kernel]
-        a.num_ctas = int(num_ctas)
-        a.prune_threshold = float(prune_threshold)  # non-zero: the library refuses (fails closed)
-        a.dq_mode = _DQ_MODES[dq_mode]
-        a.H_kv = H_kv
-        lib = _abi.load()
-        need = lib.attn_bwd_workspace_bytes(ctypes.byref(a))
-        self.workspace = workspace if workspace is not None else _workspace(need, dev)
-        a.workspace = self.workspace.data_ptr()
-        a.workspace_bytes = self.workspace.numel() * self.workspace.element_size()
-        self.args = a
-        self._lib = lib
+        cu_q, cu_k = self.cu_q, self.cu_k
+        # a non-zero prune_threshold: the library refuses (fails closed)
+        self.args = _abi.BwdArgs.from_buffer_copy(_host.BWD.pack(
+            *_fields(q, "q"), *_fields(k, "k"), *_fields(v, "v"), *_fields(o, "o"), *_fields(dout, "dout"),
+            lse.data_ptr(), *_fields(self.dq, "dq"), *_fields(self.dk, "dk"), *_fields(self.dv, "dv"),
+            Tq, Tk, H, D, _host.f32(scale) if scale is not None else D ** -0.5,
+            ATTN_CAUSAL if causal else ATTN_FULL, _dtype_code(q.dtype), _dtype_code(o.dtype), _dtype_code(gdt),
+            (cu_q.numel() - 1) if cu_q is not None else 1, cu_q.data_ptr() if cu_q is not None else 0,
+            cu_k.data_ptr() if cu_k is not None else 0, 0, 0, _KERNELS[kernel], int(num_ctas),
+            _host.f32(prune_threshold), _DQ_MODES[dq_mode], H_kv))
+        self._index = dev.index
+        self._at = ctypes.addressof(self.args)
+        if workspace is None:
+            workspace = _workspace(_host.entry("attn_bwd_workspace_bytes")(self._at), dev)
+        self.workspace = workspace
+        self.args.workspace = workspace.data_ptr()
+        self.args.workspace_bytes = workspace.numel() * workspace.element_size()
+        self._lib = _abi.load()
 
-    def _call(self, fn, name, stream):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        check(fn(ctypes.byref(self.args), ctypes.c_void_p(s.cuda_stream)), name)
+    def _call(self, name, stream):
+        s = _host.raw_stream(self._index) if stream is None else stream.cuda_stream
+        _host.call(self._index, _host.entry(name), name, self._at, s)
 
     def preprocess(self, stream=None):
-        self._call(self._lib.attn_bwd_preprocess, "attn_bwd_preprocess", stream)
+        self._call("attn_bwd_preprocess", stream)
 
     def dkdv(self, stream=None):
-        self._call(self._lib.attn_bwd_dkdv, "attn_bwd_dkdv", stream)
+        self._call("attn_bwd_dkdv", stream)
 
     def dq_stage(self, stream=None):
-        self._call(self._lib.attn_bwd_dq, "attn_bwd_dq", stream)
+        self._call("attn_bwd_dq", stream)
 
     def run(self, stream=None):
-        self._call(self._lib.attn_bwd, "attn_bwd", stream)
+        self._call("attn_bwd", stream)
         return self.dq, self.dk, self.dv
 
     def selected_kernel(self) -> str:

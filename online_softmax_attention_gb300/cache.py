@@ -17,34 +17,11 @@ what a list gets wrong is reported by ``device_status()`` and changes nothing.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from . import _abi
+from . import _abi, _host
 
 _DT = {torch.float16: _abi.ATTN_F16, torch.bfloat16: _abi.ATTN_BF16, torch.float32: _abi.ATTN_F32}
-
-
-def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-class _on:
-    """Makes `device` current for a call when another one is."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, device: torch.device):
-        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
 
 
 def _ints(x, device: torch.device, name: str) -> torch.Tensor:
@@ -60,19 +37,20 @@ def _ints(x, device: torch.device, name: str) -> torch.Tensor:
     return x.to(device=device, dtype=torch.int32).contiguous()
 
 
-def _rows(t: torch.Tensor, name: str, heads: int | None, D: int, dtype: torch.dtype, device) -> _abi.AttnTensor:
-    """A (tokens, heads, D) view for the library."""
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be (tokens, {heads if heads is not None else 'heads'}, {D}), got {tuple(t.shape)}")
+def _rows(t: torch.Tensor, name: str, heads: int | None, D: int, dtype: torch.dtype, device) -> tuple[int, int, int]:
+    """Address, token stride and head stride of a (tokens, heads, D) tensor."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be (tokens, {heads if heads is not None else 'heads'}, {D}), got {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on the cache's device {device}, got {t.device}")
-    if t.stride(2) != 1:
+    st, sh, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name}: the D axis must be contiguous")
     # a size-1 axis is never stepped along, so any aligned stride describes it
-    return _abi.AttnTensor(t.data_ptr() if t.numel() else None, t.stride(0) if t.shape[0] > 1 else t.shape[1] * D,
-                           t.stride(1) if t.shape[1] > 1 else D)
+    return t.data_ptr(), st if shape[0] > 1 else shape[1] * D, sh if shape[1] > 1 else D
 
 
 class Cache:
@@ -96,21 +74,16 @@ class Cache:
             raise ValueError("k, v: the D axis must be contiguous")
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
         self.device = dev
-        c = _abi.Cache()
-        c.k, c.v = k.data_ptr(), v.data_ptr()
-        c.n_layers, c.n_pages, c.page_size, c.H_kv, c.D = k.shape
+        shape, self.dtype = k.shape, k.dtype
+        self.n_layers, _, _, self.n_heads, self.head_dim = shape
         # a size-1 axis is never stepped along: give it the stride of a contiguous layout
-        dense = [c.n_pages * c.page_size * c.H_kv * c.D, c.page_size * c.H_kv * c.D, c.H_kv * c.D, c.D]
-        st = [k.stride(i) if k.shape[i] > 1 else dense[i] for i in range(4)]
-        c.stride_layer, c.stride_page, c.stride_tok, c.stride_head = st
-        c.table, c.lens, c.refs = table.data_ptr(), lens.data_ptr(), refs.data_ptr()
-        c.max_seqs, c.max_pages = table.shape
-        c.table_stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
-        c.dtype = _DT[k.dtype]
-        self.args = c
-        self._ref = ctypes.byref(c)
-        self._lib = _abi.load()
-        if self._lib.attn_cache_workspace_bytes(self._ref, 0) == 0:
+        dense = (shape[1] * shape[2] * shape[3] * shape[4], shape[2] * shape[3] * shape[4], shape[3] * shape[4], shape[4])
+        self.args = _host.CACHE.pack(
+            k.data_ptr(), v.data_ptr(), *(k.stride(i) if shape[i] > 1 else dense[i] for i in range(4)),
+            table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+            table.stride(0) if table.shape[0] > 1 else table.shape[1], shape[0], shape[1], shape[2], shape[3], shape[4],
+            _DT[k.dtype], table.shape[0], table.shape[1])
+        if _host.entry("attn_cache_workspace_bytes")(self.args, 0) == 0:
             raise ValueError("unsupported cache: page_size a power of two up to 1024, D 64 or 128, "
                              "16-byte aligned rows")
 
@@ -128,7 +101,11 @@ class Cache:
 
     def _workspace(self, n: int) -> torch.Tensor:
         # torch's caching allocator returns 512-byte aligned blocks
-        return torch.empty(self._lib.attn_cache_workspace_bytes(self._ref, n), dtype=torch.uint8, device=self.device)
+        return torch.empty(_host.entry("attn_cache_workspace_bytes")(self.args, n), dtype=torch.uint8, device=self.device)
+
+    def _call(self, name: str, *args) -> None:
+        index = self.device.index
+        _host.call(index, _host.entry(name), name, self.args, *args, _host.raw_stream(index))
 
     def _lists(self, n: int | None, **lists) -> list:
         out = [_ints(x, self.device, name) for name, x in lists.items()]
@@ -142,56 +119,44 @@ class Cache:
         """Room for ``counts[i]`` more tokens of sequence ``seqs[i]``: pages and lengths."""
         seqs, counts = self._lists(None, seqs=seqs, counts=counts)
         ws = self._workspace(seqs.numel())
-        with _on(self.device):
-            _abi.check(self._lib.attn_cache_extend(self._ref, seqs.data_ptr(), counts.data_ptr(), seqs.numel(),
-                                                   ws.data_ptr(), ws.numel(), _stream(self.device)), "attn_cache_extend")
+        self._call("attn_cache_extend", seqs.data_ptr(), counts.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel())
 
     def write(self, seqs, cu_seqlens, k: torch.Tensor, v: torch.Tensor, *, layer: int = 0) -> None:
         """New rows (tokens, heads, D) of one layer: rows ``cu[i]:cu[i + 1]`` become the
         last tokens of sequence ``seqs[i]`` (``extend`` made their room)."""
-        c = self.args
         seqs = _ints(seqs, self.device, "seqs")
         cu = _ints(cu_seqlens, self.device, "cu_seqlens")
         if cu.numel() != seqs.numel() + 1:
             raise ValueError(f"cu_seqlens must have {seqs.numel() + 1} entries, got {cu.numel()}")
-        kt = _rows(k, "k", c.H_kv, c.D, self.k.dtype, self.device)
-        vt = _rows(v, "v", c.H_kv, c.D, self.k.dtype, self.device)
+        kt = _host.VIEW.pack(*_rows(k, "k", self.n_heads, self.head_dim, self.dtype, self.device))
+        vt = _host.VIEW.pack(*_rows(v, "v", self.n_heads, self.head_dim, self.dtype, self.device))
         if k.shape[0] != v.shape[0]:
             raise ValueError("k and v must have as many tokens as each other")
-        with _on(self.device):
-            _abi.check(self._lib.attn_cache_write(self._ref, int(layer), seqs.data_ptr(), cu.data_ptr(), seqs.numel(),
-                                                  ctypes.byref(kt), ctypes.byref(vt), k.shape[0],
-                                                  _stream(self.device)), "attn_cache_write")
+        self._call("attn_cache_write", int(layer), seqs.data_ptr(), cu.data_ptr(), seqs.numel(), kt, vt, k.shape[0])
 
     def fork(self, parents, children) -> None:
         """The empty sequence ``children[i]`` becomes a copy of ``parents[i]`` that shares its full pages."""
         parents, children = self._lists(None, parents=parents, children=children)
         ws = self._workspace(parents.numel())
-        with _on(self.device):
-            _abi.check(self._lib.attn_cache_fork(self._ref, parents.data_ptr(), children.data_ptr(), parents.numel(),
-                                                 ws.data_ptr(), ws.numel(), _stream(self.device)), "attn_cache_fork")
+        self._call("attn_cache_fork", parents.data_ptr(), children.data_ptr(), parents.numel(), ws.data_ptr(), ws.numel())
 
     def keep(self, seqs, n_draft, keep: torch.Tensor, n_keep) -> None:
         """Of the last ``n_draft[i]`` tokens of ``seqs[i]`` keeps the ``n_keep[i]`` at the
         ascending offsets ``keep[i, :n_keep[i]]``; the others go."""
         seqs, n_draft, n_keep = self._lists(None, seqs=seqs, n_draft=n_draft, n_keep=n_keep)
-        keep = torch.as_tensor(keep)
+        if not isinstance(keep, torch.Tensor):
+            keep = torch.as_tensor(keep)
         if keep.dim() != 2 or keep.shape[0] != seqs.numel() or keep.is_floating_point() or keep.dtype == torch.bool:
             raise ValueError(f"keep must be ({seqs.numel()}, offsets) whole numbers, got {tuple(keep.shape)}")
         keep = keep.to(device=self.device, dtype=torch.int32).contiguous()
         ws = self._workspace(seqs.numel())
-        with _on(self.device):
-            _abi.check(self._lib.attn_cache_keep(self._ref, seqs.data_ptr(), n_draft.data_ptr(),
-                                                 keep.data_ptr() if keep.numel() else None, keep.shape[1],
-                                                 n_keep.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel(),
-                                                 _stream(self.device)), "attn_cache_keep")
+        self._call("attn_cache_keep", seqs.data_ptr(), n_draft.data_ptr(), keep.data_ptr(), keep.shape[1],
+                   n_keep.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel())
 
     def free(self, seqs) -> None:
         """Empties the sequences; pages that no other sequence holds are free again."""
         seqs = _ints(seqs, self.device, "seqs")
-        with _on(self.device):
-            _abi.check(self._lib.attn_cache_free(self._ref, seqs.data_ptr(), seqs.numel(), _stream(self.device)),
-                       "attn_cache_free")
+        self._call("attn_cache_free", seqs.data_ptr(), seqs.numel())
 
     def compact(self, *, remap: torch.Tensor | None = None) -> None:
         """Moves the live pages to the front of the pool.  ``remap`` (pages,) int32 gets every page's new index."""
@@ -199,10 +164,7 @@ class Cache:
                                   remap.shape != self.refs.shape or not remap.is_contiguous()):
             raise ValueError("remap must be a contiguous int32 vector of one entry per page on the cache's device")
         ws = self._workspace(0)
-        with _on(self.device):
-            _abi.check(self._lib.attn_cache_compact(self._ref, remap.data_ptr() if remap is not None else None,
-                                                    ws.data_ptr(), ws.numel(), _stream(self.device)),
-                       "attn_cache_compact")
+        self._call("attn_cache_compact", remap.data_ptr() if remap is not None else None, ws.data_ptr(), ws.numel())
 
 
 class TreeCall:
@@ -217,56 +179,53 @@ class TreeCall:
                  mask: torch.Tensor | None = None, scale: float | None = None,
                  out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
-        c, dev = cache.args, cache.device
+        dev, D, dtype = cache.device, cache.head_dim, cache.dtype
         self.cache = cache
-        self.seqs = _ints(seqs, dev, "seqs")
-        self.cu = _ints(cu_seqlens_q, dev, "cu_seqlens_q")
-        if self.cu.numel() != self.seqs.numel() + 1:
-            raise ValueError(f"cu_seqlens_q must have {self.seqs.numel() + 1} entries, got {self.cu.numel()}")
-        a = _abi.TreeArgs()
-        a.cache = c
-        a.q = _rows(q, "q", None, c.D, cache.k.dtype, dev)
-        T, H = q.shape[:2]
-        out_dtype = out.dtype if out is not None else out_dtype or q.dtype
-        if out_dtype not in _DT:
-            raise TypeError(f"unsupported dtype {out_dtype}; use the cache's or float32")
-        self.o = out if out is not None else torch.empty((T, H, c.D), dtype=out_dtype, device=dev)
-        self.lse = lse if lse is not None else torch.empty((H, T), dtype=torch.float32, device=dev)
-        if self.o.shape != q.shape:
-            raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(self.o.shape)}")
-        if tuple(self.lse.shape) != (H, T) or self.lse.dtype != torch.float32 or not self.lse.is_contiguous() \
-                or self.lse.device != dev:
+        self.seqs = seqs = _ints(seqs, dev, "seqs")
+        self.cu = cu = _ints(cu_seqlens_q, dev, "cu_seqlens_q")
+        n = seqs.numel()
+        if cu.numel() != n + 1:
+            raise ValueError(f"cu_seqlens_q must have {n + 1} entries, got {cu.numel()}")
+        q_fields = _rows(q, "q", None, D, dtype, dev)
+        T, H, _ = shape = q.shape
+        if out is None:
+            out_dtype = out_dtype or dtype
+            out = torch.empty(shape, dtype=out_dtype, device=dev)
+        else:
+            out_dtype = out.dtype
+            if out.shape != shape:
+                raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+        if out_dtype != dtype and out_dtype != torch.float32:
+            raise TypeError(f"the output is {dtype} or float32, not {out_dtype}")
+        if lse is None:
+            lse = torch.empty((H, T), dtype=torch.float32, device=dev)
+        elif tuple(lse.shape) != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
             raise ValueError(f"lse must be contiguous float32 {(H, T)} on the cache's device")
-        a.o = _rows(self.o, "out", H, c.D, out_dtype, dev)
-        a.lse = self.lse.data_ptr() if self.lse.numel() else None
+        words = 0
         if mask is not None:
             if mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] != T or mask.shape[1] < 1 \
                     or not mask.is_contiguous() or mask.device != dev:
                 raise ValueError(f"mask must be contiguous int64 ({T}, words) on the cache's device")
-            a.mask = mask.data_ptr() if T else None
-            a.mask_words = mask.shape[1]
-        self.inputs = (q, mask)
-        a.seqs, a.cu = self.seqs.data_ptr(), self.cu.data_ptr()
-        a.layer, a.H, a.n, a.n_q = int(layer), H, self.seqs.numel(), T
-        a.scale = float(scale) if scale is not None else c.D ** -0.5
-        a.o_dtype = _DT[out_dtype]
-        self.args = a
-        self._ref = ctypes.byref(a)
-        lib = cache._lib
+            words = mask.shape[1]
+        self.o, self.lse, self.inputs = out, lse, (q, mask)
+        head = (cache.args, int(layer), H, *q_fields, *_rows(out, "out", H, D, out_dtype, dev), lse.data_ptr(),
+                seqs.data_ptr(), cu.data_ptr(), mask.data_ptr() if mask is not None else 0, n, T, words,
+                _host.f32(scale) if scale is not None else D ** -0.5, _DT[out_dtype])
         if workspace is None:
-            with _on(dev):
-                need = lib.attn_tree_workspace_bytes(self._ref)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(self._bytes(_host.TREE.pack(*head, 0, 0), dev.index), dtype=torch.uint8, device=dev)
         self.workspace = workspace
-        a.workspace = workspace.data_ptr()
-        a.workspace_bytes = workspace.numel() * workspace.element_size()
-        self._fn = lib.attn_tree_fwd
+        self.args = _host.TREE.pack(*head, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+    @staticmethod
+    def _bytes(args: bytes, index: int) -> int:
+        need = []
+        _host.call(index, lambda: need.append(_host.entry("attn_tree_workspace_bytes")(args)), "")
+        return max(need[0], 256)  # 0: arguments that the call will refuse
 
     def run(self, stream: torch.cuda.Stream | None = None):
-        dev = self.cache.device
-        s = _stream(dev) if stream is None else ctypes.c_void_p(stream.cuda_stream)
-        with _on(dev):
-            _abi.check(self._fn(self._ref, s), "attn_tree_fwd")
+        index = self.cache.device.index
+        s = _host.raw_stream(index) if stream is None else stream.cuda_stream
+        _host.call(index, _host.entry("attn_tree_fwd"), "attn_tree_fwd", self.args, s)
         return self.o, self.lse
 
 
