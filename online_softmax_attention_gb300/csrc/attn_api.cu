@@ -476,10 +476,15 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
     return ATTN_OK;
 }
 
-size_t tree_layout(const TreeParams &p, size_t &ml) {
-    const size_t rows = 2 * (size_t)tree_blocks() * (size_t)tree_rows(p);
-    ml = align256(sizeof(float) * rows * (size_t)p.D);
-    return ml + align256(sizeof(float2) * rows);
+// Lays the partial results out in the workspace; returns its bytes.
+size_t parts_layout(int blocks, int rows, int D, void *workspace, Parts &w) {
+    const size_t slots = 2 * (size_t)blocks * (size_t)rows;
+    const size_t o = align256(sizeof(float) * slots * (size_t)D), ml = align256(sizeof(float2) * slots);
+    char *at = static_cast<char *>(workspace);
+    w.o = reinterpret_cast<float *>(at);
+    w.ml = reinterpret_cast<float2 *>(at + o);
+    w.cut = reinterpret_cast<CutUnit *>(at + o + ml);
+    return o + ml + align256(sizeof(CutUnit) * (size_t)blocks);
 }
 
 int build_cache(const attn_cache *c, int n, void *workspace, size_t workspace_bytes, CacheParams &p, CachePlan &w) {
@@ -823,8 +828,8 @@ size_t attn_tree_args_size(void) { return sizeof(attn_tree_args); }
 
 size_t attn_tree_workspace_bytes(const attn_tree_args *a) {
     TreeParams p;
-    size_t ml;
-    return plan_tree(a, p, false) == ATTN_OK ? tree_layout(p, ml) : 0;
+    if (plan_tree(a, p, false) != ATTN_OK) return 0;
+    return parts_layout(tree_blocks(), tree_rows(p), p.D, nullptr, p.parts);
 }
 
 int attn_tree_fwd(const attn_tree_args *a, void *stream) {
@@ -832,11 +837,9 @@ int attn_tree_fwd(const attn_tree_args *a, void *stream) {
     const int rc = plan_tree(a, p);
     if (rc) return rc;
     if (p.n == 0 || p.n_q == 0) return ATTN_OK;
-    size_t ml;
-    if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255) || a->workspace_bytes < tree_layout(p, ml))
+    if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255) ||
+        a->workspace_bytes < parts_layout(tree_blocks(), tree_rows(p), p.D, a->workspace, p.parts))
         return ATTN_EWORKSPACE;
-    p.part_o = static_cast<float *>(a->workspace);
-    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(a->workspace) + ml);
     if (!(p.c.status = status_ptr())) return ATTN_ECUDA;
     const cudaError_t e = launch_tree_fwd(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);

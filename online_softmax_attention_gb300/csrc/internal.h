@@ -123,6 +123,33 @@ struct CachePlan {
 };
 constexpr int kPlanHdr = 64;
 
+// Partial results of units that are cut between blocks (stretch.cuh): two slots
+// for each block of the grid, and the blocks' notes for the merge.
+struct CutUnit {
+    int last;     // block that holds the unit's last part; <= the writing block: nothing to merge
+    int q0, hk;   // first query row (token) of the entry; key head
+    int base;     // first (token, head of the group) row of the unit
+    int rows;     // such rows of the whole entry
+    int pad[3];
+};
+struct Parts {
+    float *o;       // (2 blocks, rows, D) f32 sums relative to the row's max
+    float2 *ml;     // (2 blocks, rows): max in log2 units, sum
+    CutUnit *cut;   // (blocks)
+};
+
+// Merge of cut units.  Row r of a slot is row base + (r / tile_rows) * tile_live +
+// r % tile_rows of the entry (r % tile_rows < tile_live; the others do not exist).
+struct PartsMergeParams {
+    Parts parts;
+    void *o;
+    float *lse;
+    int64_t o_st, o_sh;
+    int n_q, group, D, o_dtype;
+    int rows, tile_rows, tile_live, blocks;
+};
+cudaError_t launch_parts_merge(const PartsMergeParams &p, cudaStream_t s);
+
 // Attention of new tokens over the cache (attn_tree_args).
 struct TreeParams {
     CacheParams c;          // k, v: the layer's
@@ -136,10 +163,7 @@ struct TreeParams {
     int H, group, D;
     float scale_log2;
     int dtype, o_dtype;
-    // partial results of split units: two slots for each block of the grid, rows
-    // (f32 sums relative to the row's max; max in log2 units, sum) in row order
-    float *part_o;          // (2 blocks, tree_rows, D)
-    float2 *part_ml;        // (2 blocks, tree_rows)
+    Parts parts;
 };
 // Query rows (token, head of the group) of a work unit, and the grid.
 int tree_rows(const TreeParams &p);

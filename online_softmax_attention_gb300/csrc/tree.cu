@@ -5,13 +5,8 @@
 // keys, a key before the new tokens always visible, a new one by the mask.
 //
 // Decomposition.  A unit is (entry, key head, tile of kRows query rows); its
-// keys are cut in tiles of 32 (16 for rows over 256 bytes).  All units' key tiles stand in one line, and block
-// b of the grid (one per SM) takes the b-th equal stretch of it, whatever the
-// lengths: every block derives its stretch from the lengths alone, so there is
-// no schedule to prepare and no atomic.  A stretch covers whole units, which it
-// writes out, and at most two cut ones, whose partial sums go to the block's two
-// workspace slots; a second kernel merges them in block order (the result does
-// not depend on timing).
+// keys are cut in tiles of 32 (16 for rows over 256 bytes), and every block (one
+// per SM) takes an equal stretch of all units' tiles (stretch.cuh).
 //
 // Inside a block the four warps take the stretch's tiles in turn, each with a
 // ring of cp.async stages of its own (no block-wide barrier in the loop), and
@@ -27,7 +22,7 @@
 #include "../../include/attn.h"
 #include <type_traits>
 
-#include "common.cuh"
+#include "stretch.cuh"
 
 namespace attn {
 
@@ -99,7 +94,7 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     }
 }
 
-// ---- the line of key tiles -------------------------------------------------------
+// ---- the entries ----------------------------------------------------------------
 
 struct Entry {
     int s, L, T, q0;   // sequence, cached tokens, new tokens, first query row
@@ -124,72 +119,6 @@ __device__ __forceinline__ Entry entry_at(const TreeParams &p, int i, int rows, 
     e.key_tiles = (e.L + keys - 1) / keys;
     e.tiles = (long long)p.c.H * e.row_tiles * e.key_tiles;
     return e;
-}
-
-// Sum of `x` over the block's threads, and the sum over the threads before this one.
-__device__ __forceinline__ long long block_prefix(long long x, long long &total) {
-    __shared__ long long s_sum[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long y = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = y;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += s_sum[w];
-        total += s_sum[w];
-    }
-    return before + y - x;
-}
-
-struct Line {
-    long long total, share;  // key tiles in all; of a block
-};
-
-// The stretch's length: equal, and a multiple of the warps' turn where it is long enough.
-__device__ __forceinline__ Line line_of(const TreeParams &p, int rows, int keys) {
-    long long total = 0;
-    for (int base = 0; base < p.n; base += kThreads) {
-        const int i = base + threadIdx.x;
-        const long long t = i < p.n ? entry_at(p, i, rows, keys, blockIdx.x == 0).tiles : 0;
-        long long sum;
-        block_prefix(t, sum);
-        total += sum;
-    }
-    Line l;
-    l.total = total;
-    l.share = (total + gridDim.x - 1) / gridDim.x;
-    if (l.share > kWarps) l.share = (l.share + kWarps - 1) / kWarps * kWarps;
-    return l;
-}
-
-// The entry that tile `at` of the line lies in, and the line's tiles before the entry.
-__device__ __forceinline__ int entry_of(const TreeParams &p, int rows, int keys, long long at, long long &before) {
-    __shared__ int s_entry;
-    __shared__ long long s_before;
-    long long carry = 0;
-    for (int base = 0; base < p.n; base += kThreads) {
-        const int i = base + threadIdx.x;
-        const long long t = i < p.n ? entry_at(p, i, rows, keys, false).tiles : 0;
-        long long sum;
-        const long long mine = carry + block_prefix(t, sum);
-        if (at >= mine && at < mine + t) {
-            s_entry = i;
-            s_before = mine;
-        }
-        carry += sum;
-        if (at < carry) break;  // the same for every thread
-    }
-    __syncthreads();
-    before = s_before;
-    return s_entry;
 }
 
 // ---- attention kernel -------------------------------------------------------------
@@ -221,12 +150,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     pdl_trigger();
     pdl_wait();
 
-    const Line line = line_of(p, kRows, kKeys);
-    long long at = blockIdx.x * line.share;
-    const long long end = min(at + line.share, line.total);
-    if (at >= end) return;
-    long long before;
-    int ei = entry_of(p, kRows, kKeys, at, before);
+    Stretch st;
+    const bool any = find_stretch<kWarps>(
+        p.n, kWarps, [&](int i, bool report) { return entry_at(p, i, kRows, kKeys, report).tiles; }, st);
+    if (!any) {
+        if (tid == 0) p.parts.cut[blockIdx.x].last = -1;
+        return;
+    }
+    long long at = st.at, before = st.before;
+    const long long end = st.end;
+    int ei = st.entry;
     Entry e = entry_at(p, ei, kRows, kKeys, false);
 
     while (at < end) {
@@ -242,6 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
         const int live_rows = min(kRows, e.T * p.group - row0);
         const int ctx = e.L - e.T;  // tokens before the new ones
         at += t1 - t0;
+        if (at == end && tid == 0) {  // a unit that begins here and goes on behind the stretch: noted for the merge
+            const long long last = (before + (long long)(unit + 1) * e.key_tiles - 1) / st.share;
+            p.parts.cut[blockIdx.x] = CutUnit{t0 == 0 ? (int)last : -1, e.q0, hk, row0, e.T * p.group, {0, 0, 0}};
+        }
 
         // query rows: (token, head of the group), row-major; 16-byte chunks swizzled
         // by the row's low bits so that ldmatrix reads are conflict-free
@@ -560,62 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
                 if (d == 0 && p.lse)
                     p.lse[(int64_t)head * p.n_q + e.q0 + t] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
             } else {
-                store4(p.part_o + ((int64_t)slot * kRows + r) * D + d, acc);
-                if (d == 0) p.part_ml[(int64_t)slot * kRows + r] = make_float2(mx, sum);
+                store4(p.parts.o + ((int64_t)slot * kRows + r) * D + d, acc);
+                if (d == 0) p.parts.ml[(int64_t)slot * kRows + r] = make_float2(mx, sum);
             }
         }
         __syncthreads();  // the rings and the query rows may be overwritten
-    }
-}
-
-// ---- merge of cut units ---------------------------------------------------------------
-
-// Block (b, y): the unit that is cut at the end of block b's stretch and begins in
-// it, if there is one: its parts are slot 1 of block b and slot 0 of the blocks
-// behind it.  One warp per row.
-template <typename Tout, int D>
-__global__ void __launch_bounds__(kThreads) tree_merge_kernel(const TreeParams p, int rows, int keys) {
-    pdl_trigger();
-    pdl_wait();
-    const Line line = line_of(p, rows, keys);
-    const long long begin = blockIdx.x * line.share, end = begin + line.share;
-    if (end >= line.total) return;
-    long long before;
-    const int ei = entry_of(p, rows, keys, end - 1, before);
-    const Entry e = entry_at(p, ei, rows, keys, false);
-    const int unit = (int)((end - 1 - before) / e.key_tiles);
-    const long long u0 = before + (long long)unit * e.key_tiles, u1 = u0 + e.key_tiles;
-    if (u0 < begin || u1 <= end) return;  // begins before this block, or is not cut here
-    const int last = (int)((u1 - 1) / line.share);
-    const int hk = unit / e.row_tiles, row0 = (unit - hk * e.row_tiles) * rows;
-    const int live_rows = min(rows, e.T * p.group - row0);
-    const int lane = threadIdx.x & 31, d = lane * (D / 32);
-    for (int r = blockIdx.y * kWarps + (threadIdx.x >> 5); r < live_rows; r += gridDim.y * kWarps) {
-        auto slot = [&](int b) { return (int64_t)(b == (int)blockIdx.x ? 2 * b + 1 : 2 * b) * rows + r; };
-        float mx = -INFINITY;
-        for (int b = blockIdx.x + lane; b <= last; b += 32) mx = fmaxf(mx, p.part_ml[slot(b)].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_use = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc[D / 32];
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
-#pragma unroll 4
-        for (int b = blockIdx.x; b <= last; ++b) {
-            const float2 ml = p.part_ml[slot(b)];
-            const float f = exp2_approx(ml.x - m_use);
-            const float *part = p.part_o + slot(b) * D + d;
-            sum = fmaf(f, ml.y, sum);
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(f, part[j], acc[j]);
-        }
-        const int t = (row0 + r) / p.group, head = hk * p.group + (row0 + r) - t * p.group;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        Tout *orow = static_cast<Tout *>(p.o) + (e.q0 + t) * p.o_st + head * p.o_sh + d;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) orow[j] = from_f32<Tout>(acc[j] * inv);
-        if (lane == 0 && p.lse)
-            p.lse[(int64_t)head * p.n_q + e.q0 + t] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
     }
 }
 
@@ -629,10 +515,19 @@ cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
     e = launch_pdl(kern, dim3(blocks), dim3(kThreads), C::kSmem, s, p);
     count_launch();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(tree_merge_kernel<Tout, D>, dim3(blocks, C::kRows / kWarps), dim3(kThreads), 0, s, p, C::kRows,
-                   C::kKeys);
-    count_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
+    PartsMergeParams m;
+    m.parts = p.parts;
+    m.o = p.o;
+    m.lse = p.lse;
+    m.o_st = p.o_st;
+    m.o_sh = p.o_sh;
+    m.n_q = p.n_q;
+    m.group = p.group;
+    m.D = p.D;
+    m.o_dtype = p.o_dtype;
+    m.rows = m.tile_rows = m.tile_live = C::kRows;
+    m.blocks = blocks;
+    return launch_parts_merge(m, s);
 }
 
 template <typename T, typename Tout, int D>
