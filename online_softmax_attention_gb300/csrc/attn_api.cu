@@ -158,6 +158,21 @@ int auto_splits(const FwdParams &p, bool use_tc) {
     return c >= 2 ? (int)c : 1;
 }
 
+// Lays the partial results out in the workspace; returns its bytes.
+size_t parts_layout(int blocks, int rows, int D, void *workspace, Parts &w) {
+    const size_t slots = 2 * (size_t)blocks * (size_t)rows;
+    const size_t o = align256(sizeof(float) * slots * (size_t)D), ml = align256(sizeof(float2) * slots);
+    char *at = static_cast<char *>(workspace);
+    w.o = reinterpret_cast<float *>(at);
+    w.ml = reinterpret_cast<float2 *>(at + o);
+    w.cut = reinterpret_cast<CutUnit *>(at + o + ml);
+    return o + ml + align256(sizeof(CutUnit) * (size_t)blocks);
+}
+
+// The packed kernel's blocks each scan all sequences' lengths (384 at a time, a few
+// microseconds for this many); batches of more sequences take the prepared schedule.
+constexpr int kPackedMaxSeqs = 2048;
+
 struct FwdLayout {
     size_t o_parts, lse_parts, split_ops, total;
 };
@@ -185,6 +200,10 @@ size_t split_op_bytes(const FwdParams &p, bool use_tc) {
 }
 
 FwdLayout fwd_layout_of(const FwdParams &p, bool use_tc) {
+    if (p.packed) {
+        Parts w;
+        return FwdLayout{0, 0, 0, parts_layout(sm_count(), kGroupRows, p.D, nullptr, w)};
+    }
     return fwd_layout(p.n_seq, p.n_q, p.H, p.D, p.n_splits, split_op_bytes(p, use_tc));
 }
 
@@ -239,7 +258,11 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     rc = choose_tc(a->kernel, tc_fwd_supported(p), use_tc);
     if (rc) return rc;
     if (p.qk_fp8 && !use_tc) return ATTN_EUNSUPPORTED;  // no CUDA-core fp8 path
-    p.n_splits = p.prune ? 1 : (a->num_splits > 0 ? a->num_splits : auto_splits(p, use_tc));
+    // grouped heads: packed query rows (group_tc.cu), which balance by themselves; a caller
+    // that fixes the splits or the grid gets the ungrouped kernel's schedule
+    p.packed = p.group > 1 && use_tc && !p.qk_fp8 && !p.prune && a->num_splits == 0 && a->num_ctas == 0 &&
+               a->n_seq <= kPackedMaxSeqs && a->n_k > 0 && group_supported(p.dtype, p.D, p.group);
+    p.n_splits = p.prune || p.packed ? 1 : (a->num_splits > 0 ? a->num_splits : auto_splits(p, use_tc));
     // work items (tiles x heads x splits) are numbered in int32
     const int64_t tiles = (int64_t)a->H * ((int64_t)a->n_q / kSimtBlock + a->n_seq + 1);
     if (tiles * p.n_splits >= (int64_t)1 << 31) return ATTN_EUNSUPPORTED;
@@ -476,17 +499,6 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
     return ATTN_OK;
 }
 
-// Lays the partial results out in the workspace; returns its bytes.
-size_t parts_layout(int blocks, int rows, int D, void *workspace, Parts &w) {
-    const size_t slots = 2 * (size_t)blocks * (size_t)rows;
-    const size_t o = align256(sizeof(float) * slots * (size_t)D), ml = align256(sizeof(float2) * slots);
-    char *at = static_cast<char *>(workspace);
-    w.o = reinterpret_cast<float *>(at);
-    w.ml = reinterpret_cast<float2 *>(at + o);
-    w.cut = reinterpret_cast<CutUnit *>(at + o + ml);
-    return o + ml + align256(sizeof(CutUnit) * (size_t)blocks);
-}
-
 int build_cache(const attn_cache *c, int n, void *workspace, size_t workspace_bytes, CacheParams &p, CachePlan &w) {
     const int rc = plan_cache(c, p);
     if (rc) return rc;
@@ -553,6 +565,25 @@ int attn_fwd(const attn_fwd_args *a, void *stream) {
                      p.qk_fp8 ? "e4m3+" : "", dtype_name(a->dtype), dtype_name(a->o_dtype),
                      use_tc ? "tc" : "simt", p.n_splits, (double)a->prune_threshold);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.packed) {
+        GroupParams g = {};
+        g.q = p.q; g.o = p.o; g.lse = p.lse;
+        g.q_st = p.q_st; g.q_sh = p.q_sh; g.o_st = p.o_st; g.o_sh = p.o_sh;
+        g.n = p.n_seq; g.n_q = p.n_q; g.H = p.H; g.Hkv = p.Hkv; g.group = p.group; g.D = p.D;
+        g.cu_q = p.cu_q;
+        g.causal = p.causal;
+        g.k = p.k; g.v = p.v;
+        g.k_st = p.k_st; g.k_sh = p.k_sh; g.v_st = p.v_st; g.v_sh = p.v_sh;
+        g.n_k = p.n_k;
+        g.cu_k = p.cu_k;
+        g.scale_log2 = p.scale_log2;
+        g.dtype = p.dtype; g.o_dtype = p.o_dtype;
+        parts_layout(sm_count(), kGroupRows, p.D, a->workspace, g.parts);
+        g.status = p.status;
+        g.watchdog_cycles = p.watchdog_cycles;
+        const cudaError_t e = launch_group(g, s);
+        return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+    }
     const int block = use_tc ? tc_fwd_block_rows(p) : kSimtBlock;
     // One sequence whose work items all fit in one wave of the default grid:
     // static schedule (CTA i runs item i), no preparation launch.
@@ -841,6 +872,7 @@ int attn_tree_fwd(const attn_tree_args *a, void *stream) {
         a->workspace_bytes < parts_layout(tree_blocks(), tree_rows(p), p.D, a->workspace, p.parts))
         return ATTN_EWORKSPACE;
     if (!(p.c.status = status_ptr())) return ATTN_ECUDA;
+    p.watchdog_cycles = watchdog_cycles();
     const cudaError_t e = launch_tree_fwd(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
 }

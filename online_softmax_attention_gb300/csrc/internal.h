@@ -51,6 +51,8 @@ struct FwdParams {
     // f32 inputs on the tensor cores: workspace region for the bf16 parts of
     // q, k and v (see fwd_x3.cu), else null
     void *split_ws;
+    // grouped heads with packed query rows (group_tc.cu)
+    int packed;
 };
 
 // Key-tile range [begin, end) of chunk c when n_tiles key tiles are cut into
@@ -164,10 +166,43 @@ struct TreeParams {
     float scale_log2;
     int dtype, o_dtype;
     Parts parts;
+    long long watchdog_cycles;
 };
-// Query rows (token, head of the group) of a work unit, and the grid.
+// Query rows (token, head of the group) of a work unit (kGroupRows: the
+// tensor-core kernel of group_tc.cu), and the grid.
 int tree_rows(const TreeParams &p);
 int tree_blocks();
+
+// Grouped attention on the tensor cores with packed query rows (group_tc.cu):
+// over contiguous keys (prompts) or a cache.
+struct GroupParams {
+    const void *q;
+    void *o;
+    float *lse;
+    int64_t q_st, q_sh, o_st, o_sh;  // elements
+    int n, n_q, H, Hkv, group, D;
+    const int *cu_q;                 // n + 1 offsets, or null: one entry of n_q
+    int causal;                      // contiguous keys: query i sees keys up to i; else all
+    // contiguous keys: k, v views and their offsets (null: one entry of n_k)
+    const void *k, *v;
+    int64_t k_st, k_sh, v_st, v_sh;
+    int n_k;
+    const int *cu_k;
+    // cached keys: the layer's pools, the entries' sequences, the new tokens' mask
+    int paged;
+    CacheParams c;
+    const int *seqs;
+    const unsigned long long *mask;
+    int mask_words;
+    float scale_log2;
+    int dtype, o_dtype;
+    Parts parts;
+    int *status;
+    long long watchdog_cycles;
+};
+constexpr int kGroupRows = 256;  // query rows of a unit (two 128-row tiles)
+bool group_supported(int dtype, int D, int group);
+cudaError_t launch_group(const GroupParams &p, cudaStream_t s);
 cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s);
 
 cudaError_t launch_cache_extend(const CacheParams &c, const CachePlan &w, const int *seqs, const int *counts, int n,

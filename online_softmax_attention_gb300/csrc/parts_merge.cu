@@ -63,7 +63,9 @@ __global__ void __launch_bounds__(32 * kWarps) parts_merge_kernel(const PartsMer
 
 template <typename Tout>
 cudaError_t launch_typed(const PartsMergeParams &p, cudaStream_t s) {
-    const dim3 grid(p.blocks, (p.rows + kWarps - 1) / kWarps);
+    // up to 16 blocks a unit: most blocks find no note and leave at once
+    const int y = (p.rows + kWarps - 1) / kWarps;
+    const dim3 grid(p.blocks, y < 16 ? y : 16);
     if (p.D == 64) return launch_pdl(parts_merge_kernel<Tout, 64>, grid, dim3(32 * kWarps), 0, s, p);
     return launch_pdl(parts_merge_kernel<Tout, 128>, grid, dim3(32 * kWarps), 0, s, p);
 }

@@ -19,6 +19,11 @@ constexpr int kDtypeE4M3 = 16;
 bool make_tile_map(CUtensorMap *m, const void *ptr, int dtype, int D, int tokens, int H,
                    int64_t stride_tok, int64_t stride_head, int box_rows = 128);
 
+// A 16-bit map of `rank` (3 or 4) axes, innermost first: dims in elements,
+// strides in bytes of axes 1 .., box in elements; 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *ptr, int dtype, int rank, const uint64_t *dims, const uint64_t *strides,
+              const uint32_t *box);
+
 // Whether the tensor-core kernels cover these arguments (dtype, D, strides).
 bool tc_fwd_supported(const FwdParams &p);
 bool tc_bwd_supported(const BwdParams &p);

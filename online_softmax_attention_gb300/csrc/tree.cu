@@ -552,13 +552,34 @@ cudaError_t launch_out(const TreeParams &p, cudaStream_t s) {
 
 int tree_blocks() { return sm_count(); }
 
-// 32 rows a unit where the entries have more than 16 on average: the keys of a
-// unit are read once for all its rows.
+// Rows by the entries' average: the keys of a unit are read once for all its
+// rows, so entries of more rows take larger units.
 int tree_rows(const TreeParams &p) {
-    return p.dtype != ATTN_F32 && p.n > 0 && (int64_t)p.n_q * p.group > (int64_t)16 * p.n ? 32 : 16;
+    if (p.dtype == ATTN_F32 || p.n < 1) return 16;
+    const int64_t rows = (int64_t)p.n_q * p.group;
+    if (rows > (int64_t)32 * p.n && p.c.page_shift >= 3 && group_supported(p.dtype, p.D, p.group)) return kGroupRows;
+    return rows > (int64_t)16 * p.n ? 32 : 16;
 }
 
 cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s) {
+    if (tree_rows(p) == kGroupRows) {
+        GroupParams g = {};
+        g.q = p.q; g.o = p.o; g.lse = p.lse;
+        g.q_st = p.q_st; g.q_sh = p.q_sh; g.o_st = p.o_st; g.o_sh = p.o_sh;
+        g.n = p.n; g.n_q = p.n_q; g.H = p.H; g.Hkv = p.c.H; g.group = p.group; g.D = p.D;
+        g.cu_q = p.cu;
+        g.paged = 1;
+        g.c = p.c;
+        g.seqs = p.seqs;
+        g.mask = p.mask;
+        g.mask_words = p.mask_words;
+        g.scale_log2 = p.scale_log2;
+        g.dtype = p.dtype; g.o_dtype = p.o_dtype;
+        g.parts = p.parts;
+        g.status = p.c.status;
+        g.watchdog_cycles = p.watchdog_cycles;
+        return launch_group(g, s);
+    }
     switch (p.dtype) {
     case ATTN_F16: return launch_out<__half>(p, s);
     case ATTN_BF16: return launch_out<__nv_bfloat16>(p, s);

@@ -168,13 +168,13 @@ def test_shared_heads_sum_their_gradients_in_a_fixed_order():
 
 
 def test_equal_to_repeated_heads():
-    """The forward and dq do the same arithmetic as on repeated key / value heads."""
+    """The unpacked forward and dq do the same arithmetic as on repeated key / value heads."""
     lens, g = [200, 77], 3
     x, cu = make(lens, 6, 2, 64, torch.float16, 20, True)
     c = {n: t.cuda() for n, t in x.items()}
     k, v = (c[n].repeat_interleave(g, 1) for n in "kv")
-    o, lse = attn.fwd(c["q"], c["k"], c["v"], cu_seqlens_q=cu)
-    o2, lse2 = attn.fwd(c["q"], k, v, cu_seqlens_q=cu)
+    o, lse = attn.fwd(c["q"], c["k"], c["v"], cu_seqlens_q=cu, num_splits=1)
+    o2, lse2 = attn.fwd(c["q"], k, v, cu_seqlens_q=cu, num_splits=1)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     dq = attn.bwd(c["q"], c["k"], c["v"], o, lse, c["do"], cu_seqlens_q=cu)[0]
     assert torch.equal(dq, attn.bwd(c["q"], k, v, o, lse, c["do"], cu_seqlens_q=cu)[0])
