@@ -43,6 +43,12 @@ constexpr int kThreads = 384;
 constexpr int kSegs = 4;                // ring of unit parts
 constexpr int kSegConsumers = 1 + 8;    // MMA warp, softmax warps
 constexpr float kRescaleThreshold = 8.f;  // log2 units, as fwd_tc.cu
+// What a unit costs besides its key tiles, in key tiles (about 1.7 us each): the
+// queries' loads, the masked tile, the epilogue.
+#ifndef ATTN_GROUP_LEAD
+#define ATTN_GROUP_LEAD 2
+#endif
+constexpr int kLead = ATTN_GROUP_LEAD;
 
 template <int D>
 struct Cfg {
@@ -71,6 +77,7 @@ struct Seg {
     int nkv;          // the larger one; -1: the stretch is done
     int j0;
     int L, ctx;       // keys; keys that every row sees
+    int end[NQT];     // keys that any row of each tile may see
     int slot;         // workspace slot of a cut unit; -1: the whole unit
 };
 
@@ -168,8 +175,8 @@ __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, 
     return e;
 }
 
-__device__ __forceinline__ long long entry_tiles(const GroupParams &p, const Entry &e, int per) {
-    return e.T > 0 ? p.Hkv * unit_tiles(p, e, per, e.units) : 0;
+__device__ __forceinline__ long long entry_work(const GroupParams &p, const Entry &e, int per) {
+    return e.T > 0 ? work_of((long long)p.Hkv * e.units, p.Hkv * unit_tiles(p, e, per, e.units)) : 0;
 }
 
 // Bounded wait for outstanding TMA writes before the CTA exits after an abort.
@@ -198,6 +205,7 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
     auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, wd));
     };
+    const bool ordered = p.paged ? p.mask == nullptr : p.causal != 0;
     // pages: this lane's piece of a key tile
     const int psz = p.paged ? min(1 << p.c.page_shift, BN) : BN, pieces = BN / psz;
     Entry e = {};
@@ -210,22 +218,23 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
         return 0;  // any page that exists: the entry's result is reported as invalid
     };
 
-    long long at = st.at;
-    int ei = st.entry, hk = 0, unit = 0, t0 = 0;
-    if (at < st.end) {
+    long long u0 = st.end;  // where the unit begins in the line
+    int ei = st.entry, hk = 0, unit = 0;
+    if (st.at < st.end) {
         e = entry_at(p, ei, per, false);
-        const long long per_head = unit_tiles(p, e, per, e.units);
-        long long off = at - st.before;
+        auto length = [&](int n) { return unit_tiles(p, e, per, n) + (long long)st.lead * n; };  // of n units
+        const long long per_head = length(e.units);
+        long long off = st.at - st.before;
         hk = (int)(off / per_head);
         off -= hk * per_head;
         int lo = 0, hi = e.units - 1;  // the last unit that begins at or before `off`
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (unit_tiles(p, e, per, mid) <= off) lo = mid;
+            if (length(mid) <= off) lo = mid;
             else hi = mid - 1;
         }
         unit = lo;
-        t0 = (int)(off - unit_tiles(p, e, per, lo));
+        u0 = st.before + hk * per_head + length(lo);
     }
     bool ok = true;
     int i = 0;
@@ -240,14 +249,30 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
         ++i;
         return true;
     };
-    while (at < st.end) {
+    // the next unit of the line, if one begins before the stretch ends
+    auto next_unit = [&](int n_unit) {
+        u0 += st.lead + n_unit;
+        if (++unit < e.units) return;
+        unit = 0;
+        if (++hk < p.Hkv) return;
+        hk = 0;
+        if (u0 < st.end) {
+            do e = entry_at(p, ++ei, per, false);
+            while (e.T == 0);
+        }
+    };
+    while (u0 < st.end) {
+        const int n_unit = tiles_to(p, e, (unit + 1) * per);
+        const int t0 = st.tile(st.at, u0, n_unit), t1 = st.tile(st.end, u0, n_unit);
+        if (t0 >= t1) {
+            next_unit(n_unit);
+            continue;
+        }
         Seg g;
         g.q0 = e.q0;
         g.hk = hk;
         g.L = e.L;
         g.ctx = e.ctx;
-        const int n_unit = tiles_to(p, e, (unit + 1) * per);
-        const int t1 = (int)min((long long)n_unit, t0 + (st.end - at));
         g.j0 = t0;
         g.nkv = t1 - t0;
 #pragma unroll
@@ -255,14 +280,13 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
             g.tok[t] = unit * per + t * tok_tile;
             g.live[t] = max(0, min(tok_tile, e.T - g.tok[t])) * p.group;
             g.n[t] = g.live[t] > 0 ? max(0, min(tiles_to(p, e, g.tok[t] + tok_tile), t1) - t0) : 0;
+            g.end[t] = ordered ? min(e.L, e.ctx + min(g.tok[t] + tok_tile, e.T)) : e.L;
         }
-        const bool cut_behind = t1 < n_unit;
-        g.slot = t0 == 0 && !cut_behind ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
-        at += t1 - t0;
-        if (at == st.end && lane == 0) {  // a unit that begins here and goes on behind the stretch: for the merge
-            const long long last = (at - t1 + n_unit - 1) / st.share;
-            p.parts.cut[blockIdx.x] =
-                CutUnit{t0 == 0 && cut_behind ? (int)last : -1, e.q0, hk, unit * per * p.group, e.T * p.group, {0, 0, 0}};
+        g.slot = t1 - t0 == n_unit ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
+        if (t0 == 0 && t1 < n_unit && lane == 0) {  // begins here and goes on behind the stretch: for the merge
+            long long last = (u0 + st.lead + n_unit - 1) / st.share;
+            if (st.tile(last * st.share, u0, n_unit) == n_unit) --last;
+            p.parts.cut[blockIdx.x] = CutUnit{(int)last, e.q0, hk, unit * per * p.group, e.T * p.group, {0, 0, 0}};
         }
         ok = publish(g);
         if (!ok) break;
@@ -319,17 +343,7 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
             if (j + 1 < t1) page = page_at(j + 1);
         }
         if (!ok) break;
-        t0 = 0;
-        if (++unit == e.units) {
-            unit = 0;
-            if (++hk == p.Hkv) {
-                hk = 0;
-                if (at < st.end) {
-                    do e = entry_at(p, ++ei, per, false);
-                    while (e.T == 0);
-                }
-            }
-        }
+        next_unit(n_unit);
     }
     if (ok) {
         Seg g;
@@ -346,6 +360,10 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
     }
 }
 
+// Of a key tile whose first `left` keys a query tile may see, the 16-key MMA steps
+// that hold them (one at least: an entry without keys).
+__device__ __forceinline__ int key_steps(int left) { return min(BN / 16, max(1, (left + 15) >> 4)); }
+
 // ---- warp 1: MMA issuer (the whole warp, one elected lane issuing) ----------------------
 
 template <int D, bool kBF16>
@@ -354,7 +372,9 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
     using C = Cfg<D>;
     const GroupParams &p = a.p;
     // a negative scale negates Q in the score MMA, so the softmax always scales by |scale|
-    const uint32_t idS = idesc_f16(kBF16, BM, BN, 0) | (p.scale_log2 < 0.f ? (1u << 13) : 0u);
+    const uint32_t negate = p.scale_log2 < 0.f ? (1u << 13) : 0u;
+    const uint32_t idS = idesc_f16(kBF16, BM, BN, 0) | negate;
+    auto idS_of = [&](int steps) { return idesc_f16(kBF16, BM, 0, 0) | negate | ((uint32_t)(2 * steps) << 17); };
     constexpr uint32_t idO = idesc_f16(kBF16, BM, D, 1);
     uint32_t q_cnt[NQT] = {0, 0}, p_cnt[NQT] = {0, 0}, of_cnt[NQT] = {0, 0};
     RingPos<C::kKStages> kr;
@@ -362,25 +382,31 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
     const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(sK, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sV, C::kBoxBytes, 1024);
-    auto issue_s = [&](int t, uint32_t kslot) {  // S_t = Q_t K^T
+    auto issue_s = [&](int t, uint32_t kslot, int steps) {  // S_t = Q_t K^T over 16 * steps keys
+        const uint32_t id = steps == BN / 16 ? idS : idS_of(steps);
         const uint64_t qa = q_desc + sdesc_step(t * C::kTileBytes);
         const uint64_t ka = k_desc + sdesc_step(kslot * C::kTileBytes);
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = sdesc_step((kk >> 2) * C::kBoxBytes + (kk & 3) * 32);
-                mma_ss(tmem + BN * t, qa + off, ka + off, idS, kk > 0);
+                mma_ss(tmem + BN * t, qa + off, ka + off, id, kk > 0);
             }
             tc_commit(smem_u32(&bars.s_full[t]));
         }
         __syncwarp();
     };
-    auto issue_pv = [&](int t, uint32_t vslot, bool acc) {  // U_t (+)= P_t V
+    auto issue_pv = [&](int t, uint32_t vslot, bool acc, int steps) {  // U_t (+)= P_t V over 16 * steps keys
         const uint64_t va = v_desc + sdesc_step(vslot * C::kTileBytes);
         if (elect_one()) {
+            if (steps == BN / 16) {
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-                mma_ts(tmem + 256 + D * t, tmem + BN * t + 8 * kk, va + sdesc_step(kk * 2048), idO, acc || kk > 0);
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    mma_ts(tmem + 256 + D * t, tmem + BN * t + 8 * kk, va + sdesc_step(kk * 2048), idO, acc || kk > 0);
+            } else {
+                for (int kk = 0; kk < steps; ++kk)
+                    mma_ts(tmem + 256 + D * t, tmem + BN * t + 8 * kk, va + sdesc_step(kk * 2048), idO, acc || kk > 0);
+            }
         }
         __syncwarp();
     };
@@ -395,6 +421,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         const int slot = i % kSegs;
         if (!wait(bars.seg_full[slot], (i / kSegs) & 1)) return;
         const int n0 = segs[slot].n[0], n1 = segs[slot].n[1], nkv = segs[slot].nkv;
+        const int key0 = BN * segs[slot].j0, left[NQT] = {segs[slot].end[0] - key0, segs[slot].end[1] - key0};
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
         if (nkv < 0) return;
@@ -412,7 +439,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
 #pragma unroll
         for (int t = 0; t < NQT; ++t) {
             if (n[t] == 0) continue;
-            issue_s(t, ks);
+            issue_s(t, ks, key_steps(left[t]));
             if (n[t] == 1) commit(bars.q_empty[t]);
         }
         commit(bars.k_empty[ks]);
@@ -432,7 +459,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
                     ++of_cnt[t];
                 }
                 tc_fence_after();
-                issue_pv(t, vs, j > 0);
+                issue_pv(t, vs, j > 0, key_steps(left[t] - BN * j));
                 if (j == n[t] - 1) commit(bars.o_done[t]);
                 if (j + 1 < n[t]) {
                     if (!have_next_k) {
@@ -442,7 +469,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
                         have_next_k = true;
                         tc_fence_after();
                     }
-                    issue_s(t, nks);
+                    issue_s(t, nks, key_steps(left[t] - BN * (j + 1)));
                     if (j + 1 == n[t] - 1) commit(bars.q_empty[t]);
                 }
             }
@@ -463,6 +490,12 @@ __device__ __forceinline__ uint32_t mask_bits(const unsigned long long *row, int
     unsigned long long x = w < words ? row[w] >> sh : 0ull;
     if (sh > 32 && w + 1 < words) x |= row[w + 1] << (64 - sh);
     return (uint32_t)x;
+}
+
+// Bits of the keys [u, u + 32) that are below `lim`.
+__device__ __forceinline__ uint32_t bits_below(int lim, int u) {
+    const int n = lim - u;
+    return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
 }
 
 // As store_rows_chunk (sm100.cuh) for rows at any addresses: at[k] is the address
@@ -517,12 +550,31 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
     const int quarter = warp & 3;     // TMEM lane quarter this warp may access
     const int lrow = 32 * quarter + lane;
     const int my_tok = lrow / p.group;  // token of this row within the tile
+    // tokens (low half) and heads (high half) of the rows whose pieces this lane stores
+    uint32_t out_at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = 32 * quarter + (lane & ~3) + k, tk = r / p.group;
+        out_at[k] = (uint32_t)tk | (uint32_t)(r - tk * p.group) << 16;
+    }
     const uint32_t s_addr = tmem_addr(tmem, 32 * quarter, BN * t);
     const uint32_t o_addr = tmem_addr(tmem, 32 * quarter, 256 + D * t);
     // as in fwd_tc.cu: |scale| (the score MMA negated S), never 0 so that -inf stays -inf
     const float sl2 = fmaxf(fabsf(p.scale_log2), FLT_MIN);
     const bool ordered = p.paged ? p.mask == nullptr : p.causal != 0;
     uint32_t s_cnt = 0, o_cnt = 0, kv_base = 0;
+    // U_t *= alpha; U_t is stable once S_j(t) has completed, after PV_{j-1}(t)
+    auto scale_u = [&](float alpha) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[32];
+            tmem_ld_x32(o_addr + 32 * c, u);
+            tmem_ld_wait(u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+            tmem_st_x32(o_addr + 32 * c, u);
+        }
+    };
 
     for (int i = 0;; ++i) {
         const int slot = i % kSegs;
@@ -530,6 +582,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         if (!__all_sync(0xffffffffu, ok)) return;
         const Seg &sg = segs[slot];
         const int nkv = sg.nkv, n = sg.n[t], n_first = sg.n[0], live = sg.live[t], tok = sg.tok[t], j0 = sg.j0;
+        const int end = sg.end[t], end_first = sg.end[0];
         const int L = sg.L, ctx = sg.ctx, q0 = sg.q0, hk = sg.hk, part = sg.slot;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
@@ -552,6 +605,84 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
+            const int key0 = BN * (j0 + j);
+            const int steps = key_steps(end - key0);
+            if (L - key0 < 16 * steps && (t == 0 || j >= n_first || L - key0 >= 16 * key_steps(end_first - key0))) {
+                // V rows of the last MMA step behind the entry's end (another sequence's, stale
+                // slots; NaN times p = 0 would be NaN): zeroed, by the query tile whose value
+                // contraction comes first.  (V landed with K, before the scores waited for.)
+                const int first = max(0, L - key0), chunks = (16 * steps - first) * 8;  // 16-byte chunks of a box
+                const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + first * 128;
+#pragma unroll
+                for (int b = 0; b < C::kBoxes; ++b)
+                    if (lrow < chunks) st_shared_v4(base + b * C::kBoxBytes + 16 * lrow, 0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            // the tile reaches the end, or new tokens that not every row sees
+            const bool masked = key0 + BN > L || key0 + BN > ctx + (ordered ? tok + 1 : 0);
+            const int lim = min(L - key0, ordered ? ctx + token + 1 - key0 : BN);  // keys [0, lim) admitted, but for the mask
+            auto visible = [&](int c) -> uint32_t {  // of the keys [32 c, 32 c + 32) of a masked tile
+                uint32_t bits = bits_below(lim, 32 * c);
+                if (p.mask) bits &= mrow ? mask_bits(mrow, p.mask_words, key0 + 32 * c - ctx) : 0u;
+                return bits;
+            };
+            if (masked) {
+                // masked or short: 32 keys at a time, scores read twice (for the max, then for p).
+                // A loop, and the only masked code: straight-line code for 128 masked columns is
+                // fetched anew for each unit's few masked tiles, which cost more than it computed
+                const int chunks = (steps + 1) >> 1;
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t r[32];
+                    tmem_ld_x32(s_addr + 32 * c, r);
+                    const uint32_t bits = visible(c);
+                    tmem_ld_wait(r);
+                    float x[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? __uint_as_float(r[e]) : -INFINITY;
+                    mx = fmaxf(mx, row_max<32>(x));
+                }
+                mx *= sl2;
+                const float m_new = fmaxf(m, mx);
+                const bool rescale = j > 0 && __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
+                float alpha = 1.f;
+                if (j == 0) {
+                    m = m_new;
+                } else if (rescale) {
+                    alpha = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
+                    m = m_new;
+                }
+                const float m_use = m == -INFINITY ? 0.f : m;
+                float sum = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t r[32], pk[16];
+                    tmem_ld_x32(s_addr + 32 * c, r);
+                    const uint32_t bits = visible(c);
+                    tmem_ld_wait(r);
+                    float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float x = (bits >> e) & 1 ? fmaf(__uint_as_float(r[e]), sl2, -m_use) : -INFINITY;
+                        const float pv = exp2_approx(x);
+                        part_sum[e & 3] += pv;
+                        r[e] = __float_as_uint(pv);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), kBF16);
+                    sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+                    // P of 32 keys takes 16 columns: those of scores read before
+                    tmem_st_x16(s_addr + 16 * c, pk);
+                }
+                l = l * alpha + sum;
+                if (rescale) scale_u(alpha);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(smem_u32(&bars.p_full[t]));
+                continue;
+            }
             uint32_t r[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_x32(s_addr + 32 * c, r[c]);
@@ -560,40 +691,6 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             float s[BN];
 #pragma unroll
             for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(r[c >> 5][c & 31]);
-
-            const int key0 = BN * (j0 + j);
-            // the tile reaches the end, or new tokens that not every row sees
-            const bool tail = key0 + BN > L;
-            if (tail || key0 + BN > ctx + (ordered ? tok + 1 : 0)) {
-                if (p.mask) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int left = L - key0 - 32 * w;
-                        uint32_t bits = mrow && left > 0 ? mask_bits(mrow, p.mask_words, key0 + 32 * w - ctx) : 0u;
-                        if (left < 32) bits &= left > 0 ? (1u << left) - 1 : 0u;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((bits >> c) & 1)) s[32 * w + c] = -INFINITY;
-                    }
-                } else {
-                    const int lim = min(L - key0, ordered ? ctx + token + 1 - key0 : BN);  // keys [0, lim) admitted
-#pragma unroll
-                    for (int c = 0; c < BN; ++c)
-                        if (c >= lim) s[c] = -INFINITY;
-                }
-            }
-            if (tail && (t == 0 || j >= n_first)) {
-                // V rows behind the end (another sequence's, stale slots; NaN times p = 0 would
-                // be NaN): zeroed by the query tile whose value contraction comes first
-                // (V landed with K, before the scores that this warp has waited for)
-                const int first = max(0, L - key0), chunks = (BN - first) * 8;  // 16-byte chunks of a box
-                const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + first * 128;
-                for (int x = lrow; x < chunks * C::kBoxes; x += BM) {
-                    const int b = x / chunks;
-                    st_shared_v4(base + b * C::kBoxBytes + 16 * (x - b * chunks), 0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-            }
             const float mx = row_max<BN>(s) * sl2;
             const float m_new = fmaxf(m, mx);
             // refresh the max only when it grew by more than 2^8 somewhere in the warp; a row
@@ -626,18 +723,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
             const float2 a03 = __fadd2_rn(a01, a23);
             l = l * alpha + (a03.x + a03.y);
-            if (rescale) {
-                // U_t is stable here: S_j(t) completed after PV_{j-1}(t)
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t u[32];
-                    tmem_ld_x32(o_addr + 32 * c, u);
-                    tmem_ld_wait(u);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                    tmem_st_x32(o_addr + 32 * c, u);
-                }
-            }
+            if (rescale) scale_u(alpha);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive_warp(smem_u32(&bars.p_full[t]));
@@ -652,21 +738,17 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             const float inv = l > 0.f ? 1.f / l : 0.f;
             Tout *at[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 32 * quarter + (lane & ~3) + k, tk = r / p.group;
-                at[k] = r < live ? static_cast<Tout *>(p.o) + (int64_t)(q0 + tok + tk) * p.o_st +
-                                       (int64_t)(hk * p.group + r - tk * p.group) * p.o_sh
-                                 : nullptr;
-            }
+            for (int k = 0; k < 4; ++k)
+                at[k] = 32 * quarter + (lane & ~3) + k < live
+                            ? static_cast<Tout *>(p.o) + (int64_t)(q0 + tok + (int)(out_at[k] & 0xffff)) * p.o_st +
+                                  (int64_t)(hk * p.group + (int)(out_at[k] >> 16)) * p.o_sh
+                            : nullptr;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t u[32];
                 tmem_ld_x32(o_addr + 32 * c, u);
                 tmem_ld_wait(u);
-                // (the row's own factor, before the lanes exchange pieces of rows)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * inv);
-                store_rows_at<Tout>(u, 1.f, at, 32 * c, lane);
+                store_rows_at<Tout>(u, inv, at, 32 * c, lane);
             }
             if (lrow < live && p.lse)
                 p.lse[(int64_t)(hk * p.group + lrow - my_tok * p.group) * p.n_q + q0 + token] =
@@ -746,8 +828,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     const int per = NQT * (BM / a.p.group);
     Stretch st;
     const bool any = find_stretch<kThreads / 32>(
-        a.p.n, 1, [&](int i, bool report) { return entry_tiles(a.p, entry_at(a.p, i, per, report), per); }, st);
-    if (!any && threadIdx.x == 0) a.p.parts.cut[blockIdx.x].last = -1;
+        a.p.n, 1, kLead, [&](int i, bool report) { return entry_work(a.p, entry_at(a.p, i, per, report), per); }, st);
+    if (!any) st.end = st.at;
+    if (threadIdx.x == 0) a.p.parts.cut[blockIdx.x].last = -1;  // the loading warp may put a unit there
+    __syncthreads();
 
     if (warp < 4) {
         regs_dec<C::kRegsProducer>();

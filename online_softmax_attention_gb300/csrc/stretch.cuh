@@ -44,47 +44,70 @@ __device__ __forceinline__ long long block_prefix(long long x, long long &total)
     return before + y - x;
 }
 
+// Work of an entry: its units and the key tiles they scan, in one word, so that
+// one prefix sum adds up both (fewer than 2^24 units and 2^40 tiles in all).
+__device__ __forceinline__ long long work_of(long long units, long long tiles) { return units << 40 | tiles; }
+__device__ __forceinline__ long long work_units(long long w) { return w >> 40; }
+__device__ __forceinline__ long long work_tiles(long long w) { return w & ((1ll << 40) - 1); }
+
 struct Stretch {
-    long long at, end;   // the block's tiles of the line
-    long long share;     // tiles of a block (the last ones may have fewer)
-    long long before;    // tiles of the entries before the first one
-    int entry;           // entry that tile `at` lies in
+    long long at, end;   // the block's part of the line
+    long long share;     // length of a block's part (the last ones may be shorter)
+    long long before;    // length of the line before entry `entry`
+    int entry;           // entry that position `at` lies in
+    int lead, snap;      // of a unit of n tiles: see tile()
+
+    // A unit takes lead + n positions: `lead` stands for what a unit costs besides its
+    // tiles (loading queries, masks, writing out).  Tile at which position x cuts the
+    // unit that begins at u0; a cut that would part fewer than `snap` tiles moves to
+    // the unit's edge.
+    __device__ __forceinline__ int tile(long long x, long long u0, int n) const {
+        const long long o = x - u0 - lead;
+        return o <= 0 || o < snap ? 0 : o >= n || o > n - snap ? n : (int)o;
+    }
 };
 
-// The block's stretch; tiles(i, report): key tiles of entry i's units.  The
-// share is a multiple of `turn` where it is longer than that.  False: no work.
+// The block's stretch; work(i, report): work_of entry i.  A unit counts `lead` more
+// positions than tiles where blocks have `kLeadShare` tiles and more; the share is a
+// multiple of `turn` where it is longer than that.  False: no work.
+constexpr int kLeadShare = 12;
 template <int kWarps, typename F>
-__device__ __forceinline__ bool find_stretch(int n, int turn, F tiles, Stretch &s) {
+__device__ __forceinline__ bool find_stretch(int n, int turn, int lead, F work, Stretch &s) {
     __shared__ int s_entry;
     __shared__ long long s_before;
     long long total = 0, mine = 0, count = 0;
     for (int base = 0; base < n; base += 32 * kWarps) {
         const int i = base + threadIdx.x;
-        count = i < n ? tiles(i, blockIdx.x == 0) : 0;
+        count = i < n ? work(i, blockIdx.x == 0) : 0;
         long long sum;
         mine = total + block_prefix<kWarps>(count, sum);
         total += sum;
     }
-    s.share = (total + gridDim.x - 1) / gridDim.x;
+    const bool long_enough = work_tiles(total) >= (long long)kLeadShare * gridDim.x;
+    s.lead = long_enough ? lead : 0;
+    s.snap = long_enough && lead ? 2 : 0;
+    auto length = [&](long long w) { return work_tiles(w) + s.lead * work_units(w); };
+    const long long all = length(total);
+    s.share = (all + gridDim.x - 1) / gridDim.x;
     if (s.share > turn) s.share = (s.share + turn - 1) / turn * turn;
     s.at = blockIdx.x * s.share;
-    s.end = min(s.at + s.share, total);
+    s.end = min(s.at + s.share, all);
     if (s.at >= s.end) return false;
     // the entry: in hand if one pass covered them all
     long long carry = 0;
     for (int base = 0; base < n; base += 32 * kWarps) {
         const int i = base + threadIdx.x;
         if (n > 32 * kWarps) {
-            count = i < n ? tiles(i, false) : 0;
+            count = i < n ? work(i, false) : 0;
             long long sum;
             mine = carry + block_prefix<kWarps>(count, sum);
             carry += sum;
         }
-        if (s.at >= mine && s.at < mine + count) {
+        if (s.at >= length(mine) && s.at < length(mine + count)) {
             s_entry = i;
-            s_before = mine;
+            s_before = length(mine);
         }
-        if (n > 32 * kWarps && s.at < carry) break;  // the same for every thread
+        if (n > 32 * kWarps && s.at < length(carry)) break;  // the same for every thread
     }
     __syncthreads();
     s.entry = s_entry;

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
 
     Stretch st;
     const bool any = find_stretch<kWarps>(
-        p.n, kWarps, [&](int i, bool report) { return entry_at(p, i, kRows, kKeys, report).tiles; }, st);
+        p.n, kWarps, 0, [&](int i, bool report) { return work_of(0, entry_at(p, i, kRows, kKeys, report).tiles); }, st);
     if (!any) {
         if (tid == 0) p.parts.cut[blockIdx.x].last = -1;
         return;
