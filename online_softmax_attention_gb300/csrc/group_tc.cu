@@ -580,109 +580,45 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         const int slot = i % kSegs;
         bool ok = mbar_wait(smem_u32(&bars.seg_full[slot]), (i / kSegs) & 1, wd);
         if (!__all_sync(0xffffffffu, ok)) return;
+        // read where it is needed, so that the inner loop keeps its registers; given back at the end
         const Seg &sg = segs[slot];
-        const int nkv = sg.nkv, n = sg.n[t], n_first = sg.n[0], live = sg.live[t], tok = sg.tok[t], j0 = sg.j0;
-        const int end = sg.end[t], end_first = sg.end[0];
-        const int L = sg.L, ctx = sg.ctx, q0 = sg.q0, hk = sg.hk, part = sg.slot;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
+        const int nkv = sg.nkv, n = sg.n[t];
         if (nkv < 0) return;
         const uint32_t kv0 = kv_base;  // key tiles this block took before this part
         kv_base += nkv;
-        const int64_t part_row = (int64_t)part * kGroupRows + BM * t;
         if (n == 0) {
             // rows of a cut unit that see none of this part's keys
-            if (lrow < live) p.parts.ml[part_row + lrow] = make_float2(-INFINITY, 0.f);
+            if (lrow < sg.live[t])
+                p.parts.ml[(int64_t)sg.slot * kGroupRows + BM * t + lrow] = make_float2(-INFINITY, 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
             continue;
         }
-        const int token = tok + my_tok;  // of the entry
-        const unsigned long long *mrow =
-            p.mask && lrow < live ? p.mask + (int64_t)(q0 + token) * p.mask_words : nullptr;
+        // tiles whose keys every row of the query tile sees
+        const int plain = max(0, min(n, (min(sg.L, sg.ctx + (ordered ? sg.tok[t] + 1 : 0)) >> 7) - sg.j0));
 
         float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < n; ++j) {
+        // the running max refreshed with a tile's largest score: only when it grew by more than
+        // 2^8 somewhere in the warp (else the stale max is kept, which leaves O = U / l exact);
+        // the factor for l and U
+        auto refresh = [&](float mx, bool first, bool &rescale) -> float {
+            const float m_new = fmaxf(m, mx);
+            rescale = !first && __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
+            float alpha = 1.f;
+            if (first) {
+                m = m_new;
+            } else if (rescale) {
+                alpha = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
+                m = m_new;
+            }
+            return alpha;
+        };
+        int j = 0;
+        for (; j < plain; ++j) {
             ok = mbar_wait(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
-            const int key0 = BN * (j0 + j);
-            const int steps = key_steps(end - key0);
-            if (L - key0 < 16 * steps && (t == 0 || j >= n_first || L - key0 >= 16 * key_steps(end_first - key0))) {
-                // V rows of the last MMA step behind the entry's end (another sequence's, stale
-                // slots; NaN times p = 0 would be NaN): zeroed, by the query tile whose value
-                // contraction comes first.  (V landed with K, before the scores waited for.)
-                const int first = max(0, L - key0), chunks = (16 * steps - first) * 8;  // 16-byte chunks of a box
-                const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + first * 128;
-#pragma unroll
-                for (int b = 0; b < C::kBoxes; ++b)
-                    if (lrow < chunks) st_shared_v4(base + b * C::kBoxBytes + 16 * lrow, 0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
-            // the tile reaches the end, or new tokens that not every row sees
-            const bool masked = key0 + BN > L || key0 + BN > ctx + (ordered ? tok + 1 : 0);
-            const int lim = min(L - key0, ordered ? ctx + token + 1 - key0 : BN);  // keys [0, lim) admitted, but for the mask
-            auto visible = [&](int c) -> uint32_t {  // of the keys [32 c, 32 c + 32) of a masked tile
-                uint32_t bits = bits_below(lim, 32 * c);
-                if (p.mask) bits &= mrow ? mask_bits(mrow, p.mask_words, key0 + 32 * c - ctx) : 0u;
-                return bits;
-            };
-            if (masked) {
-                // masked or short: 32 keys at a time, scores read twice (for the max, then for p).
-                // A loop, and the only masked code: straight-line code for 128 masked columns is
-                // fetched anew for each unit's few masked tiles, which cost more than it computed
-                const int chunks = (steps + 1) >> 1;
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    uint32_t r[32];
-                    tmem_ld_x32(s_addr + 32 * c, r);
-                    const uint32_t bits = visible(c);
-                    tmem_ld_wait(r);
-                    float x[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? __uint_as_float(r[e]) : -INFINITY;
-                    mx = fmaxf(mx, row_max<32>(x));
-                }
-                mx *= sl2;
-                const float m_new = fmaxf(m, mx);
-                const bool rescale = j > 0 && __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
-                float alpha = 1.f;
-                if (j == 0) {
-                    m = m_new;
-                } else if (rescale) {
-                    alpha = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
-                    m = m_new;
-                }
-                const float m_use = m == -INFINITY ? 0.f : m;
-                float sum = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    uint32_t r[32], pk[16];
-                    tmem_ld_x32(s_addr + 32 * c, r);
-                    const uint32_t bits = visible(c);
-                    tmem_ld_wait(r);
-                    float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float x = (bits >> e) & 1 ? fmaf(__uint_as_float(r[e]), sl2, -m_use) : -INFINITY;
-                        const float pv = exp2_approx(x);
-                        part_sum[e & 3] += pv;
-                        r[e] = __float_as_uint(pv);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), kBF16);
-                    sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
-                    // P of 32 keys takes 16 columns: those of scores read before
-                    tmem_st_x16(s_addr + 16 * c, pk);
-                }
-                l = l * alpha + sum;
-                if (rescale) scale_u(alpha);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive_warp(smem_u32(&bars.p_full[t]));
-                continue;
-            }
             uint32_t r[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_x32(s_addr + 32 * c, r[c]);
@@ -691,18 +627,8 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             float s[BN];
 #pragma unroll
             for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(r[c >> 5][c & 31]);
-            const float mx = row_max<BN>(s) * sl2;
-            const float m_new = fmaxf(m, mx);
-            // refresh the max only when it grew by more than 2^8 somewhere in the warp; a row
-            // that has admitted nothing yet takes its first finite max at once
-            const bool rescale = j > 0 && __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
-            float alpha = 1.f;
-            if (j == 0) {
-                m = m_new;
-            } else if (rescale) {
-                alpha = m == -INFINITY ? 0.f : exp2_approx(m - m_new);
-                m = m_new;
-            }
+            bool rescale;
+            const float alpha = refresh(row_max<BN>(s) * sl2, j == 0, rescale);
             const float m_use = m == -INFINITY ? 0.f : m;
             // p = 2^(s * scale * log2e - m): packed FMA pairs, four packed partial sums
             const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_use, -m_use);
@@ -728,6 +654,85 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             tc_fence_before();
             mbar_arrive_warp(smem_u32(&bars.p_full[t]));
         }
+        for (; j < n; ++j) {
+            // masked tiles, 32 keys at a time, scores read twice (for the max, then for p).  A loop,
+            // and the only masked code: straight-line code for 128 masked columns is fetched anew
+            // for each unit's few masked tiles, which cost more than it computed (107 -> 98 us on
+            // 48 packed prompts of 9 to 420 tokens)
+            const int key0 = BN * (sg.j0 + j), left = sg.L - key0;
+            const int steps = key_steps(sg.end[t] - key0);
+            const int token = sg.tok[t] + my_tok;
+            const int lim = min(left, ordered ? sg.ctx + token + 1 - key0 : BN);  // keys [0, lim) admitted, but for the mask
+            const unsigned long long *mrow =
+                p.mask && lrow < sg.live[t] ? p.mask + (int64_t)(sg.q0 + token) * p.mask_words : nullptr;
+            auto visible = [&](int c) -> uint32_t {  // of the keys [32 c, 32 c + 32)
+                uint32_t bits = bits_below(lim, 32 * c);
+                if (p.mask) bits &= mrow ? mask_bits(mrow, p.mask_words, key0 + 32 * c - sg.ctx) : 0u;
+                return bits;
+            };
+            ok = mbar_wait(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
+            ++s_cnt;
+            if (!__all_sync(0xffffffffu, ok)) return;
+            tc_fence_after();
+            if (left < 16 * steps && (t == 0 || j >= sg.n[0] || left >= 16 * key_steps(sg.end[0] - key0))) {
+                // V rows of the last MMA step behind the entry's end (another sequence's, stale
+                // slots; NaN times p = 0 would be NaN): zeroed, by the query tile whose value
+                // contraction comes first.  (V landed with K, before the scores waited for.)
+                const int first = max(0, left), chunks = (16 * steps - first) * 8;  // 16-byte chunks of a box
+                const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + first * 128;
+#pragma unroll
+                for (int b = 0; b < C::kBoxes; ++b)
+                    if (lrow < chunks) st_shared_v4(base + b * C::kBoxBytes + 16 * lrow, 0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            const int chunks = (steps + 1) >> 1;
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t r[32];
+                tmem_ld_x32(s_addr + 32 * c, r);
+                const uint32_t bits = visible(c);
+                tmem_ld_wait(r);
+                float x[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? __uint_as_float(r[e]) : -INFINITY;
+                mx = fmaxf(mx, row_max<32>(x));
+            }
+            bool rescale;
+            const float alpha = refresh(mx * sl2, j == 0, rescale);
+            const float m_use = m == -INFINITY ? 0.f : m;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t r[32], pk[16];
+                tmem_ld_x32(s_addr + 32 * c, r);
+                const uint32_t bits = visible(c);
+                tmem_ld_wait(r);
+                float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float x = (bits >> e) & 1 ? fmaf(__uint_as_float(r[e]), sl2, -m_use) : -INFINITY;
+                    const float pv = exp2_approx(x);
+                    part_sum[e & 3] += pv;
+                    r[e] = __float_as_uint(pv);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    pk[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), kBF16);
+                sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+                // P of 32 keys takes 16 columns: those of scores read before
+                tmem_st_x16(s_addr + 16 * c, pk);
+            }
+            l = l * alpha + sum;
+            if (rescale) scale_u(alpha);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(smem_u32(&bars.p_full[t]));
+        }
+        const int live = sg.live[t], tok = sg.tok[t], q0 = sg.q0, hk = sg.hk, part = sg.slot, token = tok + my_tok;
+        const int64_t part_row = (int64_t)part * kGroupRows + BM * t;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
 
         // epilogue: O = U / l and lse, or the part's U, m and l
         ok = mbar_wait(smem_u32(&bars.o_done[t]), o_cnt & 1, wd);
