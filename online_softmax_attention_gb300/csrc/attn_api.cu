@@ -593,8 +593,8 @@ int attn_fwd(const attn_fwd_args *a, void *stream) {
         p.static_items = (int)items;
     cudaError_t e = cudaSuccess;
     if (!p.static_items)
-        e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.H, block, p.causal, 0, p.n_splits,
-                        p.sched, p.status, s);
+        e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.causal, {{{p.H, block, 0, p.n_splits, p.sched}, {}}}, 1,
+                        p.status, s);
     if (e != cudaSuccess) return set_cuda_error(e);
     const int grid = p.static_items ? p.static_items : a->num_ctas;
     if (p.n_splits == 1) {
@@ -654,11 +654,10 @@ int attn_bwd_preprocess(const attn_bwd_args *a, void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int kv_block = use_tc ? tc_bwd_kv_block(p) : kSimtBlock;
     const int q_block = use_tc ? tc_bwd_q_block(p) : kSimtBlock;
-    cudaError_t e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.Hkv, kv_block, p.causal, 1,
-                                1, p.sched_kv, p.status, s);
-    if (e == cudaSuccess && !p.dq_accum)  // the fused dq needs no query-block schedule
-        e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.H, q_block, p.causal, 0,
-                        1, p.sched_q, p.status, s);
+    // (the fused dq needs no query-block schedule)
+    cudaError_t e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.causal,
+                                {{{p.Hkv, kv_block, 1, 1, p.sched_kv}, {p.H, q_block, 0, 1, p.sched_q}}},
+                                p.dq_accum ? 1 : 2, p.status, s);
     if (e == cudaSuccess) e = launch_bwd_preprocess(p, s);
     if (e == cudaSuccess && p.dq_accum) e = launch_dq_accum_zero(p, s);
     if (e != cudaSuccess) return set_cuda_error(e);

@@ -6,8 +6,8 @@
 // Dr = sum(dO * O) and nests that recompute each pair's p, dp and
 // ds = p * (dp - Dr): one over the keys accumulating dk and dv, one over the
 // query rows accumulating dq, each owning what it writes.  Here:
-//   preprocess  Dr_i = <dO_i, O_i> (f32) and lse2_i = lse_i * log2(e), one warp
-//               per (row, head);
+//   preprocess  Dr_i = <dO_i, O_i> (f32) and lse2_i = lse_i * log2(e), a group of
+//               lanes per (row, head);
 //   dkdv        one work item per (sequence, key head, 64-key block): loop over the
 //               64-row query blocks of the head's group that can see the block, recompute
 //               P = 2^(s*scale*log2e - lse*log2e), dV += P^T dO, dP = dO V^T,
@@ -87,59 +87,80 @@ __device__ __forceinline__ void tile_nt(float (&acc)[4][4], const float *A, cons
 
 // ---- preprocess: Dr = rowsum(dO * O), and lse in the base-2 domain ----------
 
-constexpr int kRowDotRows = 4;  // rows per warp with loads in flight at once
+constexpr int kRowDotRows = 4;  // rows per lane group with loads in flight at once
 
-// One warp per row r = t * H + h (token t, head h); each pass of a warp issues
-// the loads of kRowDotRows rows before reducing any, so that enough bytes are
-// in flight per SM to cover the HBM latency.  Rows are numbered in int64
-// (n_q * H * 32 threads can exceed 2^32); a warp's rows are nwarps apart, so
-// (t, h) advance by a fixed step without a division per row.
+// The dot of four columns, as every form of this sum takes it.
+__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+
+// 16-byte loads: 8 columns a lane of 16-bit rows (16 lanes a row at D = 128), 4 of f32
+// rows.  A lane of 8 columns keeps the sums of its two halves apart until the last
+// step, which is the order in which a 32-lane xor reduction over 4-column lanes adds.
+// A group takes rows in an order of 8 tokens of one head, then the next head: reads
+// stay dense over the heads, and the (H, n_q) statistics are read and written 32 bytes
+// at a time.  Each pass of a group issues the loads of kRowDotRows rows before reducing
+// any, so that enough bytes are in flight per SM to cover the HBM latency.
 template <typename Tin, typename To, int D>
 __global__ void __launch_bounds__(256) row_dot_kernel(const BwdParams p) {
+    constexpr int U = kRowDotRows;
+    constexpr int E = sizeof(Tin) == 2 ? 8 : 4;  // columns a lane
+    constexpr int L = D / E;                     // lanes a row
+    constexpr int kTok = 8;                      // tokens of a head in a row
     pdl_trigger();
     pdl_wait();
-    static_assert(D <= 128, "one 4-column chunk per lane");
-    constexpr int U = kRowDotRows;
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = (int64_t)p.n_q * p.H;
-    const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    const int64_t r_first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int64_t step_t = nwarps / p.H;
-    const int step_h = (int)(nwarps - step_t * p.H);
-    int64_t t = r_first / p.H;
-    int h = (int)(r_first - t * p.H);
-    const int d = 4 * lane;  // lanes past D idle
-    for (int64_t r0 = r_first; r0 < rows; r0 += U * nwarps) {
+    const int lane = threadIdx.x % L, d = E * lane;
+    const int groups = (int)(gridDim.x * (blockDim.x / L));  // a multiple of kTok
+    const int g = (int)(blockIdx.x * (blockDim.x / L) + threadIdx.x / L);
+    const int in = g % kTok;
+    const int64_t blocks = (int64_t)((p.n_q + kTok - 1) / kTok) * p.H;  // (token block, head) pairs, head fastest
+    const int step = groups / kTok, step_t = step / p.H, step_h = step - step_t * p.H;
+    int64_t b = g / kTok;
+    int tb = (int)(b / p.H), h = (int)(b - (int64_t)tb * p.H);
+    for (; b < blocks; ) {
         // all loads of the pass (lse included) are issued before any store
-        float4 a[U], b[U];
-        float x[U];
+        float4 x[U][E / 4], y[U][E / 4];
+        float lse[U];
         int64_t at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool live = r0 + u * nwarps < rows;
-            at[u] = (int64_t)h * p.n_q + t;
-            a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            x[u] = 0.f;
-            if (live && d < D) {
-                a[u] = load4(static_cast<const Tin *>(p.dout) + t * p.do_st + (int64_t)h * p.do_sh + d);
-                b[u] = load4(static_cast<const To *>(p.o) + t * p.o_st + (int64_t)h * p.o_sh + d);
+            const int64_t t = (int64_t)tb * kTok + in;
+            const bool live = b < blocks && t < p.n_q;
+            at[u] = live ? (int64_t)h * p.n_q + t : -1;
+            lse[u] = 0.f;
+#pragma unroll
+            for (int k = 0; k < E / 4; ++k) x[u][k] = y[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) {
+                const Tin *gx = static_cast<const Tin *>(p.dout) + t * p.do_st + (int64_t)h * p.do_sh + d;
+                const To *gy = static_cast<const To *>(p.o) + t * p.o_st + (int64_t)h * p.o_sh + d;
+                if constexpr (sizeof(Tin) == 2) load8(gx, x[u][0], x[u][1]);
+                else x[u][0] = load4(gx);
+                if constexpr (sizeof(To) == 2) load8(gy, y[u][0], y[u][1]);
+                else {
+#pragma unroll
+                    for (int k = 0; k < E / 4; ++k) y[u][k] = load4(gy + 4 * k);
+                }
+                if (lane == 0) lse[u] = __ldg(p.lse + at[u]);
             }
-            if (live && lane == 0) x[u] = __ldg(p.lse + at[u]);
-            t += step_t;
+            b += step;
+            tb += step_t;
             h += step_h;
             if (h >= p.H) {
                 h -= p.H;
-                ++t;
+                ++tb;
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float acc = a[u].x * b[u].x + a[u].y * b[u].y + a[u].z * b[u].z + a[u].w * b[u].w;
+            float s[E / 4];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (lane == 0 && r0 + u * nwarps < rows) {
+            for (int k = 0; k < E / 4; ++k) s[k] = dot4(x[u][k], y[u][k]);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < E / 4; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+            const float acc = E == 8 ? s[0] + s[E / 4 - 1] : s[0];
+            if (lane == 0 && at[u] >= 0) {
                 p.dr[at[u]] = acc;
-                p.lse2[at[u]] = x[u] == -INFINITY ? INFINITY : x[u] * kLog2e;
+                p.lse2[at[u]] = lse[u] == -INFINITY ? INFINITY : lse[u] * kLog2e;
             }
         }
     }
@@ -441,15 +462,16 @@ cudaError_t bwd_d(const BwdParams &p, int num_ctas, cudaStream_t s, bool dkdv) {
 
 template <typename Tin, typename To, int D>
 cudaError_t row_dot_typed(const BwdParams &p, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.n_q * p.H;
+    const int64_t rows = (int64_t)(p.n_q + 7) / 8 * 8 * p.H;  // whole 8-token blocks
     if (rows == 0) return cudaSuccess;
-    // 8 warps per block, kRowDotRows rows per warp and pass; at most one wave of
-    // resident blocks (a second wave would leave the first one's SMs idle at its tail)
+    // kRowDotRows rows per lane group and pass; at most one wave of resident blocks (a
+    // second wave would leave the first one's SMs idle at its tail)
     static int per_sm = 0;  // resident blocks per SM of this instantiation
     if (per_sm == 0 &&
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, row_dot_kernel<Tin, To, D>, 256, 0) != cudaSuccess)
         per_sm = 1;
-    const int64_t want = (rows + 8 * kRowDotRows - 1) / (8 * kRowDotRows);
+    const int64_t per_block = 256 / (D / (sizeof(Tin) == 2 ? 8 : 4)) * kRowDotRows;
+    const int64_t want = (rows + per_block - 1) / per_block;
     const int64_t cap = (int64_t)(per_sm > 0 ? per_sm : 1) * sm_count();
     const cudaError_t e = launch_pdl(row_dot_kernel<Tin, To, D>, dim3((int)(want < cap ? want : cap)), dim3(256), 0, s, p);
     count_launch();

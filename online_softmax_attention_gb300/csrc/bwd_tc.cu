@@ -96,52 +96,71 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, long l
     }
 }
 
-// The scheduler ring shared by both kernels: the producer fetches item
-// indices from the global counter, the MMA thread and 8 elementwise warps read them.
+// The scheduler ring shared by both kernels: the producer fetches item indices
+// from the global counter and looks the item up (sequence, offsets, blocks); the
+// MMA warp and 8 elementwise warps read what it found, so that none of them
+// waits for those loads at every item (short sequences have many).
+template <typename Info>
 struct SchedRing {
     uint64_t full[2], empty[2];
     int item[2];
+    Info info[2];
 };
 
-__device__ __forceinline__ bool sched_publish(SchedRing &r, int i, int *counter, int &w, const Watchdog &wd) {
+template <typename Info, typename F>
+__device__ __forceinline__ bool sched_publish(SchedRing<Info> &r, int i, int *counter, int total, F look_up, int &w,
+                                              Info &info, const Watchdog &wd) {
     const int slot = i & 1;
     if (!mbar_wait(smem_u32(&r.empty[slot]), ((i >> 1) & 1) ^ 1, wd)) return false;
     w = atomicAdd(counter, 1);
     r.item[slot] = w;
+    if (w < total) {
+        info = look_up(w);
+        r.info[slot] = info;
+    }
     mbar_arrive(smem_u32(&r.full[slot]));
     return true;
 }
 
-__device__ __forceinline__ bool sched_take(SchedRing &r, int i, int &w, const Watchdog &wd) {
+template <typename Info>
+__device__ __forceinline__ bool sched_take(SchedRing<Info> &r, int i, int &w, Info &info, const Watchdog &wd) {
     const int slot = i & 1;
     if (!mbar_wait(smem_u32(&r.full[slot]), (i >> 1) & 1, wd)) return false;
     w = r.item[slot];
+    info = r.info[slot];
     mbar_arrive(smem_u32(&r.empty[slot]));
     return true;
 }
 
-// warp-wide versions: every lane waits (the same observations), one lane
-// fetches / arrives, every lane gets the item
-__device__ __forceinline__ bool sched_publish_warp(SchedRing &r, int i, int *counter, int &w, const Watchdog &wd) {
+// warp-wide versions: every lane waits (the same observations) and looks the
+// item up, one lane fetches, writes and arrives
+template <typename Info, typename F>
+__device__ __forceinline__ bool sched_publish_warp(SchedRing<Info> &r, int i, int *counter, int total, F look_up,
+                                                   int &w, Info &info, const Watchdog &wd) {
     const int slot = i & 1;
     const bool ok = mbar_wait(smem_u32(&r.empty[slot]), ((i >> 1) & 1) ^ 1, wd);
     if (!__all_sync(0xffffffffu, ok)) return false;
     int v = 0;
     const bool lead = elect_one();
+    if (lead) v = atomicAdd(counter, 1);
+    w = (int)from_leader((uint32_t)v, lead);
+    if (w < total) info = look_up(w);
     if (lead) {
-        v = atomicAdd(counter, 1);
-        r.item[slot] = v;
+        r.item[slot] = w;
+        if (w < total) r.info[slot] = info;
         mbar_arrive(smem_u32(&r.full[slot]));
     }
-    w = (int)from_leader((uint32_t)v, lead);
+    __syncwarp();
     return true;
 }
 
-__device__ __forceinline__ bool sched_take_warp(SchedRing &r, int i, int &w, const Watchdog &wd) {
+template <typename Info>
+__device__ __forceinline__ bool sched_take_warp(SchedRing<Info> &r, int i, int &w, Info &info, const Watchdog &wd) {
     const int slot = i & 1;
     const bool ok = mbar_wait(smem_u32(&r.full[slot]), (i >> 1) & 1, wd);
     if (!__all_sync(0xffffffffu, ok)) return false;
     w = r.item[slot];
+    info = r.info[slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&r.empty[slot]));
     return true;
@@ -182,7 +201,7 @@ struct __align__(8) DkdvBars {
     uint64_t mma_drain;       // abort path: completion of the MMAs already issued
     uint64_t dq_full, dq_free; // fused dQ: a block's dQ partial is in TMEM / has been read out
     uint64_t dv_done;          // fused dQ: dV of a block has read its dO tile (the slot may take dS)
-    SchedRing sched;
+    SchedRing<DkdvInfo> sched;
 };
 
 // Two producer warps, each run by all its 32 lanes in step (uniform waits, one
@@ -218,13 +237,14 @@ __device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, u
     };
     for (int i = 0;; ++i) {
         int w;
+        DkdvInfo f;
         if (dout_role) {
-            if (!sched_take_warp(bars.sched, i, w, wd)) break;
+            if (!sched_take_warp(bars.sched, i, w, f, wd)) break;
         } else {
-            if (!sched_publish_warp(bars.sched, i, p.sched_kv.hdr, w, wd)) break;
+            if (!sched_publish_warp(bars.sched, i, p.sched_kv.hdr, total, [&](int x) { return dkdv_info(p, x); }, w, f, wd))
+                break;
         }
         if (w >= total) break;
-        const DkdvInfo f = dkdv_info(p, w);
         if (f.nq == 0) continue;
         bool ok = true;
         if (dout_role) {
@@ -320,9 +340,9 @@ __device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint32
 
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_take_warp(bars.sched, i, w, wd)) return;
+        DkdvInfo f;
+        if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
-        const DkdvInfo f = dkdv_info(p, w);
         if (f.nq == 0) continue;
         if (!wait(bars.kv_full, kv_cnt & 1)) return;
         ++kv_cnt;
@@ -461,9 +481,9 @@ __device__ void dkdvq_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint3
 
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_take(bars.sched, i, w, wd)) return;
+        DkdvInfo f;
+        if (!sched_take(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
-        const DkdvInfo f = dkdv_info(p, w);
         if (f.nq == 0) continue;
         if (!mbar_wait(smem_u32(&bars.kv_full), kv_cnt & 1, wd)) return;
         ++kv_cnt;
@@ -541,9 +561,9 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
 
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_take_warp(bars.sched, i, w, wd)) return;
+        DkdvInfo f;
+        if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
-        const DkdvInfo f = dkdv_info(p, w);
         const int key = f.key0 + kl;
         const bool live = key < f.Lk;
         Tg *dst = static_cast<Tg *>(wg == 0 ? p.dv : p.dk) +
@@ -718,9 +738,9 @@ __device__ void dkdvq_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *sta
 
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_take_warp(bars.sched, i, w, wd)) return;
+        DkdvInfo f;
+        if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
-        const DkdvInfo f = dkdv_info(p, w);
         const int key = f.key0 + kl;
         const bool live = key < f.Lk;
         Tg *dst = static_cast<Tg *>(wg == 0 ? p.dv : p.dk) +
@@ -958,7 +978,7 @@ struct __align__(8) DqBars {
     // one barrier its early arrival would complete the wrong phase
     uint64_t ds_ready[2];
     uint64_t mma_drain;  // abort path: completion of the MMAs already issued
-    SchedRing sched;
+    SchedRing<DqInfo> sched;
 };
 
 template <int D>
@@ -990,9 +1010,9 @@ __device__ void dq_producer(const TcBwdArgs &a, DqBars &bars, uint32_t sQ, uint3
     };
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_publish(bars.sched, i, p.sched_q.hdr, w, wd)) break;
+        DqInfo f;
+        if (!sched_publish(bars.sched, i, p.sched_q.hdr, total, [&](int x) { return dq_info(p, x); }, w, f, wd)) break;
         if (w >= total) break;
-        const DqInfo f = dq_info(p, w);
         if (f.nk == 0) continue;
         if (!mbar_wait(smem_u32(&bars.q_empty), (q_uses & 1) ^ 1, wd)) break;
         {
@@ -1053,9 +1073,9 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars &bars, uint32_t sQ, uint32_t s
 
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_take_warp(bars.sched, i, w, wd)) return;
+        DqInfo f;
+        if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
-        const DqInfo f = dq_info(p, w);
         if (f.nk == 0) continue;
         if (!wait(bars.q_full, q_cnt & 1)) return;
         ++q_cnt;
@@ -1153,9 +1173,9 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars &bars, uint32_t tmem, 
 
     for (int i = 0;; ++i) {
         int w;
-        if (!sched_take_warp(bars.sched, i, w, wd)) return;
+        DqInfo f;
+        if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
-        const DqInfo f = dq_info(p, w);
         const int row = f.row0 + rl;
         const bool live = row < f.Lq;
         const int64_t at = (int64_t)f.h * p.n_q + f.q_start + row;

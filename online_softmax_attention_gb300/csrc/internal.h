@@ -244,11 +244,18 @@ struct BwdParams {
 };
 
 // Schedule preparation: validates cu_seqlens on the device and writes the
-// prefix of item counts for tiles of `block` rows of the `cu_rows` side.
-// Each tile counts as `splits` work items (split-K), numbered tile-major.
-cudaError_t launch_prep(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int n_q, int n_k,
-                        int H, int block, int causal, int rows_are_keys, int splits, Sched sched,
-                        int *status, cudaStream_t s);
+// prefix of item counts for tiles of `block` rows of the query or key side, of H
+// heads.  Each tile counts as `splits` work items (split-K), numbered tile-major.
+// One launch prepares one or two schedules.
+struct PrepJob {
+    int H, block, rows_are_keys, splits;
+    Sched sched;
+};
+struct PrepJobs {
+    PrepJob job[2];
+};
+cudaError_t launch_prep(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int n_q, int n_k, int causal,
+                        const PrepJobs &jobs, int n_jobs, int *status, cudaStream_t s);
 
 // Merge of partial results (split-K): one warp per (query row, head).
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t s);

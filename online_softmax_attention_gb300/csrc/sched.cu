@@ -15,10 +15,13 @@ namespace {
 
 constexpr int kPrepThreads = 1024;
 
+// Block b prepares schedule b (the backward's two in one launch).
 __global__ void __launch_bounds__(kPrepThreads)
 prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int n_seq,
-            int n_q, int n_k, int H, int block, int causal, int rows_are_keys, int splits,
-            int *hdr, int *prefix, int *status) {
+            int n_q, int n_k, int causal, const PrepJobs jobs, int *status) {
+    const PrepJob &job = jobs.job[blockIdx.x];
+    const int H = job.H, block = job.block, rows_are_keys = job.rows_are_keys, splits = job.splits;
+    int *hdr = job.sched.hdr, *prefix = const_cast<int *>(job.sched.prefix);
     __shared__ int s_bad;
     __shared__ int s_warp[kPrepThreads / 32];
     __shared__ long long s_carry;
@@ -87,12 +90,10 @@ prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, 
 
 }  // namespace
 
-cudaError_t launch_prep(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int n_q, int n_k,
-                        int H, int block, int causal, int rows_are_keys, int splits, Sched sched,
-                        int *status, cudaStream_t s) {
-    cudaError_t e = launch_pdl(prep_kernel, dim3(1), dim3(kPrepThreads), 0, s, cu_q, cu_k, n_seq, n_q, n_k, H,
-                               block, causal, rows_are_keys, splits, sched.hdr,
-                               const_cast<int *>(sched.prefix), status);
+cudaError_t launch_prep(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int n_q, int n_k, int causal,
+                        const PrepJobs &jobs, int n_jobs, int *status, cudaStream_t s) {
+    cudaError_t e = launch_pdl(prep_kernel, dim3(n_jobs), dim3(kPrepThreads), 0, s, cu_q, cu_k, n_seq, n_q, n_k,
+                               causal, jobs, status);
     count_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }
