@@ -39,15 +39,17 @@ def f32(x: float) -> float:
     return x if -_FLOAT_MAX <= x <= _FLOAT_MAX or x != x else ctypes.c_float(x).value
 
 
-def call(index: int, fn, where: str, *args) -> None:
-    """`fn(*args)` with device `index` current; an error code becomes an exception."""
+def call(index: int, fn, where: str | None, *args) -> int:
+    """`fn(*args)` with device `index` current.  With `where`, the result is a status
+    and an error becomes an exception."""
     if index == _current_device():
         rc = fn(*args)
     else:
         with torch.cuda.device(index):
             rc = fn(*args)
-    if rc:
+    if rc and where is not None:
         _abi.check(rc, where)
+    return rc
 
 
 _fast = {}

@@ -76,6 +76,7 @@ class Cache:
         self.device = dev
         shape, self.dtype = k.shape, k.dtype
         self.n_layers, _, _, self.n_heads, self.head_dim = shape
+        self.max_seqs = table.shape[0]
         # a size-1 axis is never stepped along: give it the stride of a contiguous layout
         dense = (shape[1] * shape[2] * shape[3] * shape[4], shape[2] * shape[3] * shape[4], shape[3] * shape[4], shape[4])
         self.args = _host.CACHE.pack(
@@ -83,9 +84,15 @@ class Cache:
             table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
             table.stride(0) if table.shape[0] > 1 else table.shape[1], shape[0], shape[1], shape[2], shape[3], shape[4],
             _DT[k.dtype], table.shape[0], table.shape[1])
-        if _host.entry("attn_cache_workspace_bytes")(self.args, 0) == 0:
+        need = _host.entry("attn_cache_workspace_bytes")
+        if need(self.args, 0) == 0:
             raise ValueError("unsupported cache: page_size a power of two up to 1024, D 64 or 128, "
                              "16-byte aligned rows")
+        # the operations' scratch, for lists of as many entries as there are sequences: they
+        # change the cache, so they run in one order, and one workspace serves them all
+        self._need = need
+        self._plan = torch.empty(need(self.args, self.max_seqs), dtype=torch.uint8, device=dev)
+        self._plan_at, self._plan_bytes = self._plan.data_ptr(), self._plan.numel()
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, page_size: int, n_heads: int, head_dim: int, *, max_seqs: int,
@@ -99,9 +106,13 @@ class Cache:
         return cls(k, v, table, torch.zeros(max_seqs, dtype=torch.int32, device=dev),
                    torch.zeros(n_pages, dtype=torch.int32, device=dev))
 
-    def _workspace(self, n: int) -> torch.Tensor:
-        # torch's caching allocator returns 512-byte aligned blocks
-        return torch.empty(_host.entry("attn_cache_workspace_bytes")(self.args, n), dtype=torch.uint8, device=self.device)
+    def _workspace(self, n: int):
+        """Address and bytes of scratch for a list of n entries, and what keeps it alive."""
+        if n <= self.max_seqs:
+            return self._plan_at, self._plan_bytes, None
+        # a list with repeats, which the library refuses: scratch of its own
+        ws = torch.empty(self._need(self.args, n), dtype=torch.uint8, device=self.device)
+        return ws.data_ptr(), ws.numel(), ws
 
     def _call(self, name: str, *args) -> None:
         index = self.device.index
@@ -118,8 +129,8 @@ class Cache:
     def extend(self, seqs, counts) -> None:
         """Room for ``counts[i]`` more tokens of sequence ``seqs[i]``: pages and lengths."""
         seqs, counts = self._lists(None, seqs=seqs, counts=counts)
-        ws = self._workspace(seqs.numel())
-        self._call("attn_cache_extend", seqs.data_ptr(), counts.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel())
+        at, size, _ws = self._workspace(seqs.numel())
+        self._call("attn_cache_extend", seqs.data_ptr(), counts.data_ptr(), seqs.numel(), at, size)
 
     def write(self, seqs, cu_seqlens, k: torch.Tensor, v: torch.Tensor, *, layer: int = 0) -> None:
         """New rows (tokens, heads, D) of one layer: rows ``cu[i]:cu[i + 1]`` become the
@@ -137,8 +148,8 @@ class Cache:
     def fork(self, parents, children) -> None:
         """The empty sequence ``children[i]`` becomes a copy of ``parents[i]`` that shares its full pages."""
         parents, children = self._lists(None, parents=parents, children=children)
-        ws = self._workspace(parents.numel())
-        self._call("attn_cache_fork", parents.data_ptr(), children.data_ptr(), parents.numel(), ws.data_ptr(), ws.numel())
+        at, size, _ws = self._workspace(parents.numel())
+        self._call("attn_cache_fork", parents.data_ptr(), children.data_ptr(), parents.numel(), at, size)
 
     def keep(self, seqs, n_draft, keep: torch.Tensor, n_keep) -> None:
         """Of the last ``n_draft[i]`` tokens of ``seqs[i]`` keeps the ``n_keep[i]`` at the
@@ -149,9 +160,9 @@ class Cache:
         if keep.dim() != 2 or keep.shape[0] != seqs.numel() or keep.is_floating_point() or keep.dtype == torch.bool:
             raise ValueError(f"keep must be ({seqs.numel()}, offsets) whole numbers, got {tuple(keep.shape)}")
         keep = keep.to(device=self.device, dtype=torch.int32).contiguous()
-        ws = self._workspace(seqs.numel())
+        at, size, _ws = self._workspace(seqs.numel())
         self._call("attn_cache_keep", seqs.data_ptr(), n_draft.data_ptr(), keep.data_ptr(), keep.shape[1],
-                   n_keep.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel())
+                   n_keep.data_ptr(), seqs.numel(), at, size)
 
     def free(self, seqs) -> None:
         """Empties the sequences; pages that no other sequence holds are free again."""
@@ -163,8 +174,8 @@ class Cache:
         if remap is not None and (remap.dtype != torch.int32 or remap.device != self.device or
                                   remap.shape != self.refs.shape or not remap.is_contiguous()):
             raise ValueError("remap must be a contiguous int32 vector of one entry per page on the cache's device")
-        ws = self._workspace(0)
-        self._call("attn_cache_compact", remap.data_ptr() if remap is not None else None, ws.data_ptr(), ws.numel())
+        at, size, _ws = self._workspace(0)
+        self._call("attn_cache_compact", remap.data_ptr() if remap is not None else None, at, size)
 
 
 class TreeCall:
@@ -212,15 +223,11 @@ class TreeCall:
                 seqs.data_ptr(), cu.data_ptr(), mask.data_ptr() if mask is not None else 0, n, T, words,
                 _host.f32(scale) if scale is not None else D ** -0.5, _DT[out_dtype])
         if workspace is None:
-            workspace = torch.empty(self._bytes(_host.TREE.pack(*head, 0, 0), dev.index), dtype=torch.uint8, device=dev)
+            # (0 bytes: arguments that the call will refuse)
+            workspace = torch.empty(_host.call(dev.index, _host.entry("attn_tree_workspace_bytes"), None, _host.TREE.pack(*head, 0, 0)) or 256,
+                                    dtype=torch.uint8, device=dev)
         self.workspace = workspace
         self.args = _host.TREE.pack(*head, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-
-    @staticmethod
-    def _bytes(args: bytes, index: int) -> int:
-        need = []
-        _host.call(index, lambda: need.append(_host.entry("attn_tree_workspace_bytes")(args)), "")
-        return max(need[0], 256)  # 0: arguments that the call will refuse
 
     def run(self, stream: torch.cuda.Stream | None = None):
         index = self.cache.device.index

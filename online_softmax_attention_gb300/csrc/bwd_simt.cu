@@ -87,7 +87,7 @@ __device__ __forceinline__ void tile_nt(float (&acc)[4][4], const float *A, cons
 
 // ---- preprocess: Dr = rowsum(dO * O), and lse in the base-2 domain ----------
 
-constexpr int kRowDotRows = 4;  // rows per lane group with loads in flight at once
+constexpr int kRowDotRows = 2;  // rows per lane group with loads in flight at once
 
 // The dot of four columns, as every form of this sum takes it.
 __device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
@@ -99,6 +99,9 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a
 // stay dense over the heads, and the (H, n_q) statistics are read and written 32 bytes
 // at a time.  Each pass of a group issues the loads of kRowDotRows rows before reducing
 // any, so that enough bytes are in flight per SM to cover the HBM latency.
+// HBM-bound: with the schedules' launch 46 us for 16384 x 32 rows of D = 128 in bf16,
+// 5.8 TB/s (2 rows a group; 4: 47.8 us, 8: 53 us; 8-byte loads of 4 columns a lane in
+// 32-lane groups took 46 us for half as many rows).
 template <typename Tin, typename To, int D>
 __global__ void __launch_bounds__(256) row_dot_kernel(const BwdParams p) {
     constexpr int U = kRowDotRows;
@@ -117,7 +120,9 @@ __global__ void __launch_bounds__(256) row_dot_kernel(const BwdParams p) {
     int tb = (int)(b / p.H), h = (int)(b - (int64_t)tb * p.H);
     for (; b < blocks; ) {
         // all loads of the pass (lse included) are issued before any store
-        float4 x[U][E / 4], y[U][E / 4];
+        // (as loaded: 16 bytes of dO, and 16 or 32 of O; converted after the last load)
+        constexpr int Y = E * (int)sizeof(To) / 16;
+        uint4 x[U], y[U][Y];
         float lse[U];
         int64_t at[U];
 #pragma unroll
@@ -126,18 +131,15 @@ __global__ void __launch_bounds__(256) row_dot_kernel(const BwdParams p) {
             const bool live = b < blocks && t < p.n_q;
             at[u] = live ? (int64_t)h * p.n_q + t : -1;
             lse[u] = 0.f;
+            x[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < E / 4; ++k) x[u][k] = y[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < Y; ++k) y[u][k] = make_uint4(0, 0, 0, 0);
             if (live) {
                 const Tin *gx = static_cast<const Tin *>(p.dout) + t * p.do_st + (int64_t)h * p.do_sh + d;
                 const To *gy = static_cast<const To *>(p.o) + t * p.o_st + (int64_t)h * p.o_sh + d;
-                if constexpr (sizeof(Tin) == 2) load8(gx, x[u][0], x[u][1]);
-                else x[u][0] = load4(gx);
-                if constexpr (sizeof(To) == 2) load8(gy, y[u][0], y[u][1]);
-                else {
+                x[u] = *reinterpret_cast<const uint4 *>(gx);
 #pragma unroll
-                    for (int k = 0; k < E / 4; ++k) y[u][k] = load4(gy + 4 * k);
-                }
+                for (int k = 0; k < Y; ++k) y[u][k] = reinterpret_cast<const uint4 *>(gy)[k];
                 if (lane == 0) lse[u] = __ldg(p.lse + at[u]);
             }
             b += step;
@@ -152,7 +154,9 @@ __global__ void __launch_bounds__(256) row_dot_kernel(const BwdParams p) {
         for (int u = 0; u < U; ++u) {
             float s[E / 4];
 #pragma unroll
-            for (int k = 0; k < E / 4; ++k) s[k] = dot4(x[u][k], y[u][k]);
+            for (int k = 0; k < E / 4; ++k)
+                s[k] = dot4(load4(reinterpret_cast<const Tin *>(&x[u]) + 4 * k),
+                            load4(reinterpret_cast<const To *>(&y[u][0]) + 4 * k));
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1)
 #pragma unroll

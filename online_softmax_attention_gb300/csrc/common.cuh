@@ -53,15 +53,6 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Load 8 consecutive 16-bit elements (16-byte aligned).
-template <typename T16>
-__device__ __forceinline__ void load8(const T16 *p, float4 &lo, float4 &hi) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint2 a = make_uint2(u.x, u.y), b = make_uint2(u.z, u.w);
-    lo = load4(reinterpret_cast<const T16 *>(&a));
-    hi = load4(reinterpret_cast<const T16 *>(&b));
-}
-
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 __device__ __forceinline__ void store4(__half *p, float4 v) {
     __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
