@@ -373,6 +373,11 @@ def fwd(q, k, v, *, causal: bool = False, scale: float | None = None, cu_seqlens
     ``num_splits``: key splits per query tile (split-K); 0 lets the library
     choose, 1 disables splitting.  ``prune_threshold``: 0 = exact; rho in
     (0, 1] enables approximate tile pruning (full relation, one sequence)."""
+    if kernel == "auto" and not num_ctas and not num_splits and not prune_threshold:
+        r = _host.native().fwd(q, k, v, causal, scale, cu_seqlens_q, cu_seqlens_k,
+                               -1 if out_dtype is None else _dtype_code(out_dtype))
+        if r is not None:
+            return r if type(r) is tuple else check(r, "attn_fwd")
     return FwdCall(q, k, v, causal=causal, scale=scale, cu_seqlens_q=cu_seqlens_q,
                    cu_seqlens_k=cu_seqlens_k, out_dtype=out_dtype, kernel=kernel,
                    num_ctas=num_ctas, num_splits=num_splits,
@@ -389,6 +394,11 @@ def bwd(q, k, v, o, lse, dout, *, causal: bool = False, scale: float | None = No
         cu_seqlens_q=None, cu_seqlens_k=None, grad_dtype: torch.dtype | None = None,
         kernel: str = "auto", num_ctas: int = 0, dq_mode: str = "auto"):
     """Attention backward from the forward's o and lse.  Returns ``(dq, dk, dv)``."""
+    if kernel == "auto" and not num_ctas and dq_mode == "auto":
+        r = _host.native().bwd(q, k, v, o, lse, dout, causal, scale, cu_seqlens_q, cu_seqlens_k,
+                               -1 if grad_dtype is None else _dtype_code(grad_dtype))
+        if r is not None:
+            return r if type(r) is tuple else check(r, "attn_bwd")
     return BwdCall(q, k, v, o, lse, dout, causal=causal, scale=scale, cu_seqlens_q=cu_seqlens_q,
                    cu_seqlens_k=cu_seqlens_k, grad_dtype=grad_dtype, kernel=kernel,
                    num_ctas=num_ctas, dq_mode=dq_mode).run()

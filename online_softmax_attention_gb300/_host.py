@@ -4,11 +4,15 @@ A short attention call takes a few microseconds on the GPU, so the binding's
 own time decides how fast short calls follow one another.  The argument structs
 are therefore packed by one ``struct.pack`` (a ctypes field assignment costs as
 much as the whole pack), streams are passed as their raw handles, and the device
-is switched only when another one is current.
+is switched only when another one is current.  Calls whose arguments need no
+conversion skip the interpreter's share altogether (``native``).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 
 import torch
@@ -50,6 +54,31 @@ def call(index: int, fn, where: str | None, *args) -> int:
     if rc and where is not None:
         _abi.check(rc, where)
     return rc
+
+
+_NATIVE = os.path.join(os.path.dirname(_abi.LIB_PATH), "_native.so")
+# the entry points that csrc/binding.cpp calls, in its order
+_NATIVE_CALLS = ("attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_workspace_bytes", "attn_tree_fwd",
+                 "attn_tree_workspace_bytes", "attn_cache_extend", "attn_cache_fork", "attn_cache_keep",
+                 "attn_cache_free", "attn_cache_write")
+_native = None
+
+
+def native():
+    """The compiled binding (csrc/binding.cpp).  Its functions return None for
+    arguments that they leave to the Python path, or a status of the library."""
+    global _native
+    if _native is None:
+        lib = _abi.load()
+        if not os.path.exists(_NATIVE):
+            raise ImportError(f"torch binding not built ({_NATIVE} missing); run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_native", _NATIVE)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_native", loader))
+        loader.exec_module(module)
+        module.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS))
+        _native = module
+    return _native
 
 
 _fast = {}

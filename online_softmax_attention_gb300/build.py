@@ -1,17 +1,21 @@
-"""Build the CUDA library in-tree: csrc/*.cu -> _lib/libattn_gb300.so (sm_103a).
+"""Build the CUDA library in-tree: csrc/*.cu -> _lib/libattn_gb300.so (sm_103a),
+and the torch binding of its short calls: csrc/binding.cpp -> _lib/_native.so.
 
 Each translation unit is compiled by nvcc in parallel, then linked into one
-shared library with the CUDA runtime linked statically.  Rebuilds only what
-changed (object newer than its source and the shared headers).
+shared library with the CUDA runtime linked statically.  The binding is compiled
+beside them by the host compiler against the installed torch's headers.
+Rebuilds only what changed (object newer than its source and the shared headers).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libattn_gb300.so")
+NATIVE = os.path.join(OUT_DIR, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -60,6 +65,34 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    """The installed torch package's folder, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found: the binding needs its headers")
+    return os.path.dirname(spec.origin)
+
+
+def _binding(force: bool) -> None:
+    src = os.path.join(CSRC, "binding.cpp")
+    torch = _torch_dir()
+    # built anew when another torch is installed
+    deps = [src, os.path.join(ROOT, "include", "attn.h"), os.path.join(torch, "version.py")]
+    if not force and not _stale(NATIVE, deps):
+        return
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(torch, "lib")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *(x for i in inc for x in ("-I", i)), src, "-o", NATIVE + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the torch binding failed to build:\n{r.stdout}\n{r.stderr}")
+    os.replace(NATIVE + ".tmp", NATIVE)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -68,8 +101,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         for o in glob.glob(os.path.join(OBJ_DIR, "*.o")):
             os.remove(o)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_binding, force)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        binding.result()
     if force or _stale(LIB, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs, "-lpthread"]
         r = subprocess.run(cmd, capture_output=True, text=True)

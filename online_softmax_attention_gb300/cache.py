@@ -74,6 +74,8 @@ class Cache:
             raise ValueError("k, v: the D axis must be contiguous")
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
         self.device = dev
+        self._index = dev.index
+        self._native = _host.native()
         shape, self.dtype = k.shape, k.dtype
         self.n_layers, _, _, self.n_heads, self.head_dim = shape
         self.max_seqs = table.shape[0]
@@ -114,6 +116,12 @@ class Cache:
         ws = torch.empty(self._need(self.args, n), dtype=torch.uint8, device=self.device)
         return ws.data_ptr(), ws.numel(), ws
 
+    def _done(self, name: str, rc: int | None) -> bool:
+        """Whether the compiled binding made the call; an error becomes an exception."""
+        if rc:
+            _abi.check(rc, name)
+        return rc is not None
+
     def _call(self, name: str, *args) -> None:
         index = self.device.index
         _host.call(index, _host.entry(name), name, self.args, *args, _host.raw_stream(index))
@@ -128,6 +136,9 @@ class Cache:
 
     def extend(self, seqs, counts) -> None:
         """Room for ``counts[i]`` more tokens of sequence ``seqs[i]``: pages and lengths."""
+        if self._done("attn_cache_extend", self._native.extend(
+                self.args, self._index, self._plan_at, self._plan_bytes, self.max_seqs, seqs, counts)):
+            return
         seqs, counts = self._lists(None, seqs=seqs, counts=counts)
         at, size, _ws = self._workspace(seqs.numel())
         self._call("attn_cache_extend", seqs.data_ptr(), counts.data_ptr(), seqs.numel(), at, size)
@@ -135,6 +146,8 @@ class Cache:
     def write(self, seqs, cu_seqlens, k: torch.Tensor, v: torch.Tensor, *, layer: int = 0) -> None:
         """New rows (tokens, heads, D) of one layer: rows ``cu[i]:cu[i + 1]`` become the
         last tokens of sequence ``seqs[i]`` (``extend`` made their room)."""
+        if self._done("attn_cache_write", self._native.write(self.args, self._index, seqs, cu_seqlens, k, v, layer)):
+            return
         seqs = _ints(seqs, self.device, "seqs")
         cu = _ints(cu_seqlens, self.device, "cu_seqlens")
         if cu.numel() != seqs.numel() + 1:
@@ -147,6 +160,9 @@ class Cache:
 
     def fork(self, parents, children) -> None:
         """The empty sequence ``children[i]`` becomes a copy of ``parents[i]`` that shares its full pages."""
+        if self._done("attn_cache_fork", self._native.fork(
+                self.args, self._index, self._plan_at, self._plan_bytes, self.max_seqs, parents, children)):
+            return
         parents, children = self._lists(None, parents=parents, children=children)
         at, size, _ws = self._workspace(parents.numel())
         self._call("attn_cache_fork", parents.data_ptr(), children.data_ptr(), parents.numel(), at, size)
@@ -154,6 +170,9 @@ class Cache:
     def keep(self, seqs, n_draft, keep: torch.Tensor, n_keep) -> None:
         """Of the last ``n_draft[i]`` tokens of ``seqs[i]`` keeps the ``n_keep[i]`` at the
         ascending offsets ``keep[i, :n_keep[i]]``; the others go."""
+        if self._done("attn_cache_keep", self._native.keep(
+                self.args, self._index, self._plan_at, self._plan_bytes, self.max_seqs, seqs, n_draft, keep, n_keep)):
+            return
         seqs, n_draft, n_keep = self._lists(None, seqs=seqs, n_draft=n_draft, n_keep=n_keep)
         if not isinstance(keep, torch.Tensor):
             keep = torch.as_tensor(keep)
@@ -166,6 +185,8 @@ class Cache:
 
     def free(self, seqs) -> None:
         """Empties the sequences; pages that no other sequence holds are free again."""
+        if self._done("attn_cache_free", self._native.free(self.args, self._index, seqs)):
+            return
         seqs = _ints(seqs, self.device, "seqs")
         self._call("attn_cache_free", seqs.data_ptr(), seqs.numel())
 
@@ -242,4 +263,8 @@ def tree_fwd(q, cache: Cache, seqs, cu_seqlens_q, *, layer: int = 0, mask: torch
 
     Rows ``cu[i]:cu[i + 1]`` of q are the last tokens of sequence ``seqs[i]``: one token
     (decoding), a chunk, or with ``mask`` a tree of drafts (see ``TreeCall``)."""
-    return TreeCall(q, cache, seqs, cu_seqlens_q, layer=layer, mask=mask, scale=scale, out_dtype=out_dtype).run()
+    r = _host.native().tree(cache.args, cache._index, q, seqs, cu_seqlens_q, mask, layer, scale,
+                            -1 if out_dtype is None else _DT.get(out_dtype, 99))
+    if r is None:
+        return TreeCall(q, cache, seqs, cu_seqlens_q, layer=layer, mask=mask, scale=scale, out_dtype=out_dtype).run()
+    return r if type(r) is tuple else _abi.check(r, "attn_tree_fwd")
