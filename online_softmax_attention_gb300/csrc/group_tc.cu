@@ -105,26 +105,27 @@ __device__ __forceinline__ int tiles_to(const GroupParams &p, const Entry &e, in
     return max(1, cdiv(ordered ? min(e.L, e.ctx + min(tok, e.T)) : e.L, BN));
 }
 
-// sum over i < n of floor((a i + b) / m), a, b, m >= 0 (the Euclid-like recursion)
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
-    long long r = 0;
-    while (n > 0) {
-        r += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
-        a %= m;
-        b %= m;
-        const long long y = a * n + b;
-        if (y < m) break;
+// sum over i < n of floor((a i + b) / 128), a >= 0, b >= 0 (the Euclid-like
+// recursion; after the first step everything is below 128 n)
+__device__ __forceinline__ long long floor_sum(int n0, int a0, int b0) {
+    long long r = (long long)(a0 >> 7) * ((long long)n0 * (n0 - 1) / 2) + (long long)(b0 >> 7) * n0;
+    uint32_t n = n0, m = BN, a = a0 & (BN - 1), b = b0 & (BN - 1);
+    for (;;) {
+        const uint32_t y = a * n + b;
+        if (y < m) return r;
         n = y / m;
-        b = y % m;
-        const long long t = m;
+        b = y - n * m;
+        const uint32_t t = m;
         m = a;
         a = t;
+        r += (long long)(a / m) * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
+        a %= m;
+        b %= m;
     }
-    return r;
 }
 
 // key tiles of the first n units of a key head
-__device__ long long unit_tiles(const GroupParams &p, const Entry &e, int per, int n) {
+__device__ __forceinline__ long long unit_tiles(const GroupParams &p, const Entry &e, int per, int n) {
     const int full = tiles_to(p, e, 1), last = tiles_to(p, e, e.T);
     if (full == last) return (long long)n * last;
     if (n <= 8) {
@@ -134,7 +135,7 @@ __device__ long long unit_tiles(const GroupParams &p, const Entry &e, int per, i
     }
     // units before the entry's last one hold `per` tokens: ceil((ctx + (i + 1) per) / 128)
     const int whole = min(n, e.units - 1);
-    return floor_sum(whole, BN, per, (long long)e.ctx + per + BN - 1) + (n > whole ? last : 0);
+    return floor_sum(whole, per, e.ctx + per + BN - 1) + (n > whole ? last : 0);
 }
 
 __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, bool report) {
@@ -220,22 +221,36 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
 
     long long u0 = st.end;  // where the unit begins in the line
     int ei = st.entry, hk = 0, unit = 0;
-    if (st.at < st.end) {
-        e = entry_at(p, ei, per, false);
-        auto length = [&](int n) { return unit_tiles(p, e, per, n) + (long long)st.lead * n; };  // of n units
-        const long long per_head = length(e.units);
+    bool fresh = st.at < st.end;  // the first entry, in whose middle the stretch may begin
+    auto enter = [&]() {          // entry ei or the next one with work
+        for (;; ++ei) {
+            e = entry_at(p, ei, per, false);
+            if (e.T > 0) break;
+        }
+        if (!fresh) return;
+        fresh = false;
+        const long long per_head = st.length(st.work) / p.Hkv;
         long long off = st.at - st.before;
         hk = (int)(off / per_head);
         off -= hk * per_head;
-        int lo = 0, hi = e.units - 1;  // the last unit that begins at or before `off`
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (length(mid) <= off) lo = mid;
-            else hi = mid - 1;
+        // the last unit that begins at or before `off`
+        int lo = 0, hi = e.units;
+        long long begin = 0;
+#pragma unroll 1
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            const long long len = unit_tiles(p, e, per, mid) + (long long)st.lead * mid;
+            if (len <= off) {
+                lo = mid;
+                begin = len;
+            } else {
+                hi = mid;
+            }
         }
         unit = lo;
-        u0 = st.before + hk * per_head + length(lo);
-    }
+        u0 = st.before + hk * per_head + begin;
+    };
+    if (fresh) u0 = st.before;
     bool ok = true;
     int i = 0;
     auto publish = [&](const Seg &g) -> bool {
@@ -249,19 +264,21 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
         ++i;
         return true;
     };
-    // the next unit of the line, if one begins before the stretch ends
+    // the next unit of the line
+    bool entered = false;
     auto next_unit = [&](int n_unit) {
         u0 += st.lead + n_unit;
         if (++unit < e.units) return;
         unit = 0;
         if (++hk < p.Hkv) return;
         hk = 0;
-        if (u0 < st.end) {
-            do e = entry_at(p, ++ei, per, false);
-            while (e.T == 0);
-        }
+        ++ei;
+        entered = false;
     };
+#pragma unroll 1
     while (u0 < st.end) {
+        if (!entered) enter();
+        entered = true;
         const int n_unit = tiles_to(p, e, (unit + 1) * per);
         const int t0 = st.tile(st.at, u0, n_unit), t1 = st.tile(st.end, u0, n_unit);
         if (t0 >= t1) {
@@ -376,7 +393,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
     const uint32_t idS = idesc_f16(kBF16, BM, BN, 0) | negate;
     auto idS_of = [&](int steps) { return idesc_f16(kBF16, BM, 0, 0) | negate | ((uint32_t)(2 * steps) << 17); };
     constexpr uint32_t idO = idesc_f16(kBF16, BM, D, 1);
-    uint32_t q_cnt[NQT] = {0, 0}, p_cnt[NQT] = {0, 0}, of_cnt[NQT] = {0, 0};
+    uint32_t q_ph = 0, p_ph = 0, of_ph = 3;  // bit t: the parity that query tile t waits for next
     RingPos<C::kKStages> kr;
     RingPos<C::kVStages> vr;
     const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024);
@@ -421,60 +438,58 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         const int slot = i % kSegs;
         if (!wait(bars.seg_full[slot], (i / kSegs) & 1)) return;
         const int n0 = segs[slot].n[0], n1 = segs[slot].n[1], nkv = segs[slot].nkv;
-        const int key0 = BN * segs[slot].j0, left[NQT] = {segs[slot].end[0] - key0, segs[slot].end[1] - key0};
+        const int key0 = BN * segs[slot].j0, left0 = segs[slot].end[0] - key0, left1 = segs[slot].end[1] - key0;
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
         if (nkv < 0) return;
-        const int n[NQT] = {n0, n1};
-#pragma unroll
-        for (int t = 0; t < NQT; ++t) {
-            if (n[t] == 0) continue;
-            if (!wait(bars.q_full[t], q_cnt[t] & 1)) return;
-            ++q_cnt[t];
-        }
         const uint32_t ks = kr.slot();
-        if (!wait(bars.k_full[ks], kr.phase())) return;
-        ++kr.i;
-        tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < NQT; ++t) {
-            if (n[t] == 0) continue;
-            issue_s(t, ks, key_steps(left[t]));
-            if (n[t] == 1) commit(bars.q_empty[t]);
+            const int n = t ? n1 : n0;
+            if (n == 0) continue;
+            if (!wait(bars.q_full[t], (q_ph >> t) & 1)) return;
+            q_ph ^= 1u << t;
+            if (!wait(bars.k_full[ks], kr.phase())) return;
+            tc_fence_after();
+            issue_s(t, ks, key_steps(t ? left1 : left0));
+            if (n == 1) commit(bars.q_empty[t]);
         }
+        ++kr.i;
         commit(bars.k_empty[ks]);
         for (int j = 0; j < nkv; ++j) {
             const uint32_t vs = vr.slot();  // V_j landed with K_j
             ++vr.i;
             bool have_next_k = false;
-            uint32_t nks = 0;
-#pragma unroll
+            const uint32_t nks = kr.slot();
+#pragma unroll 1
             for (int t = 0; t < NQT; ++t) {
-                if (j >= n[t]) continue;
-                if (!wait(bars.p_full[t], p_cnt[t] & 1)) return;
-                ++p_cnt[t];
+                const int n = t ? n1 : n0, left = (t ? left1 : left0) - BN * j;
+                if (j >= n) continue;
+                if (!wait(bars.p_full[t], (p_ph >> t) & 1)) return;
+                p_ph ^= 1u << t;
                 if (j == 0) {
                     // the previous part's epilogue of this tile has read U_t
-                    if (!wait(bars.o_free[t], (of_cnt[t] & 1) ^ 1)) return;
-                    ++of_cnt[t];
+                    if (!wait(bars.o_free[t], (of_ph >> t) & 1)) return;
+                    of_ph ^= 1u << t;
                 }
                 tc_fence_after();
-                issue_pv(t, vs, j > 0, key_steps(left[t] - BN * j));
-                if (j == n[t] - 1) commit(bars.o_done[t]);
-                if (j + 1 < n[t]) {
+                issue_pv(t, vs, j > 0, key_steps(left));
+                if (j == n - 1) commit(bars.o_done[t]);
+                if (j + 1 < n) {
                     if (!have_next_k) {
-                        nks = kr.slot();
                         if (!wait(bars.k_full[nks], kr.phase())) return;
-                        ++kr.i;
                         have_next_k = true;
                         tc_fence_after();
                     }
-                    issue_s(t, nks, key_steps(left[t] - BN * (j + 1)));
-                    if (j + 1 == n[t] - 1) commit(bars.q_empty[t]);
+                    issue_s(t, nks, key_steps(left - BN));
+                    if (j + 1 == n - 1) commit(bars.q_empty[t]);
                 }
             }
             commit(bars.v_empty[vs]);
-            if (have_next_k) commit(bars.k_empty[nks]);
+            if (have_next_k) {
+                ++kr.i;
+                commit(bars.k_empty[nks]);
+            }
         }
     }
 }

@@ -54,6 +54,7 @@ struct Stretch {
     long long at, end;   // the block's part of the line
     long long share;     // length of a block's part (the last ones may be shorter)
     long long before;    // length of the line before entry `entry`
+    long long work;      // work_of the entry
     int entry;           // entry that position `at` lies in
     int lead, snap;      // of a unit of n tiles: see tile()
 
@@ -65,6 +66,7 @@ struct Stretch {
         const long long o = x - u0 - lead;
         return o <= 0 || o < snap ? 0 : o >= n || o > n - snap ? n : (int)o;
     }
+    __device__ __forceinline__ long long length(long long w) const { return work_tiles(w) + lead * work_units(w); }
 };
 
 // The block's stretch; work(i, report): work_of entry i.  A unit counts `lead` more
@@ -74,44 +76,47 @@ constexpr int kLeadShare = 12;
 template <int kWarps, typename F>
 __device__ __forceinline__ bool find_stretch(int n, int turn, int lead, F work, Stretch &s) {
     __shared__ int s_entry;
-    __shared__ long long s_before;
+    __shared__ long long s_before, s_work;
     long long total = 0, mine = 0, count = 0;
-    for (int base = 0; base < n; base += 32 * kWarps) {
-        const int i = base + threadIdx.x;
-        count = i < n ? work(i, blockIdx.x == 0) : 0;
-        long long sum;
-        mine = total + block_prefix<kWarps>(count, sum);
-        total += sum;
-    }
-    const bool long_enough = work_tiles(total) >= (long long)kLeadShare * gridDim.x;
-    s.lead = long_enough ? lead : 0;
-    s.snap = long_enough && lead ? 2 : 0;
-    auto length = [&](long long w) { return work_tiles(w) + s.lead * work_units(w); };
-    const long long all = length(total);
-    s.share = (all + gridDim.x - 1) / gridDim.x;
-    if (s.share > turn) s.share = (s.share + turn - 1) / turn * turn;
-    s.at = blockIdx.x * s.share;
-    s.end = min(s.at + s.share, all);
-    if (s.at >= s.end) return false;
-    // the entry: in hand if one pass covered them all
-    long long carry = 0;
-    for (int base = 0; base < n; base += 32 * kWarps) {
-        const int i = base + threadIdx.x;
-        if (n > 32 * kWarps) {
-            count = i < n ? work(i, false) : 0;
-            long long sum;
-            mine = carry + block_prefix<kWarps>(count, sum);
-            carry += sum;
+    // pass 0 adds all entries up; pass 1 looks for the block's first one (its threads
+    // have their entry in hand already where one step covers them all)
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        long long carry = 0;
+#pragma unroll 1
+        for (int base = 0; base < n; base += 32 * kWarps) {
+            const int i = base + threadIdx.x;
+            if (pass == 0 || n > 32 * kWarps) {
+                count = i < n ? work(i, pass == 0 && blockIdx.x == 0) : 0;
+                long long sum;
+                mine = carry + block_prefix<kWarps>(count, sum);
+                carry += sum;
+            }
+            if (pass == 0) continue;
+            if (s.at >= s.length(mine) && s.at < s.length(mine + count)) {
+                s_entry = i;
+                s_before = s.length(mine);
+                s_work = count;
+            }
+            if (n > 32 * kWarps && s.at < s.length(carry)) break;  // the same for every thread
         }
-        if (s.at >= length(mine) && s.at < length(mine + count)) {
-            s_entry = i;
-            s_before = length(mine);
-        }
-        if (n > 32 * kWarps && s.at < length(carry)) break;  // the same for every thread
+        if (pass == 1) break;
+        total = carry;
+        const bool long_enough = work_tiles(total) >= (long long)kLeadShare * gridDim.x;
+        s.lead = long_enough ? lead : 0;
+        s.snap = long_enough && lead ? 2 : 0;
+        const long long all = s.length(total);
+        s.share = all < 0x7fffffff - gridDim.x ? (long long)(((uint32_t)all + gridDim.x - 1) / gridDim.x)
+                                               : (all + gridDim.x - 1) / gridDim.x;
+        if (s.share > turn) s.share = (s.share + turn - 1) / turn * turn;
+        s.at = blockIdx.x * s.share;
+        s.end = min(s.at + s.share, all);
+        if (s.at >= s.end) return false;
     }
     __syncthreads();
     s.entry = s_entry;
     s.before = s_before;
+    s.work = s_work;
     return true;
 }
 
