@@ -457,14 +457,14 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         ++kr.i;
         commit(bars.k_empty[ks]);
         for (int j = 0; j < nkv; ++j) {
-            const uint32_t vs = vr.slot();  // V_j landed with K_j
+            const uint32_t vs = vr.slot(), nks = kr.slot();  // V_j landed with K_j
             ++vr.i;
             bool have_next_k = false;
-            const uint32_t nks = kr.slot();
 #pragma unroll 1
             for (int t = 0; t < NQT; ++t) {
                 const int n = t ? n1 : n0, left = (t ? left1 : left0) - BN * j;
                 if (j >= n) continue;
+                const int steps = key_steps(left), next_steps = key_steps(left - BN);
                 if (!wait(bars.p_full[t], (p_ph >> t) & 1)) return;
                 p_ph ^= 1u << t;
                 if (j == 0) {
@@ -473,7 +473,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
                     of_ph ^= 1u << t;
                 }
                 tc_fence_after();
-                issue_pv(t, vs, j > 0, key_steps(left));
+                issue_pv(t, vs, j > 0, steps);
                 if (j == n - 1) commit(bars.o_done[t]);
                 if (j + 1 < n) {
                     if (!have_next_k) {
@@ -481,7 +481,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
                         have_next_k = true;
                         tc_fence_after();
                     }
-                    issue_s(t, nks, key_steps(left - BN));
+                    issue_s(t, nks, next_steps);
                     if (j + 1 == n - 1) commit(bars.q_empty[t]);
                 }
             }
@@ -774,18 +774,18 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
                 p.lse[(int64_t)(hk * p.group + lrow - my_tok * p.group) * p.n_q + q0 + token] =
                     l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
         } else {
-            float *at[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 32 * quarter + (lane & ~3) + k;
-                at[k] = r < live ? p.parts.o + (part_row + r) * D : nullptr;
-            }
+            // (at most two parts a block: a row a lane, in little code)
+            float *row = p.parts.o + (part_row + lrow) * D;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D; c += 32) {
                 uint32_t u[32];
-                tmem_ld_x32(o_addr + 32 * c, u);
+                tmem_ld_x32(o_addr + c, u);
                 tmem_ld_wait(u);
-                store_rows_at<float>(u, 1.f, at, 32 * c, lane);
+                if (lrow < live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(row + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                }
             }
             if (lrow < live) p.parts.ml[part_row + lrow] = make_float2(m, l);
         }
