@@ -3,11 +3,12 @@
 // U_c, m = max m_c, l = sum 2^(m_c - m) l_c and O = sum 2^(m_c - m) U_c / l, the
 // (m, l, U) combination of the online-softmax recurrence, in block order.
 //
-// A fixed grid: every block reads all notes (32 bytes for each block of the
-// attention kernel), lists the units that were cut, and takes (unit, row) items in
-// turn, one warp per row, D / 32 columns a lane.  Latency-bound: the notes, the parts'
-// (m, l), then the parts, a few of them at a time in flight; 8
-// blocks an SM (63 drafts of 8 sequences: 119 us with 12, 122 with 6, 137 with 2).
+// Block (b, y) merges rows y, y + gridDim.y, ... (times the warps) of the unit
+// that block b of the attention kernel noted as begun and cut, if it did; one
+// warp per row, D / 32 columns a lane.  Latency-bound: a note, the parts' (m, l),
+// then the parts, a few of them at a time in flight.  (A fixed grid that first
+// lists the noted units, so that no block finds none, was slower: the list's
+// latency is longer than what the empty blocks take.)
 #include "../../include/attn.h"
 #include "common.cuh"
 
@@ -16,36 +17,17 @@ namespace attn {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMaxBlocks = 1024;  // of the attention kernel (one per SM)
 
 template <typename Tout, int D>
 __global__ void __launch_bounds__(32 * kWarps) parts_merge_kernel(const PartsMergeParams p) {
     constexpr int kCols = D / 32;
-    __shared__ int s_cut[kMaxBlocks];
-    __shared__ uint32_t s_mask[kMaxBlocks / 32];
     pdl_trigger();
     pdl_wait();
+    const CutUnit u = p.parts.cut[blockIdx.x];
+    const int first = blockIdx.x;
+    if (u.last <= first) return;
     const int lane = threadIdx.x & 31, d = lane * kCols;
-    // the cut units in ascending order, the same list in every block
-    const int words = (p.blocks + 31) / 32;
-    for (int w = threadIdx.x >> 5; w < words; w += kWarps) {
-        const int b = 32 * w + lane;
-        const uint32_t m = __ballot_sync(0xffffffffu, b < p.blocks && p.parts.cut[b].last > b);
-        if (lane == 0) s_mask[w] = m;
-    }
-    __syncthreads();
-    int count = 0;
-    for (int w = 0; w < words; ++w) {
-        const uint32_t m = s_mask[w];
-        if ((int)(threadIdx.x >> 5) == w % kWarps && (m >> lane & 1))
-            s_cut[count + __popc(m & ((1u << lane) - 1))] = 32 * w + lane;
-        count += __popc(m);
-    }
-    __syncthreads();
-    const int items = count * p.rows;
-    for (int x = blockIdx.x * kWarps + (threadIdx.x >> 5); x < items; x += gridDim.x * kWarps) {
-        const int first = s_cut[x / p.rows], r = x % p.rows;
-        const CutUnit u = p.parts.cut[first];
+    for (int r = blockIdx.y * kWarps + (threadIdx.x >> 5); r < p.rows; r += gridDim.y * kWarps) {
         const int tile = r / p.tile_rows, in = r - tile * p.tile_rows, row = u.base + tile * p.tile_live + in;
         if (in >= p.tile_live || row >= u.rows) continue;
         auto slot = [&](int b) { return (int64_t)(b == first ? 2 * b + 1 : 2 * b) * p.rows + r; };
@@ -84,9 +66,8 @@ __global__ void __launch_bounds__(32 * kWarps) parts_merge_kernel(const PartsMer
 
 template <typename Tout>
 cudaError_t launch_typed(const PartsMergeParams &p, cudaStream_t s) {
-    if (p.blocks > kMaxBlocks) return cudaErrorInvalidValue;
-    const int64_t want = ((int64_t)p.blocks * p.rows + kWarps - 1) / kWarps, cap = 8 * (int64_t)sm_count();
-    const dim3 grid((int)(want < cap ? want : cap));
+    const int y = (p.rows + kWarps - 1) / kWarps;
+    const dim3 grid(p.blocks, y < 16 ? y : 16);
     if (p.D == 64) return launch_pdl(parts_merge_kernel<Tout, 64>, grid, dim3(32 * kWarps), 0, s, p);
     return launch_pdl(parts_merge_kernel<Tout, 128>, grid, dim3(32 * kWarps), 0, s, p);
 }

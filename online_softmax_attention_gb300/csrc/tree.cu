@@ -11,10 +11,11 @@
 // Inside a block the four warps take the stretch's tiles in turn, each with a
 // ring of cp.async stages of its own (no block-wide barrier in the loop), and
 // combine their (m, l, U) through shared memory at the unit's end.  16-bit
-// types use mma.sync m16n8k16: with 16 or 32 query rows the contraction does 16
-// to 32 operations per cached byte, far below what even that path sustains
-// beside the HBM rate, and its row granularity fits a group's few rows, where
-// tcgen05 tiles would be 128 rows high.  f32 caches use FFMA, one key per lane.
+// types use mma.sync m16n8k16: with 16 query rows the contraction does 16
+// operations per cached byte, far below what even that path sustains beside the
+// HBM rate, and its row granularity fits a group's few rows, where tcgen05 tiles
+// would be 128 rows high (entries of more rows go to group_tc.cu).  f32 caches use
+// FFMA, one key per lane.
 //
 // Bound: HBM, the cache rows of every sequence read once.  Rows past L are
 // zero-filled by cp.async and never read from memory, so stale slots (NaN
@@ -31,9 +32,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 
-template <typename T, int D, int MT>
+template <typename T, int D>
 struct Cfg {
-    static constexpr int kRows = 16 * MT;
+    static constexpr int kRows = 16;
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kKeys = kRowBytes > 256 ? 16 : 32;  // keys of a tile
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
@@ -136,9 +137,9 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int token, int he
     store4(static_cast<Tout *>(p.o) + token * p.o_st + head * p.o_sh + d, v);
 }
 
-template <typename T, typename Tout, int D, int MT>
+template <typename T, typename Tout, int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
-    using C = Cfg<T, D, MT>;
+    using C = Cfg<T, D>;
     constexpr int kRows = C::kRows, kKeys = C::kKeys;
     constexpr bool kMma = sizeof(T) == 2;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -229,28 +230,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
         }
         __syncthreads();  // the query rows are in shared memory
 
-        float m[MT][2], l[MT][2], u[MT][kMma ? D / 8 : 1][4];   // mma: rows lane / 4 and + 8 of each m-tile
+        float m[2], l[2], u[kMma ? D / 8 : 1][4];                                        // mma: rows lane / 4 and + 8
         float sm[kMma ? 1 : kRows], sl[kMma ? 1 : kRows], su[kMma ? 1 : kRows][D / 32];  // FFMA: every row
-        uint32_t qf[MT == 1 && kMma ? D / 16 : 1][4];
+        uint32_t qf[kMma ? D / 16 : 1][4];
         const uint32_t q_a = smem_addr(sQ);
-        // ldmatrix address of the 16 x 16 block (rows of m-tile mt, columns 16 kk ..)
-        auto q_block = [&](int mt, int kk) -> uint32_t {
-            const int r = 16 * mt + (lane & 15), ch = 2 * kk + (lane >> 4);
-            return q_a + r * C::kRowBytes + 16 * (ch ^ (r & 7));
-        };
         if constexpr (kMma) {
+            m[0] = m[1] = -INFINITY;
+            l[0] = l[1] = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                m[mt][0] = m[mt][1] = -INFINITY;
-                l[mt][0] = l[mt][1] = 0.f;
+            for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j)
+                for (int k = 0; k < 4; ++k) u[j][k] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) u[mt][j][k] = 0.f;
-            }
-            if constexpr (MT == 1) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) ldsm4(q_block(0, kk), qf[kk]);
+            for (int kk = 0; kk < D / 16; ++kk) {  // the 16 x 16 block of columns 16 kk ..
+                const int r = lane & 15, ch = 2 * kk + (lane >> 4);
+                ldsm4(q_a + r * C::kRowBytes + 16 * (ch ^ (r & 7)), qf[kk]);
             }
         } else {
 #pragma unroll
@@ -277,113 +271,83 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
             const int key0 = tile * kKeys;
             const bool masked = key0 + kKeys > ctx;  // the tile reaches the new tokens or the end
             if constexpr (kMma) {
-                float sc[MT][kKeys / 8][4];
+                float sc[kKeys / 8][4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
-                    for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) sc[mt][j][k] = 0.f;
+                    for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
                 // S = Q K^T: one ldmatrix gives the B operands of 16 keys x 16 columns
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t qa[MT][4];
-                    if constexpr (MT > 1) {
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) ldsm4(q_block(mt, kk), qa[mt]);
-                    }
+                for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
                     for (int j = 0; j < kKeys / 16; ++j) {
                         const int r = 16 * j + (lane & 7) + ((lane >> 4) << 3), ch = 2 * kk + ((lane >> 3) & 1);
                         uint32_t b[4];
                         ldsm4(k_a + r * C::kRowBytes + 16 * (ch ^ (r & 7)), b);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const uint32_t(&a)[4] = MT == 1 ? qf[MT == 1 ? kk : 0] : qa[mt];
-                            mma16816<T>(sc[mt][2 * j], a, b[0], b[1]);
-                            mma16816<T>(sc[mt][2 * j + 1], a, b[2], b[3]);
-                        }
+                        mma16816<T>(sc[2 * j], qf[kk], b[0], b[1]);
+                        mma16816<T>(sc[2 * j + 1], qf[kk], b[2], b[3]);
                     }
-                }
+                // into log2 units, then the mask: lane holds rows lane / 4 (+ 8), columns 2 (lane % 4) (+ 1) of each 8
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    // into log2 units, then the mask: lane holds rows lane / 4 (+ 8), columns 2 (lane % 4) (+ 1) of each 8
+                for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
-                    for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) sc[mt][j][k] *= p.scale_log2;
-                    if (masked) {
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int t = min((row0 + 16 * mt + 8 * hf + (lane >> 2)) / p.group, e.T - 1);
-#pragma unroll
-                            for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int key = key0 + 8 * j + 2 * (lane & 3) + k;
-                                    if (key >= e.L || !sees(p, e, t, key - ctx)) sc[mt][j][2 * hf + k] = -INFINITY;
-                                }
-                        }
-                    }
-                    uint32_t pf[kKeys / 16][4];
+                    for (int k = 0; k < 4; ++k) sc[j][k] *= p.scale_log2;
+                if (masked) {
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < kKeys / 8; ++j) mx = fmaxf(mx, fmaxf(sc[mt][j][2 * hf], sc[mt][j][2 * hf + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float m_new = fmaxf(m[mt][hf], mx);
-                        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                        const float alpha = exp2_approx(m[mt][hf] - m_use);
-                        m[mt][hf] = m_new;
-                        float sum = 0.f;
+                        const int t = min((row0 + 8 * hf + (lane >> 2)) / p.group, e.T - 1);
 #pragma unroll
                         for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const float x = exp2_approx(sc[mt][j][2 * hf + k] - m_use);
-                                sc[mt][j][2 * hf + k] = x;
-                                sum += x;
+                                const int key = key0 + 8 * j + 2 * (lane & 3) + k;
+                                if (key >= e.L || !sees(p, e, t, key - ctx)) sc[j][2 * hf + k] = -INFINITY;
                             }
-                        l[mt][hf] = l[mt][hf] * alpha + sum;  // this lane's columns; joined at the unit's end
-#pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            u[mt][j][2 * hf] *= alpha;
-                            u[mt][j][2 * hf + 1] *= alpha;
-                        }
                     }
-                    // P in the value type (the MMA's operand): rounding to nearest, as the other kernels
-#pragma unroll
-                    for (int j = 0; j < kKeys / 16; ++j) {
-                        pf[j][0] = pack_pair<T>(sc[mt][2 * j][0], sc[mt][2 * j][1]);
-                        pf[j][1] = pack_pair<T>(sc[mt][2 * j][2], sc[mt][2 * j][3]);
-                        pf[j][2] = pack_pair<T>(sc[mt][2 * j + 1][0], sc[mt][2 * j + 1][1]);
-                        pf[j][3] = pack_pair<T>(sc[mt][2 * j + 1][2], sc[mt][2 * j + 1][3]);
-                    }
-                    // kept in sc's registers for the value contraction below
-#pragma unroll
-                    for (int j = 0; j < kKeys / 16; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) sc[mt][j][k] = __uint_as_float(pf[j][k]);
                 }
-                // U += P V: transposed ldmatrix gives the B operands of 16 keys x 16 columns
 #pragma unroll
-                for (int j = 0; j < kKeys / 16; ++j)
+                for (int hf = 0; hf < 2; ++hf) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < kKeys / 8; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * hf], sc[j][2 * hf + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float m_new = fmaxf(m[hf], mx);
+                    const float m_use = m_new == -INFINITY ? 0.f : m_new;
+                    const float alpha = exp2_approx(m[hf] - m_use);
+                    m[hf] = m_new;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float x = exp2_approx(sc[j][2 * hf + k] - m_use);
+                            sc[j][2 * hf + k] = x;
+                            sum += x;
+                        }
+                    l[hf] = l[hf] * alpha + sum;  // this lane's columns; joined at the unit's end
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        u[j][2 * hf] *= alpha;
+                        u[j][2 * hf + 1] *= alpha;
+                    }
+                }
+                // U += P V, P in the value type (the MMA's operand; rounded to nearest, as in the
+                // other kernels): transposed ldmatrix gives the B operands of 16 keys x 16 columns
+#pragma unroll
+                for (int j = 0; j < kKeys / 16; ++j) {
+                    const uint32_t pf[4] = {pack_pair<T>(sc[2 * j][0], sc[2 * j][1]), pack_pair<T>(sc[2 * j][2], sc[2 * j][3]),
+                                            pack_pair<T>(sc[2 * j + 1][0], sc[2 * j + 1][1]),
+                                            pack_pair<T>(sc[2 * j + 1][2], sc[2 * j + 1][3])};
 #pragma unroll
                     for (int dd = 0; dd < D / 16; ++dd) {
                         const int r = 16 * j + (lane & 15), ch = 2 * dd + (lane >> 4);
                         uint32_t b[4];
                         ldsm4_t(v_a + r * C::kRowBytes + 16 * (ch ^ (r & 7)), b);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t a[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) a[k] = __float_as_uint(sc[mt][j][k]);
-                            mma16816<T>(u[mt][2 * dd], a, b[0], b[1]);
-                            mma16816<T>(u[mt][2 * dd + 1], a, b[2], b[3]);
-                        }
+                        mma16816<T>(u[2 * dd], pf, b[0], b[1]);
+                        mma16816<T>(u[2 * dd + 1], pf, b[2], b[3]);
                     }
+                }
             } else {
                 // FFMA: lane = key; the row's products with every query row
                 float sc[kRows];
@@ -444,19 +408,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
         float *s_u = reinterpret_cast<float *>(smem) + warp * kRows * D;
         if constexpr (kMma) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int hf = 0; hf < 2; ++hf) {
+                float sum = l[hf];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int r = 8 * hf + (lane >> 2);
+                if ((lane & 3) == 0) s_ml[warp * kRows + r] = make_float2(m[hf], sum);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float sum = l[mt][hf];
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    const int r = 16 * mt + 8 * hf + (lane >> 2);
-                    if ((lane & 3) == 0) s_ml[warp * kRows + r] = make_float2(m[mt][hf], sum);
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j)
-                        *reinterpret_cast<float2 *>(s_u + r * D + 8 * j + 2 * (lane & 3)) =
-                            make_float2(u[mt][j][2 * hf], u[mt][j][2 * hf + 1]);
-                }
+                for (int j = 0; j < D / 8; ++j)
+                    *reinterpret_cast<float2 *>(s_u + r * D + 8 * j + 2 * (lane & 3)) =
+                        make_float2(u[j][2 * hf], u[j][2 * hf + 1]);
+            }
         } else {
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
@@ -505,10 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     }
 }
 
-template <typename T, typename Tout, int D, int MT>
+template <typename T, typename Tout, int D>
 cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
-    using C = Cfg<T, D, MT>;
-    auto kern = tree_kernel<T, Tout, D, MT>;
+    using C = Cfg<T, D>;
+    auto kern = tree_kernel<T, Tout, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int blocks = tree_blocks();
@@ -530,16 +492,9 @@ cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
     return launch_parts_merge(m, s);
 }
 
-template <typename T, typename Tout, int D>
-cudaError_t launch_rows(const TreeParams &p, cudaStream_t s) {
-    if constexpr (sizeof(T) == 2)
-        if (tree_rows(p) == 32) return launch_typed<T, Tout, D, 2>(p, s);
-    return launch_typed<T, Tout, D, 1>(p, s);
-}
-
 template <typename T, typename Tout>
 cudaError_t launch_d(const TreeParams &p, cudaStream_t s) {
-    return p.D == 64 ? launch_rows<T, Tout, 64>(p, s) : launch_rows<T, Tout, 128>(p, s);
+    return p.D == 64 ? launch_typed<T, Tout, 64>(p, s) : launch_typed<T, Tout, 128>(p, s);
 }
 
 template <typename T>
@@ -552,13 +507,14 @@ cudaError_t launch_out(const TreeParams &p, cudaStream_t s) {
 
 int tree_blocks() { return sm_count(); }
 
-// Rows by the entries' average: the keys of a unit are read once for all its
-// rows, so entries of more rows take larger units.
+// Entries of more than 16 rows on average take the tensor-core kernel's units: the
+// keys are read once for up to 256 rows (32 sequences of 2000-4000 tokens, 32 key heads'
+// rows each, D = 128: 84 us; two 16-row units here: 102).  With 16 rows it is this
+// kernel that is faster (75 against 84 us; 4 rows: 71 against 82), without a 128-row
+// tile's latency per key tile.  Pages of fewer than 8 rows have no TMA box.
 int tree_rows(const TreeParams &p) {
-    if (p.dtype == ATTN_F32 || p.n < 1) return 16;
-    const int64_t rows = (int64_t)p.n_q * p.group;
-    if (rows > (int64_t)32 * p.n && p.c.page_shift >= 3 && group_supported(p.dtype, p.D, p.group)) return kGroupRows;
-    return rows > (int64_t)16 * p.n ? 32 : 16;
+    const bool many = (int64_t)p.n_q * p.group > (int64_t)16 * p.n;
+    return many && p.c.page_shift >= 3 && group_supported(p.dtype, p.D, p.group) ? kGroupRows : 16;
 }
 
 cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s) {
