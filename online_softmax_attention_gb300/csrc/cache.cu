@@ -438,8 +438,14 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const Cache
 
 // ---- write -----------------------------------------------------------------------------
 
-// One warp per new row: its entry by binary search in cu, its place from the
-// sequence's length, then the row's H * D elements of k and v.
+// One warp per new row.  Its data (the first kAhead 16-byte chunks a lane of k and of
+// v) is loaded first, and lands while the warp looks its place up: a chain of five
+// dependent loads (offsets, sequence, length, page, count), which is what bounds
+// the small calls that decoding and drafting make.  The entry is the last one whose
+// offset is at most the row: counted by the lanes together for short lists, by
+// binary search for long ones.
+constexpr int kAhead = 4;
+
 __global__ void __launch_bounds__(kCopyThreads)
     write_kernel(const CacheParams c, int layer, const int *seqs, const int *cu, int n,
                  const char *kb, const char *vb, int64_t ks_tok, int64_t ks_head,
@@ -450,15 +456,33 @@ __global__ void __launch_bounds__(kCopyThreads)
     const int warps = gridDim.x * (kCopyThreads / 32);
     const int per_row = c.row_bytes >> 4, per_tok = c.H * per_row;
     for (int64_t r = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); r < n_rows; r += warps) {
-        if (r >= cu[n]) break;  // rows behind the last entry
-        // the last entry whose offset is <= r (empty entries before it share its offset)
-        int lo = 0, hi = n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= r) lo = mid;
-            else hi = mid - 1;
+        uint4 kr[kAhead], vr[kAhead];
+        auto load = [&](int x0) {
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int x = x0 + 32 * q + lane, h = x / per_row, ch = 16 * (x - h * per_row);
+                if (x < per_tok) {
+                    kr[q] = *reinterpret_cast<const uint4 *>(kb + r * ks_tok + h * ks_head + ch);
+                    vr[q] = *reinterpret_cast<const uint4 *>(vb + r * vs_tok + h * vs_head + ch);
+                }
+            }
+        };
+        load(0);
+        int lo = 0;
+        if (n <= 256) {
+            int below = 0;
+            for (int j = lane; j < n; j += 32) below += cu[j] <= r;
+            lo = max(0, __reduce_add_sync(0xffffffffu, below) - 1);
+        } else {
+            int hi = n - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cu[mid] <= r) lo = mid;
+                else hi = mid - 1;
+            }
         }
         const int s = seqs[lo], begin = cu[lo], end = cu[lo + 1];
+        if (r >= cu[n]) break;  // rows behind the last entry
         bool bad = !in_range(s, c.max_seqs) || r < begin || r >= end || end > n_rows;
         for (int j = lane; j < lo; j += 32) bad = bad || seqs[j] == s;  // an earlier entry has the sequence
         int64_t off = 0;
@@ -475,12 +499,16 @@ __global__ void __launch_bounds__(kCopyThreads)
             if (lane == 0) report_status(c.status, ATTN_EINVAL);
             continue;
         }
-        for (int x = lane; x < per_tok; x += 32) {
-            const int h = x / per_row, ch = 16 * (x - h * per_row);
-            const uint4 kr = *reinterpret_cast<const uint4 *>(kb + r * ks_tok + h * ks_head + ch);
-            const uint4 vr = *reinterpret_cast<const uint4 *>(vb + r * vs_tok + h * vs_head + ch);
-            *reinterpret_cast<uint4 *>(c.k + off + h * c.b_head + ch) = kr;
-            *reinterpret_cast<uint4 *>(c.v + off + h * c.b_head + ch) = vr;
+        for (int x0 = 0; x0 < per_tok; x0 += 32 * kAhead) {
+            if (x0) load(x0);
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int x = x0 + 32 * q + lane, h = x / per_row, ch = 16 * (x - h * per_row);
+                if (x < per_tok) {
+                    *reinterpret_cast<uint4 *>(c.k + off + h * c.b_head + ch) = kr[q];
+                    *reinterpret_cast<uint4 *>(c.v + off + h * c.b_head + ch) = vr[q];
+                }
+            }
         }
     }
 }
