@@ -64,7 +64,7 @@ struct Stretch {
     // the unit's edge.
     __device__ __forceinline__ int tile(long long x, long long u0, int n) const {
         const long long o = x - u0 - lead;
-        return o <= 0 || o < snap ? 0 : o >= n || o > n - snap ? n : (int)o;
+        return o >= n ? n : o <= 0 || o < snap ? 0 : o > n - snap ? n : (int)o;
     }
     __device__ __forceinline__ long long length(long long w) const { return work_tiles(w) + lead * work_units(w); }
 };
