@@ -90,8 +90,26 @@ struct WorkItem {
     int b, h, t, ntiles, c;
 };
 
+// The heads of a sequence in batches of about kBatchItems items (four a CTA), tile by
+// tile over a batch's heads: the CTAs running at the same time still share the batch's
+// rows in L2, and under the causal relation a batch ends with its shortest items.  For
+// the grouped dK / dV items, which loop over every query head of the group: a head's
+// long items no longer start last (2 x 4096 rows, 8 key heads of 4 query heads each:
+// the step 988 -> 918 us, dq items in the same order).  Ungrouped items are shorter, and lose more to L2 than to
+// the tail (32 packed sequences' forward 811 -> 840 us).
+constexpr int kBatchItems = 608;
+
+// Item r of the `per_head * H` of a sequence: its head and tile.
+__device__ __forceinline__ void batch_item(int r, int per_head, int H, int &h, int &t) {
+    const int heads = min(H, (kBatchItems + per_head - 1) / per_head);  // of a batch
+    const int h0 = r / (heads * per_head) * heads;
+    const int rem = r - h0 * per_head, here = min(heads, H - h0);
+    t = rem / here;
+    h = h0 + rem - t * here;
+}
+
 __device__ __forceinline__ WorkItem map_item(int w, const int *prefix, int n_seq, int H,
-                                             bool descending, int splits = 1) {
+                                             bool descending, int splits = 1, bool batched = false) {
     int lo = 0, hi = n_seq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -101,6 +119,11 @@ __device__ __forceinline__ WorkItem map_item(int w, const int *prefix, int n_seq
     const int base = __ldg(prefix + lo);
     const int per_head = (__ldg(prefix + lo + 1) - base) / H;  // tiles * splits
     const int r = w - base;
+    if (batched) {  // (no splits)
+        int h, t;
+        batch_item(r, per_head, H, h, t);
+        return {lo, h, descending ? per_head - 1 - t : t, per_head, 0};
+    }
     const int h = r / per_head;
     const int rem = r - h * per_head;
     int t = splits == 1 ? rem : rem / splits;
