@@ -128,11 +128,19 @@ int check_common(int n_q, int n_k, int H, int H_kv, int D, int relation, int dty
     return ATTN_OK;
 }
 
-size_t sched_bytes(int n_seq) { return align256(sizeof(int) * (size_t)(kSchedHeaderInts + n_seq + 1)); }
+size_t sched_bytes(int n_seq, bool ordered = false) {
+    return align256(sizeof(int) * (size_t)(kSchedHeaderInts + n_seq + 1 + (ordered ? n_seq : 0)));
+}
 
-Sched sched_at(void *base) {
+// The backward takes the sequences longest-first: its items are a head's whole pass
+// over the queries, and one that starts late runs alone.
+bool sorted_schedule(int n_seq) { return n_seq > 1 && n_seq <= kSortedSeqs; }
+
+
+// order_seqs > 0: with room for the order of that many sequences.
+Sched sched_at(void *base, int order_seqs = 0) {
     int *p = static_cast<int *>(base);
-    return Sched{p, p + kSchedHeaderInts};
+    return Sched{p, p + kSchedHeaderInts, order_seqs > 0 ? p + kSchedHeaderInts + order_seqs + 1 : nullptr};
 }
 
 // ---- forward ---------------------------------------------------------------
@@ -325,8 +333,8 @@ BwdLayout bwd_layout(int n_seq, int H, int n_q, int D, bool fused) {
     BwdLayout L;
     const size_t rows = align256(sizeof(float) * (size_t)H * (size_t)(n_q > 0 ? n_q : 1));
     L.kv = 0;
-    L.q = sched_bytes(n_seq);
-    L.dr = L.q + sched_bytes(n_seq);
+    L.q = sched_bytes(n_seq, sorted_schedule(n_seq));
+    L.dr = 2 * L.q;
     L.lse2 = L.dr + rows;
     L.dqa = L.lse2 + rows;
     L.total = L.dqa + (fused ? align256(sizeof(float) * (size_t)H * (size_t)(n_q > 0 ? n_q : 0) * (size_t)D) : 0);
@@ -392,8 +400,8 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     const bool fused = bwd_fused(a);
     const BwdLayout L = bwd_layout(a->n_seq, a->H, a->n_q, a->D, fused);
     char *ws = static_cast<char *>(a->workspace);
-    p.sched_kv = sched_at(ws + L.kv);
-    p.sched_q = sched_at(ws + L.q);
+    p.sched_kv = sched_at(ws + L.kv, sorted_schedule(a->n_seq) ? a->n_seq : 0);
+    p.sched_q = sched_at(ws + L.q, sorted_schedule(a->n_seq) ? a->n_seq : 0);
     p.dr = reinterpret_cast<float *>(ws + L.dr);
     p.lse2 = reinterpret_cast<float *>(ws + L.lse2);
     p.dq_accum = fused ? reinterpret_cast<float *>(ws + L.dqa) : nullptr;

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
         __syncthreads();
         if (w >= total) break;
         // causal: earlier key blocks are seen by more query blocks, so run them first
-        const WorkItem it = map_item(w, p.sched_kv.prefix, p.n_seq, p.Hkv, false);
+        const WorkItem it = map_item(w, p.sched_kv, p.n_seq, p.Hkv, false);
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
         const int w = s_w;
         __syncthreads();
         if (w >= total) break;
-        const WorkItem it = map_item(w, p.sched_q.prefix, p.n_seq, p.H, true);
+        const WorkItem it = map_item(w, p.sched_q, p.n_seq, p.H, true);
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);

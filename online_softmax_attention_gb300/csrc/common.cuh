@@ -108,8 +108,9 @@ __device__ __forceinline__ void batch_item(int r, int per_head, int H, int &h, i
     h = h0 + rem - t * here;
 }
 
-__device__ __forceinline__ WorkItem map_item(int w, const int *prefix, int n_seq, int H,
+__device__ __forceinline__ WorkItem map_item(int w, const Sched &sched, int n_seq, int H,
                                              bool descending, int splits = 1, bool batched = false) {
+    const int *prefix = sched.prefix;
     int lo = 0, hi = n_seq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -119,6 +120,7 @@ __device__ __forceinline__ WorkItem map_item(int w, const int *prefix, int n_seq
     const int base = __ldg(prefix + lo);
     const int per_head = (__ldg(prefix + lo + 1) - base) / H;  // tiles * splits
     const int r = w - base;
+    if (sched.order) lo = __ldg(sched.order + lo);
     if (batched) {  // (no splits)
         int h, t;
         batch_item(r, per_head, H, h, t);

@@ -10,12 +10,16 @@
 namespace attn {
 
 // Schedule block in the workspace: [0] dynamic work counter, [1] item count,
-// then the per-sequence prefix of item counts (n_seq + 1 ints).
+// then the per-sequence prefix of item counts (n_seq + 1 ints), and for the
+// backward of up to kSortedSeqs sequences the sequences longest-first (n_seq ints),
+// to which the prefix then refers by position.
 constexpr int kSchedHeaderInts = 16;
+constexpr int kSortedSeqs = 1024;
 
 struct Sched {
     int *hdr;          // counter, total
     const int *prefix; // n_seq + 1 entries
+    int *order;        // n_seq entries, or null: sequences as they are
 };
 
 struct FwdParams {

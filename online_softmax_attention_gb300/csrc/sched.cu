@@ -21,7 +21,8 @@ prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, 
             int n_q, int n_k, int causal, const PrepJobs jobs, int *status) {
     const PrepJob &job = jobs.job[blockIdx.x];
     const int H = job.H, block = job.block, rows_are_keys = job.rows_are_keys, splits = job.splits;
-    int *hdr = job.sched.hdr, *prefix = const_cast<int *>(job.sched.prefix);
+    int *hdr = job.sched.hdr, *prefix = const_cast<int *>(job.sched.prefix), *order = job.sched.order;
+    __shared__ int s_len[kSortedSeqs], s_order[kSortedSeqs];
     __shared__ int s_bad;
     __shared__ int s_warp[kPrepThreads / 32];
     __shared__ long long s_carry;
@@ -46,12 +47,29 @@ prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, 
     __syncthreads();
     bad = s_bad;
 
+    auto length = [&](int b) {
+        return rows_are_keys ? ((cu_k ? cu_k[b + 1] - cu_k[b] : n_k)) : ((cu_q ? cu_q[b + 1] - cu_q[b] : n_q));
+    };
+    // longest sequences first, equal ones as they are: a sequence's place is the number
+    // that go before it (n_seq <= kSortedSeqs = the block's threads)
+    if (order) {
+        if (tid < n_seq) s_len[tid] = length(tid);
+        __syncthreads();
+        if (tid < n_seq) {
+            const int mine = s_len[tid];
+            int place = 0;
+            for (int j = 0; j < n_seq; ++j) place += s_len[j] > mine || (s_len[j] == mine && j < tid);
+            s_order[place] = tid;
+            order[place] = tid;
+        }
+        __syncthreads();
+    }
+
     for (int base = 0; base < n_seq; base += kPrepThreads) {
         const int b = base + tid;
         int cnt = 0;
         if (b < n_seq && !bad) {
-            const int len = rows_are_keys ? ((cu_k ? cu_k[b + 1] - cu_k[b] : n_k))
-                                          : ((cu_q ? cu_q[b + 1] - cu_q[b] : n_q));
+            const int len = order ? s_len[s_order[b]] : length(b);
             cnt = (len + block - 1) / block * H * splits;
         }
         // inclusive scan across the block
