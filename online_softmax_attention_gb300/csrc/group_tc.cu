@@ -204,7 +204,7 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
     uint32_t q_uses[NQT] = {0, 0};
     bool q_pending[NQT] = {false, false};
     auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, wd));
+        return __all_sync(0xffffffffu, mbar_wait_small(smem_u32(&bar), parity, wd));
     };
     const bool ordered = p.paged ? p.mask == nullptr : p.causal != 0;
     // pages: this lane's piece of a key tile
@@ -428,7 +428,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         __syncwarp();
     };
     auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, wd));
+        return __all_sync(0xffffffffu, mbar_wait_small(smem_u32(&bar), parity, wd));
     };
     auto commit = [&](uint64_t &bar) {
         if (elect_one()) tc_commit(smem_u32(&bar));
@@ -593,7 +593,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
 
     for (int i = 0;; ++i) {
         const int slot = i % kSegs;
-        bool ok = mbar_wait(smem_u32(&bars.seg_full[slot]), (i / kSegs) & 1, wd);
+        bool ok = mbar_wait_small(smem_u32(&bars.seg_full[slot]), (i / kSegs) & 1, wd);
         if (!__all_sync(0xffffffffu, ok)) return;
         // read where it is needed, so that the inner loop keeps its registers; given back at the end
         const Seg &sg = segs[slot];
@@ -630,7 +630,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         };
         int j = 0;
         for (; j < plain; ++j) {
-            ok = mbar_wait(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
+            ok = mbar_wait_small(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
@@ -685,7 +685,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
                 if (p.mask) bits &= mrow ? mask_bits(mrow, p.mask_words, key0 + 32 * c - sg.ctx) : 0u;
                 return bits;
             };
-            ok = mbar_wait(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
+            ok = mbar_wait_small(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
@@ -750,7 +750,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
 
         // epilogue: O = U / l and lse, or the part's U, m and l
-        ok = mbar_wait(smem_u32(&bars.o_done[t]), o_cnt & 1, wd);
+        ok = mbar_wait_small(smem_u32(&bars.o_done[t]), o_cnt & 1, wd);
         ++o_cnt;
         if (!__all_sync(0xffffffffu, ok)) return;
         tc_fence_after();

@@ -93,17 +93,42 @@ struct Watchdog {
 // short budget run out.
 constexpr long long kPolledBudget = 1ll << 20;
 
-// A wait ran out: end the CTA's others too, and record it.  (Out of line: the
-// waits stand in many places, and code that never runs still takes room in the
-// instruction cache between the code that does.)
+// Wait for the phase of parity `parity` to complete.  Returns false if the
+// CTA is aborting (this wait timed out, or another one did).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Watchdog &wd) {
+    if (wd.budget < kPolledBudget) {
+        const long long t0 = clock64();
+        for (;;) {
+            if (mbar_test_wait(bar, parity)) return true;
+            if (*reinterpret_cast<volatile int *>(wd.abort_flag)) return false;
+            if (clock64() - t0 > wd.budget) {
+                *reinterpret_cast<volatile int *>(wd.abort_flag) = 1;
+                report_status(wd.status, ATTN_ETIMEOUT);
+                return false;
+            }
+        }
+    }
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(wd.abort_flag)) return false;
+        if (clock64() - t0 > wd.budget) {
+            *reinterpret_cast<volatile int *>(wd.abort_flag) = 1;
+            report_status(wd.status, ATTN_ETIMEOUT);
+            return false;
+        }
+    }
+}
+
+// The same in less code, for kernels whose roles together outgrow the instruction
+// cache: one loop for both ways of waiting, and the timeout out of line.  (The
+// backward's kernels, which fit, are 2 % faster with the form above.)
 static __device__ __noinline__ void wait_expired(int *abort_flag, int *status) {
     *reinterpret_cast<volatile int *>(abort_flag) = 1;
     report_status(status, ATTN_ETIMEOUT);
 }
-
-// Wait for the phase of parity `parity` to complete.  Returns false if the
-// CTA is aborting (this wait timed out, or another one did).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Watchdog &wd) {
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, const Watchdog &wd) {
     const bool polled = wd.budget < kPolledBudget;
     if (!polled && mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
