@@ -149,7 +149,13 @@ typedef struct attn_fwd_args {
  * query heads: query head h attends to key / value head h / G (integer
  * division).  In the backward dk and dv hold H_kv heads too, each the sum over
  * its group's query heads, added in f32 in a fixed order and rounded once.
- * H_kv must divide H (ATTN_EINVAL). */
+ * H_kv must divide H (ATTN_EINVAL).  f16 / bf16 inputs with G > 1 run a
+ * tensor-core kernel that packs the (token, head of the group) rows of a key head
+ * into its tiles, when the library chooses the schedule (num_splits = 0 and
+ * num_ctas = 0, at most 2048 sequences, G <= 128, no fp8 or pruning): two
+ * launches, no schedule preparation; key ranges cut between CTAs are merged
+ * from the workspace (about 40 MB at D = 128).  With that kernel the rows of other
+ * sequences, and rows behind the last one, may hold anything, NaN included. */
 
 /* fp8 queries and keys (qk_fp8 = 1; no counterpart on the pages, a use of the
  * sm_103a tensor cores' 8-bit score contraction): q and k hold e4m3 values,

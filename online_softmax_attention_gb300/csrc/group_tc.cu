@@ -44,11 +44,11 @@ constexpr int kSegs = 4;                // ring of unit parts
 constexpr int kSegConsumers = 1 + 8;    // MMA warp, softmax warps
 constexpr float kRescaleThreshold = 8.f;  // log2 units, as fwd_tc.cu
 // What a unit costs besides its key tiles, in key tiles (about 1.7 us each): the
-// queries' loads, the masked tile, the epilogue.
-#ifndef ATTN_GROUP_LEAD
-#define ATTN_GROUP_LEAD 2
-#endif
-constexpr int kLead = ATTN_GROUP_LEAD;
+// queries' loads, the masked tile, the epilogue.  (48 packed prompts of 9 to 420
+// tokens, 24 packed training rows' step, 3 prompts of 5000 to 8192: 60 / 192 / 950 us
+// with 1, 62 / 187 / 957 with 2, 63 / 194 / 965 with 3; 100 / 252 / 1070 with 0,
+// measured on an earlier form whose other steps were slower.)
+constexpr int kLead = 2;
 
 template <int D>
 struct Cfg {

@@ -114,6 +114,18 @@ def test_backward_tensor_cores(lens, hq, hkv, dtype, d, dq_mode):
         check_grad(g, r, f"{name} {lens}")
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float16, 64)])
+def test_backward_of_many_blocks(dtype, d):
+    """Several key blocks and query blocks a head, sequences taken longest-first, heads in batches."""
+    lens = [90, 1300, 260, 0, 700]
+    x, cu = make(lens, 8, 2, d, dtype, 22, True)
+    c = {n: t.cuda() for n, t in x.items()}
+    o, lse = attn.fwd(c["q"], c["k"], c["v"], causal=True, cu_seqlens_q=cu)
+    got = attn.bwd(c["q"], c["k"], c["v"], o, lse, c["do"], causal=True, cu_seqlens_q=cu)
+    for name, g, r in zip(("dq", "dk", "dv"), got, gradients(x, lens, d ** -0.5)):
+        check_grad(g, r, name)
+
+
 @pytest.mark.parametrize("kernel,dtype,causal", [("simt", torch.float32, True), ("simt", torch.float32, False),
                                                  ("simt", torch.float16, True), ("tc", torch.bfloat16, False)])
 def test_backward_other_kernels(kernel, dtype, causal):

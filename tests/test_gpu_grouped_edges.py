@@ -261,3 +261,70 @@ def test_both_bindings_make_the_same_calls():
         cache.write(ds, dc, q, q)  # six heads, not two
     with pytest.raises(ValueError):
         cache.extend(ds, dc)
+
+
+@pytest.mark.parametrize("page,news", [(256, [40, 1]), (1024, [40, 30]), (8, [33, 64])])
+def test_page_sizes_around_a_key_tile(page, news):
+    cache, model, seqs, g = make([1500, 130], page, 2, 128, torch.bfloat16, 68, layout="hnd")
+    q = torch.randn(sum(news), 8, 128, generator=g).bfloat16()
+    run(cache, model, seqs, news, q, what=f"page {page}")
+
+
+def test_fp8_and_pruned_forwards_with_shared_heads():
+    """The forward's other options map key heads too: as on repeated heads, bit for bit."""
+    x, _ = make_packed([300], 8, 2, 128, torch.bfloat16, 69)
+    q, k, v = (x[n].cuda() for n in "qkv")
+    k4, v4 = k.repeat_interleave(4, 1), v.repeat_interleave(4, 1)
+    e4m3 = torch.float8_e4m3fn
+    a = attn.fwd(q.to(e4m3), k.to(e4m3), v, causal=True)
+    b = attn.fwd(q.to(e4m3), k4.to(e4m3), v4, causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = attn.fwd(q, k, v, prune_threshold=0.5), attn.fwd(q, k4, v4, prune_threshold=0.5)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_the_allocation_free_forward_with_shared_heads():
+    import ctypes
+    lib = _abi.load()
+    lens = [200, 30]
+    x, cu = make_packed(lens, 8, 2, 64, torch.float16, 70)
+    c = {n: t.cuda() for n, t in x.items()}
+    want = attn.fwd(c["q"], c["k"], c["v"], causal=True, cu_seqlens_q=cu, num_splits=1)
+    call = attn.FwdCall(c["q"], c["k"], c["v"], causal=True, cu_seqlens_q=cu)
+    call.args.workspace, call.args.workspace_bytes = None, 0
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.attn_fwd_noalloc(ctypes.byref(call.args), s) == 0
+    assert torch.equal(call.o, want[0]) and torch.equal(call.lse, want[1])
+
+
+def test_one_sequence_in_two_entries():
+    """Reads may name a sequence twice: the same queries give the same rows."""
+    cache, _, seqs, g = make([500, 60], 16, 2, 64, torch.float16, 71)
+    q = torch.randn(3, 8, 64, generator=g).half().cuda()
+    o, lse = attn.tree_fwd(torch.cat([q, q]), cache, [seqs[0], seqs[0]], [0, 3, 6])
+    one = attn.tree_fwd(q, cache, [seqs[0]], [0, 3])
+    # (cuts differ with the number of entries: equal up to rounding)
+    assert torch.allclose(o[:3].float(), one[0].float(), atol=2e-3, rtol=2e-3)
+    assert torch.allclose(o[3:].float(), one[0].float(), atol=2e-3, rtol=2e-3)
+    assert torch.allclose(lse[:, :3], one[1], atol=1e-4) and torch.allclose(lse[:, 3:], one[1], atol=1e-4)
+
+
+def test_caches_that_are_refused():
+    k = torch.zeros(1, 4, 16, 2, 64, dtype=torch.float16, device="cuda")
+    i = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    n, r = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (2, 4))
+    with pytest.raises(ValueError, match="same strides"):
+        attn.Cache(k, k.permute(0, 1, 3, 2, 4).contiguous().permute(0, 1, 3, 2, 4), i, n, r)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        attn.Cache(k, k.clone(), i.t(), r, r)
+    with pytest.raises(TypeError):
+        attn.Cache(k, k.clone(), i.long(), n, r)
+    with pytest.raises(ValueError, match="unsupported"):
+        attn.Cache(k[:, :, :12], k.clone()[:, :, :12], i, n, r)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        attn.Cache(k, k.clone(), i.cpu(), n, r)
+    c = attn.Cache(k, k.clone(), i, n, r)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.free([1 << 32])
+    with pytest.raises(ValueError):
+        c.compact(remap=i)
