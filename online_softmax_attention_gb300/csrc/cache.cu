@@ -482,8 +482,9 @@ __global__ void __launch_bounds__(kCopyThreads)
             }
         }
         const int s = seqs[lo], begin = cu[lo], end = cu[lo + 1];
-        if (r >= cu[n]) break;  // rows behind the last entry
-        bool bad = !in_range(s, c.max_seqs) || r < begin || r >= end || end > n_rows;
+        // rows behind the last entry (a last offset below the one before it is reported instead)
+        if (lo == n - 1 && 0 <= begin && begin <= end && end <= r) break;
+        bool bad = !in_range(s, c.max_seqs) || begin < 0 || r < begin || r >= end || end > n_rows;
         for (int j = lane; j < lo; j += 32) bad = bad || seqs[j] == s;  // an earlier entry has the sequence
         int64_t off = 0;
         if (!__any_sync(0xffffffffu, bad)) {

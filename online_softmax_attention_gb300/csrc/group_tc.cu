@@ -144,7 +144,7 @@ __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, 
     if (p.cu_q) {
         e.q0 = p.cu_q[i];
         e.T = p.cu_q[i + 1] - e.q0;
-        ok = e.q0 >= 0 && e.T >= 0 && p.cu_q[i + 1] <= p.n_q;
+        ok = e.q0 >= 0 && e.q0 <= p.cu_q[i + 1] && p.cu_q[i + 1] <= p.n_q;  // (e.T may have wrapped)
     } else {
         e.q0 = 0;
         e.T = p.n_q;
@@ -163,9 +163,9 @@ __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, 
         if (p.cu_k) {
             e.k0 = p.cu_k[i];
             e.L = p.cu_k[i + 1] - e.k0;
-            ok = ok && e.k0 >= 0 && e.L >= 0 && p.cu_k[i + 1] <= p.n_k;
+            ok = ok && e.k0 >= 0 && e.k0 <= p.cu_k[i + 1] && p.cu_k[i + 1] <= p.n_k;
         }
-        ok = ok && (!p.causal || e.T == e.L);
+        ok = ok && (i > 0 || (e.q0 == 0 && e.k0 == 0)) && (!p.causal || e.T == e.L);
         e.ctx = p.causal ? 0 : e.L;
     }
     if (!ok) {

@@ -108,7 +108,7 @@ __device__ __forceinline__ Entry entry_at(const TreeParams &p, int i, int rows, 
     e.q0 = p.cu[i];
     e.T = p.cu[i + 1] - e.q0;
     e.s = p.seqs[i];
-    bool ok = (unsigned)e.s < (unsigned)p.c.max_seqs && e.q0 >= 0 && e.T >= 0 && p.cu[i + 1] <= p.n_q;
+    bool ok = (unsigned)e.s < (unsigned)p.c.max_seqs && e.q0 >= 0 && e.q0 <= p.cu[i + 1] && p.cu[i + 1] <= p.n_q;
     e.L = ok ? p.c.lens[e.s] : 0;
     ok = ok && e.L >= e.T && (long long)e.L <= (long long)p.c.max_pages << p.c.page_shift &&
          (!p.mask || e.T <= 64 * p.mask_words);

@@ -328,3 +328,45 @@ def test_caches_that_are_refused():
         c.free([1 << 32])
     with pytest.raises(ValueError):
         c.compact(remap=i)
+
+
+LOW = -2 ** 31
+
+
+@pytest.mark.parametrize("cq,ck,causal", [([0, 64, LOW], [0, 64, LOW], True), ([0, 1, LOW], [0, 64, 64], False),
+                                          ([0, 64, 64], [0, 1, LOW], False), ([LOW, 64], [LOW, 64], True),
+                                          ([3, 64], [3, 64], True)])
+def test_offsets_whose_difference_wraps_are_refused(cq, ck, causal):
+    x, _ = make_packed([64], 4, 2, 64, torch.float16, 71)
+    c = {n: t.cuda() for n, t in x.items()}
+    attn.fwd(c["q"], c["k"], c["v"], causal=causal, cu_seqlens_q=torch.tensor(cq, dtype=torch.int32).cuda(),
+             cu_seqlens_k=torch.tensor(ck, dtype=torch.int32).cuda())
+    assert attn.device_status() == _abi.ATTN_EINVAL
+    assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("cu", [[LOW, 3, 40], [-5, 3, 40], [0, LOW, 40], [0, 1, LOW]])
+def test_cache_offsets_below_zero_are_refused(cu):
+    cache, _, seqs, g = make([50, 60], 16, 2, 64, torch.float16, 72)
+    before = cache.k.clone()
+    offsets = torch.tensor(cu, dtype=torch.int32).cuda()
+    rows = torch.randn(40, 2, 64, generator=g).half().cuda()
+    free = torch.tensor([i for i in range(4) if i not in seqs][:2], dtype=torch.int32).cuda()  # of length 0
+    for list_ in (free, torch.tensor(seqs, dtype=torch.int32).cuda()):
+        attn.device_status()
+        cache.write(list_, offsets, rows, rows)
+        entry = range(2) if list_ is free else [i for i in range(2) if not 0 <= cu[i] <= cu[i + 1] <= 40]
+        for i in entry:  # (a valid entry's rows are written)
+            for page in cache.table[int(list_[i])].tolist():
+                if 0 <= page < cache.k.shape[1]:
+                    assert torch.equal(cache.k[:, page].view(torch.int16), before[:, page].view(torch.int16))
+        if list_ is free or cu[2] == 40:
+            assert attn.device_status() == _abi.ATTN_EINVAL
+        for heads in (2, 8):  # the 16-row kernel, the packed one
+            call = attn.TreeCall(torch.randn(40, heads, 64, generator=g).half().cuda(), cache, list_, offsets)
+            call.o.fill_(5.0)
+            o, _ = call.run()
+            for i in entry:
+                if 0 <= cu[i] < cu[i + 1]:
+                    assert (o[cu[i]:cu[i + 1]] == 5).all()
+            assert attn.device_status() == _abi.ATTN_EINVAL
