@@ -45,7 +45,9 @@ __global__ void __launch_bounds__(32 * kWarps) parts_merge_kernel(const PartsMer
             float v[kCols];
             if constexpr (kCols == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(part);
             else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(part);
-            if (ml.x == -INFINITY) continue;  // a part that admits no key: its sums may not have been written
+            // a part that admits no key: its sums may not have been written (a query of NaN has the
+            // same max, but a sum of NaN, which has to reach the output)
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;
             const float f = exp2_approx(ml.x - mx);
             sum = fmaf(f, ml.y, sum);
 #pragma unroll

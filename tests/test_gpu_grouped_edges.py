@@ -370,3 +370,25 @@ def test_cache_offsets_below_zero_are_refused(cu):
                 if 0 <= cu[i] < cu[i + 1]:
                     assert (o[cu[i]:cu[i + 1]] == 5).all()
             assert attn.device_status() == _abi.ATTN_EINVAL
+
+
+@pytest.mark.parametrize("dtype,n,news,heads", [(torch.bfloat16, 9000, 1, 4), (torch.float32, 9000, 1, 4),
+                                                (torch.float16, 9000, 40, 8)])
+def test_a_query_of_nan_gives_nan_in_cut_units(dtype, n, news, heads):
+    """One long sequence, whose units are cut between blocks: its parts are merged."""
+    cache, _, seqs, g = make([n], 16, 1, 64, dtype, 73)
+    q = torch.randn(news, heads, 64, generator=g).to(dtype)
+    q[0, 1] = float("nan")
+    o, _ = attn.tree_fwd(q.cuda(), cache, seqs, [0, news])
+    want = torch.zeros(news, heads, dtype=torch.bool)
+    want[0, 1] = True
+    assert torch.equal(o.isnan().all(2).cpu(), want) and torch.equal(o.isnan().any(2).cpu(), want)
+
+
+def test_a_query_of_nan_gives_nan_in_a_cut_prompt():
+    x, cu = make_packed([6000], 8, 1, 128, torch.bfloat16, 74)
+    x["q"][4500, 3] = float("nan")
+    o, _ = attn.fwd(*(x[n].cuda() for n in "qkv"), causal=True, cu_seqlens_q=cu)
+    want = torch.zeros(6000, 8, dtype=torch.bool)
+    want[4500, 3] = True
+    assert torch.equal(o.isnan().all(2).cpu(), want) and torch.equal(o.isnan().any(2).cpu(), want)
