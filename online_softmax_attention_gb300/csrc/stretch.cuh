@@ -45,10 +45,13 @@ __device__ __forceinline__ long long block_prefix(long long x, long long &total)
 }
 
 // Work of an entry: its units and the key tiles they scan, in one word, so that
-// one prefix sum adds up both (fewer than 2^24 units and 2^40 tiles in all).
-__device__ __forceinline__ long long work_of(long long units, long long tiles) { return units << 40 | tiles; }
-__device__ __forceinline__ long long work_units(long long w) { return w >> 40; }
-__device__ __forceinline__ long long work_tiles(long long w) { return w & ((1ll << 40) - 1); }
+// one prefix sum adds up both: fewer than 2^27 units (rows are fewer than 2^31, and a
+// unit has more than 16 on average, or there are 2048 entries of 2^14 key heads at the
+// most) and fewer than 2^36 tiles (at 16 KiB of keys and values and more each, 1 PB).
+constexpr int kTileBits = 36;
+__device__ __forceinline__ long long work_of(long long units, long long tiles) { return units << kTileBits | tiles; }
+__device__ __forceinline__ long long work_units(long long w) { return w >> kTileBits; }
+__device__ __forceinline__ long long work_tiles(long long w) { return w & ((1ll << kTileBits) - 1); }
 
 struct Stretch {
     long long at, end;   // the block's part of the line

@@ -392,3 +392,25 @@ def test_a_query_of_nan_gives_nan_in_a_cut_prompt():
     want = torch.zeros(6000, 8, dtype=torch.bool)
     want[4500, 3] = True
     assert torch.equal(o.isnan().all(2).cpu(), want) and torch.equal(o.isnan().any(2).cpu(), want)
+
+
+def test_as_many_units_as_heads_and_sequences_allow():
+    """2048 sequences of one token and 4096 key heads, a unit each: the output is the token's value row."""
+    n, hkv = 2048, 4096
+    g = torch.Generator(device="cuda").manual_seed(75)
+    q = torch.randn(n, 2 * hkv, 64, generator=g, device="cuda", dtype=torch.float16)
+    k, v = (torch.randn(n, hkv, 64, generator=g, device="cuda", dtype=torch.float16) for _ in range(2))
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    call = attn.FwdCall(q, k, v, causal=True, cu_seqlens_q=cu, out=torch.full_like(q, 5.0))
+    o, _ = call.run()
+    assert attn.device_status() == 0
+    # one key: p = 1 and l = 1 exactly
+    assert torch.equal(o.view(n, hkv, 2, 64), v.unsqueeze(2).expand(n, hkv, 2, 64))
+
+
+def test_more_key_heads_than_the_packed_kernel_takes():
+    hkv = (1 << 14) + 1
+    x, cu = make_packed([1, 1], 2, 1, 64, torch.float16, 76)
+    q, k, v = (x[n].cuda().repeat(1, hkv, 1) for n in "qkv")
+    o, _ = attn.fwd(q, k, v, causal=True, cu_seqlens_q=cu)
+    assert torch.equal(o, v.repeat_interleave(2, 1)) and attn.device_status() == 0
