@@ -260,3 +260,37 @@ def test_a_captured_loop():
              lambda x: x.write(0, [2, 0, 1], [0, 4, 8, 12], k.float().cpu().numpy(), v.float().cpu().numpy()))
     same(c, m)
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("device", ["cuda", "cpu"])
+def test_entries_past_32_bits_are_not_cut(device):
+    """64-bit lists whose low 32 bits would be a good entry."""
+    c, m = make()
+    fill(c, m, [40, 17, 32])
+    far = 1 << 32
+    def refuses(f):
+        attn.device_status()
+        if device == "cpu":
+            with pytest.raises(ValueError, match="32 bits"):
+                f()
+        else:
+            f()
+            assert attn.device_status() == _abi.ATTN_EINVAL
+        same(c, m)
+    def t(*x):
+        return torch.tensor(x, device=device)
+    k, v = (torch.ones(2, 3, 64).half().cuda() for _ in range(2))
+    refuses(lambda: c.extend(t(far), t(1)))
+    refuses(lambda: c.extend(t(0), t(far + 1)))
+    refuses(lambda: c.fork(t(0), t(far + 5)))
+    refuses(lambda: c.free(t(1 - far)))
+    refuses(lambda: c.write(t(far), t(0, 2), k, v))
+    refuses(lambda: c.write(t(0), t(0, far + 2), k, v))
+    refuses(lambda: c.keep(t(0), t(3), t(far + 1).view(1, 1), t(1)))
+    refuses(lambda: c.keep(t(0), t(3), t(1).view(1, 1), t(far + 1)))
+    q = torch.ones(2, 3, 64).half().cuda()
+    refuses(lambda: attn.tree_fwd(q, c, t(far), t(0, 2)))
+    c.extend(t(0, 2), t(3, 1))  # 64-bit lists that fit
+    m.extend([0, 2], [3, 1])
+    same(c, m)
+    assert attn.device_status() == 0
