@@ -289,7 +289,7 @@ typedef struct attn_cache {
     int32_t H_kv, D;          /* heads; head dim (64 or 128) */
     int32_t dtype;            /* attn_dtype */
     int32_t max_seqs;         /* rows of table, 1..ATTN_CACHE_MAX_SEQS */
-    int32_t max_pages;        /* pages a sequence can hold */
+    int32_t max_pages;        /* pages a sequence can hold; max_pages * page_size <= 2^31 - 2^16 */
 } attn_cache;
 
 #define ATTN_CACHE_MAX_SEQS 262144
@@ -449,7 +449,7 @@ ATTN_API int attn_cache_extend(const attn_cache *c, const int32_t *seqs, const i
 
 /* Writes new k and v rows (n_rows, H_kv, D) of one layer: rows
  * [cu[i], cu[i + 1]) become the last cu[i + 1] - cu[i] tokens of sequence
- * seqs[i] (cu: n + 1 offsets from 0; rows from cu[n] on are not read).  An
+ * seqs[i] (cu: n + 1 offsets from 0; rows from cu[n] on are left out).  An
  * entry that does not fit, that repeats an earlier entry's sequence, or a row
  * whose page other sequences hold too is skipped and reported as ATTN_EINVAL;
  * the others are written. */

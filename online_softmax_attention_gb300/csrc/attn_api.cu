@@ -430,8 +430,9 @@ int plan_cache(const attn_cache *c, CacheParams &p) {
     if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) ||
         c->max_seqs > ATTN_CACHE_MAX_SEQS || c->H_kv > 4096 || c->n_layers > 32767)
         return ATTN_EUNSUPPORTED;
-    // token positions are int32
-    if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31 || c->n_pages > (1 << 30)) return ATTN_EUNSUPPORTED;
+    // token positions are int32, with room for rounding up to a tile or a page
+    if ((int64_t)c->max_pages * c->page_size > ((int64_t)1 << 31) - (1 << 16) || c->n_pages > (1 << 30))
+        return ATTN_EUNSUPPORTED;
     const int64_t es = (int64_t)elem_size(c->dtype);
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return ATTN_EINVAL;
     for (int64_t st : {c->stride_layer, c->stride_page, c->stride_tok, c->stride_head})

@@ -166,3 +166,13 @@ def test_k_and_v_of_two_shapes_are_refused():
     q, k, v = (torch.zeros(8, h, 64, dtype=torch.float16) for h in (4, 2, 4))
     with pytest.raises(ValueError, match="k and v must both"):
         attn.fwd(q, k, v, causal=True)
+
+
+@pytest.mark.parametrize("page", [1, 16, 1024])
+def test_positions_keep_clear_of_32_bits(page):
+    """A sequence of almost 2^31 tokens: rounding its length up to a tile or a page would overflow."""
+    lib, most = _abi.load(), ((1 << 31) - (1 << 16)) // page
+    for pages, ok in ((most, True), (most + 1, False), (((1 << 31) - 1) // page, False)):
+        c = _cache(page_size=page, max_pages=pages, table_stride=pages)
+        assert (lib.attn_cache_workspace_bytes(ctypes.byref(c), 1) > 0) == ok
+        assert lib.attn_cache_free(ctypes.byref(c), A, 0, None) == (0 if ok else _abi.ATTN_EUNSUPPORTED)
