@@ -258,6 +258,8 @@ class TreeCall:
             # (0 bytes: arguments that the call will refuse)
             workspace = torch.empty(_host.call(dev.index, _host.entry("attn_tree_workspace_bytes"), None, _host.TREE.pack(*head, 0, 0)) or 256,
                                     dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on the cache's device {dev}")
         self.workspace = workspace
         self.args = _host.TREE.pack(*head, workspace.data_ptr(), workspace.numel() * workspace.element_size())
 

@@ -241,3 +241,17 @@ def test_serving(dtype, d):
         want = attention(q1, torch.cat([ks[0], k1]), torch.cat([vs[0], v1]), np.ones((1, 41), bool), d ** -0.5)
         assert_output(o, lse, want, dtype, f"decode {s}")
     assert attn.device_status() == 0
+
+
+def test_workspaces_that_are_refused():
+    cache, _, seqs, g = make([50], 16, 2, 64, torch.float16, 47)
+    q = torch.randn(1, 4, 64, generator=g).half().cuda()
+    need = attn.TreeCall(q, cache, seqs, [0, 1]).workspace.numel()
+    with pytest.raises(ValueError, match="workspace"):
+        attn.TreeCall(q, cache, seqs, [0, 1], workspace=torch.empty(need, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        attn.TreeCall(q, cache, seqs, [0, 1], workspace=torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2])
+    for ws in (torch.empty(need - 256, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 256, dtype=torch.uint8, device="cuda")[16:]):  # too small; not 256-byte aligned
+        with pytest.raises(attn.AttnError):
+            attn.TreeCall(q, cache, seqs, [0, 1], workspace=ws).run()
