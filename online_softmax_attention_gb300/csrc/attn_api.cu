@@ -180,8 +180,6 @@ size_t parts_layout(int blocks, int rows, int D, void *workspace, Parts &w) {
 // The packed kernel's blocks each scan all sequences' lengths (384 at a time, a few
 // microseconds for this many); batches of more sequences take the prepared schedule.
 constexpr int kPackedMaxSeqs = 2048;
-// its count of units (stretch.cuh) holds for any batch of this many key heads
-constexpr int kPackedMaxHeads = 1 << 14;
 
 struct FwdLayout {
     size_t o_parts, lse_parts, split_ops, total;
@@ -271,7 +269,7 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     // grouped heads: packed query rows (group_tc.cu), which balance by themselves; a caller
     // that fixes the splits or the grid gets the ungrouped kernel's schedule
     p.packed = p.group > 1 && use_tc && !p.qk_fp8 && !p.prune && a->num_splits == 0 && a->num_ctas == 0 &&
-               a->n_seq <= kPackedMaxSeqs && p.Hkv <= kPackedMaxHeads && a->n_k > 0 && group_supported(p.dtype, p.D, p.group);
+               a->n_seq <= kPackedMaxSeqs && a->n_k > 0 && group_supported(p.dtype, p.D, p.group);
     p.n_splits = p.prune || p.packed ? 1 : (a->num_splits > 0 ? a->num_splits : auto_splits(p, use_tc));
     // work items (tiles x heads x splits) are numbered in int32
     const int64_t tiles = (int64_t)a->H * ((int64_t)a->n_q / kSimtBlock + a->n_seq + 1);

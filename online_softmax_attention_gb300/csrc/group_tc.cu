@@ -101,41 +101,12 @@ struct Entry {
 
 // key tiles that tokens [0, tok) of the entry need at most
 __device__ __forceinline__ int tiles_to(const GroupParams &p, const Entry &e, int tok) {
-    const bool ordered = p.paged ? p.mask == nullptr : p.causal != 0;
-    return max(1, cdiv(ordered ? min(e.L, e.ctx + min(tok, e.T)) : e.L, BN));
-}
-
-// sum over i < n of floor((a i + b) / 128), a >= 0, b >= 0 (the Euclid-like
-// recursion; after the first step everything is below 128 n)
-__device__ __forceinline__ long long floor_sum(int n0, int a0, int b0) {
-    long long r = (long long)(a0 >> 7) * ((long long)n0 * (n0 - 1) / 2) + (long long)(b0 >> 7) * n0;
-    uint32_t n = n0, m = BN, a = a0 & (BN - 1), b = b0 & (BN - 1);
-    for (;;) {
-        const uint32_t y = a * n + b;
-        if (y < m) return r;
-        n = y / m;
-        b = y - n * m;
-        const uint32_t t = m;
-        m = a;
-        a = t;
-        r += (long long)(a / m) * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
-        a %= m;
-        b %= m;
-    }
+    return attn::tiles_to(p.paged ? p.mask == nullptr : p.causal != 0, e.L, e.ctx, e.T, tok);
 }
 
 // key tiles of the first n units of a key head
 __device__ __forceinline__ long long unit_tiles(const GroupParams &p, const Entry &e, int per, int n) {
-    const int full = tiles_to(p, e, 1), last = tiles_to(p, e, e.T);
-    if (full == last) return (long long)n * last;
-    if (n <= 8) {
-        long long r = 0;
-        for (int i = 0; i < n; ++i) r += tiles_to(p, e, (i + 1) * per);
-        return r;
-    }
-    // units before the entry's last one hold `per` tokens: ceil((ctx + (i + 1) per) / 128)
-    const int whole = min(n, e.units - 1);
-    return floor_sum(whole, per, e.ctx + per + BN - 1) + (n > whole ? last : 0);
+    return attn::unit_tiles(p.paged ? p.mask == nullptr : p.causal != 0, e.L, e.ctx, e.T, e.units, per, n);
 }
 
 __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, bool report) {
@@ -176,8 +147,8 @@ __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, 
     return e;
 }
 
-__device__ __forceinline__ long long entry_work(const GroupParams &p, const Entry &e, int per) {
-    return e.T > 0 ? work_of((long long)p.Hkv * e.units, p.Hkv * unit_tiles(p, e, per, e.units)) : 0;
+__device__ __forceinline__ Work entry_work(const GroupParams &p, const Entry &e, int per) {
+    return e.T > 0 ? Work{(long long)p.Hkv * e.units, p.Hkv * unit_tiles(p, e, per, e.units)} : Work{0, 0};
 }
 
 // Bounded wait for outstanding TMA writes before the CTA exits after an abort.
@@ -301,9 +272,7 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg *segs, const Stretc
         }
         g.slot = t1 - t0 == n_unit ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
         if (t0 == 0 && t1 < n_unit && lane == 0) {  // begins here and goes on behind the stretch: for the merge
-            long long last = (u0 + st.lead + n_unit - 1) / st.share;
-            if (st.tile(last * st.share, u0, n_unit) == n_unit) --last;
-            p.parts.cut[blockIdx.x] = CutUnit{(int)last, e.q0, hk, unit * per * p.group, e.T * p.group, {0, 0, 0}};
+            p.parts.cut[blockIdx.x] = CutUnit{st.last_block(u0, n_unit), e.q0, hk, unit * per * p.group, e.T * p.group, {0, 0, 0}};
         }
         ok = publish(g);
         if (!ok) break;
@@ -847,8 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     pdl_wait();
     const int per = NQT * (BM / a.p.group);
     Stretch st;
-    const bool any = find_stretch<kThreads / 32>(
-        a.p.n, 1, kLead, [&](int i, bool report) { return entry_work(a.p, entry_at(a.p, i, per, report), per); }, st);
+    const bool any = find_stretch<kThreads / 32, kLead>(
+        a.p.n, 1, [&](int i, bool report) { return entry_work(a.p, entry_at(a.p, i, per, report), per); }, st);
     if (!any) st.end = st.at;
     if (threadIdx.x == 0) a.p.parts.cut[blockIdx.x].last = -1;  // the loading warp may put a unit there
     __syncthreads();

@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     pdl_wait();
 
     Stretch st;
-    const bool any = find_stretch<kWarps>(
-        p.n, kWarps, 0, [&](int i, bool report) { return work_of(0, entry_at(p, i, kRows, kKeys, report).tiles); }, st);
+    const bool any = find_stretch<kWarps, 0>(
+        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at(p, i, kRows, kKeys, report).tiles}; }, st);
     if (!any) {
         if (tid == 0) p.parts.cut[blockIdx.x].last = -1;
         return;
