@@ -475,13 +475,15 @@ ATTN_API int attn_cache_keep(const attn_cache *c, const int32_t *seqs, const int
                              void *workspace, size_t workspace_bytes, void *stream);
 
 /* Releases the pages of the sequences and empties them.  A sequence listed
- * twice is released once; entries out of range are skipped and reported. */
+ * twice is released once; entries out of range, and sequences whose length is
+ * not in [0, max_pages * page_size], are left as they are and reported. */
 ATTN_API int attn_cache_free(const attn_cache *c, const int32_t *seqs, int32_t n, void *stream);
 
 /* Moves the live pages to the front: with L live pages, those at or above L
  * move, in ascending order, to the free pages below L (all layers, k and v);
  * the tables and counts follow.  remap (n_pages entries, or NULL) gets every
- * page's new index, for references that the caller holds. */
+ * page's new index, for references that the caller holds.  With a length among
+ * all of lens that does not fit, nothing moves, and it is reported. */
 ATTN_API int attn_cache_compact(const attn_cache *c, int32_t *remap, void *workspace,
                                 size_t workspace_bytes, void *stream);
 

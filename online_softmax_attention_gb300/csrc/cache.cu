@@ -17,6 +17,7 @@
 // plans, one block's read of the counts (4 bytes a page).
 #include "../../include/attn.h"
 #include "common.cuh"
+#include "pages.h"
 
 namespace attn {
 
@@ -26,8 +27,11 @@ constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kSeenWords = ATTN_CACHE_MAX_SEQS / 32;  // bitmap of listed sequences (32 KiB)
 
-__device__ __forceinline__ int pages_of(const CacheParams &c, int tokens) {
-    return (tokens + (1 << c.page_shift) - 1) >> c.page_shift;
+__device__ __forceinline__ int pages_of(const CacheParams &c, int tokens) { return attn::pages_of(tokens, c.page_shift); }
+
+// Every length read from `lens` is checked before it places anything.
+__device__ __forceinline__ bool length_fits(const CacheParams &c, int len) {
+    return attn::length_fits(len, c.max_pages, c.page_shift);
 }
 
 __device__ __forceinline__ bool in_range(int x, int n) { return (unsigned)x < (unsigned)n; }
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) alloc_plan_kernel(const CachePar
             bad = !in_range(s, c.max_seqs) || (kFork ? !in_range(other, c.max_seqs) : other < 0);
             if (!bad) {
                 len = c.lens[s];
-                bad = len < 0 || pages_of(c, len) > c.max_pages || !list_once(seen, kFork ? other : s);
+                bad = !length_fits(c, len) || !list_once(seen, kFork ? other : s);
             }
             if (!bad) {
                 const int tail = len & (page - 1);
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const CachePara
         const int s = seqs[i], d = n_draft[i], k = n_keep[i];
         bool bad = !in_range(s, c.max_seqs);
         const int len = bad ? 0 : c.lens[s];
-        bad = bad || len < 0 || pages_of(c, len) > c.max_pages || d < 0 || d > len || k < 0 || k > d || k > keep_stride;
+        bad = bad || !length_fits(c, len) || d < 0 || d > len || k < 0 || k > d || k > keep_stride;
         if (lane == 0 && !bad) bad = !list_once(seen, s);
         if (!__any_sync(0xffffffffu, bad)) {
             const int base = len - d;
@@ -343,8 +347,8 @@ __global__ void __launch_bounds__(kCopyThreads) keep_move_kernel(const CachePara
 
 // ---- free ------------------------------------------------------------------------------
 
-// One block per entry.  The length is taken by an exchange, so that a sequence
-// listed twice is released once.
+// One block per entry.  The block that exchanges the length for 0 releases the pages, so
+// that a sequence listed twice is released once.
 __global__ void __launch_bounds__(kCopyThreads) free_kernel(const CacheParams c, const int *seqs) {
     __shared__ int s_len;
     pdl_trigger();
@@ -354,9 +358,14 @@ __global__ void __launch_bounds__(kCopyThreads) free_kernel(const CacheParams c,
         if (threadIdx.x == 0) report_status(c.status, ATTN_EINVAL);
         return;
     }
-    if (threadIdx.x == 0) s_len = atomicExch(&c.lens[s], 0);
+    if (threadIdx.x == 0) {
+        const int len = *const_cast<volatile int *>(&c.lens[s]);
+        s_len = 0;
+        if (!length_fits(c, len)) report_status(c.status, ATTN_EINVAL);
+        else if (atomicCAS(&c.lens[s], len, 0) == len) s_len = len;
+    }
     __syncthreads();
-    const int held = min(pages_of(c, max(s_len, 0)), c.max_pages);
+    const int held = pages_of(c, s_len);
     for (int k = threadIdx.x; k < held; k += kCopyThreads) {
         const int p = table_at(c, s, k);
         if (in_range(p, c.n_pages) && atomicSub(&c.refs[p], 1) > 0) continue;
@@ -369,7 +378,8 @@ __global__ void __launch_bounds__(kCopyThreads) free_kernel(const CacheParams c,
 
 // Plan: L = live pages (hdr[1]); the j-th live page at or above L (from[j])
 // moves to the j-th free page below L (pages[j]); as many of one as of the
-// other (hdr[2]).  remap: every page's new index.
+// other (hdr[2]).  remap: every page's new index.  With a length among lens that does
+// not fit, whose table cannot follow, L is the whole pool and nothing moves.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CacheParams c, const CachePlan w) {
     __shared__ int s_warp[32];
     pdl_trigger();
@@ -382,6 +392,12 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CacheP
     }
     int front;
     block_scan(live, s_warp, front);
+    bool bad = false;
+    for (int s = threadIdx.x; s < c.max_seqs; s += kPlanThreads) bad = bad || !length_fits(c, c.lens[s]);
+    if (__syncthreads_or(bad)) {
+        front = c.n_pages;
+        if (threadIdx.x == 0) report_status(c.status, ATTN_EINVAL);
+    }
     int holes = 0, movers = 0;
     for (int64_t base = 0; base < c.n_pages; base += 32 * kPlanThreads) {
         const int64_t at = base + 32 * threadIdx.x;
@@ -426,7 +442,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const Cache
     }
     const int front = w.hdr[1];
     for (int s = blockIdx.x; s < c.max_seqs; s += gridDim.x) {
-        const int held = min(pages_of(c, max(c.lens[s], 0)), c.max_pages);
+        const int held = pages_of(c, c.lens[s]);
         int *row = c.table + (int64_t)s * c.table_stride;
         for (int k = threadIdx.x; k < held; k += kCopyThreads) {
             const int p = row[k];
@@ -489,7 +505,7 @@ __global__ void __launch_bounds__(kCopyThreads)
         int64_t off = 0;
         if (!__any_sync(0xffffffffu, bad)) {
             const int len = c.lens[s], t = (int)(len - end + r);
-            bad = len < end - begin || pages_of(c, len) > c.max_pages;
+            bad = len < end - begin || !length_fits(c, len);
             if (!bad) {
                 const int p = table_at(c, s, t >> c.page_shift);
                 bad = !in_range(p, c.n_pages) || c.refs[p] > 1;

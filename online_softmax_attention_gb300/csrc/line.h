@@ -2,11 +2,7 @@
 // plain functions of their arguments, compiled for the host too.
 #pragma once
 
-#if defined(__CUDACC__)
-#define ATTN_HD __host__ __device__ __forceinline__
-#else
-#define ATTN_HD inline
-#endif
+#include "hd.h"
 
 namespace attn {
 
