@@ -103,15 +103,22 @@ def _kv_shape(k: torch.Tensor, v: torch.Tensor, D: int):
     return k.shape[0], k.shape[1]
 
 
-def _cu(cu, device) -> torch.Tensor | None:
+def _offsets(cu_q, cu_k, device) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """The offset lists of a call, as many of one as of the other (None for the keys: the queries')."""
+    q = _cu(cu_q, device, "cu_seqlens_q")
+    k = _cu(cu_k, device, "cu_seqlens_k") if cu_k is not None else q
+    if q is not None and k.numel() != q.numel():
+        raise ValueError(f"cu_seqlens_k must have {q.numel()} entries, as cu_seqlens_q has, got {k.numel()}")
+    return q, k
+
+
+def _cu(cu, device, name: str) -> torch.Tensor | None:
     if cu is None:
         return None
     if isinstance(cu, torch.Tensor) and cu.dtype == torch.int32 and cu.device == device and cu.is_contiguous():
         return cu
     cu = torch.as_tensor(cu)
-    if cu.dtype != torch.int32:
-        cu = cu.to(torch.int32)
-    return cu.to(device).contiguous()
+    return _host.int32(cu if cu.dtype == torch.int32 else cu.to(torch.int64), device, name)
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -145,8 +152,7 @@ class FwdCall:
         Tq, H, D = q.shape
         Tk, H_kv = _kv_shape(k, v, D)
         out_dtype = out_dtype or v.dtype
-        self.cu_q = _cu(cu_seqlens_q, dev)
-        self.cu_k = _cu(cu_seqlens_k if cu_seqlens_k is not None else cu_seqlens_q, dev)
+        self.cu_q, self.cu_k = _offsets(cu_seqlens_q, cu_seqlens_k, dev)
         self.o = out if out is not None else torch.empty((Tq, H, D), dtype=out_dtype, device=dev)
         self.lse = lse if lse is not None else torch.empty((H, Tq), dtype=torch.float32, device=dev)
         self.inputs = (q, k, v)
@@ -241,8 +247,7 @@ class BwdCall:
         Tq, H, D = q.shape
         Tk, H_kv = _kv_shape(k, v, D)
         gdt = grad_dtype or q.dtype
-        self.cu_q = _cu(cu_seqlens_q, dev)
-        self.cu_k = _cu(cu_seqlens_k if cu_seqlens_k is not None else cu_seqlens_q, dev)
+        self.cu_q, self.cu_k = _offsets(cu_seqlens_q, cu_seqlens_k, dev)
         self.dq = dq if dq is not None else torch.empty((Tq, H, D), dtype=gdt, device=dev)
         self.dk = dk if dk is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
         self.dv = dv if dv is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)

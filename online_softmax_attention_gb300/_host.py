@@ -1,4 +1,4 @@
-"""What a call costs on the host: current stream, device switch, tensor views.
+"""What a call costs on the host: current stream, device switch, argument structs and lists.
 
 A short attention call takes a few microseconds on the GPU, so the binding's
 own time decides how fast short calls follow one another.  The argument structs
@@ -41,6 +41,19 @@ def f32(x: float) -> float:
     """`x` as a C float takes it (beyond its range: infinite, which the library refuses)."""
     x = float(x)
     return x if -_FLOAT_MAX <= x <= _FLOAT_MAX or x != x else ctypes.c_float(x).value
+
+
+def int32(x: torch.Tensor, device: torch.device, name: str) -> torch.Tensor:
+    """Whole numbers as int32 on the device, never cut to their low bits: host values that do
+    not fit raise, device values become the nearest int32, which no operation accepts."""
+    if x.dtype == torch.int64:
+        if x.is_cuda:
+            x = x.clamp(-2 ** 31, 2 ** 31 - 1)
+        elif x.numel() and not -2 ** 31 <= int(x.min()) <= int(x.max()) < 2 ** 31:
+            raise ValueError(f"{name}: entries must fit 32 bits")
+    elif x.dtype not in (torch.int32, torch.int16, torch.int8, torch.uint8):
+        raise ValueError(f"{name} must be whole numbers of at most 64 bits, signed, not {x.dtype}")
+    return x.to(device=device, dtype=torch.int32).contiguous()
 
 
 def call(index: int, fn, where: str | None, *args) -> int:

@@ -24,19 +24,6 @@ from . import _abi, _host
 _DT = {torch.float16: _abi.ATTN_F16, torch.bfloat16: _abi.ATTN_BF16, torch.float32: _abi.ATTN_F32}
 
 
-def _int32(x: torch.Tensor, device: torch.device, name: str) -> torch.Tensor:
-    """Whole numbers as int32 on the device, never cut to their low bits: host values that do
-    not fit raise, device values become the nearest int32, which no operation accepts."""
-    if x.dtype == torch.int64:
-        if x.is_cuda:
-            x = x.clamp(-2 ** 31, 2 ** 31 - 1)
-        elif x.numel() and not -2 ** 31 <= int(x.min()) <= int(x.max()) < 2 ** 31:
-            raise ValueError(f"{name}: entries must fit 32 bits")
-    elif x.dtype not in (torch.int32, torch.int16, torch.int8, torch.uint8):
-        raise ValueError(f"{name} must be whole numbers of at most 64 bits, signed, not {x.dtype}")
-    return x.to(device=device, dtype=torch.int32).contiguous()
-
-
 def _ints(x, device: torch.device, name: str) -> torch.Tensor:
     """A list argument as a contiguous int32 vector on the cache's device."""
     if isinstance(x, torch.Tensor) and x.dtype == torch.int32 and x.device == device and x.dim() == 1 \
@@ -45,7 +32,7 @@ def _ints(x, device: torch.device, name: str) -> torch.Tensor:
     x = torch.as_tensor(x, dtype=torch.int32 if isinstance(x, (list, tuple)) and not x else None)
     if x.dim() != 1 or x.is_floating_point() or x.dtype == torch.bool:
         raise ValueError(f"{name} must be a vector of whole numbers")
-    return _int32(x, device, name)
+    return _host.int32(x, device, name)
 
 
 def _rows(t: torch.Tensor, name: str, heads: int | None, D: int, dtype: torch.dtype, device) -> tuple[int, int, int]:
@@ -189,7 +176,7 @@ class Cache:
             keep = torch.as_tensor(keep)
         if keep.dim() != 2 or keep.shape[0] != seqs.numel() or keep.is_floating_point() or keep.dtype == torch.bool:
             raise ValueError(f"keep must be ({seqs.numel()}, offsets) whole numbers, got {tuple(keep.shape)}")
-        keep = _int32(keep, self.device, "keep")
+        keep = _host.int32(keep, self.device, "keep")
         at, size, _ws = self._workspace(seqs.numel())
         self._call("attn_cache_keep", seqs.data_ptr(), n_draft.data_ptr(), keep.data_ptr(), keep.shape[1],
                    n_keep.data_ptr(), seqs.numel(), at, size)

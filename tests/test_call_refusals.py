@@ -1,0 +1,47 @@
+"""Arguments that the prepared calls refuse on the host, before any pointer is followed
+(CPU tensors: with good arguments the last refusal is that they are not on a GPU)."""
+import pytest
+import torch
+
+import online_softmax_attention_gb300 as attn
+
+
+def tensors(hq=4, hkv=2, n=8, d=64, dtype=torch.float16):
+    return [torch.zeros(n, h, d, dtype=dtype) for h in (hq, hkv, hkv)]
+
+
+def forward(**kw):
+    q, k, v = tensors()
+    return attn.fwd(q, k, v, causal=True, **kw)
+
+
+def backward(**kw):
+    q, k, v = tensors()
+    return attn.bwd(q, k, v, q, torch.zeros(4, 8), q, causal=True, **kw)
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+def test_good_arguments_only_lack_a_gpu(call):
+    for cu in (None, [0, 3, 8], torch.tensor([0, 3, 8]), torch.tensor([0, 3, 8], dtype=torch.int32)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(cu_seqlens_q=cu)
+        with pytest.raises(ValueError, match="CUDA"):
+            call(cu_seqlens_q=cu, cu_seqlens_k=cu)
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+def test_fewer_key_offsets_than_query_offsets(call):
+    """The kernels read as many of one list as of the other."""
+    for ck in ([0, 8], [0, 1, 3, 8], torch.tensor([0, 8], dtype=torch.int32)):
+        with pytest.raises(ValueError, match="cu_seqlens_k must have 3"):
+            call(cu_seqlens_q=[0, 3, 8], cu_seqlens_k=ck)
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+@pytest.mark.parametrize("far", [(1 << 32) + 8, -(1 << 32) + 8, 1 << 31])
+def test_offsets_are_not_cut_to_32_bits(call, far):
+    for cu in ([0, far], torch.tensor([0, far])):
+        with pytest.raises(ValueError, match="cu_seqlens_q: entries must fit 32 bits"):
+            call(cu_seqlens_q=cu)
+    with pytest.raises(ValueError, match="cu_seqlens_k: entries must fit 32 bits"):
+        call(cu_seqlens_q=[0, 8], cu_seqlens_k=[0, far])

@@ -1,0 +1,24 @@
+"""Arguments of the prepared calls that only the kernels can refuse, and what is refused on the host with tensors on the GPU."""
+import pytest
+import torch
+
+import online_softmax_attention_gb300 as attn
+from online_softmax_attention_gb300 import _abi
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("hkv", [4, 2])
+@pytest.mark.parametrize("cu", [[0, (1 << 32) + 64], [0, -(1 << 32) + 64], [1 << 32, 64]])
+def test_offsets_on_the_device_are_not_cut_to_32_bits(cu, hkv):
+    """64-bit offsets whose low 32 bits would be good ones."""
+    q, k, v = (torch.randn(64, h, 64, device="cuda").half() for h in (4, hkv, hkv))
+    cu = torch.tensor(cu, device="cuda")
+    o, lse = attn.fwd(q, k, v, causal=True)
+    assert attn.device_status() == 0
+    attn.fwd(q, k, v, causal=True, cu_seqlens_q=cu)
+    assert attn.device_status() == _abi.ATTN_EINVAL
+    attn.bwd(q, k, v, o, lse, q, causal=True, cu_seqlens_q=cu)
+    assert attn.device_status() == _abi.ATTN_EINVAL
+    got = attn.fwd(q, k, v, causal=True, cu_seqlens_q=torch.tensor([0, 64], device="cuda"))
+    assert attn.device_status() == 0 and torch.equal(got[0], o)
