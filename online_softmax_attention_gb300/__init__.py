@@ -121,6 +121,27 @@ def _cu(cu, device, name: str) -> torch.Tensor | None:
     return _host.int32(cu if cu.dtype == torch.int32 else cu.to(torch.int64), device, name)
 
 
+def _fits(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype | None, device) -> None:
+    """A (tokens, heads, D) tensor that has every row of `shape` (longer axes are not looked at)."""
+    if t.dim() != 3 or any(a < b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on q's device {device}, got {t.device}")
+
+
+def _lse_fits(t: torch.Tensor, H: int, T: int, device) -> None:
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.device != device or t.numel() < H * T \
+            or (t.dim() > 1 and min(H, T) > 1 and t.shape[-1] != T):
+        raise ValueError(f"lse must be contiguous float32 {(H, T)} on {device}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _workspace_fits(t: torch.Tensor, device) -> None:
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor:
     # torch's caching allocator returns 512-byte aligned blocks
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -156,6 +177,10 @@ class FwdCall:
         self.o = out if out is not None else torch.empty((Tq, H, D), dtype=out_dtype, device=dev)
         self.lse = lse if lse is not None else torch.empty((H, Tq), dtype=torch.float32, device=dev)
         self.inputs = (q, k, v)
+        _fits(k, "k", (Tk, H_kv, D), None, dev)
+        _fits(v, "v", (Tk, H_kv, D), None, dev)
+        _fits(self.o, "out", (Tq, H, D), None, dev)
+        _lse_fits(self.lse, H, Tq, dev)
         # pruned-tile counter (device, int64 storage of the library's uint64)
         self.pruned_tiles = torch.zeros(1, dtype=torch.int64, device=dev) if prune_threshold else None
         cu_q, cu_k = self.cu_q, self.cu_k
@@ -171,6 +196,8 @@ class FwdCall:
         self._at = ctypes.addressof(self.args)
         if workspace is None:
             workspace = _workspace(_host.entry("attn_fwd_workspace_bytes")(self._at), dev)
+        else:
+            _workspace_fits(workspace, dev)
         self.workspace = workspace
         self.args.workspace = workspace.data_ptr()
         self.args.workspace_bytes = workspace.numel() * workspace.element_size()

@@ -45,3 +45,21 @@ def test_offsets_are_not_cut_to_32_bits(call, far):
             call(cu_seqlens_q=cu)
     with pytest.raises(ValueError, match="cu_seqlens_k: entries must fit 32 bits"):
         call(cu_seqlens_q=[0, 8], cu_seqlens_k=[0, far])
+
+
+def prepared(**kw):
+    q, k, v = tensors()
+    return attn.FwdCall(q, k, v, causal=True, **kw)
+
+
+def test_outputs_that_a_forward_would_write_past():
+    for out in (torch.empty(8, 2, 64), torch.empty(7, 4, 64), torch.empty(8, 4, 32), torch.empty(32, 64)):
+        with pytest.raises(ValueError, match="out must be"):
+            prepared(out=out.half())
+    for lse in (torch.empty(4, 8).half(), torch.empty(2, 8), torch.empty(8, 4), torch.empty(4, 16)[:, ::2],
+                torch.empty(31)):
+        with pytest.raises(ValueError, match="lse must be"):
+            prepared(lse=lse)
+    for good in (torch.empty(9, 6, 64), torch.empty(8, 4, 64)):  # a buffer with room is written in part
+        with pytest.raises(ValueError, match="CUDA"):
+            prepared(out=good.half(), lse=torch.empty(4, 8))

@@ -22,3 +22,20 @@ def test_offsets_on_the_device_are_not_cut_to_32_bits(cu, hkv):
     assert attn.device_status() == _abi.ATTN_EINVAL
     got = attn.fwd(q, k, v, causal=True, cu_seqlens_q=torch.tensor([0, 64], device="cuda"))
     assert attn.device_status() == 0 and torch.equal(got[0], o)
+
+
+def test_outputs_and_workspaces_of_a_forward():
+    q, k, v = (torch.randn(64, h, 64, device="cuda").half() for h in (4, 2, 2))
+    want = attn.fwd(q, k, v, causal=True)
+    need = attn.FwdCall(q, k, v, causal=True).workspace.numel()
+    for kw in (dict(out=torch.empty(64, 4, 64).half()), dict(out=torch.empty_like(k)), dict(lse=torch.empty(4, 64)),
+               dict(workspace=torch.empty(need, dtype=torch.uint8)),
+               dict(workspace=torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            attn.FwdCall(q, k, v, causal=True, **kw)
+    with pytest.raises(ValueError):
+        attn.fwd(q, k.cpu(), v)
+    out, lse = torch.zeros(70, 6, 64, dtype=torch.float16, device="cuda"), torch.zeros(4, 64, device="cuda")
+    attn.FwdCall(q, k, v, causal=True, out=out, lse=lse).run()
+    assert torch.equal(out[:64, :4], want[0]) and torch.equal(lse, want[1])
+    assert not out[64:].any() and not out[:, 4:].any()
