@@ -279,6 +279,13 @@ class BwdCall:
         self.dk = dk if dk is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
         self.dv = dv if dv is not None else torch.empty((Tk, H_kv, D), dtype=gdt, device=dev)
         self.inputs = (q, k, v, o, lse, dout)
+        # one dtype is passed on for all inputs but o, and one for the gradients
+        for t, name, heads, dtype in ((k, "k", H_kv, q.dtype), (v, "v", H_kv, q.dtype), (self.dk, "dk", H_kv, gdt),
+                                      (self.dv, "dv", H_kv, gdt)):
+            _fits(t, name, (Tk, heads, D), dtype, dev)
+        for t, name, dtype in ((o, "o", None), (dout, "dout", q.dtype), (self.dq, "dq", gdt)):
+            _fits(t, name, (Tq, H, D), dtype, dev)
+        _lse_fits(lse, H, Tq, dev)
         cu_q, cu_k = self.cu_q, self.cu_k
         # a non-zero prune_threshold: the library refuses (fails closed)
         self.args = _abi.BwdArgs.from_buffer_copy(_host.BWD.pack(
@@ -293,6 +300,8 @@ class BwdCall:
         self._at = ctypes.addressof(self.args)
         if workspace is None:
             workspace = _workspace(_host.entry("attn_bwd_workspace_bytes")(self._at), dev)
+        else:
+            _workspace_fits(workspace, dev)
         self.workspace = workspace
         self.args.workspace = workspace.data_ptr()
         self.args.workspace_bytes = workspace.numel() * workspace.element_size()

@@ -63,3 +63,40 @@ def test_outputs_that_a_forward_would_write_past():
     for good in (torch.empty(9, 6, 64), torch.empty(8, 4, 64)):  # a buffer with room is written in part
         with pytest.raises(ValueError, match="CUDA"):
             prepared(out=good.half(), lse=torch.empty(4, 8))
+
+
+def gradients(**kw):
+    q, k, v = tensors()
+    a = dict(q=q, k=k, v=v, o=q, lse=torch.zeros(4, 8), dout=q)
+    a.update(kw)
+    return attn.BwdCall(causal=True, **a)
+
+
+def test_inputs_that_a_backward_would_read_past():
+    for name, t in (("o", torch.empty(8, 2, 64)), ("o", torch.empty(7, 4, 64)), ("dout", torch.empty(8, 2, 64)),
+                    ("dout", torch.empty(5, 4, 64)), ("dout", torch.empty(8, 4, 32))):
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            gradients(**{name: t.half()})
+    for lse in (torch.empty(2, 8), torch.empty(8, 4), torch.empty(4, 8).half(), torch.empty(4, 8, dtype=torch.float64),
+                torch.empty(8, 4).t(), torch.empty(16)):
+        with pytest.raises(ValueError, match="lse must be"):
+            gradients(lse=lse)
+    with pytest.raises(ValueError, match="CUDA"):
+        gradients(o=torch.empty(9, 4, 64), lse=torch.empty(32))  # f32 outputs, room, a flat lse
+
+
+def test_inputs_of_another_type_in_a_backward():
+    """One type is passed on for q, k, v and dout: another's bits would be read as it."""
+    for name, t in (("k", torch.empty(8, 2, 64)), ("v", torch.empty(8, 2, 64).bfloat16()), ("dout", torch.empty(8, 4, 64))):
+        with pytest.raises(TypeError, match=f"{name} must be torch.float16"):
+            gradients(**{name: t})
+
+
+def test_gradients_that_a_backward_would_write_past():
+    for name, t in (("dq", torch.empty(8, 2, 64)), ("dk", torch.empty(7, 2, 64)), ("dv", torch.empty(8, 1, 64))):
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            gradients(**{name: t.half()})
+        with pytest.raises(TypeError, match="torch.float32"):
+            gradients(grad_dtype=torch.float32, **{name: torch.empty(8, 4, 64).half()})
+    with pytest.raises(ValueError, match="CUDA"):
+        gradients(grad_dtype=torch.float32, dk=torch.empty(9, 2, 64), dq=torch.empty(8, 4, 64))

@@ -39,3 +39,26 @@ def test_outputs_and_workspaces_of_a_forward():
     attn.FwdCall(q, k, v, causal=True, out=out, lse=lse).run()
     assert torch.equal(out[:64, :4], want[0]) and torch.equal(lse, want[1])
     assert not out[64:].any() and not out[:, 4:].any()
+
+
+def test_arguments_of_a_backward():
+    q, k, v = (torch.randn(64, h, 64, device="cuda").half() for h in (4, 2, 2))
+    o, lse = attn.fwd(q, k, v, causal=True)
+    want = attn.bwd(q, k, v, o, lse, q, causal=True)
+    need = attn.BwdCall(q, k, v, o, lse, q, causal=True).workspace.numel()
+    for kw in (dict(dk=torch.empty(64, 2, 64).half()), dict(workspace=torch.empty(need, dtype=torch.uint8)),
+               dict(workspace=torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            attn.BwdCall(q, k, v, o, lse, q, causal=True, **kw)
+    for bad in ((q, k, v, k, lse, q), (q, k, v, o, lse, k), (q, k, v, o, lse.cpu(), q), (q, k, v, o, lse.t(), q),
+                (q, k, v, o.cpu(), lse, q)):
+        with pytest.raises(ValueError):
+            attn.bwd(*bad, causal=True)
+    with pytest.raises(TypeError):
+        attn.bwd(q, k, v, o, lse, q.float(), causal=True)
+    with pytest.raises(TypeError):
+        attn.bwd(q, k.bfloat16(), v, o, lse, q, causal=True)
+    dk = torch.zeros(70, 5, 64, dtype=torch.float16, device="cuda")
+    got = attn.BwdCall(q, k, v, o, lse, q, causal=True, dk=dk[:, 1:]).run()
+    assert torch.equal(got[0], want[0]) and torch.equal(dk[:64, 1:3], want[1]) and torch.equal(got[2], want[2])
+    assert not dk[64:].any() and not dk[:, 0].any() and not dk[:, 3:].any()
