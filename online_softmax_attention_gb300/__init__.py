@@ -96,9 +96,11 @@ def _view(t: torch.Tensor | None, name: str) -> _abi.AttnTensor:
 
 
 def _kv_shape(k: torch.Tensor, v: torch.Tensor, D: int):
-    """(tokens, heads) of k and v, which share one shape and q's D.  Fewer heads
-    than q has are grouped heads: the library checks that they divide q's."""
-    if k.dim() != 3 or tuple(v.shape) != tuple(k.shape) or k.shape[2] != D or k.shape[1] < 1:
+    """(tokens, heads) of k, which v shares with it and q's D (rows of v behind the last
+    key are not read).  Fewer heads than q has are grouped heads: the library checks that
+    they divide q's."""
+    if k.dim() != 3 or v.dim() != 3 or v.shape[0] < k.shape[0] or v.shape[1:] != k.shape[1:] or k.shape[2] != D \
+            or k.shape[1] < 1:
         raise ValueError(f"k and v must both be (tokens, heads, {D}), got {tuple(k.shape)} and {tuple(v.shape)}")
     return k.shape[0], k.shape[1]
 

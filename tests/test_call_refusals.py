@@ -100,3 +100,11 @@ def test_gradients_that_a_backward_would_write_past():
             gradients(grad_dtype=torch.float32, **{name: torch.empty(8, 4, 64).half()})
     with pytest.raises(ValueError, match="CUDA"):
         gradients(grad_dtype=torch.float32, dk=torch.empty(9, 2, 64), dq=torch.empty(8, 4, 64))
+
+
+def test_values_longer_than_the_keys_are_not_refused():
+    q, k, v = tensors()
+    with pytest.raises(ValueError, match="CUDA"):
+        attn.fwd(q, k[:5], v)
+    with pytest.raises(ValueError, match="k and v must both"):
+        attn.fwd(q, k, v[:5])

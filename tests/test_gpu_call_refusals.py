@@ -62,3 +62,14 @@ def test_arguments_of_a_backward():
     got = attn.BwdCall(q, k, v, o, lse, q, causal=True, dk=dk[:, 1:]).run()
     assert torch.equal(got[0], want[0]) and torch.equal(dk[:64, 1:3], want[1]) and torch.equal(got[2], want[2])
     assert not dk[64:].any() and not dk[:, 0].any() and not dk[:, 3:].any()
+
+
+@pytest.mark.parametrize("hkv", [4, 2])
+def test_values_longer_than_the_keys(hkv):
+    """A value buffer with room behind the last key."""
+    q, k, v = (torch.randn(64, h, 64, device="cuda").half() for h in (4, hkv, hkv))
+    want = attn.fwd(q, k[:40], v[:40].clone())
+    o, lse = attn.fwd(q, k[:40], v)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    for a, b in zip(attn.bwd(q, k[:40], v, o, lse, q), attn.bwd(q, k[:40], v[:40], o, lse, q)):
+        assert torch.equal(a, b)
