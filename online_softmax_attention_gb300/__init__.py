@@ -16,7 +16,8 @@ argument structs:
 * ``tree_fwd(q, cache, seqs, cu_seqlens_q, mask=...)`` -> ``(o, lse)``:
   attention of new tokens (one, a chunk, a tree of drafts) over the cache
 * ``FwdCall`` / ``BwdCall`` / ``TreeCall`` hold prepared argument structs for repeated
-  launches (the benchmark and CUDA-graph capture use them).
+  launches (the benchmark and CUDA-graph capture use them); they hold the workspace too,
+  so they have to live until their runs are done, and as long as a graph that captured one.
 
 Tensors are (tokens, heads, D) with the D axis contiguous; any token / head
 strides whose rows stay 16-byte aligned are accepted (for example an (H, N, D)

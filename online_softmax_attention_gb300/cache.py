@@ -5,8 +5,9 @@ A ``Cache`` is a view of the caller's tensors: the pools ``k`` and ``v``
 (layers, pages, page_size, heads, D), the page ``table`` (sequences, pages a
 sequence can hold), the sequences' ``lens`` and the pages' reference counts
 ``refs`` (0 = free), the last three int32.  The operations change those tensors
-on the current stream without synchronising, so a captured loop can hold them;
-what a list gets wrong is reported by ``device_status()`` and changes nothing.
+on the current stream without synchronising, so a captured loop can hold them
+(it needs those tensors, not the ``Cache``); what a list gets wrong is reported by
+``device_status()`` and changes nothing.
 
     cache = Cache.empty(layers, pages, page_size, heads, D, max_seqs=64, max_pages=256)
     o, lse = fwd(q, k, v, causal=True, cu_seqlens_q=cu)       # the prompts
@@ -88,11 +89,6 @@ class Cache:
         if need(self.args, 0) == 0:
             raise ValueError("unsupported cache: page_size a power of two up to 1024, D 64 or 128, "
                              "16-byte aligned rows")
-        # the operations' scratch, for lists of as many entries as there are sequences: they
-        # change the cache, so they run in one order, and one workspace serves them all
-        self._need = need
-        self._plan = torch.empty(need(self.args, self.max_seqs), dtype=torch.uint8, device=dev)
-        self._plan_at, self._plan_bytes = self._plan.data_ptr(), self._plan.numel()
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, page_size: int, n_heads: int, head_dim: int, *, max_seqs: int,
@@ -106,13 +102,11 @@ class Cache:
         return cls(k, v, table, torch.zeros(max_seqs, dtype=torch.int32, device=dev),
                    torch.zeros(n_pages, dtype=torch.int32, device=dev))
 
-    def _workspace(self, n: int):
-        """Address and bytes of scratch for a list of n entries, and what keeps it alive."""
-        if n <= self.max_seqs:
-            return self._plan_at, self._plan_bytes, None
-        # a list with repeats, which the library refuses: scratch of its own
-        ws = torch.empty(self._need(self.args, n), dtype=torch.uint8, device=self.device)
-        return ws.data_ptr(), ws.numel(), ws
+    def _workspace(self, n: int) -> torch.Tensor:
+        """Scratch of one call with a list of n entries, from the stream that the call runs on (or
+        the graph that captures it), so that it lives as long as the call needs it."""
+        need = _host.entry("attn_cache_workspace_bytes")
+        return torch.empty(need(self.args, n), dtype=torch.uint8, device=self.device)
 
     def _done(self, name: str, rc: int | None) -> bool:
         """Whether the compiled binding made the call; an error becomes an exception."""
@@ -134,12 +128,11 @@ class Cache:
 
     def extend(self, seqs, counts) -> None:
         """Room for ``counts[i]`` more tokens of sequence ``seqs[i]``: pages and lengths."""
-        if self._done("attn_cache_extend", self._native.extend(
-                self.args, self._index, self._plan_at, self._plan_bytes, self.max_seqs, seqs, counts)):
+        if self._done("attn_cache_extend", self._native.extend(self.args, self._index, seqs, counts)):
             return
         seqs, counts = self._lists(None, seqs=seqs, counts=counts)
-        at, size, _ws = self._workspace(seqs.numel())
-        self._call("attn_cache_extend", seqs.data_ptr(), counts.data_ptr(), seqs.numel(), at, size)
+        ws = self._workspace(seqs.numel())
+        self._call("attn_cache_extend", seqs.data_ptr(), counts.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel())
 
     def write(self, seqs, cu_seqlens, k: torch.Tensor, v: torch.Tensor, *, layer: int = 0) -> None:
         """New rows (tokens, heads, D) of one layer: rows ``cu[i]:cu[i + 1]`` become the
@@ -158,18 +151,16 @@ class Cache:
 
     def fork(self, parents, children) -> None:
         """The empty sequence ``children[i]`` becomes a copy of ``parents[i]`` that shares its full pages."""
-        if self._done("attn_cache_fork", self._native.fork(
-                self.args, self._index, self._plan_at, self._plan_bytes, self.max_seqs, parents, children)):
+        if self._done("attn_cache_fork", self._native.fork(self.args, self._index, parents, children)):
             return
         parents, children = self._lists(None, parents=parents, children=children)
-        at, size, _ws = self._workspace(parents.numel())
-        self._call("attn_cache_fork", parents.data_ptr(), children.data_ptr(), parents.numel(), at, size)
+        ws = self._workspace(parents.numel())
+        self._call("attn_cache_fork", parents.data_ptr(), children.data_ptr(), parents.numel(), ws.data_ptr(), ws.numel())
 
     def keep(self, seqs, n_draft, keep: torch.Tensor, n_keep) -> None:
         """Of the last ``n_draft[i]`` tokens of ``seqs[i]`` keeps the ``n_keep[i]`` at the
         ascending offsets ``keep[i, :n_keep[i]]``; the others go."""
-        if self._done("attn_cache_keep", self._native.keep(
-                self.args, self._index, self._plan_at, self._plan_bytes, self.max_seqs, seqs, n_draft, keep, n_keep)):
+        if self._done("attn_cache_keep", self._native.keep(self.args, self._index, seqs, n_draft, keep, n_keep)):
             return
         seqs, n_draft, n_keep = self._lists(None, seqs=seqs, n_draft=n_draft, n_keep=n_keep)
         if not isinstance(keep, torch.Tensor):
@@ -177,9 +168,9 @@ class Cache:
         if keep.dim() != 2 or keep.shape[0] != seqs.numel() or keep.is_floating_point() or keep.dtype == torch.bool:
             raise ValueError(f"keep must be ({seqs.numel()}, offsets) whole numbers, got {tuple(keep.shape)}")
         keep = _host.int32(keep, self.device, "keep")
-        at, size, _ws = self._workspace(seqs.numel())
+        ws = self._workspace(seqs.numel())
         self._call("attn_cache_keep", seqs.data_ptr(), n_draft.data_ptr(), keep.data_ptr(), keep.shape[1],
-                   n_keep.data_ptr(), seqs.numel(), at, size)
+                   n_keep.data_ptr(), seqs.numel(), ws.data_ptr(), ws.numel())
 
     def free(self, seqs) -> None:
         """Empties the sequences; pages that no other sequence holds are free again."""
@@ -193,13 +184,15 @@ class Cache:
         if remap is not None and (remap.dtype != torch.int32 or remap.device != self.device or
                                   remap.shape != self.refs.shape or not remap.is_contiguous()):
             raise ValueError("remap must be a contiguous int32 vector of one entry per page on the cache's device")
-        at, size, _ws = self._workspace(0)
-        self._call("attn_cache_compact", remap.data_ptr() if remap is not None else None, at, size)
+        ws = self._workspace(0)
+        self._call("attn_cache_compact", remap.data_ptr() if remap is not None else None, ws.data_ptr(),
+                   ws.numel())
 
 
 class TreeCall:
     """Prepared attention of new tokens over a cache: holds the argument struct,
-    outputs and workspace.  Lengths and tables are read when it runs.
+    outputs and workspace.  Lengths and tables are read when it runs.  It has to live
+    until its runs are done, and as long as a graph that captured one.
 
     ``mask`` (n_q, words) int64: bit u of row t (bit u % 64 of word u // 64) lets
     new token t see new token u; without it a new token sees those up to itself.

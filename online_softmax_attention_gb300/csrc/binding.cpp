@@ -34,6 +34,7 @@ struct Api {
     decltype(&attn_bwd_workspace_bytes) bwd_bytes;
     decltype(&attn_tree_fwd) tree;
     decltype(&attn_tree_workspace_bytes) tree_bytes;
+    decltype(&attn_cache_workspace_bytes) cache_bytes;
     decltype(&attn_cache_extend) extend;
     decltype(&attn_cache_fork) fork;
     decltype(&attn_cache_keep) keep;
@@ -296,47 +297,31 @@ PyObject *py_write(PyObject *, PyObject *const *args, Py_ssize_t n) {
                             (int32_t)k->size(0), stream_of(dev)));
 }
 
-// The scratch of a cache: its address and bytes.
-bool plan_of(PyObject *at, PyObject *size, PyObject *most, const Tensor *list, void *&ws, size_t &bytes) {
-    long n;
-    if (!PyLong_Check(at) || !PyLong_Check(size) || !as_long(most, n) || list->size(0) > n) return false;
-    ws = PyLong_AsVoidPtr(at);
-    bytes = PyLong_AsSize_t(size);
-    if (PyErr_Occurred()) {
-        PyErr_Clear();
-        return false;
-    }
-    return true;
-}
-
-// extend / fork(cache, device, scratch, bytes, most, a, b) -> status | None
+// extend / fork(cache, device, a, b) -> status | None
 template <bool kFork>
 PyObject *py_alloc(PyObject *, PyObject *const *args, Py_ssize_t n) {
     attn_cache c;
     int dev;
-    NEED(n == 7 && cache_of(args[0], args[1], c, dev));
-    const Tensor *x = tensor(args[5]), *y = tensor(args[6]);
-    void *ws;
-    size_t bytes;
-    NEED(ints(x, dev) && ints(y, dev) && x->size(0) == y->size(0) &&
-         plan_of(args[2], args[3], args[4], x, ws, bytes));
-    return status((kFork ? api.fork : api.extend)(&c, int_ptr(x), int_ptr(y), (int32_t)x->size(0), ws, bytes,
-                                                  stream_of(dev)));
+    NEED(n == 4 && cache_of(args[0], args[1], c, dev));
+    const Tensor *x = tensor(args[2]), *y = tensor(args[3]);
+    NEED(ints(x, dev) && ints(y, dev) && x->size(0) == y->size(0) && fits(x->size(0)));
+    const Tensor ws = scratch(api.cache_bytes(&c, (int32_t)x->size(0)), dev);
+    return status((kFork ? api.fork : api.extend)(&c, int_ptr(x), int_ptr(y), (int32_t)x->size(0), ws.data_ptr(),
+                                                  (size_t)ws.size(0), stream_of(dev)));
 }
 
-// keep(cache, device, scratch, bytes, most, seqs, n_draft, keep, n_keep) -> status | None
+// keep(cache, device, seqs, n_draft, keep, n_keep) -> status | None
 PyObject *py_keep(PyObject *, PyObject *const *args, Py_ssize_t n) {
     attn_cache c;
     int dev;
-    NEED(n == 9 && cache_of(args[0], args[1], c, dev));
-    const Tensor *s = tensor(args[5]), *d = tensor(args[6]), *k = tensor(args[7]), *m = tensor(args[8]);
-    void *ws;
-    size_t bytes;
+    NEED(n == 6 && cache_of(args[0], args[1], c, dev));
+    const Tensor *s = tensor(args[2]), *d = tensor(args[3]), *k = tensor(args[4]), *m = tensor(args[5]);
     NEED(ints(s, dev) && ints(d, dev) && ints(m, dev) && on(k, dev) && k->dim() == 2 &&
-         k->scalar_type() == at::kInt && k->is_contiguous() && plan_of(args[2], args[3], args[4], s, ws, bytes));
+         k->scalar_type() == at::kInt && k->is_contiguous() && fits(s->size(0)));
     NEED(d->size(0) == s->size(0) && m->size(0) == s->size(0) && k->size(0) == s->size(0));
-    return status(api.keep(&c, int_ptr(s), int_ptr(d), int_ptr(k), k->size(1), int_ptr(m), (int32_t)s->size(0), ws,
-                           bytes, stream_of(dev)));
+    const Tensor ws = scratch(api.cache_bytes(&c, (int32_t)s->size(0)), dev);
+    return status(api.keep(&c, int_ptr(s), int_ptr(d), int_ptr(k), k->size(1), int_ptr(m), (int32_t)s->size(0),
+                           ws.data_ptr(), (size_t)ws.size(0), stream_of(dev)));
 }
 
 // free(cache, device, seqs) -> status | None
