@@ -584,10 +584,12 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         float m = -INFINITY, l = 0.f;
         // the running max refreshed with a tile's largest score: only when it grew by more than
         // 2^8 somewhere in the warp (else the stale max is kept, which leaves O = U / l exact);
-        // the factor for l and U
+        // the factor for l and U.  Rows that are not the entry's (another sequence's queries, or
+        // what shared memory held) have no say, so that they do not move its results' last bits
+        const float grown = lrow < sg.live[t] ? kRescaleThreshold : INFINITY;
         auto refresh = [&](float mx, bool first, bool &rescale) -> float {
             const float m_new = fmaxf(m, mx);
-            rescale = !first && __any_sync(0xffffffffu, m_new > m + kRescaleThreshold);
+            rescale = !first && __any_sync(0xffffffffu, m_new > m + grown);
             float alpha = 1.f;
             if (first) {
                 m = m_new;
