@@ -155,7 +155,9 @@ typedef struct attn_fwd_args {
  * num_ctas = 0, at most 2048 sequences, G <= 128, no fp8 or pruning): two
  * launches, no schedule preparation; key ranges cut between CTAs are merged
  * from the workspace (about 40 MB at D = 128).  With that kernel the rows of other
- * sequences, and rows behind the last one, may hold anything, NaN included. */
+ * sequences, and rows behind the last one, may hold anything, NaN included.  A
+ * row with a score of NaN gets O and lse of NaN from that kernel and from
+ * attn_tree_fwd (the other forward kernels leave lse = -inf beside that O). */
 
 /* fp8 queries and keys (qk_fp8 = 1; no counterpart on the pages, a use of the
  * sm_103a tensor cores' 8-bit score contraction): q and k hold e4m3 values,

@@ -726,7 +726,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         if (!__all_sync(0xffffffffu, ok)) return;
         tc_fence_after();
         if (part < 0) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             Tout *at[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -743,7 +743,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
             }
             if (lrow < live && p.lse)
                 p.lse[(int64_t)(hk * p.group + lrow - my_tok * p.group) * p.n_q + q0 + token] =
-                    l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                    l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
         } else {
             // (at most two parts a block: a row a lane, in little code)
             float *row = p.parts.o + (part_row + lrow) * D;

@@ -55,14 +55,14 @@ __global__ void __launch_bounds__(32 * kWarps) parts_merge_kernel(const PartsMer
         }
         const int t = row / p.group;
         const int64_t token = u.q0 + t, head = u.hk * p.group + row - t * p.group;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         Tout *orow = static_cast<Tout *>(p.o) + token * p.o_st + head * p.o_sh + d;
         if constexpr (kCols == 4) store4(orow, make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
         else {
             orow[0] = from_f32<Tout>(acc[0] * inv);
             orow[1] = from_f32<Tout>(acc[1] * inv);
         }
-        if (lane == 0 && p.lse) p.lse[head * p.n_q + token] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+        if (lane == 0 && p.lse) p.lse[head * p.n_q + token] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
     }
 }
 

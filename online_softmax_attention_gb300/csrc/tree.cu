@@ -454,10 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
             }
             if (whole) {
                 const int t = (row0 + r) / p.group, head = hk * p.group + (row0 + r) - t * p.group;
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 store_out<Tout>(p, e.q0 + t, head, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
                 if (d == 0 && p.lse)
-                    p.lse[(int64_t)head * p.n_q + e.q0 + t] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+                    p.lse[(int64_t)head * p.n_q + e.q0 + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
             } else {
                 store4(p.parts.o + ((int64_t)slot * kRows + r) * D + d, acc);
                 if (d == 0) p.parts.ml[(int64_t)slot * kRows + r] = make_float2(mx, sum);
