@@ -14,6 +14,7 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+import warnings
 
 import torch
 
@@ -77,6 +78,13 @@ _NATIVE_CALLS = ("attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_w
 _native = None
 
 
+class _NoBinding:
+    """In place of a compiled binding that was not built: every call is left to the Python path."""
+
+    def __getattr__(self, name: str):
+        return lambda *args: None
+
+
 def native():
     """The compiled binding (csrc/binding.cpp).  Its functions return None for
     arguments that they leave to the Python path, or a status of the library."""
@@ -84,8 +92,10 @@ def native():
     if _native is None:
         lib = _abi.load()
         if not os.path.exists(_NATIVE):
-            raise ImportError(f"torch binding not built ({_NATIVE} missing); run "
-                              "`python -c 'import __graft_entry__ as g; g.build()'`")
+            warnings.warn(f"the compiled torch binding is not built ({_NATIVE} is missing): calls cost more host time",
+                          RuntimeWarning, stacklevel=3)
+            _native = _NoBinding()
+            return _native
         loader = importlib.machinery.ExtensionFileLoader("_native", _NATIVE)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_native", loader))
         loader.exec_module(module)

@@ -3,7 +3,7 @@ and the torch binding of its short calls: csrc/binding.cpp -> _lib/_native.so.
 
 Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library with the CUDA runtime linked statically.  The binding is compiled
-beside them by the host compiler against the installed torch's headers.
+beside them by the host compiler against the installed torch's headers, where they are.
 Rebuilds only what changed (object newer than its source and the shared headers).
 """
 from __future__ import annotations
@@ -65,32 +65,40 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     """The installed torch package's folder, without importing it."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.origin:
-        raise RuntimeError("torch not found: the binding needs its headers")
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
-def _binding(force: bool) -> None:
+def _binding(force: bool) -> bool:
+    """Builds the torch binding.  False: torch's or Python's headers, or a host compiler, are not
+    here; the library does without (the Python binding makes the same calls, slower)."""
     src = os.path.join(CSRC, "binding.cpp")
-    torch = _torch_dir()
+    torch, cxx = _torch_dir(), shutil.which(os.environ.get("CXX") or "g++")
+    python = sysconfig.get_paths()["include"]
+    needs = [os.path.join(torch or "", "include", "torch", "csrc", "autograd", "python_variable.h"),
+             os.path.join(torch or "", "include", "c10", "cuda", "CUDAStream.h"), os.path.join(python, "Python.h")]
+    if torch is None or cxx is None or not all(os.path.exists(n) for n in needs):
+        if os.path.exists(NATIVE):
+            os.remove(NATIVE)  # it may be another torch's
+        return False
     # built anew when another torch is installed
     deps = [src, os.path.join(ROOT, "include", "attn.h"), os.path.join(torch, "version.py")]
     if not force and not _stale(NATIVE, deps):
-        return
+        return True
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+           python, os.path.join(cuda, "include")]
     lib = os.path.join(torch, "lib")
-    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            *(x for i in inc for x in ("-I", i)), src, "-o", NATIVE + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the torch binding failed to build:\n{r.stdout}\n{r.stderr}")
     os.replace(NATIVE + ".tmp", NATIVE)
+    return True
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -104,7 +112,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
         binding = ex.submit(_binding, force)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        binding.result()
+        if not binding.result():
+            print("the torch binding of short calls is not built (it needs torch's and Python's headers and a "
+                  "host compiler); calls take the Python binding", file=sys.stderr)
     if force or _stale(LIB, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs, "-lpthread"]
         r = subprocess.run(cmd, capture_output=True, text=True)
