@@ -53,6 +53,8 @@
  *  - A query row that admits no key (only an empty key sequence under
  *    ATTN_FULL) gets O = 0 and lse = -inf.
  *  - Inputs must be finite.
+ *  - Token counts are at most 2^31 - 2^16 (ATTN_EUNSUPPORTED), and so are those
+ *    of (token, head) query rows of grouped heads and over a cache.
  */
 #ifndef ATTN_GB300_ATTN_H
 #define ATTN_GB300_ATTN_H

@@ -111,6 +111,10 @@ int choose_tc(int kernel, bool tc_ok, bool &use_tc) {
     return ATTN_OK;
 }
 
+// Token counts, and (token, head) rows of grouped heads, are int32 with room for rounding
+// up to a tile or a page.
+constexpr int64_t kMostTokens = ((int64_t)1 << 31) - (1 << 16);
+
 int check_common(int n_q, int n_k, int H, int H_kv, int D, int relation, int dtype, int n_seq,
                  const int32_t *cu_q, const int32_t *cu_k, float scale) {
     if (n_q < 0 || n_k < 0 || H < 1 || n_seq < 1) return ATTN_EINVAL;
@@ -125,6 +129,8 @@ int check_common(int n_q, int n_k, int H, int H_kv, int D, int relation, int dty
     // work-item numbering is int32: H * (tiles + sequences) must fit
     const int64_t items = (int64_t)H * ((int64_t)(n_q > n_k ? n_q : n_k) / kSimtBlock + n_seq + 1);
     if (items >= (int64_t)1 << 31 || (int64_t)n_q * H >= (int64_t)1 << 31) return ATTN_EUNSUPPORTED;
+    if (n_q > kMostTokens || n_k > kMostTokens || (H_kv > 0 && H_kv < H && (int64_t)n_q * H > kMostTokens))
+        return ATTN_EUNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -428,8 +434,7 @@ int plan_cache(const attn_cache *c, CacheParams &p) {
     if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) ||
         c->max_seqs > ATTN_CACHE_MAX_SEQS || c->H_kv > 4096 || c->n_layers > 32767)
         return ATTN_EUNSUPPORTED;
-    // token positions are int32, with room for rounding up to a tile or a page
-    if ((int64_t)c->max_pages * c->page_size > ((int64_t)1 << 31) - (1 << 16) || c->n_pages > (1 << 30))
+    if ((int64_t)c->max_pages * c->page_size > kMostTokens || c->n_pages > (1 << 30))
         return ATTN_EUNSUPPORTED;
     const int64_t es = (int64_t)elem_size(c->dtype);
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return ATTN_EINVAL;
@@ -487,7 +492,7 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
         return ATTN_EINVAL;
     if (a->o_dtype != a->cache.dtype && a->o_dtype != ATTN_F32) return ATTN_EINVAL;
     if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return ATTN_EINVAL;
-    if ((int64_t)a->n_q * a->H >= (int64_t)1 << 31) return ATTN_EUNSUPPORTED;
+    if ((int64_t)a->n_q * a->H > kMostTokens) return ATTN_EUNSUPPORTED;
     const bool any = a->n_q > 0 && a->n > 0;
     if (check_views && any &&
         (!valid_view(a->q, a->cache.dtype, true) || !valid_view(a->o, a->o_dtype, true) || !aligned4(a->seqs) ||
