@@ -15,14 +15,17 @@ namespace {
 
 constexpr int kPrepThreads = 1024;
 
-// Block b prepares schedule b (the backward's two in one launch).
+// Block b prepares schedule b (the backward's two in one launch).  kOrdered: some of them
+// take the sequences longest-first.  (Without it, a kernel of its own, and the jobs are read
+// where they are passed: one kernel with a copy of them cost a forward 1 us.)
+template <bool kOrdered>
 __global__ void __launch_bounds__(kPrepThreads)
 prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int n_seq,
-            int n_q, int n_k, int causal, const PrepJobs jobs, int *status) {
+            int n_q, int n_k, int causal, const __grid_constant__ PrepJobs jobs, int *status) {
     const PrepJob &job = jobs.job[blockIdx.x];
     const int H = job.H, block = job.block, rows_are_keys = job.rows_are_keys, splits = job.splits;
-    int *hdr = job.sched.hdr, *prefix = const_cast<int *>(job.sched.prefix), *order = job.sched.order;
-    __shared__ int s_len[kSortedSeqs], s_order[kSortedSeqs];
+    int *hdr = job.sched.hdr, *prefix = const_cast<int *>(job.sched.prefix), *order = kOrdered ? job.sched.order : nullptr;
+    __shared__ int s_len[kOrdered ? kSortedSeqs : 1], s_order[kOrdered ? kSortedSeqs : 1];
     __shared__ int s_bad;
     __shared__ int s_warp[kPrepThreads / 32];
     __shared__ long long s_carry;
@@ -110,8 +113,10 @@ prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, 
 
 cudaError_t launch_prep(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int n_q, int n_k, int causal,
                         const PrepJobs &jobs, int n_jobs, int *status, cudaStream_t s) {
-    cudaError_t e = launch_pdl(prep_kernel, dim3(n_jobs), dim3(kPrepThreads), 0, s, cu_q, cu_k, n_seq, n_q, n_k,
-                               causal, jobs, status);
+    bool ordered = false;
+    for (int i = 0; i < n_jobs; ++i) ordered = ordered || jobs.job[i].sched.order;
+    cudaError_t e = launch_pdl(ordered ? prep_kernel<true> : prep_kernel<false>, dim3(n_jobs), dim3(kPrepThreads), 0, s,
+                               cu_q, cu_k, n_seq, n_q, n_k, causal, jobs, status);
     count_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }
