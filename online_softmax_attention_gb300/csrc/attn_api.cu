@@ -259,6 +259,7 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     p.n_q = a->n_q; p.n_k = a->n_k; p.H = a->H; p.D = a->D;
     p.Hkv = a->H_kv > 0 ? a->H_kv : a->H;
     p.group = p.H / p.Hkv;
+    p.group_inv = group_inverse(p.group);
     p.scale = a->scale;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.causal = a->relation == ATTN_CAUSAL;
@@ -397,6 +398,7 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     p.n_q = a->n_q; p.n_k = a->n_k; p.H = a->H; p.D = a->D;
     p.Hkv = a->H_kv > 0 ? a->H_kv : a->H;
     p.group = p.H / p.Hkv;
+    p.group_inv = group_inverse(p.group);
     p.scale = a->scale;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.causal = a->relation == ATTN_CAUSAL;

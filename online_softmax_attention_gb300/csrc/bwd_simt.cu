@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
 
         const int n_keys = p.causal ? min(Lk, row0 + B) : Lk;
         const int n_tiles = (n_keys + B - 1) / B;
-        const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)(h / p.group) * p.k_sh;
-        const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)(h / p.group) * p.v_sh;
+        const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)key_head(h, p.group_inv) * p.k_sh;
+        const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)key_head(h, p.group_inv) * p.v_sh;
 
         for (int kt = 0; kt < n_tiles; ++kt) {
             const int key0 = kt * B;

@@ -959,7 +959,7 @@ __device__ __forceinline__ DqInfo dq_info(const BwdParams &p, int w) {
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
     f.h = it.h;
-    f.hk = it.h / p.group;
+    f.hk = key_head(it.h, p.group_inv);
     f.row0 = it.t * BT;
     f.nk = p.causal ? cdiv(min(f.Lk, f.row0 + BT), BT) : cdiv(f.Lk, BT);
     return f;

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
         // split-K: this item scans chunk it.c of the row's key tiles
         const KeyChunk chunk = key_chunk((n_keys + BK - 1) / BK, p.n_splits, it.c);
         float m_run = -INFINITY;  // tile pruning: largest score of the admitted tiles (log2 units)
-        const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)(h / p.group) * p.k_sh;
-        const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)(h / p.group) * p.v_sh;
+        const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)key_head(h, p.group_inv) * p.k_sh;
+        const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)key_head(h, p.group_inv) * p.v_sh;
 
         if constexpr (kAsync) {
             if (chunk.begin < chunk.end) {

@@ -132,7 +132,6 @@ struct PruneShared {
 
 struct ItemInfo {
     int q_start, Lq, k_start, Lk, h, row0;
-    int hk;      // key / value head of the item's query head (grouped heads)
     int c;       // key split (split-K chunk) of this item
     int j0;      // first key tile of the chunk
     int n[NQT];  // key tiles each query tile scans, from j0 on
@@ -154,7 +153,6 @@ __device__ __forceinline__ ItemInfo item_info(const FwdParams &p, int w) {
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
     f.h = it.h;
-    f.hk = it.h / p.group;
     f.c = it.c;
     f.row0 = it.t * kItemRows;
     int full[NQT], most = 0;
@@ -237,6 +235,7 @@ __device__ void producer(const TcFwdArgs &a, FwdBars &bars, int *sched_item, uin
         w = (int)from_leader((uint32_t)w, lead);
         if (w >= total) break;
         const ItemInfo f = item_info(p, w);
+        const int hk = key_head(f.h, p.group_inv);
         bool ok = true;
 #pragma unroll
         for (int t = 0; t < NQT; ++t) {
@@ -257,7 +256,7 @@ __device__ void producer(const TcFwdArgs &a, FwdBars &bars, int *sched_item, uin
             q_pending[t] = true;
         }
         if (!ok) break;
-        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), f.hk);
+        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), hk);
         if (!ok) break;
     }
     if (aborting(wd) && (threadIdx.x & 31) == 0) {

@@ -172,11 +172,12 @@ struct SplitParams {
     SplitJob job[3];
 };
 
-__global__ void __launch_bounds__(256) split_parts_kernel(const SplitParams sp) {
+__global__ void __launch_bounds__(256) split_parts_kernel(const __grid_constant__ SplitParams sp) {
     pdl_trigger();
     pdl_wait();
     constexpr int C4 = D / 4;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+#pragma unroll 1
     for (int j = 0; j < 3; ++j) {
         const SplitJob &jb = sp.job[j];
         const int64_t n4 = (int64_t)jb.tokens * jb.H * C4;
@@ -233,6 +234,7 @@ __device__ void producer(const X3Args &a, X3Bars &bars, int *sched_item, uint32_
         mbar_arrive(smem_u32(&bars.sched_full[slot]));
         if (w >= total) break;
         const ItemInfo f = item_info(p, w);
+        const int hk = key_head(f.h, p.group_inv);
         bool ok = true;
 #pragma unroll
         for (int t = 0; t < NQT; ++t) {
@@ -249,7 +251,7 @@ __device__ void producer(const X3Args &a, X3Bars &bars, int *sched_item, uint32_
             q_pending[t] = true;
         }
         if (!ok) break;
-        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), f.h / p.group);
+        for (int j = 0; j < f.nkv && ok; ++j) ok = load_kv(f.k_start + BN * (f.j0 + j), hk);
         if (!ok) break;
     }
     if (aborting(wd)) {

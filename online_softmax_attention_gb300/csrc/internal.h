@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "heads.h"
+
 namespace attn {
 
 // Schedule block in the workspace: [0] dynamic work counter, [1] item count,
@@ -29,6 +31,7 @@ struct FwdParams {
     int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;
     int n_q, n_k, H, D;
     int Hkv, group;    // key / value heads; query heads that share one (H = Hkv * group)
+    unsigned long long group_inv;  // group_inverse(group)
     float scale;       // score scale
     float scale_log2;  // scale * log2(e)
     int causal;
@@ -230,6 +233,7 @@ struct BwdParams {
     int64_t dq_st, dq_sh, dk_st, dk_sh, dv_st, dv_sh;
     int n_q, n_k, H, D;
     int Hkv, group;     // key / value heads; query heads that share one (H = Hkv * group)
+    unsigned long long group_inv;  // group_inverse(group)
     float scale, scale_log2;
     int causal;
     int dtype, o_dtype, grad_dtype;
