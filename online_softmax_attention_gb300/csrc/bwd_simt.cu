@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
         __syncthreads();
         if (w >= total) break;
         // causal: earlier key blocks are seen by more query blocks, so run them first
-        const WorkItem it = map_item(w, p.sched_kv, p.n_seq, p.Hkv, false);
+        const WorkItem it = map_item<true>(w, p.sched_kv, p.n_seq, p.Hkv, false);
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);
@@ -225,62 +225,62 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
 
         const int qb_first = p.causal ? key0 / B : 0;
         const int qb_end = (Lq + B - 1) / B;
-        const int per_head = max(0, qb_end - qb_first);
-
         // the query blocks of every query head that shares this key / value head
-        for (int x = 0; x < per_head * p.group; ++x) {
-            const int g = x / per_head, hq = h * p.group + g;
-            const int row0 = (qb_first + x - g * per_head) * B;
+        for (int hq = h * p.group; hq < (h + 1) * p.group; ++hq) {
             const Tin *qbase = gq + (int64_t)q_start * p.q_st + (int64_t)hq * p.q_sh;
             const Tin *dobase = gdo + (int64_t)q_start * p.do_st + (int64_t)hq * p.do_sh;
             const int64_t stat_base = (int64_t)hq * p.n_q + q_start;
-            __syncthreads();
-            stage_tile<Tin, D>(sQ, qbase, p.q_st, row0, Lq);
-            stage_tile<Tin, D>(sdO, dobase, p.do_st, row0, Lq);
-            stage_row_stats(s_lse2, s_dr, p.lse, p.dr, stat_base, row0, Lq);
-            __syncthreads();
 
-            float s[4][4], dp[4][4];
-            tile_nt<D>(s, sQ, sK, tx, ty);
-            tile_nt<D>(dp, sdO, sV, tx, ty);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int rl = ty + 16 * r, row = row0 + rl;
-                const float l2 = s_lse2[rl], drr = s_dr[rl];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int key = key0 + tx + 16 * c;
-                    const bool ok = key < Lk && (!p.causal || key <= row);
-                    const float pr = ok ? exp2_approx(s[r][c] * p.scale_log2 - l2) : 0.f;
-                    sP[rl * LDP + tx + 16 * c] = pr;
-                    sdS[rl * LDP + tx + 16 * c] = pr * (dp[r][c] - drr);
-                }
-            }
-            __syncthreads();
+            for (int qb = qb_first; qb < qb_end; ++qb) {
+                const int row0 = qb * B;
+                __syncthreads();
+                stage_tile<Tin, D>(sQ, qbase, p.q_st, row0, Lq);
+                stage_tile<Tin, D>(sdO, dobase, p.do_st, row0, Lq);
+                stage_row_stats(s_lse2, s_dr, p.lse, p.dr, stat_base, row0, Lq);
+                __syncthreads();
 
-            // dV[key] += sum_row P[row][key] dO[row];  dK[key] += sum_row dS[row][key] Q[row]
-#pragma unroll 2
-            for (int row = 0; row < B; ++row) {
-                float pk[4], sk[4];
+                float s[4][4], dp[4][4];
+                tile_nt<D>(s, sQ, sK, tx, ty);
+                tile_nt<D>(dp, sdO, sV, tx, ty);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    pk[r] = sP[row * LDP + ty + 16 * r];
-                    sk[r] = sdS[row * LDP + ty + 16 * r];
-                }
+                    const int rl = ty + 16 * r, row = row0 + rl;
+                    const float l2 = s_lse2[rl], drr = s_dr[rl];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float4 o4 = *reinterpret_cast<const float4 *>(sdO + row * LD + 64 * g + 4 * tx);
-                    const float4 q4 = *reinterpret_cast<const float4 *>(sQ + row * LD + 64 * g + 4 * tx);
+                    for (int c = 0; c < 4; ++c) {
+                        const int key = key0 + tx + 16 * c;
+                        const bool ok = key < Lk && (!p.causal || key <= row);
+                        const float pr = ok ? exp2_approx(s[r][c] * p.scale_log2 - l2) : 0.f;
+                        sP[rl * LDP + tx + 16 * c] = pr;
+                        sdS[rl * LDP + tx + 16 * c] = pr * (dp[r][c] - drr);
+                    }
+                }
+                __syncthreads();
+
+                // dV[key] += sum_row P[row][key] dO[row];  dK[key] += sum_row dS[row][key] Q[row]
+#pragma unroll 2
+                for (int row = 0; row < B; ++row) {
+                    float pk[4], sk[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        dv[r][4 * g + 0] = fmaf(pk[r], o4.x, dv[r][4 * g + 0]);
-                        dv[r][4 * g + 1] = fmaf(pk[r], o4.y, dv[r][4 * g + 1]);
-                        dv[r][4 * g + 2] = fmaf(pk[r], o4.z, dv[r][4 * g + 2]);
-                        dv[r][4 * g + 3] = fmaf(pk[r], o4.w, dv[r][4 * g + 3]);
-                        dk[r][4 * g + 0] = fmaf(sk[r], q4.x, dk[r][4 * g + 0]);
-                        dk[r][4 * g + 1] = fmaf(sk[r], q4.y, dk[r][4 * g + 1]);
-                        dk[r][4 * g + 2] = fmaf(sk[r], q4.z, dk[r][4 * g + 2]);
-                        dk[r][4 * g + 3] = fmaf(sk[r], q4.w, dk[r][4 * g + 3]);
+                        pk[r] = sP[row * LDP + ty + 16 * r];
+                        sk[r] = sdS[row * LDP + ty + 16 * r];
+                    }
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const float4 o4 = *reinterpret_cast<const float4 *>(sdO + row * LD + 64 * g + 4 * tx);
+                        const float4 q4 = *reinterpret_cast<const float4 *>(sQ + row * LD + 64 * g + 4 * tx);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            dv[r][4 * g + 0] = fmaf(pk[r], o4.x, dv[r][4 * g + 0]);
+                            dv[r][4 * g + 1] = fmaf(pk[r], o4.y, dv[r][4 * g + 1]);
+                            dv[r][4 * g + 2] = fmaf(pk[r], o4.z, dv[r][4 * g + 2]);
+                            dv[r][4 * g + 3] = fmaf(pk[r], o4.w, dv[r][4 * g + 3]);
+                            dk[r][4 * g + 0] = fmaf(sk[r], q4.x, dk[r][4 * g + 0]);
+                            dk[r][4 * g + 1] = fmaf(sk[r], q4.y, dk[r][4 * g + 1]);
+                            dk[r][4 * g + 2] = fmaf(sk[r], q4.z, dk[r][4 * g + 2]);
+                            dk[r][4 * g + 3] = fmaf(sk[r], q4.w, dk[r][4 * g + 3]);
+                        }
                     }
                 }
             }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
         const int w = s_w;
         __syncthreads();
         if (w >= total) break;
-        const WorkItem it = map_item(w, p.sched_q, p.n_seq, p.H, true);
+        const WorkItem it = map_item<true>(w, p.sched_q, p.n_seq, p.H, true);
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);

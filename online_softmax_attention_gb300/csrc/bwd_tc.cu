@@ -180,7 +180,7 @@ struct DkdvInfo {
 };
 
 __device__ __forceinline__ DkdvInfo dkdv_info(const BwdParams &p, int w) {
-    const WorkItem it = map_item(w, p.sched_kv, p.n_seq, p.Hkv, false, 1, p.group > 1);
+    const WorkItem it = map_item<true>(w, p.sched_kv, p.n_seq, p.Hkv, false, 1, p.group > 1);
     DkdvInfo f;
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
@@ -954,7 +954,7 @@ struct DqInfo {
 };
 
 __device__ __forceinline__ DqInfo dq_info(const BwdParams &p, int w) {
-    const WorkItem it = map_item(w, p.sched_q, p.n_seq, p.H, true, 1, p.group > 1);
+    const WorkItem it = map_item<true>(w, p.sched_q, p.n_seq, p.H, true, 1, p.group > 1);
     DqInfo f;
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);

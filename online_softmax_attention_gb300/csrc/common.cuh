@@ -108,6 +108,8 @@ __device__ __forceinline__ void batch_item(int r, int per_head, int H, int &h, i
     h = h0 + rem - t * here;
 }
 
+// kOrdered: schedules whose sequences may stand in another order (the backward's).
+template <bool kOrdered>
 __device__ __forceinline__ WorkItem map_item(int w, const Sched &sched, int n_seq, int H,
                                              bool descending, int splits = 1, bool batched = false) {
     const int *prefix = sched.prefix;
@@ -120,7 +122,7 @@ __device__ __forceinline__ WorkItem map_item(int w, const Sched &sched, int n_se
     const int base = __ldg(prefix + lo);
     const int per_head = (__ldg(prefix + lo + 1) - base) / H;  // tiles * splits
     const int r = w - base;
-    if (sched.order) lo = __ldg(sched.order + lo);
+    if (kOrdered && sched.order) lo = __ldg(sched.order + lo);
     if (batched) {  // (no splits)
         int h, t;
         batch_item(r, per_head, H, h, t);

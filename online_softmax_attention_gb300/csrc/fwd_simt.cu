@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
         __syncthreads();
         if (w >= total) break;
         const WorkItem it = p.static_items > 0 ? map_item_single(w, p.static_items, p.H, true, p.n_splits)
-                                               : map_item(w, p.sched, p.n_seq, p.H, true, p.n_splits);
+                                               : map_item<false>(w, p.sched, p.n_seq, p.H, true, p.n_splits);
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);

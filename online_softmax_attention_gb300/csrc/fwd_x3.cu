@@ -98,7 +98,7 @@ __device__ __forceinline__ int total_items(const FwdParams &p) {
 
 __device__ __forceinline__ ItemInfo item_info(const FwdParams &p, int w) {
     const WorkItem it = p.static_items > 0 ? map_item_single(w, p.static_items, p.H, true, p.n_splits)
-                                           : map_item(w, p.sched, p.n_seq, p.H, true, p.n_splits);
+                                           : map_item<false>(w, p.sched, p.n_seq, p.H, true, p.n_splits);
     ItemInfo f;
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
