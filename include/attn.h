@@ -276,11 +276,16 @@ typedef struct attn_csr_args {
  *
  * The operations below run on `stream`, read and write only device memory and
  * do not synchronise, so a captured loop can hold them.  They validate on the
- * device: a list with an entry out of range, a sequence listed twice (except in
- * attn_cache_free), or lengths that do not fit leaves the whole cache as it
- * was, and attn_device_status() reports ATTN_EINVAL (ATTN_ENOPAGES when the
- * free pages do not suffice).  Operations on one cache must be ordered by the
- * caller (one stream); reads of it may overlap. */
+ * device, and attn_device_status() reports ATTN_EINVAL.  For attn_cache_extend,
+ * _fork and _keep a list with an entry out of range, a sequence listed twice, or
+ * lengths that do not fit leaves the whole cache as it was (so do too few free
+ * pages, ATTN_ENOPAGES), and so does a length that does not fit for
+ * attn_cache_compact; attn_cache_write and _free leave out the entries that are
+ * wrong and do the others.  The tables and counts are the cache's own state: a
+ * page index outside the pool is reported and never followed where a call meets
+ * it, but fork (among the pages to be shared), keep and free (among those to be
+ * released) and compact have then done the rest.  Operations on one cache must be
+ * ordered by the caller (one stream); reads of it may overlap. */
 typedef struct attn_cache {
     void *k, *v;              /* (n_layers, n_pages, page_size, H_kv, D) dtype */
     int64_t stride_layer, stride_page, stride_tok, stride_head; /* elements, of both k and v */

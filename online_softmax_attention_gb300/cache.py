@@ -7,7 +7,7 @@ sequence can hold), the sequences' ``lens`` and the pages' reference counts
 ``refs`` (0 = free), the last three int32.  The operations change those tensors
 on the current stream without synchronising, so a captured loop can hold them
 (it needs those tensors, not the ``Cache``); what a list gets wrong is reported by
-``device_status()`` and changes nothing.
+``device_status()`` and changes nothing (``write`` and ``free`` do the other entries).
 
     cache = Cache.empty(layers, pages, page_size, heads, D, max_seqs=64, max_pages=256)
     o, lse = fwd(q, k, v, causal=True, cu_seqlens_q=cu)       # the prompts
