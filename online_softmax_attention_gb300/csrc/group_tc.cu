@@ -45,10 +45,10 @@ constexpr int kSegConsumers = 1 + 8;    // MMA warp, softmax warps
 constexpr float kRescaleThreshold = 8.f;  // log2 units, as fwd_tc.cu
 // What a unit costs besides its key tiles, in key tiles (about 1.7 us each): the
 // queries' loads, the masked tile, the epilogue.  (48 packed prompts of 9 to 420
-// tokens, 24 packed training rows' step, 3 prompts of 5000 to 8192: 60 / 192 / 950 us
-// with 1, 62 / 187 / 957 with 2, 63 / 194 / 965 with 3; 100 / 252 / 1070 with 0,
-// measured on an earlier form whose other steps were slower.)
-constexpr int kLead = 2;
+// tokens, 24 packed training rows' step, 3 prompts of 5000 to 8192, trees of 63 drafts:
+// 73.6 / 194.6 / 960 / 120.2 us with 0, 61.6 / 182.4 / 924 / 118.8 with 1,
+// 63.1 / 183.1 / 940 / 119.0 with 2, 63.4 / 184.9 / 947 / 117.4 with 3.)
+constexpr int kLead = 1;
 
 template <int D>
 struct Cfg {
@@ -642,9 +642,9 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg *segs, uint
         }
         for (; j < n; ++j) {
             // masked tiles, 32 keys at a time, scores read twice (for the max, then for p).  A loop,
-            // and the only masked code: straight-line code for 128 masked columns is fetched anew
-            // for each unit's few masked tiles, which cost more than it computed (107 -> 98 us on
-            // 48 packed prompts of 9 to 420 tokens)
+            // and the only masked code: unrolled over the 128 columns it is fetched anew for each
+            // unit's few masked tiles, which costs more than it computes (48 packed prompts of 9 to
+            // 420 tokens 63 -> 85 us, long prompts the same)
             const int key0 = BN * (sg.j0 + j), left = sg.L - key0;
             const int steps = key_steps(sg.end[t] - key0);
             const int token = sg.tok[t] + my_tok;

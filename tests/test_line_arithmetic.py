@@ -112,7 +112,7 @@ def check_cuts(lib, units, blocks, turn, lead):
         u0 += n + s[3]
 
 
-@pytest.mark.parametrize("turn,lead", [(1, 2), (4, 0)])
+@pytest.mark.parametrize("turn,lead", [(1, 1), (1, 2), (4, 0)])
 def test_every_tile_is_taken_once(lib, turn, lead):
     r = random.Random(3)
     for _ in range(60):
@@ -122,7 +122,7 @@ def test_every_tile_is_taken_once(lib, turn, lead):
         check_cuts(lib, [1] * (24 * n), 2 * n, turn, lead)
 
 
-@pytest.mark.parametrize("turn,lead", [(1, 2), (4, 0)])
+@pytest.mark.parametrize("turn,lead", [(1, 1), (1, 2), (4, 0)])
 @pytest.mark.parametrize("units,tiles", [(1 << 20, 1 << 36), (1 << 20, (1 << 36) + 5), (8 << 18, 1 << 40), (1 << 28, 1 << 52)])
 def test_totals_past_2_36_tiles(lib, units, tiles, turn, lead):
     """Chunks of 2^19 tokens whose 16-row units scan 2^15 tiles for each of 8 key heads, and beyond:
