@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
 
         const int qb_first = p.causal ? key0 / B : 0;
         const int qb_end = (Lq + B - 1) / B;
+
         // the query blocks of every query head that shares this key / value head
         for (int hq = h * p.group; hq < (h + 1) * p.group; ++hq) {
             const Tin *qbase = gq + (int64_t)q_start * p.q_st + (int64_t)hq * p.q_sh;
