@@ -1010,8 +1010,8 @@ def main():
                     ("fwd", "tc"): [csrc + "fwd_tc.cu"] + tc_shared,
                     ("bwd_dkdv", "simt"): [csrc + "bwd_simt.cu"] + shared,
                     ("bwd_dq", "simt"): [csrc + "bwd_simt.cu"] + shared,
-                    ("bwd_dkdv", "tc"): [csrc + "bwd_tc.cu"] + tc_shared,
-                    ("bwd_dq", "tc"): [csrc + "bwd_tc.cu"] + tc_shared}
+                    ("bwd_dkdv", "tc"): [csrc + "bwd_tc.cu", csrc + "bwd_tc.cuh"] + tc_shared,
+                    ("bwd_dq", "tc"): [csrc + "bwd_tc.cu", csrc + "bwd_tc.cuh"] + tc_shared}
     using_tc = family[dominant] == "tc"
     achieved = stage_flops[dominant] / (stage_ms[dominant] * 1e-3) / 1e12
     region_s = ms * args.steps * 1e-3

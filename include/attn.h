@@ -66,7 +66,7 @@
 extern "C" {
 #endif
 
-#define ATTN_ABI_VERSION 7
+#define ATTN_ABI_VERSION 8
 
 #if defined(__GNUC__)
 #define ATTN_API __attribute__((visibility("default")))
@@ -144,7 +144,21 @@ typedef struct attn_fwd_args {
                                forward adds the number of pruned tiles to it */
     int32_t qk_fp8;       /* 0: q and k are `dtype`; 1: q and k are fp8 e4m3 (see below) */
     int32_t H_kv;         /* heads of k and v: 0 = H; else a divisor of H (grouped heads, below) */
+    int32_t window;       /* sliding window (below): 0 = none; else the last keys a query sees */
+    int32_t sinks;        /* with a window: the first keys that every query sees beside it */
 } attn_fwd_args;
+
+/* Sliding windows with sinks (window, sinks in the forward, the backward and over a
+ * cache; no counterpart on the pages): of the keys that a query would see without a
+ * window, in order, it sees the first `sinks` and the last `window` (all of them where
+ * they are no more than both together).  So query i of a sequence sees key j <= i if
+ * i - j < window or j < sinks, and work and reads go with window + sinks, not with
+ * the sequence.  Causal relation only; window > 0 (or none: both 0, ATTN_EINVAL else); no
+ * fp8, no pruning, no ATTN_DQ_FUSED (ATTN_EUNSUPPORTED).  A window as long as all the keys
+ * is none.  f16 / bf16 inputs run the kernel that packs grouped heads' rows (for ungrouped
+ * heads too, and any number of sequences), which takes neither num_splits > 1 nor
+ * num_ctas > 0 (ATTN_EUNSUPPORTED) and whose workspace attn_fwd_noalloc does not have;
+ * with ATTN_KERNEL_SIMT, groups of more than 128 or f32 inputs, the CUDA-core kernels. */
 
 /* Grouped heads (H_kv in the forward and the backward; no counterpart on the
  * pages): k and v hold H_kv heads, each shared by a group of G = H / H_kv
@@ -208,6 +222,7 @@ typedef struct attn_bwd_args {
                               defined, and a non-zero value returns ATTN_EUNSUPPORTED */
     int32_t dq_mode;      /* attn_dq_mode */
     int32_t H_kv;         /* heads of k, v, dk and dv: 0 = H; else a divisor of H */
+    int32_t window, sinks; /* as in the forward */
 } attn_bwd_args;
 
 /* Partial attention results over disjoint key sets, to be merged
@@ -277,7 +292,7 @@ typedef struct attn_csr_args {
  * The operations below run on `stream`, read and write only device memory and
  * do not synchronise, so a captured loop can hold them.  They validate on the
  * device, and attn_device_status() reports ATTN_EINVAL.  For attn_cache_extend,
- * _fork and _keep a list with an entry out of range, a sequence listed twice, or
+ * _fork, _keep and _evict a list with an entry out of range, a sequence listed twice, or
  * lengths that do not fit leaves the whole cache as it was (so do too few free
  * pages, ATTN_ENOPAGES), and so does a length that does not fit for
  * attn_cache_compact; attn_cache_write and _free leave out the entries that are
@@ -336,7 +351,47 @@ typedef struct attn_tree_args {
     int32_t o_dtype;      /* the cache's dtype or ATTN_F32 */
     void *workspace;      /* attn_tree_workspace_bytes() bytes, 256-byte aligned */
     size_t workspace_bytes;
+    /* sliding window, 0 = none: of the tokens that a new one would see without it -- those
+     * before the new ones, then new ones, in the cache's order -- it sees the first `sinks`
+     * and the last `window`.  Cached rows that no new token of an entry sees are not read,
+     * but for those that share a tile with ones that are. */
+    int32_t window, sinks;
 } attn_tree_args;
+
+/* The attention that cached tokens get, accumulated: which of them a sequence can do without
+ * (attn_cache_evict).  With w the layer's row of the entry's sequence,
+ *     w[j] = (j < L - fresh ? w[j] : 0) + sum_{t, h} exp(scale <q_th, k_j> - lse_th)
+ * for every token j < L of the sequence, over its query rows (new tokens t, all query heads
+ * h) that see j: those of attn_tree_fwd without a mask, whose lse this takes.  The sum is
+ * taken in f32 in a fixed order.  A row with an lse of -inf (it saw nothing) adds nothing.
+ * Entries from w[L] on are left as they are.  An entry that does not fit (as in
+ * attn_tree_args; L > cols; fresh not in [0, L]) or whose sequence is listed more than
+ * once is left out and reported as ATTN_EINVAL. */
+typedef struct attn_weigh_args {
+    attn_cache cache;       /* k of the layer is read; H_kv divides H; dtype also of q */
+    int32_t layer;
+    int32_t H;              /* query heads */
+    attn_tensor q;          /* in: (n_q, H, D), the query rows of attn_tree_fwd */
+    const float *lse;       /* in: (H, n_q) f32, natural log, from attn_tree_fwd */
+    float *weights;         /* in, out: the layer's (max_seqs, cols) f32, contiguous rows */
+    int64_t weights_stride; /* elements between its rows, >= cols */
+    int32_t cols;           /* tokens that a row has room for */
+    int32_t n;              /* entries */
+    int32_t n_q;            /* query rows */
+    float scale;            /* as in attn_tree_fwd */
+    int32_t window, sinks;  /* as in attn_tree_fwd */
+    const int32_t *seqs;    /* device, n sequences */
+    const int32_t *cu;      /* device, n + 1 offsets from 0 */
+    const int32_t *fresh;   /* device, n: last tokens whose weight starts anew; NULL: the new ones */
+} attn_weigh_args;
+
+/* The weights by which attn_cache_evict chooses: (n_layers, max_seqs, cols) f32. */
+typedef struct attn_weights {
+    float *ptr;
+    int64_t stride_layer, stride_seq; /* elements; tokens are contiguous */
+    int32_t n_layers;                 /* >= 1; need not be the cache's */
+    int32_t cols;
+} attn_weights;
 
 /* Library ABI version (ATTN_ABI_VERSION) and struct sizes, for bindings to
  * check their mirrors of the structs above. */
@@ -347,6 +402,8 @@ ATTN_API size_t attn_merge_args_size(void);
 ATTN_API size_t attn_csr_args_size(void);
 ATTN_API size_t attn_cache_size(void);
 ATTN_API size_t attn_tree_args_size(void);
+ATTN_API size_t attn_weigh_args_size(void);
+ATTN_API size_t attn_weights_size(void);
 
 /* Bytes of device workspace the call needs (depends on n_seq, H, n_q, and
  * for the forward on the number of key splits: n_splits > 1 adds the partial
@@ -495,6 +552,29 @@ ATTN_API int attn_cache_free(const attn_cache *c, const int32_t *seqs, int32_t n
  * all of lens that does not fit, nothing moves, and it is reported. */
 ATTN_API int attn_cache_compact(const attn_cache *c, int32_t *remap, void *workspace,
                                 size_t workspace_bytes, void *stream);
+
+/* Adds the attention that cached tokens get from new ones to their weights (see
+ * attn_weigh_args).  One kernel on `stream`; no workspace.  Calls on the same rows of
+ * weights must be ordered by the caller. */
+ATTN_API int attn_cache_weigh(const attn_weigh_args *a, void *stream);
+
+/* Cuts every listed sequence of more than budgets[i] tokens to that many: its first `sinks`,
+ * its last `recent`, and the heaviest of the others by the sum of their weights over the
+ * layers (taken in f64, rounded to f32; equal weights: the lower token first; NaN is
+ * lighter than every number).  The kept rows move down in order, in all layers of the cache,
+ * and their weights in all layers of w; the pages behind the new end are released.  Rows
+ * and weights behind the new end keep what they hold.  Shorter sequences stay as they are.
+ * sinks >= 0, recent >= 0.  A list is done as a whole or not at all: an entry out of
+ * range, a sequence listed twice, a negative budget, sinks + recent above the budget of a
+ * sequence that is cut, a length above cols, a page index outside the pool, or a row that
+ * would move into a page that other sequences hold too: ATTN_EINVAL. */
+ATTN_API int attn_cache_evict(const attn_cache *c, const int32_t *seqs, const int32_t *budgets, int32_t n,
+                              const attn_weights *w, int32_t sinks, int32_t recent, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace attn_cache_evict needs for a list of n entries and weights of `cols`
+ * tokens (256-byte aligned device memory); 0 for bad arguments. */
+ATTN_API size_t attn_cache_evict_workspace_bytes(const attn_cache *c, int32_t n, int32_t cols);
 
 /* Forward for callers that cannot allocate device memory (no counterpart on
  * the pages; a deployment convenience).  Same arguments and results as

@@ -12,7 +12,8 @@ argument structs:
 * ``csr_fwd(row_ptr, col, v, scores=... | q=..., k=...)`` -> ``(o, lse)``:
   attention over a general CSR relation (softmax over each row's edges)
 * ``Cache``: a paged key / value cache -- ``extend``, ``write``, ``fork``,
-  ``keep``, ``free``, ``compact``
+  ``keep``, ``free``, ``compact``; ``weigh`` adds up the attention that cached tokens
+  get, ``evict`` cuts sequences to their heaviest tokens
 * ``tree_fwd(q, cache, seqs, cu_seqlens_q, mask=...)`` -> ``(o, lse)``:
   attention of new tokens (one, a chunk, a tree of drafts) over the cache
 * ``FwdCall`` / ``BwdCall`` / ``TreeCall`` hold prepared argument structs for repeated
@@ -23,7 +24,9 @@ Tensors are (tokens, heads, D) with the D axis contiguous; any token / head
 strides whose rows stay 16-byte aligned are accepted (for example an (H, N, D)
 tensor viewed as (N, H, D)).  k and v may have fewer heads than q, each shared
 by a group of query heads (query head h reads head h // (H / H_kv)); dk and dv
-then have their heads.  ``cu_seqlens`` follow flash-attn's varlen
+then have their heads.  With ``window=W, sinks=S`` (``fwd``, ``bwd``, ``tree_fwd``,
+``Cache.weigh``; causal) a query sees the first S and the last W of the keys that it would
+see without.  ``cu_seqlens`` follow flash-attn's varlen
 convention ``[0, L1, L1+L2, ...]`` as int32.
 """
 from __future__ import annotations
@@ -163,7 +166,8 @@ class FwdCall:
                  cu_seqlens_q=None, cu_seqlens_k=None, out_dtype: torch.dtype | None = None,
                  kernel: str = "auto", num_ctas: int = 0, num_splits: int = 0,
                  prune_threshold: float = 0.0, out: torch.Tensor | None = None,
-                 lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+                 lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 window: int | None = None, sinks: int = 0):
         # fp8 (e4m3) queries and keys with a 16-bit v: the tensor-core kernel
         # contracts the scores in fp8 (attn.h, qk_fp8)
         qk_fp8 = q.dtype == _E4M3 and _E4M3 is not None
@@ -194,7 +198,7 @@ class FwdCall:
             (cu_q.numel() - 1) if cu_q is not None else 1, cu_q.data_ptr() if cu_q is not None else 0,
             cu_k.data_ptr() if cu_k is not None else 0, 0, 0, _KERNELS[kernel], int(num_ctas), int(num_splits),
             _host.f32(prune_threshold), self.pruned_tiles.data_ptr() if self.pruned_tiles is not None else 0,
-            1 if qk_fp8 else 0, H_kv))
+            1 if qk_fp8 else 0, H_kv, *_host.window(window, sinks)))
         self._index = dev.index
         self._at = ctypes.addressof(self.args)
         if workspace is None:
@@ -272,7 +276,7 @@ class BwdCall:
                  cu_seqlens_q=None, cu_seqlens_k=None, grad_dtype: torch.dtype | None = None,
                  kernel: str = "auto", num_ctas: int = 0, dq=None, dk=None, dv=None,
                  workspace: torch.Tensor | None = None, prune_threshold: float = 0.0,
-                 dq_mode: str = "auto"):
+                 dq_mode: str = "auto", window: int | None = None, sinks: int = 0):
         dev = q.device
         Tq, H, D = q.shape
         Tk, H_kv = _kv_shape(k, v, D)
@@ -298,7 +302,7 @@ class BwdCall:
             ATTN_CAUSAL if causal else ATTN_FULL, _dtype_code(q.dtype), _dtype_code(o.dtype), _dtype_code(gdt),
             (cu_q.numel() - 1) if cu_q is not None else 1, cu_q.data_ptr() if cu_q is not None else 0,
             cu_k.data_ptr() if cu_k is not None else 0, 0, 0, _KERNELS[kernel], int(num_ctas),
-            _host.f32(prune_threshold), _DQ_MODES[dq_mode], H_kv))
+            _host.f32(prune_threshold), _DQ_MODES[dq_mode], H_kv, *_host.window(window, sinks)))
         self._index = dev.index
         self._at = ctypes.addressof(self.args)
         if workspace is None:
@@ -411,21 +415,24 @@ def csr_fwd(row_ptr, col, v, *, scores=None, q=None, k=None, scale: float | None
 
 def fwd(q, k, v, *, causal: bool = False, scale: float | None = None, cu_seqlens_q=None,
         cu_seqlens_k=None, out_dtype: torch.dtype | None = None, kernel: str = "auto",
-        num_ctas: int = 0, num_splits: int = 0, prune_threshold: float = 0.0):
+        num_ctas: int = 0, num_splits: int = 0, prune_threshold: float = 0.0,
+        window: int | None = None, sinks: int = 0):
     """Attention forward.  Returns ``(o, lse)``; lse is (H, T_q) f32, natural log.
+
+    ``window``: a causal query i sees key j if i - j < window or j < ``sinks`` (None: all).
 
     ``num_splits``: key splits per query tile (split-K); 0 lets the library
     choose, 1 disables splitting.  ``prune_threshold``: 0 = exact; rho in
     (0, 1] enables approximate tile pruning (full relation, one sequence)."""
     if kernel == "auto" and not num_ctas and not num_splits and not prune_threshold:
         r = _host.native().fwd(q, k, v, causal, scale, cu_seqlens_q, cu_seqlens_k,
-                               -1 if out_dtype is None else _dtype_code(out_dtype))
+                               -1 if out_dtype is None else _dtype_code(out_dtype), window, sinks)
         if r is not None:
             return r if type(r) is tuple else check(r, "attn_fwd")
     return FwdCall(q, k, v, causal=causal, scale=scale, cu_seqlens_q=cu_seqlens_q,
                    cu_seqlens_k=cu_seqlens_k, out_dtype=out_dtype, kernel=kernel,
                    num_ctas=num_ctas, num_splits=num_splits,
-                   prune_threshold=prune_threshold).run()
+                   prune_threshold=prune_threshold, window=window, sinks=sinks).run()
 
 
 def merge(o_parts, lse_parts, *, out_dtype: torch.dtype = torch.float32):
@@ -436,13 +443,14 @@ def merge(o_parts, lse_parts, *, out_dtype: torch.dtype = torch.float32):
 
 def bwd(q, k, v, o, lse, dout, *, causal: bool = False, scale: float | None = None,
         cu_seqlens_q=None, cu_seqlens_k=None, grad_dtype: torch.dtype | None = None,
-        kernel: str = "auto", num_ctas: int = 0, dq_mode: str = "auto"):
-    """Attention backward from the forward's o and lse.  Returns ``(dq, dk, dv)``."""
+        kernel: str = "auto", num_ctas: int = 0, dq_mode: str = "auto", window: int | None = None, sinks: int = 0):
+    """Attention backward from the forward's o and lse.  Returns ``(dq, dk, dv)``.
+    ``window`` and ``sinks`` are those of the forward."""
     if kernel == "auto" and not num_ctas and dq_mode == "auto":
         r = _host.native().bwd(q, k, v, o, lse, dout, causal, scale, cu_seqlens_q, cu_seqlens_k,
-                               -1 if grad_dtype is None else _dtype_code(grad_dtype))
+                               -1 if grad_dtype is None else _dtype_code(grad_dtype), window, sinks)
         if r is not None:
             return r if type(r) is tuple else check(r, "attn_bwd")
     return BwdCall(q, k, v, o, lse, dout, causal=causal, scale=scale, cu_seqlens_q=cu_seqlens_q,
                    cu_seqlens_k=cu_seqlens_k, grad_dtype=grad_dtype, kernel=kernel,
-                   num_ctas=num_ctas, dq_mode=dq_mode).run()
+                   num_ctas=num_ctas, dq_mode=dq_mode, window=window, sinks=sinks).run()

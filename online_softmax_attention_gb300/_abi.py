@@ -12,7 +12,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libattn_gb300.so")
 
-ABI_VERSION = 7
+ABI_VERSION = 8
 
 ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED, ATTN_ECUDA, ATTN_ETIMEOUT, ATTN_EWORKSPACE = 0, -1, -2, -3, -4, -5
 ATTN_ENOPAGES = -6
@@ -36,6 +36,8 @@ EXPORTS = (
     "attn_cache_size", "attn_tree_args_size", "attn_tree_fwd", "attn_tree_workspace_bytes",
     "attn_cache_workspace_bytes", "attn_cache_extend", "attn_cache_write", "attn_cache_fork",
     "attn_cache_keep", "attn_cache_free", "attn_cache_compact",
+    "attn_weigh_args_size", "attn_weights_size", "attn_cache_weigh", "attn_cache_evict",
+    "attn_cache_evict_workspace_bytes",
 )
 
 
@@ -56,6 +58,7 @@ class FwdArgs(ctypes.Structure):
         ("kernel", ctypes.c_int32), ("num_ctas", ctypes.c_int32), ("num_splits", ctypes.c_int32),
         ("prune_threshold", ctypes.c_float), ("pruned_tiles", ctypes.c_void_p),
         ("qk_fp8", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
     ]
 
 
@@ -97,6 +100,24 @@ class TreeArgs(ctypes.Structure):
         ("mask", ctypes.c_void_p), ("n", ctypes.c_int32), ("n_q", ctypes.c_int32),
         ("mask_words", ctypes.c_int32), ("scale", ctypes.c_float), ("o_dtype", ctypes.c_int32),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+    ]
+
+
+class WeighArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", Cache), ("layer", ctypes.c_int32), ("H", ctypes.c_int32), ("q", AttnTensor),
+        ("lse", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("weights_stride", ctypes.c_int64),
+        ("cols", ctypes.c_int32), ("n", ctypes.c_int32), ("n_q", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+        ("seqs", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("fresh", ctypes.c_void_p),
+    ]
+
+
+class Weights(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p), ("stride_layer", ctypes.c_int64), ("stride_seq", ctypes.c_int64),
+        ("n_layers", ctypes.c_int32), ("cols", ctypes.c_int32),
     ]
 
 
@@ -112,6 +133,7 @@ class BwdArgs(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("kernel", ctypes.c_int32), ("num_ctas", ctypes.c_int32),
         ("prune_threshold", ctypes.c_float), ("dq_mode", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
     ]
 
 
@@ -132,7 +154,7 @@ def load() -> ctypes.CDLL:
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     fa, ba, ma = ctypes.POINTER(FwdArgs), ctypes.POINTER(BwdArgs), ctypes.POINTER(MergeArgs)
     ca, cc, ta = ctypes.POINTER(CsrArgs), ctypes.POINTER(Cache), ctypes.POINTER(TreeArgs)
-    at = ctypes.POINTER(AttnTensor)
+    at, wa, wt = ctypes.POINTER(AttnTensor), ctypes.POINTER(WeighArgs), ctypes.POINTER(Weights)
     sigs = {
         "attn_abi_version": (ctypes.c_int, []),
         "attn_fwd_args_size": (sz, []),
@@ -170,6 +192,11 @@ def load() -> ctypes.CDLL:
         "attn_cache_keep": (ctypes.c_int, [cc, vp, vp, vp, ctypes.c_int64, vp, i32, vp, sz, vp]),
         "attn_cache_free": (ctypes.c_int, [cc, vp, i32, vp]),
         "attn_cache_compact": (ctypes.c_int, [cc, vp, vp, sz, vp]),
+        "attn_weigh_args_size": (sz, []),
+        "attn_weights_size": (sz, []),
+        "attn_cache_weigh": (ctypes.c_int, [wa, vp]),
+        "attn_cache_evict": (ctypes.c_int, [cc, vp, vp, i32, wt, i32, i32, vp, sz, vp]),
+        "attn_cache_evict_workspace_bytes": (sz, [cc, i32, i32]),
         "attn_launch_count": (ctypes.c_uint64, []),
         "attn_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "attn_last_error_string": (ctypes.c_char_p, []),
@@ -185,7 +212,9 @@ def load() -> ctypes.CDLL:
             lib.attn_merge_args_size() != ctypes.sizeof(MergeArgs) or \
             lib.attn_csr_args_size() != ctypes.sizeof(CsrArgs) or \
             lib.attn_cache_size() != ctypes.sizeof(Cache) or \
-            lib.attn_tree_args_size() != ctypes.sizeof(TreeArgs):
+            lib.attn_tree_args_size() != ctypes.sizeof(TreeArgs) or \
+            lib.attn_weigh_args_size() != ctypes.sizeof(WeighArgs) or \
+            lib.attn_weights_size() != ctypes.sizeof(Weights):
         raise ImportError("libattn_gb300 struct layout does not match the binding")
     _lib = lib
     return lib

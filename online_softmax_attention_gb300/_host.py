@@ -25,13 +25,15 @@ _current_device = torch._C._cuda_getDevice
 
 # native layouts of the argument structs in include/attn.h, field by field
 _TENSOR = "Pqq"
-FWD = struct.Struct("@" + _TENSOR * 4 + "P" + "iiii" + "f" + "iiii" + "PP" + "PN" + "iii" + "f" + "P" + "ii" + "0P")
-BWD = struct.Struct("@" + _TENSOR * 5 + "P" + _TENSOR * 3 + "iiii" + "f" + "iiiii" + "PP" + "PN" + "ii" + "f" + "ii" + "0P")
+FWD = struct.Struct("@" + _TENSOR * 4 + "P" + "iiii" + "f" + "iiii" + "PP" + "PN" + "iii" + "f" + "P" + "iiii" + "0P")
+BWD = struct.Struct("@" + _TENSOR * 5 + "P" + _TENSOR * 3 + "iiii" + "f" + "iiiii" + "PP" + "PN" + "ii" + "f" + "iiii" + "0P")
 CACHE = struct.Struct("@" + "PP" + "qqqq" + "PPP" + "q" + "iiiiiiii" + "0P")
-TREE = struct.Struct("@" + "%ds" % CACHE.size + "ii" + _TENSOR * 2 + "PPPP" + "iii" + "f" + "i" + "PN" + "0P")
+TREE = struct.Struct("@" + "%ds" % CACHE.size + "ii" + _TENSOR * 2 + "PPPP" + "iii" + "f" + "i" + "PN" + "ii" + "0P")
+WEIGH = struct.Struct("@" + "%ds" % CACHE.size + "ii" + _TENSOR + "PP" + "q" + "iii" + "f" + "ii" + "PPP" + "0P")
+WEIGHTS = struct.Struct("@" + "Pqq" + "ii" + "0P")
 VIEW = struct.Struct("@" + _TENSOR)
 for _s, _c in ((FWD, _abi.FwdArgs), (BWD, _abi.BwdArgs), (CACHE, _abi.Cache), (TREE, _abi.TreeArgs),
-               (VIEW, _abi.AttnTensor)):
+               (WEIGH, _abi.WeighArgs), (WEIGHTS, _abi.Weights), (VIEW, _abi.AttnTensor)):
     if _s.size != ctypes.sizeof(_c):
         raise ImportError(f"packed layout of {_c.__name__} does not match its fields")
 
@@ -42,6 +44,18 @@ def f32(x: float) -> float:
     """`x` as a C float takes it (beyond its range: infinite, which the library refuses)."""
     x = float(x)
     return x if -_FLOAT_MAX <= x <= _FLOAT_MAX or x != x else ctypes.c_float(x).value
+
+
+def window(window, sinks) -> tuple[int, int]:
+    """A sliding window's arguments as the structs take them (none: 0 and 0)."""
+    for x, name in ((window, "window"), (sinks, "sinks")):
+        if not (isinstance(x, int) or (x is None and name == "window")) or isinstance(x, bool):
+            raise TypeError(f"{name} must be a whole number, got {x!r}")
+    if (window is not None and not 1 <= window < 2 ** 31) or not 0 <= sinks < 2 ** 31:
+        raise ValueError(f"window must be 1 or more (None: no window) and sinks 0 or more, got {window} and {sinks}")
+    if window is None and sinks:
+        raise ValueError("sinks need a window")
+    return window or 0, sinks
 
 
 def int32(x: torch.Tensor, device: torch.device, name: str) -> torch.Tensor:

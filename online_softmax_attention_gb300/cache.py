@@ -15,6 +15,12 @@ on the current stream without synchronising, so a captured loop can hold them
     cache.write(seqs, cu, k, v, layer=0)                      # their rows
     cache.extend(seqs, ones); cache.write(seqs, cu1, k1, v1)  # a new token each
     o1, lse1 = tree_fwd(q1, cache, seqs, cu1)                 # over the cache
+
+A cache that stays within a budget: ``weights = cache.new_weights()``; after each
+``tree_fwd``, ``cache.weigh(seqs, cu1, q1, lse1, weights)`` adds the attention that every cached
+token got; ``cache.evict(seqs, budgets, weights)`` keeps the heaviest.  The weights are the
+caller's: after ``fork`` copy the parents' rows to the children's, weigh drafted tokens
+after ``keep``, and start a sequence anew with ``fresh``.
 """
 from __future__ import annotations
 
@@ -118,6 +124,10 @@ class Cache:
         index = self.device.index
         _host.call(index, _host.entry(name), name, self.args, *args, _host.raw_stream(index))
 
+    def _call_packed(self, name: str, args: bytes) -> None:
+        index = self.device.index
+        _host.call(index, _host.entry(name), name, args, _host.raw_stream(index))
+
     def _lists(self, n: int | None, **lists) -> list:
         out = [_ints(x, self.device, name) for name, x in lists.items()]
         n = out[0].numel() if n is None else n
@@ -188,6 +198,64 @@ class Cache:
         self._call("attn_cache_compact", remap.data_ptr() if remap is not None else None, ws.data_ptr(),
                    ws.numel())
 
+    def new_weights(self, n_layers: int | None = None) -> torch.Tensor:
+        """Weights of 0 for ``weigh`` and ``evict``: (layers, sequences, tokens a sequence can hold) float32."""
+        return torch.zeros((n_layers or self.n_layers, self.max_seqs, self.table.shape[1] * self.k.shape[2]),
+                           dtype=torch.float32, device=self.device)
+
+    def _weights(self, weights: torch.Tensor) -> torch.Tensor:
+        if weights.dim() != 3 or weights.dtype != torch.float32 or weights.device != self.device \
+                or weights.shape[0] < 1 or weights.shape[1] != self.max_seqs or (weights.shape[2] > 1 and weights.stride(2) != 1) \
+                or weights.stride(0) < 0 or (self.max_seqs > 1 and weights.stride(1) < weights.shape[2]) \
+                or (weights.shape[0] > 1 and weights.stride(0) < weights.stride(1) * (self.max_seqs - 1) + weights.shape[2]):
+            raise ValueError(f"weights must be float32 (layers, {self.max_seqs}, tokens) with rows of their own on the "
+                             f"cache's device {self.device}, got {weights.dtype} {tuple(weights.shape)}")
+        return weights
+
+    def weigh(self, seqs, cu_seqlens_q, q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, *, layer: int = 0,
+              scale: float | None = None, window: int | None = None, sinks: int = 0, fresh=None) -> None:
+        """Adds to ``weights[layer, seqs[i], j]`` the attention that token j of sequence ``seqs[i]``
+        gets from the query rows ``cu[i]:cu[i + 1]`` of q, summed over rows and heads.
+
+        The arguments are those of ``tree_fwd`` (without a mask), ``lse`` what it returned.  The
+        last ``fresh[i]`` tokens' weights start anew (None: the new tokens', ``cu[i + 1] - cu[i]``)."""
+        dev, D = self.device, self.head_dim
+        seqs, cu = _ints(seqs, dev, "seqs"), _ints(cu_seqlens_q, dev, "cu_seqlens_q")
+        n = seqs.numel()
+        if cu.numel() != n + 1:
+            raise ValueError(f"cu_seqlens_q must have {n + 1} entries, got {cu.numel()}")
+        if fresh is not None:
+            fresh, = self._lists(n, fresh=fresh)
+        w = self._weights(weights)
+        if not 0 <= int(layer) < min(self.n_layers, w.shape[0]):
+            raise ValueError(f"layer must be one of {min(self.n_layers, w.shape[0])}, got {layer}")
+        q_fields = _rows(q, "q", None, D, self.dtype, dev)
+        T, H, _ = q.shape
+        if tuple(lse.shape) != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError(f"lse must be contiguous float32 {(H, T)} on the cache's device")
+        self._call_packed("attn_cache_weigh", _host.WEIGH.pack(
+            self.args, int(layer), H, *q_fields, lse.data_ptr(), w[int(layer)].data_ptr(),
+            w.stride(1) if self.max_seqs > 1 else w.shape[2], w.shape[2], n, T,
+            _host.f32(scale) if scale is not None else D ** -0.5, *_host.window(window, sinks), seqs.data_ptr(),
+            cu.data_ptr(), fresh.data_ptr() if fresh is not None else 0))
+
+    def evict(self, seqs, budgets, weights: torch.Tensor, *, sinks: int = 0, recent: int = 0) -> None:
+        """Cuts every sequence ``seqs[i]`` of more than ``budgets[i]`` tokens to that many: the first
+        ``sinks``, the last ``recent`` and the heaviest others by ``weights`` summed over its
+        layers (equal ones: the first).  Rows and weights move down; a whole list or nothing."""
+        seqs, budgets = self._lists(None, seqs=seqs, budgets=budgets)
+        w = self._weights(weights)
+        for x, name in ((sinks, "sinks"), (recent, "recent")):
+            if not isinstance(x, int) or isinstance(x, bool) or not 0 <= x < 2 ** 31:
+                raise ValueError(f"{name} must be a whole number, 0 or more, got {x!r}")
+        packed = _host.WEIGHTS.pack(w.data_ptr(), w.stride(0) if w.shape[0] > 1 else w.shape[1] * w.shape[2],
+                                    w.stride(1) if self.max_seqs > 1 else w.shape[2], w.shape[0], w.shape[2])
+        n = seqs.numel()
+        ws = torch.empty(_host.entry("attn_cache_evict_workspace_bytes")(self.args, n, w.shape[2]), dtype=torch.uint8,
+                         device=self.device)
+        self._call("attn_cache_evict", seqs.data_ptr(), budgets.data_ptr(), n, packed, sinks, recent, ws.data_ptr(),
+                   ws.numel())
+
 
 class TreeCall:
     """Prepared attention of new tokens over a cache: holds the argument struct,
@@ -196,12 +264,15 @@ class TreeCall:
 
     ``mask`` (n_q, words) int64: bit u of row t (bit u % 64 of word u // 64) lets
     new token t see new token u; without it a new token sees those up to itself.
+    ``window``: of what a new token would see so, it sees the first ``sinks`` tokens and the
+    last ``window`` (None: all).
     """
 
     def __init__(self, q: torch.Tensor, cache: Cache, seqs, cu_seqlens_q, *, layer: int = 0,
                  mask: torch.Tensor | None = None, scale: float | None = None,
                  out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
-                 lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+                 lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 window: int | None = None, sinks: int = 0):
         dev, D, dtype = cache.device, cache.head_dim, cache.dtype
         self.cache = cache
         self.seqs = seqs = _ints(seqs, dev, "seqs")
@@ -234,14 +305,15 @@ class TreeCall:
         head = (cache.args, int(layer), H, *q_fields, *_rows(out, "out", H, D, out_dtype, dev), lse.data_ptr(),
                 seqs.data_ptr(), cu.data_ptr(), mask.data_ptr() if mask is not None else 0, n, T, words,
                 _host.f32(scale) if scale is not None else D ** -0.5, _DT[out_dtype])
+        window = _host.window(window, sinks)
         if workspace is None:
             # (0 bytes: arguments that the call will refuse)
-            workspace = torch.empty(_host.call(dev.index, _host.entry("attn_tree_workspace_bytes"), None, _host.TREE.pack(*head, 0, 0)) or 256,
+            workspace = torch.empty(_host.call(dev.index, _host.entry("attn_tree_workspace_bytes"), None, _host.TREE.pack(*head, 0, 0, *window)) or 256,
                                     dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous on the cache's device {dev}")
         self.workspace = workspace
-        self.args = _host.TREE.pack(*head, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        self.args = _host.TREE.pack(*head, workspace.data_ptr(), workspace.numel() * workspace.element_size(), *window)
 
     def run(self, stream: torch.cuda.Stream | None = None):
         index = self.cache.device.index
@@ -251,13 +323,15 @@ class TreeCall:
 
 
 def tree_fwd(q, cache: Cache, seqs, cu_seqlens_q, *, layer: int = 0, mask: torch.Tensor | None = None,
-             scale: float | None = None, out_dtype: torch.dtype | None = None):
+             scale: float | None = None, out_dtype: torch.dtype | None = None, window: int | None = None, sinks: int = 0):
     """Attention of new tokens over the cache.  Returns ``(o, lse)``; lse is (H, T) f32, natural log.
 
     Rows ``cu[i]:cu[i + 1]`` of q are the last tokens of sequence ``seqs[i]``: one token
-    (decoding), a chunk, or with ``mask`` a tree of drafts (see ``TreeCall``)."""
+    (decoding), a chunk, or with ``mask`` a tree of drafts; ``window`` and ``sinks`` bound what
+    they see (see ``TreeCall``)."""
     r = _host.native().tree(cache.args, cache._index, q, seqs, cu_seqlens_q, mask, layer, scale,
-                            -1 if out_dtype is None else _DT.get(out_dtype, 99))
+                            -1 if out_dtype is None else _DT.get(out_dtype, 99), window, sinks)
     if r is None:
-        return TreeCall(q, cache, seqs, cu_seqlens_q, layer=layer, mask=mask, scale=scale, out_dtype=out_dtype).run()
+        return TreeCall(q, cache, seqs, cu_seqlens_q, layer=layer, mask=mask, scale=scale, out_dtype=out_dtype,
+                        window=window, sinks=sinks).run()
     return r if type(r) is tuple else _abi.check(r, "attn_tree_fwd")

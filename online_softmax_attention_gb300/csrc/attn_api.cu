@@ -187,6 +187,12 @@ size_t parts_layout(int blocks, int rows, int D, void *workspace, Parts &w) {
 // microseconds for this many); batches of more sequences take the prepared schedule.
 constexpr int kPackedMaxSeqs = 2048;
 
+// A sliding window's arguments: 0 and 0, or window > 0 and the causal relation.
+int check_window(int window, int sinks, int relation) {
+    if (window < 0 || sinks < 0 || (window == 0 && sinks > 0)) return ATTN_EINVAL;
+    return window > 0 && relation != ATTN_CAUSAL ? ATTN_EUNSUPPORTED : ATTN_OK;
+}
+
 struct FwdLayout {
     size_t o_parts, lse_parts, split_ops, total;
 };
@@ -243,6 +249,9 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     if (a->qk_fp8 && (a->dtype == ATTN_F32 || a->D != 128 || !(a->scale > 0.f) ||
                       a->kernel == ATTN_KERNEL_SIMT))
         return ATTN_EUNSUPPORTED;
+    rc = check_window(a->window, a->sinks, a->relation);
+    if (rc) return rc;
+    if (a->window > 0 && (rho > 0.f || a->qk_fp8)) return ATTN_EUNSUPPORTED;
     const bool any_q = a->n_q > 0, any_k = a->n_k > 0;
     const bool qk_ok = a->qk_fp8 ? valid_view_bytes(a->q, 1, any_q) && valid_view_bytes(a->k, 1, any_k)
                                  : valid_view(a->q, a->dtype, any_q) && valid_view(a->k, a->dtype, any_k);
@@ -270,13 +279,19 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     p.prune = rho > 0.f;
     p.prune_log2 = p.prune ? std::log2(rho) : 0.f;
     p.pruned_tiles = reinterpret_cast<unsigned long long *>(a->pruned_tiles);
-    rc = choose_tc(a->kernel, tc_fwd_supported(p), use_tc);
+    if (a->window < a->n_k) {  // (a longer one leaves nothing out)
+        p.window = a->window;
+        p.sinks = a->sinks;
+    }
+    rc = choose_tc(a->kernel, p.window ? group_supported(p.dtype, p.D, p.group) : tc_fwd_supported(p), use_tc);
     if (rc) return rc;
+    if (p.window && use_tc && (a->num_splits > 1 || a->num_ctas > 0)) return ATTN_EUNSUPPORTED;
     if (p.qk_fp8 && !use_tc) return ATTN_EUNSUPPORTED;  // no CUDA-core fp8 path
-    // grouped heads: packed query rows (group_tc.cu), which balance by themselves; a caller
+    // grouped heads: packed query rows (group_tc.cuh), which balance by themselves; a caller
     // that fixes the splits or the grid gets the ungrouped kernel's schedule
     p.packed = p.group > 1 && use_tc && !p.qk_fp8 && !p.prune && a->num_splits == 0 && a->num_ctas == 0 &&
                a->n_seq <= kPackedMaxSeqs && a->n_k > 0 && group_supported(p.dtype, p.D, p.group);
+    p.packed = p.packed || (p.window && use_tc);
     p.n_splits = p.prune || p.packed ? 1 : (a->num_splits > 0 ? a->num_splits : auto_splits(p, use_tc));
     // work items (tiles x heads x splits) are numbered in int32
     const int64_t tiles = (int64_t)a->H * ((int64_t)a->n_q / kSimtBlock + a->n_seq + 1);
@@ -372,6 +387,9 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     if (a->o_dtype != a->dtype && a->o_dtype != ATTN_F32) return ATTN_EINVAL;
     if (a->grad_dtype != a->dtype && a->grad_dtype != ATTN_F32) return ATTN_EINVAL;
     if (a->prune_threshold != 0.f) return ATTN_EUNSUPPORTED;  // fails closed
+    rc = check_window(a->window, a->sinks, a->relation);
+    if (rc) return rc;
+    if (a->window > 0 && a->dq_mode == ATTN_DQ_FUSED) return ATTN_EUNSUPPORTED;
     if (a->dq_mode != ATTN_DQ_AUTO && a->dq_mode != ATTN_DQ_SEPARATE && a->dq_mode != ATTN_DQ_FUSED)
         return ATTN_EINVAL;
     const bool any_q = a->n_q > 0, any_k = a->n_k > 0;
@@ -405,6 +423,10 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     p.dtype = a->dtype; p.o_dtype = a->o_dtype; p.grad_dtype = a->grad_dtype;
     p.n_seq = a->n_seq;
     p.cu_q = a->cu_seqlens_q; p.cu_k = a->cu_seqlens_k;
+    if (a->window < a->n_k) {  // (a longer one leaves nothing out)
+        p.window = a->window;
+        p.sinks = a->sinks;
+    }
     const bool fused = bwd_fused(a);
     const BwdLayout L = bwd_layout(a->n_seq, a->H, a->n_q, a->D, fused);
     char *ws = static_cast<char *>(a->workspace);
@@ -503,6 +525,7 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
     if (a->o_dtype != a->cache.dtype && a->o_dtype != ATTN_F32) return ATTN_EINVAL;
     if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return ATTN_EINVAL;
     if ((int64_t)a->n_q * a->H > kMostTokens) return ATTN_EUNSUPPORTED;
+    if (check_window(a->window, a->sinks, ATTN_CAUSAL)) return ATTN_EINVAL;
     const bool any = a->n_q > 0 && a->n > 0;
     if (check_views && any &&
         (!valid_view(a->q, a->cache.dtype, true) || !valid_view(a->o, a->o_dtype, true) || !aligned4(a->seqs) ||
@@ -520,7 +543,56 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
     p.H = a->H; p.group = a->H / a->cache.H_kv; p.D = a->cache.D;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.dtype = a->cache.dtype; p.o_dtype = a->o_dtype;
+    if (a->window < a->cache.max_pages * a->cache.page_size) {  // (a longer one leaves nothing out)
+        p.window = a->window;
+        p.sinks = a->sinks;
+    }
     return ATTN_OK;
+}
+
+// Validates the arguments of the accumulation of attention weights.
+int plan_weigh(const attn_weigh_args *a, WeighParams &p) {
+    if (!a) return ATTN_EINVAL;
+    std::memset(&p, 0, sizeof(p));
+    const int rc = plan_cache(&a->cache, p.c);
+    if (rc) return rc;
+    if (a->layer < 0 || a->layer >= a->cache.n_layers || a->H < 1 || a->H % a->cache.H_kv != 0 || a->n < 0 ||
+        a->n_q < 0 || a->cols < 0 || a->weights_stride < a->cols)
+        return ATTN_EINVAL;
+    if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return ATTN_EINVAL;
+    if ((int64_t)a->n_q * a->H > kMostTokens || a->cols > kMostTokens) return ATTN_EUNSUPPORTED;
+    if (check_window(a->window, a->sinks, ATTN_CAUSAL)) return ATTN_EINVAL;
+    if (a->n > 0 && (!aligned4(a->seqs) || !aligned4(a->cu) || (reinterpret_cast<uintptr_t>(a->fresh) & 3) ||
+                     (a->cols > 0 && !aligned4(a->weights)) || !valid_view(a->q, a->cache.dtype, a->n_q > 0) ||
+                     (a->n_q > 0 && !aligned4(a->lse))))
+        return ATTN_EINVAL;
+    p.c.k += a->layer * p.c.b_layer;
+    p.q = a->q.ptr;
+    p.q_st = a->q.stride_tok; p.q_sh = a->q.stride_head;
+    p.lse = a->lse;
+    p.weights = a->weights;
+    p.weights_stride = a->weights_stride;
+    p.seqs = a->seqs; p.cu = a->cu; p.fresh = a->fresh;
+    p.cols = a->cols; p.n = a->n; p.n_q = a->n_q;
+    p.H = a->H; p.group = a->H / a->cache.H_kv; p.D = a->cache.D; p.dtype = a->cache.dtype;
+    p.group_inv = group_inverse(p.group);
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    if (a->window < a->cache.max_pages * a->cache.page_size) {
+        p.window = a->window;
+        p.sinks = a->sinks;
+    }
+    return ATTN_OK;
+}
+
+// Lays the eviction's plan out in the workspace; returns its bytes.
+size_t evict_plan(int n, int cols, void *workspace, EvictParams &p) {
+    const size_t list = align256(sizeof(int) * ((size_t)n + 1)), rows = align256(sizeof(int) * (size_t)n * (size_t)cols);
+    char *at = static_cast<char *>(workspace);
+    p.hdr = reinterpret_cast<int *>(at);
+    p.len = reinterpret_cast<int *>(at + 256);
+    p.first = reinterpret_cast<int *>(at + 256 + list);
+    p.source = reinterpret_cast<int *>(at + 256 + 2 * list);
+    return 256 + 2 * list + rows;
 }
 
 int build_cache(const attn_cache *c, int n, void *workspace, size_t workspace_bytes, CacheParams &p, CachePlan &w) {
@@ -584,10 +656,10 @@ int attn_fwd(const attn_fwd_args *a, void *stream) {
     if (log_on())
         std::fprintf(stderr,
                      "[attn] fwd n_q=%d n_k=%d H=%d H_kv=%d D=%d n_seq=%d relation=%s dtype=%s%s o_dtype=%s "
-                     "kernel=%s splits=%d prune=%g\n",
+                     "kernel=%s splits=%d prune=%g window=%d sinks=%d\n",
                      a->n_q, a->n_k, a->H, p.Hkv, a->D, a->n_seq, p.causal ? "causal" : "full",
                      p.qk_fp8 ? "e4m3+" : "", dtype_name(a->dtype), dtype_name(a->o_dtype),
-                     use_tc ? "tc" : "simt", p.n_splits, (double)a->prune_threshold);
+                     use_tc ? "tc" : "simt", p.n_splits, (double)a->prune_threshold, p.window, p.sinks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.packed) {
         GroupParams g = {};
@@ -605,7 +677,9 @@ int attn_fwd(const attn_fwd_args *a, void *stream) {
         parts_layout(sm_count(), kGroupRows, p.D, a->workspace, g.parts);
         g.status = p.status;
         g.watchdog_cycles = p.watchdog_cycles;
-        const cudaError_t e = launch_group(g, s);
+        g.window = p.window;
+        g.sinks = p.sinks;
+        const cudaError_t e = p.window ? launch_group_window(g, s) : launch_group(g, s);
         return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
     }
     const int block = use_tc ? tc_fwd_block_rows(p) : kSimtBlock;
@@ -722,10 +796,10 @@ int attn_bwd(const attn_bwd_args *a, void *stream) {
         if (build_bwd(a, p, use_tc) == ATTN_OK)
             std::fprintf(stderr,
                          "[attn] bwd n_q=%d n_k=%d H=%d H_kv=%d D=%d n_seq=%d relation=%s dtype=%s "
-                         "grad_dtype=%s kernel=%s dq=%s\n",
+                         "grad_dtype=%s kernel=%s dq=%s window=%d sinks=%d\n",
                          a->n_q, a->n_k, a->H, p.Hkv, a->D, a->n_seq, p.causal ? "causal" : "full",
                          dtype_name(a->dtype), dtype_name(a->grad_dtype), use_tc ? "tc" : "simt",
-                         p.dq_accum ? "fused" : "separate");
+                         p.dq_accum ? "fused" : "separate", p.window, p.sinks);
     }
     int rc = attn_bwd_preprocess(a, stream);
     if (rc) return rc;
@@ -974,6 +1048,54 @@ int attn_cache_compact(const attn_cache *c, int32_t *remap, void *workspace, siz
     if (!(p.status = status_ptr())) return ATTN_ECUDA;
     const cudaError_t e = launch_cache_compact(p, w, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+size_t attn_weigh_args_size(void) { return sizeof(attn_weigh_args); }
+size_t attn_weights_size(void) { return sizeof(attn_weights); }
+
+int attn_cache_weigh(const attn_weigh_args *a, void *stream) {
+    WeighParams p;
+    const int rc = plan_weigh(a, p);
+    if (rc || a->n == 0) return rc;
+    if (!(p.c.status = status_ptr())) return ATTN_ECUDA;
+    const cudaError_t e = launch_cache_weigh(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+size_t attn_cache_evict_workspace_bytes(const attn_cache *c, int32_t n, int32_t cols) {
+    CacheParams p;
+    EvictParams e;
+    return plan_cache(c, p) != ATTN_OK || n < 0 || cols < 0 ? 0 : evict_plan(n, cols, nullptr, e);
+}
+
+int attn_cache_evict(const attn_cache *c, const int32_t *seqs, const int32_t *budgets, int32_t n, const attn_weights *w,
+                     int32_t sinks, int32_t recent, void *workspace, size_t workspace_bytes, void *stream) {
+    CacheParams p;
+    EvictParams e = {};
+    const int rc = plan_cache(c, p);
+    if (rc) return rc;
+    if (!w || n < 0 || sinks < 0 || recent < 0 || w->n_layers < 1 || w->cols < 0 || w->stride_seq < w->cols ||
+        w->stride_layer < 0)
+        return ATTN_EINVAL;
+    if (w->cols > kMostTokens) return ATTN_EUNSUPPORTED;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+        workspace_bytes < evict_plan(n, w->cols, workspace, e))
+        return ATTN_EWORKSPACE;
+    if (n == 0) return ATTN_OK;
+    if (!aligned4(seqs) || !aligned4(budgets) || (w->cols > 0 && !aligned4(w->ptr))) return ATTN_EINVAL;
+    if (!(p.status = status_ptr())) return ATTN_ECUDA;
+    e.weights = w->ptr;
+    e.w_layer = w->stride_layer;
+    e.w_seq = w->stride_seq;
+    e.w_layers = w->n_layers;
+    e.cols = w->cols;
+    e.sinks = sinks;
+    e.recent = recent;
+    e.seqs = seqs;
+    e.budgets = budgets;
+    e.n = n;
+    const cudaError_t err = launch_cache_evict(p, e, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? ATTN_OK : set_cuda_error(err);
 }
 
 int attn_cache_write(const attn_cache *c, int32_t layer, const int32_t *seqs, const int32_t *cu, int32_t n,

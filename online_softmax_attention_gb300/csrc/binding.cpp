@@ -136,6 +136,16 @@ bool as_scale(PyObject *o, int64_t D, float &v) {
 
 bool fits(int64_t n) { return n <= INT32_MAX; }
 
+// A sliding window's arguments: None and 0, or window >= 1 and sinks >= 0.
+bool windowed(PyObject *window, PyObject *sinks, int32_t &w, int32_t &s) {
+    long x = 0, y = 0;
+    if (PyBool_Check(window) || PyBool_Check(sinks) || !as_long(sinks, y) || y < 0) return false;
+    if (window == Py_None ? y != 0 : !as_long(window, x) || x < 1) return false;
+    w = (int32_t)x;
+    s = (int32_t)y;
+    return true;
+}
+
 // The device lists of offsets of a call: none, or int32 vectors.
 bool offsets(PyObject *oq, PyObject *ok, int device, const int32_t *&cq, const int32_t *&ck, int32_t &n_seq) {
     cq = ck = nullptr;
@@ -149,15 +159,16 @@ bool offsets(PyObject *oq, PyObject *ok, int device, const int32_t *&cq, const i
     return true;
 }
 
-// fwd(q, k, v, causal, scale, cu_q, cu_k, out_code) -> (o, lse) | status | None
+// fwd(q, k, v, causal, scale, cu_q, cu_k, out_code, window, sinks) -> (o, lse) | status | None
 PyObject *py_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    NEED(n == 8);
+    NEED(n == 10);
     const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *v = tensor(args[2]);
     const int dev = device_of(q);
     NEED(dev >= 0 && k && v && q->dim() == 3 && k->dim() == 3 && v->dim() == 3);
     const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
     attn_fwd_args a;
     std::memset(&a, 0, sizeof(a));
+    NEED(windowed(args[8], args[9], a.window, a.sinks));
     NEED(rows(q, dev, D, a.q) && rows(k, dev, D, a.k) && rows(v, dev, D, a.v));
     const int code = dtype_code(*q);
     NEED(code >= 0 && dtype_code(*k) == code && dtype_code(*v) == code && k->sizes() == v->sizes());
@@ -187,9 +198,9 @@ PyObject *py_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return rc ? status(rc) : pack({o, lse});
 }
 
-// bwd(q, k, v, o, lse, dout, causal, scale, cu_q, cu_k, grad_code) -> (dq, dk, dv) | status | None
+// bwd(q, k, v, o, lse, dout, causal, scale, cu_q, cu_k, grad_code, window, sinks) -> (dq, dk, dv) | status | None
 PyObject *py_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    NEED(n == 11);
+    NEED(n == 13);
     const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *v = tensor(args[2]), *o = tensor(args[3]),
                  *lse = tensor(args[4]), *d = tensor(args[5]);
     const int dev = device_of(q);
@@ -197,6 +208,7 @@ PyObject *py_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
     attn_bwd_args a;
     std::memset(&a, 0, sizeof(a));
+    NEED(windowed(args[11], args[12], a.window, a.sinks));
     NEED(rows(q, dev, D, a.q) && rows(k, dev, D, a.k) && rows(v, dev, D, a.v) && rows(o, dev, D, a.o) &&
          rows(d, dev, D, a.dout));
     const int code = dtype_code(*q), o_code = dtype_code(*o);
@@ -243,12 +255,12 @@ bool cache_of(PyObject *bytes, PyObject *index, attn_cache &c, int &dev) {
     return dev == c10::cuda::current_device();
 }
 
-// tree(cache, device, q, seqs, cu, mask, layer, scale, out_code) -> (o, lse) | status | None
+// tree(cache, device, q, seqs, cu, mask, layer, scale, out_code, window, sinks) -> (o, lse) | status | None
 PyObject *py_tree(PyObject *, PyObject *const *args, Py_ssize_t n) {
     attn_tree_args a;
     std::memset(&a, 0, sizeof(a));
     int dev;
-    NEED(n == 9 && cache_of(args[0], args[1], a.cache, dev));
+    NEED(n == 11 && cache_of(args[0], args[1], a.cache, dev) && windowed(args[9], args[10], a.window, a.sinks));
     const Tensor *q = tensor(args[2]), *seqs = tensor(args[3]), *cu = tensor(args[4]);
     long layer, out;
     NEED(q && rows(q, dev, a.cache.D, a.q) && dtype_code(*q) == a.cache.dtype && ints(seqs, dev) && ints(cu, dev));

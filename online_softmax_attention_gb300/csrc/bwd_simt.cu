@@ -18,6 +18,7 @@
 // Thread layout and shared-memory padding follow the SIMT forward kernel.
 #include "../../include/attn.h"
 #include "common.cuh"
+#include "window.h"
 
 namespace attn {
 
@@ -177,7 +178,8 @@ constexpr size_t dkdv_smem_bytes() {
     return sizeof(float) * (size_t)(4 * B * (D + 4) + 2 * B * LDP + 2 * B);
 }
 
-template <typename Tin, typename Tg, int D>
+// kWindow: a sliding window (window.h).
+template <typename Tin, typename Tg, int D, bool kWindow>
 __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
     pdl_trigger();
     pdl_wait();
@@ -224,7 +226,9 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
             for (int e = 0; e < NG * 4; ++e) dk[r][e] = dv[r][e] = 0.f;
 
         const int qb_first = p.causal ? key0 / B : 0;
-        const int qb_end = (Lq + B - 1) / B;
+        // with a window, up to the last query that still sees the block's last key (the sinks': every one)
+        const int q_end = kWindow && key0 >= p.sinks ? (int)min((long long)Lq, (long long)key0 + B - 1 + p.window) : Lq;
+        const int qb_end = (q_end + B - 1) / B;
 
         // the query blocks of every query head that shares this key / value head
         for (int hq = h * p.group; hq < (h + 1) * p.group; ++hq) {
@@ -250,7 +254,8 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int key = key0 + tx + 16 * c;
-                        const bool ok = key < Lk && (!p.causal || key <= row);
+                        bool ok = key < Lk && (!p.causal || key <= row);
+                        if (kWindow) ok = ok && (row - key < p.window || key < p.sinks);
                         const float pr = ok ? exp2_approx(s[r][c] * p.scale_log2 - l2) : 0.f;
                         sP[rl * LDP + tx + 16 * c] = pr;
                         sdS[rl * LDP + tx + 16 * c] = pr * (dp[r][c] - drr);
@@ -314,7 +319,7 @@ constexpr size_t dq_smem_bytes() {
     return sizeof(float) * (size_t)(4 * B * (D + 4) + B * LDP + 2 * B);
 }
 
-template <typename Tin, typename Tg, int D>
+template <typename Tin, typename Tg, int D, bool kWindow>
 __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
     pdl_trigger();
     pdl_wait();
@@ -360,12 +365,14 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
             for (int e = 0; e < NG * 4; ++e) dq[r][e] = 0.f;
 
         const int n_keys = p.causal ? min(Lk, row0 + B) : Lk;
-        const int n_tiles = (n_keys + B - 1) / B;
+        TileList list = {0, 0};
+        if constexpr (kWindow) list = tile_list(p.window, p.sinks, row0 + 1, B);
+        const int n_tiles = (n_keys + B - 1) / B - list.skip;
         const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)key_head(h, p.group_inv) * p.k_sh;
         const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)key_head(h, p.group_inv) * p.v_sh;
 
         for (int kt = 0; kt < n_tiles; ++kt) {
-            const int key0 = kt * B;
+            const int key0 = (kWindow ? list.at(kt) : kt) * B;
             __syncthreads();
             stage_tile<Tin, D>(sK, kbase, p.k_st, key0, Lk);
             stage_tile<Tin, D>(sV, vbase, p.v_st, key0, Lk);
@@ -381,7 +388,8 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int key = key0 + tx + 16 * c;
-                    const bool ok = key < Lk && (!p.causal || key <= row);
+                    bool ok = key < Lk && (!p.causal || key <= row);
+                    if (kWindow) ok = ok && (row - key < p.window || key < p.sinks);
                     const float pr = ok ? exp2_approx(s[r][c] * p.scale_log2 - l2) : 0.f;
                     sdS[rl * LDP + tx + 16 * c] = pr * (dp[r][c] - drr);
                 }
@@ -446,8 +454,11 @@ cudaError_t launch_persistent(K kern, size_t smem, int num_ctas, const BwdParams
 
 template <typename Tin, typename Tg, int D>
 cudaError_t bwd_typed(const BwdParams &p, int num_ctas, cudaStream_t s, bool dkdv) {
-    if (dkdv) return launch_persistent(dkdv_simt_kernel<Tin, Tg, D>, dkdv_smem_bytes<D>(), num_ctas, p, s);
-    return launch_persistent(dq_simt_kernel<Tin, Tg, D>, dq_smem_bytes<D>(), num_ctas, p, s);
+    if (dkdv)
+        return launch_persistent(p.window ? dkdv_simt_kernel<Tin, Tg, D, true> : dkdv_simt_kernel<Tin, Tg, D, false>,
+                                 dkdv_smem_bytes<D>(), num_ctas, p, s);
+    return launch_persistent(p.window ? dq_simt_kernel<Tin, Tg, D, true> : dq_simt_kernel<Tin, Tg, D, false>,
+                             dq_smem_bytes<D>(), num_ctas, p, s);
 }
 
 template <typename Tin, int D>

@@ -20,6 +20,7 @@
 // quarter warp fall on distinct banks.
 #include "../../include/attn.h"
 #include "common.cuh"
+#include "window.h"
 
 namespace attn {
 
@@ -89,7 +90,8 @@ __device__ __forceinline__ void stage_tile(float *dst, const T *src, int64_t st,
     }
 }
 
-template <typename Tin, typename Tout, int D>
+// kWindow: a sliding window (window.h).
+template <typename Tin, typename Tout, int D, bool kWindow>
 __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
     pdl_trigger();
     pdl_wait();
@@ -136,8 +138,12 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
             for (int e = 0; e < NG * 4; ++e) acc[r][e] = 0.f;
         }
         const int n_keys = p.causal ? min(Lk, row0 + BQ) : Lk;
-        // split-K: this item scans chunk it.c of the row's key tiles
-        const KeyChunk chunk = key_chunk((n_keys + BK - 1) / BK, p.n_splits, it.c);
+        // split-K: this item scans chunk it.c of the row's key tiles; with a window, of those
+        // that hold a key of it or a sink
+        TileList list = {0, 0};
+        if constexpr (kWindow) list = tile_list(p.window, p.sinks, row0 + 1, BK);
+        const KeyChunk chunk = key_chunk((n_keys + BK - 1) / BK - list.skip, p.n_splits, it.c);
+        auto key_of = [&](int kt) { return (kWindow ? list.at(kt) : kt) * BK; };
         float m_run = -INFINITY;  // tile pruning: largest score of the admitted tiles (log2 units)
         const Tin *kbase = gk + (int64_t)k_start * p.k_st + (int64_t)key_head(h, p.group_inv) * p.k_sh;
         const Tin *vbase = gv + (int64_t)k_start * p.v_st + (int64_t)key_head(h, p.group_inv) * p.v_sh;
@@ -145,12 +151,12 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
         if constexpr (kAsync) {
             if (chunk.begin < chunk.end) {
                 __syncthreads();  // the previous item's last tile is no longer read
-                stage_tile_async<D>(sKb, reinterpret_cast<const float *>(kbase), p.k_st, chunk.begin * BK, Lk);
-                stage_tile_async<D>(sVb, reinterpret_cast<const float *>(vbase), p.v_st, chunk.begin * BK, Lk);
+                stage_tile_async<D>(sKb, reinterpret_cast<const float *>(kbase), p.k_st, key_of(chunk.begin), Lk);
+                stage_tile_async<D>(sVb, reinterpret_cast<const float *>(vbase), p.v_st, key_of(chunk.begin), Lk);
             }
         }
         for (int kt = chunk.begin; kt < chunk.end; ++kt) {
-            const int key0 = kt * BK;
+            const int key0 = key_of(kt);
             __syncthreads();  // previous tile's sK / sV / sP no longer read
             float *sK = sKb, *sV = sVb;
             if constexpr (kAsync) {
@@ -160,8 +166,8 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
                 const bool more = kt + 1 < chunk.end;
                 if (more) {  // the next tile into the other buffer, read two iterations ago
                     float *nK = sKb + (buf ^ 1) * BK * LD, *nV = sVb + (buf ^ 1) * BK * LD;
-                    stage_tile_async<D>(nK, reinterpret_cast<const float *>(kbase), p.k_st, key0 + BK, Lk);
-                    stage_tile_async<D>(nV, reinterpret_cast<const float *>(vbase), p.v_st, key0 + BK, Lk);
+                    stage_tile_async<D>(nK, reinterpret_cast<const float *>(kbase), p.k_st, key_of(kt + 1), Lk);
+                    stage_tile_async<D>(nV, reinterpret_cast<const float *>(vbase), p.v_st, key_of(kt + 1), Lk);
                 }
                 cp_async_wait_all_but(more ? 2 : 0);  // this tile's two groups have landed
             } else {
@@ -208,7 +214,8 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int key = key0 + tx + 16 * c;
-                    const bool ok = key < Lk && (!p.causal || key <= row);
+                    bool ok = key < Lk && (!p.causal || key <= row);
+                    if (kWindow) ok = ok && (row - key < p.window || key < p.sinks);
                     s[r][c] = ok ? s[r][c] * p.scale_log2 : -INFINITY;
                 }
             }
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(NT) fwd_simt_kernel(const FwdParams p) {
 // resident CTAs per SM through *per_sm_out.
 template <typename Tin, typename Tout, int D>
 cudaError_t launch_typed(const FwdParams &p, int num_ctas, cudaStream_t s, int *per_sm_out) {
-    auto kern = fwd_simt_kernel<Tin, Tout, D>;
+    auto kern = p.window ? fwd_simt_kernel<Tin, Tout, D, true> : fwd_simt_kernel<Tin, Tout, D, false>;
     const size_t smem = fwd_smem_bytes<Tin, D>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -1,0 +1,8 @@
+// Grouped attention with packed query rows (group_tc.cuh) over a sliding window with sinks.
+#include "group_tc.cuh"
+
+namespace attn {
+
+cudaError_t launch_group_window(const GroupParams &p, cudaStream_t s) { return launch_group_of<true>(p, s); }
+
+}  // namespace attn

@@ -58,8 +58,9 @@ struct FwdParams {
     // f32 inputs on the tensor cores: workspace region for the bf16 parts of
     // q, k and v (see fwd_x3.cu), else null
     void *split_ws;
-    // grouped heads with packed query rows (group_tc.cu)
+    // grouped heads with packed query rows (group_tc.cuh)
     int packed;
+    int window, sinks;  // sliding window (window.h); window 0: none
 };
 
 // Key-tile range [begin, end) of chunk c when n_tiles key tiles are cut into
@@ -174,13 +175,14 @@ struct TreeParams {
     int dtype, o_dtype;
     Parts parts;
     long long watchdog_cycles;
+    int window, sinks;  // window 0: none
 };
 // Query rows (token, head of the group) of a work unit (kGroupRows: the
-// tensor-core kernel of group_tc.cu), and the grid.
+// tensor-core kernel of group_tc.cuh), and the grid.
 int tree_rows(const TreeParams &p);
 int tree_blocks();
 
-// Grouped attention on the tensor cores with packed query rows (group_tc.cu):
+// Grouped attention on the tensor cores with packed query rows (group_tc.cuh):
 // over contiguous keys (prompts) or a cache.
 struct GroupParams {
     const void *q;
@@ -206,11 +208,44 @@ struct GroupParams {
     Parts parts;
     int *status;
     long long watchdog_cycles;
+    int window, sinks;               // window 0: none
 };
 constexpr int kGroupRows = 256;  // query rows of a unit (two 128-row tiles)
 bool group_supported(int dtype, int D, int group);
 cudaError_t launch_group(const GroupParams &p, cudaStream_t s);
+cudaError_t launch_group_window(const GroupParams &p, cudaStream_t s);  // the same, window > 0 (causal)
 cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s);
+
+// Attention weight of cached tokens (attn_weigh_args; c.k: the layer's).
+struct WeighParams {
+    CacheParams c;
+    const void *q;
+    int64_t q_st, q_sh;
+    const float *lse;
+    float *weights;
+    int64_t weights_stride;
+    const int *seqs, *cu, *fresh;
+    int cols, n, n_q, H, group, D, dtype;
+    unsigned long long group_inv;  // group_inverse(group)
+    int window, sinks;
+    float scale_log2;
+};
+cudaError_t launch_cache_weigh(const WeighParams &p, cudaStream_t s);
+
+// Eviction: the weights, and what the plan hands to the kernel that moves the rows.
+struct EvictParams {
+    float *weights;
+    int64_t w_layer, w_seq;  // strides
+    int w_layers, cols;
+    int sinks, recent;
+    const int *seqs, *budgets;
+    int n;
+    int *hdr;     // [0] 1: carry out, 0: refused
+    int *len;     // n: length before the call
+    int *first;   // n: tokens that stay where they are, before the first that goes
+    int *source;  // (n, cols): the kept tokens, in order
+};
+cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaStream_t s);
 
 cudaError_t launch_cache_extend(const CacheParams &c, const CachePlan &w, const int *seqs, const int *counts, int n,
                                 cudaStream_t s);
@@ -249,6 +284,7 @@ struct BwdParams {
     Sched sched_q;      // items over query blocks (dq)
     int *status;
     long long watchdog_cycles;
+    int window, sinks;  // sliding window (window.h); window 0: none
 };
 
 // Schedule preparation: validates cu_seqlens on the device and writes the

@@ -43,5 +43,7 @@ size_t x3_split_bytes(int n_q, int n_k, int H, int Hkv);
 cudaError_t launch_fwd_x3(const FwdParams &p, int num_ctas, cudaStream_t s);
 cudaError_t launch_bwd_dkdv_tc(const BwdParams &p, int num_ctas, cudaStream_t s);
 cudaError_t launch_bwd_dq_tc(const BwdParams &p, int num_ctas, cudaStream_t s);
+// those of a window (bwd_tc_window.cu), which the two above call
+cudaError_t launch_bwd_window(const BwdParams &p, int num_ctas, cudaStream_t s, bool dkdv);
 
 }  // namespace attn

@@ -14,16 +14,22 @@
 // types use mma.sync m16n8k16: with 16 query rows the contraction does 16
 // operations per cached byte, far below what even that path sustains beside the
 // HBM rate, and its row granularity fits a group's few rows, where tcgen05 tiles
-// would be 128 rows high (entries of more rows go to group_tc.cu).  f32 caches use
+// would be 128 rows high (entries of more rows go to group_tc.cuh).  f32 caches use
 // FFMA, one key per lane.
 //
 // Bound: HBM, the cache rows of every sequence read once.  Rows past L are
 // zero-filled by cp.async and never read from memory, so stale slots (NaN
 // included) do not matter.
+//
+// kWindow: a sliding window with sinks (window.h).  An entry's key tiles are those that hold
+// a sink and those from the first new token's window on, the same for all its units (its
+// new tokens are few here; a chunk of T reads T keys more than its last row needs).
 #include "../../include/attn.h"
 #include <type_traits>
 
+#include "mma.cuh"
 #include "stretch.cuh"
+#include "window.h"
 
 namespace attn {
 
@@ -71,20 +77,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (sizeof(T) == 2) {
-        if constexpr (std::is_same<T, __nv_bfloat16>::value)
-            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-        else
-            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-}
-
-template <typename T>
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
         __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -100,9 +92,11 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 struct Entry {
     int s, L, T, q0;   // sequence, cached tokens, new tokens, first query row
     int row_tiles, key_tiles;
+    TileList list;     // the key tiles
     long long tiles;   // of all its units
 };
 
+template <bool kWindow>
 __device__ __forceinline__ Entry entry_at(const TreeParams &p, int i, int rows, int keys, bool report) {
     Entry e;
     e.q0 = p.cu[i];
@@ -118,6 +112,12 @@ __device__ __forceinline__ Entry entry_at(const TreeParams &p, int i, int rows, 
     }
     e.row_tiles = (e.T * p.group + rows - 1) / rows;
     e.key_tiles = (e.L + keys - 1) / keys;
+    e.list = {0, 0};
+    if (kWindow && e.T > 0) {
+        // (a row of a tree may see none of the new tokens)
+        e.list = tile_list(p.window, p.sinks, e.L - e.T + (p.mask ? 0 : 1), keys);
+        e.key_tiles -= e.list.skip;
+    }
     e.tiles = (long long)p.c.H * e.row_tiles * e.key_tiles;
     return e;
 }
@@ -137,7 +137,7 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int token, int he
     store4(static_cast<Tout *>(p.o) + token * p.o_st + head * p.o_sh + d, v);
 }
 
-template <typename T, typename Tout, int D>
+template <typename T, typename Tout, int D, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     using C = Cfg<T, D>;
     constexpr int kRows = C::kRows, kKeys = C::kKeys;
@@ -148,12 +148,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t *ring = smem + warp * C::kStages * 2 * C::kTileBytes;
     const uint32_t ring_a = smem_addr(ring);
+    __shared__ RowWindow s_window[kWindow ? kRows : 1];  // of the unit's rows
     pdl_trigger();
     pdl_wait();
 
     Stretch st;
     const bool any = find_stretch<kWarps, 0>(
-        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at(p, i, kRows, kKeys, report).tiles}; }, st);
+        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at<kWindow>(p, i, kRows, kKeys, report).tiles}; }, st);
     if (!any) {
         if (tid == 0) p.parts.cut[blockIdx.x].last = -1;
         return;
@@ -161,12 +162,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     long long at = st.at, before = st.before;
     const long long end = st.end;
     int ei = st.entry;
-    Entry e = entry_at(p, ei, kRows, kKeys, false);
+    Entry e = entry_at<kWindow>(p, ei, kRows, kKeys, false);
 
     while (at < end) {
         while (at >= before + e.tiles) {  // past this entry's units (empty entries too)
             before += e.tiles;
-            e = entry_at(p, ++ei, kRows, kKeys, false);
+            e = entry_at<kWindow>(p, ++ei, kRows, kKeys, false);
         }
         // the unit that tile `at` lies in, and the stretch's part [t0, t1) of its key tiles
         const int unit = (int)((at - before) / e.key_tiles);
@@ -194,16 +195,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
             *reinterpret_cast<uint4 *>(sQ + r * C::kRowBytes + 16 * (ch ^ (r & 7))) = v;
         }
 
+        if (kWindow && tid < kRows) {
+            const int t = min((row0 + tid) / p.group, e.T - 1);
+            s_window[tid] = p.mask ? tree_window(p.mask + (int64_t)(e.q0 + t) * p.mask_words, e.T, ctx, p.window, p.sinks)
+                                   : RowWindow{ctx + t + 1 - p.window, p.sinks};
+        }
+        // whether some row of the entry does not see every key of a tile before the new tokens
+        auto outside = [&](int key0) { return key0 < ctx + e.T - p.window && key0 + kKeys > p.sinks; };
+        auto hidden = [&](int row, int key) { return key < s_window[row].lo && key >= s_window[row].hi; };
+        auto key_of = [&](int tile) { return (kWindow ? e.list.at(tile) : tile) * kKeys; };
+
         // this warp's tiles: t0 + warp, t0 + warp + kWarps, ...
         const int *table = p.c.table + (int64_t)e.s * p.c.table_stride;
         const int page_mask = (1 << p.c.page_shift) - 1;
         const char *kh = p.c.k + hk * p.c.b_head, *vh = p.c.v + hk * p.c.b_head;
         auto page_at = [&](int tile) -> int {  // the page of this lane's key of the tile
-            const int key = tile * kKeys + lane;
+            const int key = key_of(tile) + lane;
             return lane < kKeys && tile < t1 && key < e.L ? table[key >> p.c.page_shift] : -1;
         };
         auto load = [&](int tile, int page, int stage) {
-            const int key = tile * kKeys + lane;
+            const int key = key_of(tile) + lane;
             const bool live = (unsigned)page < (unsigned)p.c.n_pages;
             if (!live && lane < kKeys && tile < t1 && key < e.L) report_status(p.c.status, ATTN_EINVAL);
             const long long off = live ? page * p.c.b_page + (key & page_mask) * p.c.b_tok : -1;
@@ -268,8 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
                 page = page_at(next);
             }
             const uint32_t k_a = ring_a + stage * 2 * C::kTileBytes, v_a = k_a + C::kTileBytes;
-            const int key0 = tile * kKeys;
-            const bool masked = key0 + kKeys > ctx;  // the tile reaches the new tokens or the end
+            const int key0 = key_of(tile);
+            // the tile reaches the new tokens or the end
+            const bool masked = key0 + kKeys > ctx || (kWindow && outside(key0));
             if constexpr (kMma) {
                 float sc[kKeys / 8][4];
 #pragma unroll
@@ -301,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const int key = key0 + 8 * j + 2 * (lane & 3) + k;
-                                if (key >= e.L || !sees(p, e, t, key - ctx)) sc[j][2 * hf + k] = -INFINITY;
+                                if (key >= e.L || !sees(p, e, t, key - ctx) || (kWindow && hidden(8 * hf + (lane >> 2), key)))
+                                    sc[j][2 * hf + k] = -INFINITY;
                             }
                     }
                 }
@@ -372,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
                     const int t = min((row0 + r) / p.group, e.T - 1);
                     float x = sc[r] * p.scale_log2;
                     if (lane >= kKeys) x = -INFINITY;  // (lanes without a key)
-                    if (masked && lane < kKeys && (key >= e.L || !sees(p, e, t, key - ctx))) x = -INFINITY;
+                    if (masked && lane < kKeys && (key >= e.L || !sees(p, e, t, key - ctx) || (kWindow && hidden(r, key))))
+                        x = -INFINITY;
                     float mx = x;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -470,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
 template <typename T, typename Tout, int D>
 cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
     using C = Cfg<T, D>;
-    auto kern = tree_kernel<T, Tout, D>;
+    auto kern = p.window ? tree_kernel<T, Tout, D, true> : tree_kernel<T, Tout, D, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int blocks = tree_blocks();
@@ -534,7 +548,9 @@ cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s) {
         g.parts = p.parts;
         g.status = p.c.status;
         g.watchdog_cycles = p.watchdog_cycles;
-        return launch_group(g, s);
+        g.window = p.window;
+        g.sinks = p.sinks;
+        return p.window ? launch_group_window(g, s) : launch_group(g, s);
     }
     switch (p.dtype) {
     case ATTN_F16: return launch_out<__half>(p, s);

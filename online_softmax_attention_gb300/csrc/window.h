@@ -1,0 +1,79 @@
+// Sliding windows with sinks: of the keys that a query would see without a window, in
+// order, it sees the first `sinks` and the last `window`.  Plain functions of their
+// arguments, compiled for the host too.
+//
+// A run of query rows scans the key tiles that hold a sink and those from its first row's
+// window on.  That list has one gap at most, so its j-th tile is j or, behind the
+// gap, j + skip.
+#pragma once
+
+#include "hd.h"
+#include "line.h"
+
+namespace attn {
+
+struct TileList {
+    int sinks;  // tiles before the gap
+    int skip;   // tiles that the gap leaves out
+    ATTN_HD int at(int j) const { return j < sinks ? j : j + skip; }
+};
+
+// The list in tiles of `tile` keys: `seen` >= 0 is the least number of keys that one of the
+// rows would see without a window, whose window begins at key seen - window.
+ATTN_HD TileList tile_list(int window, int sinks, int seen, int tile) {
+    const int first = seen > window ? (seen - window) / tile : 0;
+    const int held = sinks / tile + (sinks % tile != 0);
+    return held < first ? TileList{held, first - held} : TileList{first, 0};
+}
+
+// Key tiles of 128 that the gaps of the first n units leave out, of an entry whose tokens
+// each see those up to themselves: unit i begins at token i per, before which ctx keys stand.
+// sum over i < n of max(0, floor((ctx + i per + 1 - window) / 128) - tiles of the sinks)
+ATTN_HD long long skipped_tiles(int window, int sinks, int ctx, int per, int n) {
+    const long long held = sinks / 128 + (sinks % 128 != 0);
+    const long long b = (long long)ctx + 1 - window - 128 * held;  // of unit 0; the first terms may be below 0
+    const long long i0 = b >= 0 ? 0 : (per - 1 - b) / per;
+    return i0 < n ? floor_sum((int)(n - i0), per, (int)(b + i0 * per)) : 0;
+}
+
+// The keys that a row of a tree sees: below `hi`, or from `lo` on, of the ctx keys before the
+// new tokens and the new tokens u < T whose bits are set in `mask`.
+struct RowWindow {
+    int lo, hi;
+};
+
+#if defined(__CUDA_ARCH__)
+#define ATTN_POPC(x) __popcll(x)
+#else
+#define ATTN_POPC(x) __builtin_popcountll(x)
+#endif
+
+ATTN_HD RowWindow tree_window(const unsigned long long *mask, int T, int ctx, int window, int sinks) {
+    const int words = (T + 63) / 64;
+    auto word = [&](int w) -> unsigned long long {  // bits from T on do not exist
+        return w == words - 1 && (T & 63) ? mask[w] & ((1ull << (T & 63)) - 1) : mask[w];
+    };
+    int drafts = 0;  // that the row sees
+    for (int w = 0; w < words; ++w) drafts += ATTN_POPC(word(w));
+    // behind the nth of the row's drafts, 0 <= n <= drafts (its first one: n = 0)
+    auto behind = [&](int n) -> int {
+        for (int w = 0; w < words; ++w) {
+            unsigned long long x = word(w);
+            const int c = ATTN_POPC(x);
+            if (n <= c && n > 0) {
+                for (; n > 1; --n) x &= x - 1;
+                return 64 * w + ATTN_POPC((x & -x) - 1) + 1;
+            }
+            n -= c;
+        }
+        return 0;
+    };
+    RowWindow r;
+    if (drafts >= window) r.lo = ctx + behind(drafts - window);
+    else r.lo = ctx > window - drafts ? ctx - (window - drafts) : 0;
+    if (sinks <= ctx) r.hi = sinks;
+    else r.hi = sinks - ctx >= drafts ? ctx + T : ctx + behind(sinks - ctx);
+    return r;
+}
+
+}  // namespace attn
