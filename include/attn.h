@@ -365,8 +365,8 @@ typedef struct attn_tree_args {
  * h) that see j: those of attn_tree_fwd without a mask, whose lse this takes.  The sum is
  * taken in f32 in a fixed order.  A row with an lse of -inf (it saw nothing) adds nothing.
  * Entries from w[L] on are left as they are.  An entry that does not fit (as in
- * attn_tree_args; L > cols; fresh not in [0, L]) or whose sequence is listed more than
- * once is left out and reported as ATTN_EINVAL. */
+ * attn_tree_args; L > cols; fresh not in [0, L]) is left out, and a list that has a
+ * sequence more than once as a whole; both are reported as ATTN_EINVAL. */
 typedef struct attn_weigh_args {
     attn_cache cache;       /* k of the layer is read; H_kv divides H; dtype also of q */
     int32_t layer;

@@ -588,11 +588,11 @@ int plan_weigh(const attn_weigh_args *a, WeighParams &p) {
 size_t evict_plan(int n, int cols, void *workspace, EvictParams &p) {
     const size_t list = align256(sizeof(int) * ((size_t)n + 1)), rows = align256(sizeof(int) * (size_t)n * (size_t)cols);
     char *at = static_cast<char *>(workspace);
-    p.hdr = reinterpret_cast<int *>(at);
-    p.len = reinterpret_cast<int *>(at + 256);
-    p.first = reinterpret_cast<int *>(at + 256 + list);
-    p.source = reinterpret_cast<int *>(at + 256 + 2 * list);
-    return 256 + 2 * list + rows;
+    p.good = reinterpret_cast<int *>(at);
+    p.len = reinterpret_cast<int *>(at + list);
+    p.first = reinterpret_cast<int *>(at + 2 * list);
+    p.source = reinterpret_cast<int *>(at + 3 * list);
+    return 3 * list + rows;
 }
 
 int build_cache(const attn_cache *c, int n, void *workspace, size_t workspace_bytes, CacheParams &p, CachePlan &w) {

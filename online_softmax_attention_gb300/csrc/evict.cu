@@ -1,22 +1,24 @@
 // Eviction from the cache by accumulated attention weight (attn_cache_evict).
 //
-// Three kernels, the later ones launched dependently.  The check of the list (one block); a
-// block an entry that chooses the kept tokens; and the kernel that moves the kept rows, in all
-// layers, and their weights, and releases the pages behind.  The list is done as a whole or not
-// at all: what the first two find wrong clears hdr[0], and the third then changes nothing.
+// Two kernels.  A block an entry checks it and chooses the kept tokens; the other kernel, launched
+// dependently, moves the kept rows, in all layers, and their weights, and releases the pages
+// behind.  The list is done as a whole or not at all: every entry leaves a mark, and the
+// second kernel does nothing unless all of them are good.
 //
 // Choice.  A token's weight, summed over the layers in f64 and rounded to f32, becomes a whole
-// number in the same order; four passes over 8 bits each, a histogram a pass, find the
+// number in the same order; three passes over 11, 11 and 10 bits, a histogram a pass, find the
 // smallest number that is kept and how many of the tokens that have it are (the first ones).
-// A scan in token order then numbers the kept ones.  Every result is a function of the inputs.
+// A thread then numbers a run of tokens, behind two scans over the block.  Every result is a
+// function of the inputs.
 //
-// Move.  Kept token number j comes from source[j] >= j, ascending.  A block owns 512 bytes of
-// every row (32 columns of 16 bytes, one a lane) of a layer of k or v, and takes batches of
-// rows, one a warp and pass: all of a batch's rows are loaded before any is stored (a
-// barrier), and the next batch's are loaded ahead of the stores, which cannot meet
-// them: its sources lie at or behind its own places, which follow this batch's.
+// Move.  Kept token number j comes from source[j] >= j, ascending.  A cluster of 8 blocks owns up
+// to 512 bytes of every row of a layer of k or v, and moves 512 rows and more at a time:
+// all of a batch's rows are in shared memory before any is stored (a barrier over the
+// cluster), and the next batch's loads are in flight meanwhile, which the stores cannot meet:
+// their sources lie at or behind their own places, which follow this batch's.  So a sequence's
+// rows move in place, many at once, without a copy.
 //
-// Bound: HBM, the moved rows read and written once; few rows: the chain of batches.
+// Bound: HBM, the moved rows read and written once; few rows: the chain of the two kernels.
 #include "../../include/attn.h"
 #include "common.cuh"
 #include "pages.h"
@@ -33,32 +35,6 @@ __device__ __forceinline__ bool in_range(int x, int n) { return (unsigned)x < (u
 
 __device__ __forceinline__ int table_at(const CacheParams &c, int s, int slot) {
     return c.table[(int64_t)s * c.table_stride + slot];
-}
-
-__global__ void __launch_bounds__(kPlanThreads) evict_check_kernel(const CacheParams c, const EvictParams p) {
-    __shared__ uint32_t seen[ATTN_CACHE_MAX_SEQS / 32];
-    pdl_trigger();
-    pdl_wait();
-    for (int i = threadIdx.x; i < (c.max_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
-        const int s = p.seqs[i], budget = p.budgets[i];
-        if (!in_range(s, c.max_seqs) || budget < 0) {
-            bad = true;
-            continue;
-        }
-        const uint32_t bit = 1u << (s & 31);
-        const int len = c.lens[s];
-        bad = bad || (atomicOr(&seen[s >> 5], bit) & bit) || !length_fits(len, c.max_pages, c.page_shift) || len > p.cols ||
-              (len > budget && (long long)p.sinks + p.recent > budget);
-        p.len[i] = len;
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        p.hdr[0] = !bad;
-        if (bad) report_status(c.status, ATTN_EINVAL);
-    }
 }
 
 // A weight as a whole number in the same order: NaN below everything, -0 as 0.
@@ -90,62 +66,68 @@ __device__ __forceinline__ int block_prefix(int x, int *s_warp, int &total) {
     return before + y - x;
 }
 
+// The number of digit places of the passes, and the bits below a pass's digit.
+constexpr int kBins = 2048;
+
 __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheParams c, const EvictParams p) {
     extern __shared__ uint32_t held[];
-    __shared__ int bins[256], s_warp[32], s_first, s_digit, s_above;
+    __shared__ int bins[kBins], s_warp[32], s_first, s_digit, s_above;
     pdl_trigger();
     pdl_wait();
-    // (read by one thread: another block may clear it meanwhile, and nothing of this is used then)
-    if (__syncthreads_or(threadIdx.x == 0 && !p.hdr[0])) return;
-    const int i = blockIdx.x, tid = threadIdx.x, s = p.seqs[i], budget = p.budgets[i], len = p.len[i];
-    if (len <= budget) return;
+    const int i = blockIdx.x, tid = threadIdx.x, s = p.seqs[i], budget = p.budgets[i];
+    bool bad = !in_range(s, c.max_seqs) || budget < 0;
+    const int len = bad ? 0 : c.lens[s];
+    bad = bad || !length_fits(len, c.max_pages, c.page_shift) || len > p.cols ||
+          (len > budget && (long long)p.sinks + p.recent > budget);
+    for (int j = tid; j < p.n; j += kPlanThreads) bad = bad || (j != i && p.seqs[j] == s);
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        p.good[i] = !bad;
+        p.len[i] = len;
+        s_first = len;
+        if (bad) report_status(c.status, ATTN_EINVAL);
+    }
+    if (bad || len <= budget) return;
     const int sinks = p.sinks, last = len - p.recent;  // the tokens [sinks, last) are chosen from
     const int want = budget - sinks - p.recent, n = last - sinks;
     const float *w = p.weights + (int64_t)s * p.w_seq + sinks;
     auto sum_of = [&](int t) {
         double x = w[t];
+#pragma unroll 8
         for (int y = 1; y < p.w_layers; ++y) x += (double)w[(int64_t)y * p.w_layer + t];
         return order_of((float)x);
     };
     const bool keep = n <= kHeld;
-    if (keep)
-        for (int t = tid; t < n; t += kPlanThreads) held[t] = sum_of(t);
     auto number_of = [&](int t) { return keep ? held[t] : sum_of(t); };
-    if (tid == 0) s_first = len;
 
     // the smallest number that is kept: its digits from the top; `left` of those that share them so far
     uint32_t found = 0;
     int left = want;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-        if (tid < 256) bins[tid] = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && want > 0; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 0 : pass == 1 ? 21 : 10;
+        for (int b = tid; b < kBins; b += kPlanThreads) bins[b] = 0;
         __syncthreads();
-        for (int t0 = 0; t0 < n; t0 += kPlanThreads) {
-            const int t = t0 + tid;
-            const uint32_t x = t < n ? number_of(t) : 0u;
-            const bool in = t < n && (shift == 24 || (x >> (shift + 8)) == (found >> (shift + 8)));
-            // equal digits of a warp are counted together: weights of the same size share them
-            const uint32_t digit = (x >> shift) & 255u;
-            const uint32_t same = __match_any_sync(0xffffffffu, in ? digit : 256u);
-            if (in && (tid & 31) == __ffs(same) - 1) atomicAdd(&bins[digit], __popc(same));
+        for (int t = tid; t < n; t += kPlanThreads) {
+            uint32_t x;
+            if (pass == 0) {
+                x = sum_of(t);
+                if (keep) held[t] = x;
+            } else {
+                x = number_of(t);
+                if (x >> above != found >> above) continue;
+            }
+            atomicAdd(&bins[(x >> shift) & (pass == 2 ? 1023u : 2047u)], 1);
         }
         __syncthreads();
-        if (tid < 32) {  // the largest digit with at least `left` numbers from it on; lane l has digits 8 l ..
-            int mine = 0;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) mine += bins[8 * tid + b];
-            int from = mine;  // of this lane's digits and larger ones
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_down_sync(0xffffffffu, from, o);
-                if (tid + o < 32) from += y;
-            }
-            int above = from - mine;
-            if (above < left && from >= left) {
-                int b = 7;
-                while (above + bins[8 * tid + b] < left) above += bins[8 * tid + b--];
-                s_digit = 8 * tid + b;
-                s_above = above;
-            }
+        // the largest digit with at least `left` numbers from it on; a thread has two digits, the largest first
+        const int hi = kBins - 1 - 2 * tid, at_hi = bins[hi], mine = at_hi + bins[hi - 1];
+        int all;
+        const int before = block_prefix(mine, s_warp, all);
+        if (before < left && before + mine >= left) {
+            const bool first = before + at_hi >= left;
+            s_digit = first ? hi : hi - 1;
+            s_above = first ? before : before + at_hi;
         }
         __syncthreads();
         found |= (uint32_t)s_digit << shift;
@@ -153,116 +135,135 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
         __syncthreads();
     }
 
-    // number the kept ones in order
+    // number the kept ones in order, a run of tokens a thread (an odd run: its words lie in other banks)
     int *source = p.source + (int64_t)i * p.cols;
-    int kept = 0, equal = 0;  // before the tokens of this pass
-    int first = len;          // token that goes
-    for (int t0 = 0; t0 < len; t0 += kPlanThreads) {
-        const int t = t0 + tid;
-        const bool chosen = t >= sinks && t < last;
-        const uint32_t x = chosen && want > 0 ? number_of(t - sinks) : 0u;
-        const bool tie = chosen && want > 0 && x == found;
-        int ties;
-        const int rank = equal + block_prefix(tie, s_warp, ties);
-        equal += ties;
-        const bool stays = t < len && (!chosen || (want > 0 && (x > found || (tie && rank < left))));
-        int count;
-        const int to = kept + block_prefix(stays, s_warp, count);
-        kept += count;
-        if (stays) source[to] = t;
-        else if (t < len) first = min(first, t);
-    }
-    atomicMin(&s_first, first);
-    __syncthreads();
-    first = s_first;
-    if (tid == 0) p.first[i] = min(first, budget);
-    // every page from the first row that moves on exists, and those that rows move into are the sequence's own
-    bool bad = false;
-    if (first < budget) {
-        const int end = pages_of(budget, c.page_shift);
-        for (int k = (first >> c.page_shift) + tid; k < end; k += kPlanThreads) {
-            const int page = table_at(c, s, k);
-            bad = bad || !in_range(page, c.n_pages) || c.refs[page] > 1;
+    for (int t = tid; t < sinks; t += kPlanThreads) source[t] = t;
+    for (int t = tid; t < p.recent; t += kPlanThreads) source[budget - p.recent + t] = last + t;
+    const int run = ((n + kPlanThreads - 1) / kPlanThreads) | 1, t0 = min(n, tid * run), t1 = min(n, t0 + run);
+    int more = 0, equal = 0;
+    if (want > 0)
+        for (int t = t0; t < t1; ++t) {
+            const uint32_t x = number_of(t);
+            more += x > found;
+            equal += x == found;
+        }
+    int all;
+    const int ties = max(0, min(equal, left - block_prefix(equal, s_warp, all)));  // of this run that are kept
+    int to = sinks + block_prefix(more + ties, s_warp, all), taken = 0, first = len;
+    for (int t = t0; t < t1; ++t) {
+        const uint32_t x = want > 0 ? number_of(t) : 0u;
+        if (want > 0 && (x > found || (x == found && taken < ties))) {
+            taken += x == found;
+            source[to++] = sinks + t;
+        } else {
+            first = min(first, sinks + t);
         }
     }
-    for (int k = (min(first, budget) >> c.page_shift) + tid; k < pages_of(len, c.page_shift); k += kPlanThreads)
-        bad = bad || !in_range(table_at(c, s, k), c.n_pages);
+    if (first < len) atomicMin(&s_first, first);
+    __syncthreads();
+    first = min(s_first, budget);
+    if (tid == 0) p.first[i] = first;
+    // every page from the first row that moves on exists, and those that rows move into are the sequence's own
+    const int end = first < budget ? pages_of(budget, c.page_shift) : 0;
+    for (int k = (first >> c.page_shift) + tid; k < pages_of(len, c.page_shift); k += kPlanThreads) {
+        const int page = table_at(c, s, k);
+        bad = bad || !in_range(page, c.n_pages) || (k < end && c.refs[page] > 1);
+    }
     if (__syncthreads_or(bad) && tid == 0) {
-        p.hdr[0] = 0;
+        p.good[i] = 0;
         report_status(c.status, ATTN_EINVAL);
     }
 }
 
-// Moves what a warp's lanes hold of rows [first, count) to their places; load(token), store(row, value).
-// kRows rows a warp and batch.
-template <int kRows, typename V, typename L, typename S>
-__device__ __forceinline__ void move_rows(const int *source, int first, int count, L load, S store) {
-    constexpr int kWarps = kMoveThreads / 32, kBatch = kRows * kWarps;
-    const int warp = threadIdx.x >> 5;
-    V now[kRows], next[kRows];
-    auto fetch = [&](int j0, V (&v)[kRows]) {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int j = j0 + r * kWarps + warp;
-            if (j < count) v[r] = load(source[j]);
-        }
-    };
-    fetch(first, now);
-    for (int j0 = first; j0 < count; j0 += kBatch) {
-        __syncthreads();  // every warp has its rows of this batch
-        fetch(j0 + kBatch, next);
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int j = j0 + r * kWarps + warp;
-            if (j < count) store(j, now[r]);
-            now[r] = next[r];
-        }
-    }
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Block (i, y): entry i; y walks the 512-byte columns of the layers of k and v, then the layers of weights.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CacheParams c, const EvictParams p) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Cluster (i, y): entry i; y walks the strips of the layers of k and v, then the layers of weights.
+constexpr int kCluster = 8;
+constexpr int kMoveRows = 8;  // of a warp and batch, in instructions of 32 chunks of 16 bytes
+constexpr int kMoveWarps = kMoveThreads / 32;
+constexpr int kMoveBytes = kMoveWarps * kMoveRows * 512;  // of a batch
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const CacheParams c, const EvictParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
     pdl_trigger();
     pdl_wait();
-    if (!p.hdr[0]) return;
-    const int i = blockIdx.x, lane = threadIdx.x & 31, s = p.seqs[i], count = p.budgets[i], len = p.len[i];
-    if (len <= count) return;
+    bool good = true;
+    for (int j = threadIdx.x; j < p.n; j += kMoveThreads) good = good && p.good[j];
+    if (!__syncthreads_and(good)) return;
+    const int i = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = p.seqs[i], count = p.budgets[i], len = p.len[i];
+    if (len <= count) return;  // (the whole cluster)
     const int first = p.first[i];
     const int *source = p.source + (int64_t)i * p.cols;
     const int per_row = c.row_bytes >> 4, per_tok = c.H * per_row, strips = (per_tok + 31) / 32;
     const int mask = (1 << c.page_shift) - 1, pools = 2 * c.n_layers * strips;
+    // rows of fewer than 32 chunks: several an instruction
+    const int width = min(32, per_tok), sub = 32 / width, mine = lane / width, chunk = lane - mine * width;
+    const int rows = kMoveRows * sub, step = kCluster * kMoveWarps * rows;  // of a warp; of the cluster's batch
+    const int warp0 = (rank * kMoveWarps + warp) * rows;
+    const uint32_t buffers = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+    auto offset = [&](int t) -> long long {
+        return table_at(c, s, t >> c.page_shift) * c.b_page + (t & mask) * c.b_tok;
+    };
     for (int y = blockIdx.y; y < pools + p.w_layers; y += gridDim.y) {
         if (y < pools) {
-            const int layer = y / (2 * strips), rest = y - layer * 2 * strips, x = (rest >> 1) * 32 + lane, h = x / per_row;
+            const int layer = y / (2 * strips), rest = y - layer * 2 * strips, x = (rest >> 1) * 32 + chunk, h = x / per_row;
             char *col = (rest & 1 ? c.v : c.k) + layer * c.b_layer + h * c.b_head + 16 * (x - h * per_row);
-            const bool mine = x < per_tok;
-            auto row = [&](int t) {
-                return reinterpret_cast<uint4 *>(col + table_at(c, s, t >> c.page_shift) * c.b_page + (t & mask) * c.b_tok);
+            const bool live = mine < sub && x < per_tok;
+            auto load = [&](int j0, int buffer) {  // the batch that begins at row j0
+                const int j = j0 + warp0 + lane;   // lane r has the warp's row r
+                const long long from = lane < rows && j < count ? offset(source[j]) : 0;
+#pragma unroll
+                for (int r = 0; r < kMoveRows; ++r) {
+                    const int k = r * sub + mine;
+                    const long long o = __shfl_sync(0xffffffffu, from, k & 31);
+                    if (live && j0 + warp0 + k < count)
+                        cp_async16(buffers + buffer * kMoveBytes + r * kMoveThreads * 16, col + o);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            move_rows<8, uint4>(
-                source, first, count, [&](int t) { return mine ? *row(t) : make_uint4(0, 0, 0, 0); },
-                [&](int j, uint4 v) { if (mine) *row(j) = v; });
+            int buffer = 0;
+            load(first, 0);
+            for (int j0 = first; j0 < count; j0 += step) {
+                const int j = j0 + warp0 + lane;
+                const long long to = lane < rows && j < count ? offset(j) : 0;
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                cluster_barrier();  // the batch is in shared memory
+                if (j0 + step < count) load(j0 + step, buffer ^ 1);
+#pragma unroll
+                for (int r = 0; r < kMoveRows; ++r) {
+                    const int k = r * sub + mine;
+                    const long long o = __shfl_sync(0xffffffffu, to, k & 31);
+                    if (live && j0 + warp0 + k < count)
+                        *reinterpret_cast<uint4 *>(col + o) =
+                            *reinterpret_cast<const uint4 *>(smem + buffer * kMoveBytes + (r * kMoveThreads + threadIdx.x) * 16);
+                }
+                buffer ^= 1;
+            }
         } else {
-            // a token a thread: warps take 32 tokens at a time
             float *w = p.weights + (int64_t)(y - pools) * p.w_layer + (int64_t)s * p.w_seq;
-            for (int j0 = first; j0 < count; j0 += kMoveThreads * 4) {
-                float v[4];
+            constexpr int kTokens = 8, kStep = kCluster * kMoveThreads;
+            for (int j0 = first + rank * kMoveThreads + threadIdx.x; j0 - rank * kMoveThreads - (int)threadIdx.x < count;
+                 j0 += kTokens * kStep) {
+                float v[kTokens];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = j0 + r * kMoveThreads + threadIdx.x;
-                    if (j < count) v[r] = w[source[j]];
-                }
-                __syncthreads();
+                for (int r = 0; r < kTokens; ++r)
+                    if (j0 + r * kStep < count) v[r] = w[source[j0 + r * kStep]];
+                cluster_barrier();
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = j0 + r * kMoveThreads + threadIdx.x;
-                    if (j < count) w[j] = v[r];
-                }
-                __syncthreads();
+                for (int r = 0; r < kTokens; ++r)
+                    if (j0 + r * kStep < count) w[j0 + r * kStep] = v[r];
             }
         }
     }
-    if (blockIdx.y == 0) {  // the pages behind the new end
+    if (blockIdx.y == 0 && rank == 0) {  // the pages behind the new end
         for (int k = pages_of(count, c.page_shift) + threadIdx.x; k < pages_of(len, c.page_shift); k += kMoveThreads) {
             const int page = table_at(c, s, k);
             if (atomicSub(&c.refs[page], 1) > 0) continue;
@@ -276,17 +277,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const CachePar
 }  // namespace
 
 cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaStream_t s) {
-    cudaError_t e = launch_pdl(evict_check_kernel, dim3(1), dim3(kPlanThreads), 0, s, c, p);
-    count_launch();
+    const int held = 4 * (p.cols < kHeld ? p.cols : kHeld);
+    cudaError_t e = cudaFuncSetAttribute(evict_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, held);
     if (e != cudaSuccess) return e;
-    const int smem = 4 * (p.cols < kHeld ? p.cols : kHeld);
-    e = cudaFuncSetAttribute(evict_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(evict_choose_kernel, dim3(p.n), dim3(kPlanThreads), smem, s, c, p);
+    e = launch_pdl(evict_choose_kernel, dim3(p.n), dim3(kPlanThreads), held, s, c, p);
     count_launch();
     if (e != cudaSuccess) return e;
     const int64_t per_tok = (int64_t)c.H * (c.row_bytes >> 4), columns = 2 * c.n_layers * ((per_tok + 31) / 32) + p.w_layers;
-    e = launch_pdl(evict_move_kernel, dim3(p.n, (unsigned)(columns < 65535 ? columns : 65535)), dim3(kMoveThreads), 0, s, c, p);
+    e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kMoveBytes);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(evict_move_kernel, dim3(kCluster * p.n, (unsigned)(columns < 65535 ? columns : 65535)), dim3(kMoveThreads),
+                   2 * kMoveBytes, s, c, p);
     count_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -240,9 +240,9 @@ struct EvictParams {
     int sinks, recent;
     const int *seqs, *budgets;
     int n;
-    int *hdr;     // [0] 1: carry out, 0: refused
+    int *good;    // n: whether the entry can be carried out
     int *len;     // n: length before the call
-    int *first;   // n: tokens that stay where they are, before the first that goes
+    int *first;   // n, of those that are cut: tokens that stay where they are, before the first that goes
     int *source;  // (n, cols): the kept tokens, in order
 };
 cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaStream_t s);

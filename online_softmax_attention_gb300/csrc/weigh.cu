@@ -3,16 +3,18 @@
 // exp(scale <q_th, k_j> - lse_th), where t sees j.  The rows' lse is known, so there is no
 // running maximum, values are not read, and nothing is joined between blocks.
 //
-// Decomposition.  A unit is a run of keys of one entry with all its heads and rows, so that
-// one block has a token's whole sum: no atomics, a fixed order.  Its warps share the
-// (32 keys, key head) pairs; a warp holds its 32 K rows in registers, as the A operand of
-// mma.sync m16n8k16 (rows = keys), while the group's query rows pass as the B operand, eight
-// at a time.  The order of the contraction over D is free, so both operands are loaded
-// straight from memory, 16 bytes a lane: the quarter-warp's lanes c hold elements
-// [32 i + 8 c, + 8) of a row as the operands' columns (2 c, 2 c + 1, 2 c + 8, 2 c + 9) of
-// two steps.  Nothing is staged in shared memory.  Every lane sums exponentials of four
-// keys over its columns; lanes and warps are joined once a unit.  Blocks take equal
-// stretches of all units (stretch.cuh).  f32 caches use FFMA, a key a lane.
+// Decomposition.  A unit is 32 keys of one entry with all its heads and rows, and one warp has
+// all of it, so that a token's sum is in one place: no atomics, no joining, a fixed order.
+// Blocks take equal stretches of all units (stretch.cuh), their warps a unit each in turn.
+//
+// 16-bit caches.  A warp's K rows, a key head at a time, come through a ring of cp.async stages
+// of its own.  They are the A operand of mma.sync m16n8k16 (rows = keys), held in registers while
+// the group's query rows pass as the B operand, eight at a time.  The order of the
+// contraction over D is free, so both operands are read 16 bytes a lane: the quarter-warp's
+// lanes c hold elements [32 i + 8 c, + 8) of a row as the operands' columns (2 c, 2 c + 1,
+// 2 c + 8, 2 c + 9) of two steps; queries come straight from the L1.  Every lane sums
+// exponentials of four keys over its columns, and lanes are joined once a unit.  f32 caches use
+// FFMA, a key a lane.
 //
 // Bound: HBM, the K rows read once, for few rows; the mma.sync rate for many.
 #include "../../include/attn.h"
@@ -26,26 +28,34 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kKeys = 32;   // of a warp
-constexpr int kRows = 8;    // query rows at a time
+constexpr int kKeys = 32;  // of a unit
+constexpr int kRows = 8;   // query rows at a time
+
+template <typename T, int D>
+struct Cfg {
+    static constexpr bool kMma = sizeof(T) == 2;
+    static constexpr int kRowBytes = D * (int)sizeof(T);
+    static constexpr int kTileBytes = kKeys * kRowBytes;
+    // stages of a warp's ring: 24 KiB a warp keeps 128 KiB of loads in flight per SM
+    static constexpr int kStages = kMma ? 24 * 1024 / kTileBytes : 0;
+    static constexpr int kRingBytes = kWarps * kStages * kTileBytes;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
 
 struct Entry {
     int s, L, T, q0, fresh;
-    int units;  // runs of `keys` tokens
+    int units;  // runs of kKeys tokens
 };
 
-// Bitmaps of the sequences that are listed, and that are listed more than once.
-struct Listed {
-    uint32_t *once, *twice;
-};
-
-__device__ __forceinline__ Entry entry_at(const WeighParams &p, const Listed &listed, int i, int keys, bool report) {
+__device__ __forceinline__ Entry entry_at(const WeighParams &p, int i, bool report) {
     Entry e;
     e.q0 = p.cu[i];
     e.T = p.cu[i + 1] - e.q0;
     e.s = p.seqs[i];
     bool ok = (unsigned)e.s < (unsigned)p.c.max_seqs && e.q0 >= 0 && e.q0 <= p.cu[i + 1] && p.cu[i + 1] <= p.n_q;
-    ok = ok && !((listed.twice[e.s >> 5] >> (e.s & 31)) & 1);
     e.L = ok ? p.c.lens[e.s] : 0;
     e.fresh = p.fresh ? p.fresh[i] : e.T;
     ok = ok && e.L >= e.T && e.L <= p.cols && (long long)e.L <= (long long)p.c.max_pages << p.c.page_shift &&
@@ -54,136 +64,217 @@ __device__ __forceinline__ Entry entry_at(const WeighParams &p, const Listed &li
         if (report) report_status(p.c.status, ATTN_EINVAL);
         e.L = 0;
     }
-    e.units = e.T > 0 || e.fresh > 0 ? (e.L + keys - 1) / keys : 0;
+    e.units = e.T > 0 || e.fresh > 0 ? (e.L + kKeys - 1) / kKeys : 0;
     return e;
 }
 
+// Where a warp is among the stretch's units.
+struct Cursor {
+    long long at, before;  // unit; units before the entry's
+    int ei;
+    Entry e;
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const WeighParams p) {
-    constexpr bool kMma = sizeof(T) == 2;
+__global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kernel(const WeighParams p) {
+    using C = Cfg<T, D>;
+    constexpr bool kMma = C::kMma;
     constexpr int kSteps = D / 32;  // 16-byte chunks of a row a lane
-    extern __shared__ uint32_t s_listed[];
-    __shared__ float s_sum[kWarps][kKeys];
+    extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     pdl_trigger();
     pdl_wait();
 
-    const int words = (p.c.max_seqs + 31) / 32;
-    const Listed listed{s_listed, s_listed + words};
-    for (int x = tid; x < 2 * words; x += kThreads) s_listed[x] = 0;
-    __syncthreads();
-    for (int i = tid; i < p.n; i += kThreads) {
-        const int s = p.seqs[i];
-        if ((unsigned)s >= (unsigned)p.c.max_seqs) continue;
-        const uint32_t bit = 1u << (s & 31);
-        if (atomicOr(&listed.once[s >> 5], bit) & bit) atomicOr(&listed.twice[s >> 5], bit);
+    // a list that has a sequence twice is refused: two warps would add to the same weights.  (The
+    // sequences' bits stand where the rings will.)
+    if (p.n > 1) {
+        uint32_t *seen = reinterpret_cast<uint32_t *>(smem);
+        for (int x = tid; x < (p.c.max_seqs + 31) / 32; x += kThreads) seen[x] = 0;
+        __syncthreads();
+        bool twice = false;
+        for (int i = tid; i < p.n; i += kThreads) {
+            const int s = p.seqs[i];
+            const uint32_t bit = 1u << (s & 31);
+            if ((unsigned)s < (unsigned)p.c.max_seqs) twice = twice || (atomicOr(&seen[s >> 5], bit) & bit);
+        }
+        if (__syncthreads_or(twice)) {
+            if (blockIdx.x == 0 && tid == 0) report_status(p.c.status, ATTN_EINVAL);
+            return;
+        }
     }
-    __syncthreads();
-
-    // few key heads: several runs of 32 keys a unit, so that every warp has a pair
-    const int subs = p.c.H >= kWarps ? 1 : kWarps / p.c.H, at_once = kWarps / subs;
-    const int sub = warp % subs, first_head = warp / subs, unit_keys = kKeys * subs;
     Stretch st;
     const bool any = find_stretch<kWarps, 0>(
-        p.n, 1, [&](int i, bool report) { return Work{0, entry_at(p, listed, i, unit_keys, report).units}; }, st);
+        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at(p, i, report).units}; }, st);
     if (!any) return;
-    long long before = st.before;
-    int ei = st.entry;
-    Entry e = entry_at(p, listed, ei, unit_keys, false);
-
-    for (long long at = st.at; at < st.end; ++at) {
-        while (at >= before + e.units) {
-            before += e.units;
-            e = entry_at(p, listed, ++ei, unit_keys, false);
+    Cursor now{st.at + warp, st.before, st.entry, entry_at(p, st.entry, false)};
+    // to the entry of unit cur.at, which is one of the stretch's
+    auto seek = [&](Cursor &cur) {
+        while (cur.at >= cur.before + cur.e.units) {
+            cur.before += cur.e.units;
+            cur.e = entry_at(p, ++cur.ei, false);
         }
-        const int unit0 = (int)(at - before) * unit_keys, key0 = unit0 + kKeys * sub;
-        const int ctx = e.L - e.T, rows = e.T * p.group;
-        // a run that every new token sees whole, or that none sees
-        const bool hidden = p.window && key0 + kKeys <= ctx + 1 - p.window && key0 >= p.sinks;
+    };
+    if (now.at >= st.end) return;
+    // a run that no new token sees
+    auto hidden = [&](const Entry &e, int key0) {
+        return p.window && key0 + kKeys <= e.L - e.T + 1 - p.window && key0 >= p.sinks;
+    };
+    // offset of this lane's key's row; -1: no such key, or none that is seen
+    auto row_of = [&](const Entry &e, int key0) -> long long {
+        const int key = key0 + lane;
+        if (key >= e.L || e.T == 0 || hidden(e, key0)) return -1;
+        const int page = p.c.table[(int64_t)e.s * p.c.table_stride + (key >> p.c.page_shift)];
+        if ((unsigned)page < (unsigned)p.c.n_pages)
+            return page * p.c.b_page + (key & ((1 << p.c.page_shift) - 1)) * p.c.b_tok;
+        report_status(p.c.status, ATTN_EINVAL);
+        return -1;
+    };
+
+    // the ring's next tile: key head `hk` of unit `load.at`
+    Cursor load = now;
+    int load_hk = 0;
+    long long load_off = 0;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * C::kStages * C::kTileBytes;
+    auto load_next = [&](int stage) {
+        if constexpr (kMma) {
+            if (load.at < st.end) {
+                if (load_hk == 0) {
+                    seek(load);
+                    load_off = row_of(load.e, (int)(load.at - load.before) * kKeys);
+                }
+                constexpr int kChunks = C::kRowBytes / 16, kPer = 32 / kChunks;  // of a row; rows an instruction
+                const char *kh = p.c.k + load_hk * p.c.b_head;
+#pragma unroll
+                for (int i = 0; i < kKeys / kPer; ++i) {
+                    const int r = i * kPer + lane / kChunks, ch = lane % kChunks;
+                    const long long o = __shfl_sync(0xffffffffu, load_off, r);
+                    // (two rows' halves trade places, so that the reads below meet every bank once)
+                    cp_async16(ring + stage * C::kTileBytes + r * C::kRowBytes + 16 * (ch ^ (4 * (r & 1))),
+                               kh + (o < 0 ? 0 : o + 16 * ch), o >= 0);
+                }
+                if (++load_hk == p.c.H) {
+                    load_hk = 0;
+                    load.at += kWarps;
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) load_next(s);
+
+    int stage = 0;
+    for (; now.at < st.end; now.at += kWarps) {
+        seek(now);
+        const Entry &e = now.e;
+        const int key0 = (int)(now.at - now.before) * kKeys, ctx = e.L - e.T, rows = e.T * p.group;
+        // a run that every new token sees whole
         const bool whole = key0 + kKeys <= ctx + 1 && (!p.window || key0 >= ctx + e.T - p.window || key0 + kKeys <= p.sinks);
         auto sees = [&](int t, int key) {
             return key <= ctx + t && (!p.window || key > ctx + t - p.window || key < p.sinks);
         };
-        long long off = 0;  // of this lane's key's row
-        bool live = false;
-        if (key0 + lane < e.L && !hidden) {
-            const int key = key0 + lane, page = p.c.table[(int64_t)e.s * p.c.table_stride + (key >> p.c.page_shift)];
-            live = (unsigned)page < (unsigned)p.c.n_pages;
-            if (!live) report_status(p.c.status, ATTN_EINVAL);
-            off = live ? page * p.c.b_page + (key & ((1 << p.c.page_shift) - 1)) * p.c.b_tok : 0;
-        }
-        const bool skip = !__any_sync(0xffffffffu, live);
-
-        float acc[kMma ? 4 : 1];  // keys g + 8 i; FFMA: the lane's
+        auto token_of = [&](int r) { return key_head(r, p.group_inv); };  // of row r of a head
+        // minus the lse in log2 units of row r of the head whose rows begin at lh; one that does not exist, or
+        // saw nothing, adds 2^-inf
+        auto lse_of = [&](const float *lh, int r) -> float {
+            if (r >= rows) return -INFINITY;
+            const int t = token_of(r);
+            const float x = __ldg(lh + (int64_t)(r - t * p.group) * p.n_q + t);
+            return x == -INFINITY ? -INFINITY : -x * kLog2e;
+        };
+        // the key that this lane writes, and its weight so far
+        const int mine = key0 + (kMma ? g + 8 * c : lane);
+        float *const w = p.weights + (int64_t)e.s * p.weights_stride + mine;
+        const float old = mine < e.L - e.fresh ? *w : 0.f;
+        float sum = 0.f;
+        if constexpr (kMma) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};  // keys g + 8 i
+            const bool none = e.T == 0 || hidden(e, key0);
+            uint4 q[kSteps];
+            float l0 = 0.f, l1 = 0.f;
+            // rows r0 .. of head hk: the operand's column g, and the lse of the columns 2 c, 2 c + 1
+            auto queries = [&](int hk, int r0) {
+                const T *qh = static_cast<const T *>(p.q) + (int64_t)e.q0 * p.q_st + (int64_t)hk * p.group * p.q_sh;
+                const float *lh = p.lse + (int64_t)hk * p.group * p.n_q + e.q0;
+                const int r = r0 + g, t = token_of(r);
 #pragma unroll
-        for (int i = 0; i < (kMma ? 4 : 1); ++i) acc[i] = 0.f;
-        for (int hk = first_head; hk < p.c.H && !skip && first_head < at_once; hk += at_once) {
-            const char *kh = p.c.k + hk * p.c.b_head;
-            const T *qh = static_cast<const T *>(p.q) + (int64_t)e.q0 * p.q_st + (int64_t)hk * p.group * p.q_sh;
-            const float *lh = p.lse + (int64_t)hk * p.group * p.n_q + e.q0;
-            // row r of the head: its token and head of the group
-            auto token_of = [&](int r) { return key_head(r, p.group_inv); };
-            // minus its lse in log2 units; a row that does not exist, or saw nothing, adds 2^-inf
-            auto lse_of = [&](int r) -> float {
-                if (r >= rows) return -INFINITY;
-                const int t = token_of(r);
-                const float x = __ldg(lh + (int64_t)(r - t * p.group) * p.n_q + t);
-                return x == -INFINITY ? -INFINITY : -x * kLog2e;
+                for (int s = 0; s < kSteps; ++s)
+                    q[s] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(qh + (int64_t)t * p.q_st + (r - t * p.group) * p.q_sh + 32 * s + 8 * c))
+                                    : make_uint4(0, 0, 0, 0);
+                l0 = lse_of(lh, r0 + 2 * c);
+                l1 = lse_of(lh, r0 + 2 * c + 1);
             };
-            if constexpr (kMma) {
+            if (!none) queries(0, 0);
+            for (int hk = 0; hk < p.c.H; ++hk) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages > 1 ? C::kStages - 2 : 0) : "memory");
+                __syncwarp();  // every lane's part has landed, and the stage before it has been read
+                load_next(stage == 0 ? C::kStages - 1 : stage - 1);
                 uint4 k[4][kSteps];
+                const uint8_t *tile = smem + (warp * C::kStages + stage) * C::kTileBytes;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long o = __shfl_sync(0xffffffffu, off, g + 8 * i);
-                    const bool there = __shfl_sync(0xffffffffu, (int)live, g + 8 * i);
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s)
-                        k[i][s] = there ? __ldg(reinterpret_cast<const uint4 *>(kh + o + 64 * s + 16 * c)) : make_uint4(0, 0, 0, 0);
-                }
+                        k[i][s] = *reinterpret_cast<const uint4 *>(tile + (g + 8 * i) * C::kRowBytes + 16 * ((4 * s + c) ^ (4 * (g & 1))));
+                stage = stage + 1 == C::kStages ? 0 : stage + 1;
+                if (none) continue;
                 for (int r0 = 0; r0 < rows; r0 += kRows) {
-                    uint4 q[kSteps];
-                    const int r = r0 + g, t = token_of(r);
+                    float x[2][4];
+                    const float n0 = l0, n1 = l1;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) x[m][y] = 0.f;
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s)
-                        q[s] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(qh + (int64_t)t * p.q_st + (r - t * p.group) * p.q_sh + 32 * s + 8 * c))
-                                        : make_uint4(0, 0, 0, 0);
-                    const float l0 = lse_of(r0 + 2 * c), l1 = lse_of(r0 + 2 * c + 1);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {  // 16 keys
-                        float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int s = 0; s < kSteps; ++s) {
+                        for (int m = 0; m < 2; ++m) {  // 16 keys
                             const uint4 &lo = k[2 * m][s], &hi = k[2 * m + 1][s];
                             const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-                            mma16816<T>(x, a0, q[s].x, q[s].y);
-                            mma16816<T>(x, a1, q[s].z, q[s].w);
+                            mma16816<T>(x[m], a0, q[s].x, q[s].y);
+                            mma16816<T>(x[m], a1, q[s].z, q[s].w);
                         }
+                    // the next rows' loads are in flight during the exponentials
+                    if (r0 + kRows < rows) queries(hk, r0 + kRows);
+                    else if (hk + 1 < p.c.H) queries(hk + 1, 0);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            float pv = exp2_approx(fmaf(x[y], p.scale_log2, y & 1 ? l1 : l0));
+                            float pv = exp2_approx(fmaf(x[m][y], p.scale_log2, y & 1 ? n1 : n0));
                             if (!whole && !sees(token_of(r0 + 2 * c + (y & 1)), key0 + 16 * m + g + (y & 2 ? 8 : 0))) pv = 0.f;
                             acc[2 * m + (y >> 1)] += pv;
                         }
-                    }
                 }
-            } else {
-                const float4 *kr = reinterpret_cast<const float4 *>(kh + off);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 1);
+                acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
+            }
+            sum = c == 0 ? acc[0] : c == 1 ? acc[1] : c == 2 ? acc[2] : acc[3];
+        } else {
+            const long long off = row_of(e, key0);
+            for (int hk = 0; hk < p.c.H && __any_sync(0xffffffffu, off >= 0); ++hk) {
+                const float4 *kr = reinterpret_cast<const float4 *>(p.c.k + hk * p.c.b_head + (off < 0 ? 0 : off));
+                const T *qh = static_cast<const T *>(p.q) + (int64_t)e.q0 * p.q_st + (int64_t)hk * p.group * p.q_sh;
+                const float *lh = p.lse + (int64_t)hk * p.group * p.n_q + e.q0;
                 for (int r0 = 0; r0 < rows; r0 += kRows) {
                     float x[kRows];
-                    const float *qr[kRows];
+                    const float4 *qr[kRows];
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
                         const int row = min(r0 + r, rows - 1), t = token_of(row);
-                        qr[r] = reinterpret_cast<const float *>(qh) + (int64_t)t * p.q_st + (row - t * p.group) * p.q_sh;
+                        qr[r] = reinterpret_cast<const float4 *>(qh + (int64_t)t * p.q_st + (row - t * p.group) * p.q_sh);
                         x[r] = 0.f;
                     }
 #pragma unroll 4
                     for (int d = 0; d < D / 4; ++d) {
-                        const float4 kv = live ? __ldg(kr + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float4 kv = off >= 0 ? __ldg(kr + d) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int r = 0; r < kRows; ++r) {
-                            const float4 qv = __ldg(reinterpret_cast<const float4 *>(qr[r]) + d);
+                            const float4 qv = __ldg(qr[r] + d);
                             x[r] = fmaf(qv.x, kv.x, x[r]);
                             x[r] = fmaf(qv.y, kv.y, x[r]);
                             x[r] = fmaf(qv.z, kv.z, x[r]);
@@ -192,42 +283,25 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const WeighParams p)
                     }
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        const float pv = exp2_approx(fmaf(x[r], p.scale_log2, lse_of(r0 + r)));
-                        if (whole || sees(token_of(r0 + r), key0 + lane)) acc[0] += pv;
+                        const float pv = exp2_approx(fmaf(x[r], p.scale_log2, lse_of(lh, r0 + r)));
+                        if (whole || sees(token_of(r0 + r), mine)) sum += pv;
                     }
                 }
             }
         }
-        if constexpr (kMma) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 1);
-                acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
-                if (c == 0) s_sum[warp][g + 8 * i] = acc[i];
-            }
-        } else {
-            s_sum[warp][lane] = acc[0];
-        }
-        __syncthreads();
-        const int key = unit0 + tid;
-        if (tid < unit_keys && key < e.L) {
-            float *w = p.weights + (int64_t)e.s * p.weights_stride + key;
-            float sum = key < e.L - e.fresh ? *w : 0.f;
-            float got = 0.f;
-            for (int h = 0; h < at_once; ++h) got += s_sum[h * subs + tid / kKeys][tid % kKeys];
-            *w = sum + got;
-        }
-        __syncthreads();
+        if (mine < e.L) *w = old + sum;
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const WeighParams &p, cudaStream_t s) {
     auto kern = weigh_kernel<T, D>;
-    const size_t smem = 2 * sizeof(uint32_t) * (size_t)((p.c.max_seqs + 31) / 32);
+    using C = Cfg<T, D>;
+    const size_t bits = p.n > 1 ? sizeof(uint32_t) * (size_t)((p.c.max_seqs + 31) / 32) : 0;
+    const size_t smem = C::kRingBytes > bits ? C::kRingBytes : bits;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(2 * sm_count()), dim3(kThreads), smem, s, p);
+    e = launch_pdl(kern, dim3((C::kMma ? 1 : 2) * sm_count()), dim3(kThreads), smem, s, p);
     count_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }

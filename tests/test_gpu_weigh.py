@@ -103,7 +103,7 @@ def test_entries_that_do_not_fit_are_left():
     a, b = seqs
     for bad_seqs, cu, fresh, done in (([a, 99], [0, 3, 8], None, [a]), ([-1, b], [0, 3, 8], None, [b]), ([a, b], [0, 3, 9], None, [a]),
                                       ([a, b], [3, 0, 8], None, [b]), ([a, b], [0, 3, 8], [51, 5], [b]), ([a, b], [0, 3, 8], [3, -1], [a]),
-                                      ([a, a], [0, 3, 8], None, []), ([b, 2 ** 31 - 1], [0, 3, 8], None, [])):
+                                      ([a, a], [0, 3, 8], None, []), ([b, b], [0, 3, 8], None, []), ([b, 2 ** 31 - 1], [0, 3, 8], None, [])):
         w = cache.new_weights()
         cache.weigh(bad_seqs, cu, q, lse, w, fresh=fresh)
         assert attn.device_status() == _abi.ATTN_EINVAL, (bad_seqs, cu, fresh)
