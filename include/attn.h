@@ -560,8 +560,8 @@ ATTN_API int attn_cache_weigh(const attn_weigh_args *a, void *stream);
 
 /* Cuts every listed sequence of more than budgets[i] tokens to that many: its first `sinks`,
  * its last `recent`, and the heaviest of the others by the sum of their weights over the
- * layers (taken in f64, rounded to f32; equal weights: the lower token first; NaN is
- * lighter than every number).  The kept rows move down in order, in all layers of the cache,
+ * layers (taken in twice f32's precision, rounded to f32; equal weights: the lower token
+ * first; NaN is lighter than every number).  The kept rows move down in order, in all layers of the cache,
  * and their weights in all layers of w; the pages behind the new end are released.  Rows
  * and weights behind the new end keep what they hold.  Shorter sequences stay as they are.
  * sinks >= 0, recent >= 0.  A list is done as a whole or not at all: an entry out of

@@ -12,6 +12,7 @@
 #include "../../include/attn.h"
 #include "internal.h"
 #include "tc.h"
+#include "window.h"
 
 namespace attn {
 
@@ -347,11 +348,29 @@ void split_params(const attn_fwd_args *a, const FwdParams &p, bool use_tc, FwdPa
 // ---- backward --------------------------------------------------------------
 
 struct BwdLayout {
-    size_t kv, q, dr, lse2, dqa, total;
+    size_t kv, q, dr, lse2, dqa, sinks, total;
 };
 
+// Chunks of the sinks' key blocks on the tensor cores: twice the query blocks that see a block of a
+// window, more where half a CTA's share of all blocks is more or the partial sums would pass 256
+// slots a head; none where no row is longer.  (24 rows of 30 to 1000 tokens, window 200: 82 us for dK
+// and dV with chunks as long as a window's items, 81 uncut.)
+void sink_cut(const attn_bwd_args *a, int &tiles, int &chunk) {
+    tiles = chunk = 0;
+    if (a->window <= 0 || a->window >= a->n_k || a->sinks <= 0) return;
+    const int64_t blocks = a->n_q / 128 + 1, held = ((int64_t)a->sinks + 127) / 128;
+    const int64_t n = held < blocks ? held : blocks;
+    const int64_t seen = (254 + (int64_t)a->window) / 128, heads = a->H_kv > 0 ? a->H_kv : a->H;
+    int64_t c = 2 * seen;
+    if (c < heads * blocks * seen / (2 * sm_count())) c = heads * blocks * seen / (2 * sm_count());
+    if (c < (n * blocks + 127) / 128) c = (n * blocks + 127) / 128;
+    if (blocks <= c) return;
+    tiles = (int)n;
+    chunk = (int)c;
+}
+
 // fused: room for the dq partial sums (n_q * H * D f32) after the row statistics
-BwdLayout bwd_layout(int n_seq, int H, int n_q, int D, bool fused) {
+BwdLayout bwd_layout(int n_seq, int H, int n_q, int D, bool fused, size_t sink_floats) {
     BwdLayout L;
     const size_t rows = align256(sizeof(float) * (size_t)H * (size_t)(n_q > 0 ? n_q : 1));
     L.kv = 0;
@@ -359,15 +378,13 @@ BwdLayout bwd_layout(int n_seq, int H, int n_q, int D, bool fused) {
     L.dr = 2 * L.q;
     L.lse2 = L.dr + rows;
     L.dqa = L.lse2 + rows;
-    L.total = L.dqa + (fused ? align256(sizeof(float) * (size_t)H * (size_t)(n_q > 0 ? n_q : 0) * (size_t)D) : 0);
+    L.sinks = L.dqa + (fused ? align256(sizeof(float) * (size_t)H * (size_t)(n_q > 0 ? n_q : 0) * (size_t)D) : 0);
+    L.total = L.sinks + align256(sizeof(float) * sink_floats);
     return L;
 }
 
-// Whether a backward with these arguments accumulates dq inside the dK/dV
-// kernel: the caller asked for it and the tensor-core kernels run (AUTO
-// resolves to the separate dq kernel).
-bool bwd_fused(const attn_bwd_args *a) {
-    if (a->dq_mode != ATTN_DQ_FUSED) return false;
+// Whether a backward with these arguments runs the tensor-core kernels.
+bool bwd_on_tc(const attn_bwd_args *a) {
     BwdParams t;
     std::memset(&t, 0, sizeof(t));
     t.dtype = a->dtype;
@@ -377,6 +394,19 @@ bool bwd_fused(const attn_bwd_args *a) {
     bool use_tc = false;
     if (choose_tc(a->kernel, tc_bwd_supported(t), use_tc) != ATTN_OK) return false;
     return use_tc;
+}
+
+// Whether a backward with these arguments accumulates dq inside the dK/dV
+// kernel: the caller asked for it and the tensor-core kernels run (AUTO
+// resolves to the separate dq kernel).
+bool bwd_fused(const attn_bwd_args *a) { return a->dq_mode == ATTN_DQ_FUSED && bwd_on_tc(a); }
+
+// Floats of the sinks' partial sums: two of 128 rows a slot.
+size_t sink_floats(const attn_bwd_args *a) {
+    int tiles, chunk;
+    sink_cut(a, tiles, chunk);
+    if (!chunk || !bwd_on_tc(a)) return 0;
+    return (size_t)(a->H_kv > 0 ? a->H_kv : a->H) * (size_t)sink_slot(a->n_q, tiles, chunk) * 2 * 128 * (size_t)a->D;
 }
 
 int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
@@ -428,11 +458,15 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
         p.sinks = a->sinks;
     }
     const bool fused = bwd_fused(a);
-    const BwdLayout L = bwd_layout(a->n_seq, a->H, a->n_q, a->D, fused);
+    const BwdLayout L = bwd_layout(a->n_seq, a->H, a->n_q, a->D, fused, sink_floats(a));
     char *ws = static_cast<char *>(a->workspace);
     p.dr = reinterpret_cast<float *>(ws + L.dr);
     p.lse2 = reinterpret_cast<float *>(ws + L.lse2);
     p.dq_accum = fused ? reinterpret_cast<float *>(ws + L.dqa) : nullptr;
+    if (sink_floats(a)) {
+        sink_cut(a, p.sink_tiles, p.sink_chunk);
+        p.sink_parts = reinterpret_cast<float *>(ws + L.sinks);
+    }
     p.status = status_ptr();
     p.watchdog_cycles = watchdog_cycles();
     if (!p.status) return ATTN_ECUDA;
@@ -644,7 +678,7 @@ size_t attn_merge_args_size(void) { return sizeof(attn_merge_args); }
 
 size_t attn_bwd_workspace_bytes(const attn_bwd_args *a) {
     if (!a || a->n_seq < 1 || a->H < 1 || a->n_q < 0 || a->D < 0) return 0;
-    return bwd_layout(a->n_seq, a->H, a->n_q, a->D, bwd_fused(a)).total;
+    return bwd_layout(a->n_seq, a->H, a->n_q, a->D, bwd_fused(a), sink_floats(a)).total;
 }
 
 int attn_fwd(const attn_fwd_args *a, void *stream) {
@@ -754,7 +788,7 @@ int attn_bwd_preprocess(const attn_bwd_args *a, void *stream) {
     const int q_block = use_tc ? tc_bwd_q_block(p) : kSimtBlock;
     // (the fused dq needs no query-block schedule)
     cudaError_t e = launch_prep(p.cu_q, p.cu_k, p.n_seq, p.n_q, p.n_k, p.causal,
-                                {{{p.Hkv, kv_block, 1, 1, p.sched_kv}, {p.H, q_block, 0, 1, p.sched_q}}},
+                                {{{p.Hkv, kv_block, 1, 1, p.sched_kv, p.sink_tiles, p.sink_chunk}, {p.H, q_block, 0, 1, p.sched_q}}},
                                 p.dq_accum ? 1 : 2, p.status, s);
     if (e == cudaSuccess) e = launch_bwd_preprocess(p, s);
     if (e == cudaSuccess && p.dq_accum) e = launch_dq_accum_zero(p, s);

@@ -34,8 +34,10 @@
 // lse * log2(e) and Dr come from the preprocess kernel.  All waits bounded.
 //
 // kWindow: a sliding window with sinks (window.h).  A key block is then seen by the query
-// blocks up to its last key's window (a block with a sink: by all behind it), and a query
-// block scans the key blocks that hold a sink or a key of its window; pairs outside are
+// blocks up to its last key's window, a block with a sink by all behind it: those are cut into
+// chunks, an item each, whose partial sums a small kernel adds up in order (2 rows of 8192 tokens,
+// 32 / 8 heads, window 1024: one item took as long as the other ones of a CTA together, 676 us
+// instead of SINK_US).  A query block scans the key blocks that hold a sink or a key of its window; pairs outside are
 // zeroed in P^T and dS.  Kernels of their own (bwd_tc_window.cu), so that the others keep
 // their code.
 #pragma once
@@ -187,11 +189,16 @@ struct DkdvInfo {
     int nqh;  // query blocks of one query head that can see the keys
     int nq;   // query blocks of the item: nqh of each query head that shares key head h, head by head
 };
+struct WindowDkdvInfo : DkdvInfo {
+    long long part;  // slot of the item's partial sums; -1: it has all query blocks
+};
+template <bool kWindow>
+using DkdvInfoOf = std::conditional_t<kWindow, WindowDkdvInfo, DkdvInfo>;
 
 template <bool kWindow>
-__device__ __forceinline__ DkdvInfo dkdv_info(const BwdParams &p, int w) {
+__device__ __forceinline__ DkdvInfoOf<kWindow> dkdv_info(const BwdParams &p, int w) {
     const WorkItem it = map_item<true>(w, p.sched_kv, p.n_seq, p.Hkv, false, 1, p.group > 1);
-    DkdvInfo f;
+    DkdvInfoOf<kWindow> f;
     seq_bounds(p.cu_q, p.n_q, it.b, f.q_start, f.Lq);
     seq_bounds(p.cu_k, p.n_k, it.b, f.k_start, f.Lk);
     f.h = it.h;
@@ -199,12 +206,31 @@ __device__ __forceinline__ DkdvInfo dkdv_info(const BwdParams &p, int w) {
     f.key0 = it.t * BT;
     f.qb0 = p.causal ? it.t : 0;
     f.nqh = max(0, cdiv(f.Lq, BT) - f.qb0);
-    // the last query that sees the block's last key: key0 + BT - 1 + window - 1
-    if (kWindow && f.key0 >= p.sinks) f.nqh = min(f.nqh, (int)(((long long)BT + BT - 2 + p.window) / BT));
+    if constexpr (kWindow) {
+        const int blocks = cdiv(f.Lq, BT);
+        const SinkItems sink = sink_items(blocks, p.sink_tiles, p.sink_chunk);
+        f.part = -1;
+        if (sink.chunks > 1) {
+            const int cut = sink.tiles * sink.chunks;  // the first items
+            f.t = it.t < cut ? it.t / sink.chunks : it.t - cut + sink.tiles;
+            f.key0 = f.t * BT;
+            f.qb0 = f.t;
+            if (it.t < cut) {
+                f.qb0 += (it.t - f.t * sink.chunks) * p.sink_chunk;
+                f.part = it.h * sink_slot(p.n_q, p.sink_tiles, p.sink_chunk) +
+                         sink_slot(f.q_start, p.sink_tiles, p.sink_chunk) + it.t;
+            }
+            f.nqh = max(0, blocks - f.qb0);
+            if (it.t < cut) f.nqh = min(f.nqh, p.sink_chunk);
+        }
+        // the last query that sees the block's last key: key0 + BT - 1 + window - 1
+        if (f.key0 >= p.sinks) f.nqh = min(f.nqh, (int)(((long long)BT + BT - 2 + p.window) / BT));
+    }
     f.nq = f.nqh * p.group;
     return f;
 }
 
+template <bool kWindow>
 struct __align__(8) DkdvBars {
     uint64_t kv_full, kv_empty;
     uint64_t q_full[4], q_empty[4], do_empty[4];  // q_full: the Q and dO tiles of a query block
@@ -213,7 +239,7 @@ struct __align__(8) DkdvBars {
     uint64_t mma_drain;       // abort path: completion of the MMAs already issued
     uint64_t dq_full, dq_free; // fused dQ: a block's dQ partial is in TMEM / has been read out
     uint64_t dv_done;          // fused dQ: dV of a block has read its dO tile (the slot may take dS)
-    SchedRing<DkdvInfo> sched;
+    SchedRing<DkdvInfoOf<kWindow>> sched;
 };
 
 // Two producer warps, each run by all its 32 lanes in step (uniform waits, one
@@ -221,7 +247,7 @@ struct __align__(8) DkdvBars {
 // V and the Q ring; warp 2 loads the dO ring.  Splitting them keeps a dO load from waiting
 // behind a Q slot (Q tiles are released only after dK, dO tiles after dV).
 template <int D, bool kWindow>
-__device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint32_t sV, uint32_t sQ,
+__device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars<kWindow> &bars, uint32_t sK, uint32_t sV, uint32_t sQ,
                               uint32_t sDO, bool dout_role, const Watchdog &wd) {
     using C = BCfg<D>;
     const BwdParams &p = a.p;
@@ -249,7 +275,7 @@ __device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, u
     };
     for (int i = 0;; ++i) {
         int w;
-        DkdvInfo f;
+        DkdvInfoOf<kWindow> f;
         if (dout_role) {
             if (!sched_take_warp(bars.sched, i, w, f, wd)) break;
         } else {
@@ -302,8 +328,8 @@ __device__ void dkdv_producer(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, u
     }
 }
 
-template <int D, bool kBF16>
-__device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint32_t sV, uint32_t sQ, uint32_t sDO,
+template <int D, bool kBF16, bool kWindow>
+__device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars<kWindow> &bars, uint32_t sK, uint32_t sV, uint32_t sQ, uint32_t sDO,
                          uint32_t tmem, const Watchdog &wd) {
     using C = BCfg<D>;
     const BwdParams &p = a.p;
@@ -352,7 +378,7 @@ __device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint32
 
     for (int i = 0;; ++i) {
         int w;
-        DkdvInfo f;
+        DkdvInfoOf<kWindow> f;
         if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
         if (f.nq == 0) continue;
@@ -440,7 +466,7 @@ __device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint32
 // dQ_qb: the score MMA of the next block covers the elementwise dS work, and
 // dV of the next block covers the read-out of dQ_qb.
 template <int D, bool kBF16>
-__device__ void dkdvq_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint32_t sV, uint32_t sQ,
+__device__ void dkdvq_mma(const TcBwdArgs &a, DkdvBars<false> &bars, uint32_t sK, uint32_t sV, uint32_t sQ,
                           uint32_t sDO, uint32_t sDS, uint32_t tmem, const Watchdog &wd) {
     using C = BCfg<D>;
     const BwdParams &p = a.p;
@@ -558,7 +584,7 @@ __device__ void dkdvq_mma(const TcBwdArgs &a, DkdvBars &bars, uint32_t sK, uint3
 }
 
 template <int D, bool kBF16, typename Tg, bool kWindow>
-__device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stats, uint32_t tmem,
+__device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, float *stats, uint32_t tmem,
                                  const Watchdog &wd) {
     const BwdParams &p = a.p;
     const int total = p.sched_kv.hdr[1];
@@ -573,7 +599,7 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
 
     for (int i = 0;; ++i) {
         int w;
-        DkdvInfo f;
+        DkdvInfoOf<kWindow> f;
         if (!sched_take_warp(bars.sched, i, w, f, wd)) return;
         if (w >= total) return;
         const int key = f.key0 + kl;
@@ -582,6 +608,8 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
                   (int64_t)(f.k_start + key) * (wg == 0 ? p.dv_st : p.dk_st) +
                   (int64_t)f.h * (wg == 0 ? p.dv_sh : p.dk_sh);
         if (f.nq == 0) {
+            if constexpr (kWindow)
+                if (f.part >= 0) continue;  // (a chunk behind the last query block: not read)
             if (live) zero_cols(dst, D);
             continue;
         }
@@ -702,6 +730,21 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
         const int64_t gst = wg == 0 ? p.dv_st : p.dk_st;
         Tg *wrow0 = dst - (int64_t)lane * gst;
         const int rows_live = min(32, max(0, f.Lk - (f.key0 + 32 * quarter)));
+        if constexpr (kWindow) {
+            if (f.part >= 0) {  // unscaled, for the sum over the key block's items
+                float *part = p.sink_parts + (f.part * 2 + wg) * (BT * D) + 32 * quarter * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t u[32];
+                    tmem_ld_x32(lane_base + 256 + D * wg + 32 * c, u);
+                    tmem_ld_wait(u);
+                    store_rows_chunk(u, 1.f, part + 32 * c, (int64_t)D, rows_live, lane);
+                }
+                tc_fence_before();
+                mbar_arrive_warp(smem_u32(&bars.acc_free));
+                continue;
+            }
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t u[32];
@@ -720,7 +763,7 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stat
 // dS^T, written 16-bit both to TMEM (A operand of dK) and, 128-byte swizzled,
 // to shared memory (A operand of dQ).
 template <int D, bool kBF16, typename Tg>
-__device__ void dkdvq_elementwise(const TcBwdArgs &a, DkdvBars &bars, float *stats, uint32_t sDO, uint32_t sDS,
+__device__ void dkdvq_elementwise(const TcBwdArgs &a, DkdvBars<false> &bars, float *stats, uint32_t sDO, uint32_t sDS,
                                   uint32_t tmem, const Watchdog &wd) {
     using C = BCfg<D>;
     const BwdParams &p = a.p;
@@ -893,7 +936,7 @@ template <int D, bool kBF16, typename Tg, bool kFused, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_constant__ TcBwdArgs a) {
     using C = BCfg<D>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ DkdvBars bars;
+    __shared__ DkdvBars<kWindow> bars;
     __shared__ __align__(16) float stats[2 * 2 * BT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -954,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
             if constexpr (kFused) {
                 if (lane == 0) dkdvq_mma<D, kBF16>(a, bars, sK, sV, sQ, sDO, sDS, tmem, wd);
             } else {
-                dkdv_mma<D, kBF16>(a, bars, sK, sV, sQ, sDO, tmem, wd);
+                dkdv_mma<D, kBF16, kWindow>(a, bars, sK, sV, sQ, sDO, tmem, wd);
             }
             if (lane == 0 && aborting(wd)) {  // let issued MMAs finish before TMEM is freed
                 tc_commit(smem_u32(&bars.mma_drain));
@@ -971,6 +1014,49 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// The sums of the sinks' key blocks over their items, in the items' order.  Block (head, block and
+// sequences, rows): a thread has four columns of one row of dV or dK.
+constexpr int kSinkLanes = 32;  // sequences at a time
+constexpr int sink_rows(int D) { return 128 / (D / 4); }
+
+template <typename Tg, int D>
+__global__ void __launch_bounds__(256) sink_sum_kernel(const BwdParams p) {
+    pdl_trigger();
+    pdl_wait();
+    if (p.sched_kv.hdr[1] == 0) return;  // offsets that do not fit
+    const int h = blockIdx.x, which = threadIdx.x >> 7, x = threadIdx.x & 127;
+    const int r = blockIdx.z * sink_rows(D) + x / (D / 4), d = x % (D / 4) * 4;
+    const int lane = blockIdx.y % kSinkLanes;
+    for (int b = lane; b < p.n_seq; b += kSinkLanes) {
+        int start, len;
+        seq_bounds(p.cu_q, p.n_q, b, start, len);
+        const int blocks = cdiv(len, BT);
+        const SinkItems sink = sink_items(blocks, p.sink_tiles, p.sink_chunk);
+        if (sink.chunks == 1) continue;
+        for (int t = blockIdx.y / kSinkLanes; t < sink.tiles; t += gridDim.y / kSinkLanes) {
+            const int used = cdiv(blocks - t, p.sink_chunk);  // chunks that hold a query block
+            const int key = t * BT + r;
+            if (key >= len) continue;
+            const long long slot = h * sink_slot(p.n_q, p.sink_tiles, p.sink_chunk) +
+                                   sink_slot(start, p.sink_tiles, p.sink_chunk) + t * sink.chunks;
+            const float *at = p.sink_parts + (slot * 2 + which) * (BT * D) + r * D + d;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int c = 0; c < used; ++c) {
+                const float4 v = *reinterpret_cast<const float4 *>(at + (int64_t)c * 2 * BT * D);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            const float mul = which ? p.scale : 1.f;
+            store4(static_cast<Tg *>(which ? p.dk : p.dv) + (int64_t)(start + key) * (which ? p.dk_st : p.dv_st) +
+                       (int64_t)h * (which ? p.dk_sh : p.dv_sh) + d,
+                   make_float4(sum.x * mul, sum.y * mul, sum.z * mul, sum.w * mul));
+        }
     }
 }
 
@@ -1433,7 +1519,16 @@ cudaError_t launch_typed(const TcBwdArgs &a, int num_ctas, cudaStream_t s, bool 
     if constexpr (!kWindow)  // (with a window there is no fused dq)
         if (dkdv && a.p.dq_accum)
             return launch(dkdv_tc_kernel<D, kBF16, Tg, true, false>, BCfg<D>::kDkdvSmem, a, num_ctas, s);
-    if (dkdv) return launch(dkdv_tc_kernel<D, kBF16, Tg, false, kWindow>, BCfg<D>::kDkdvSmem, a, num_ctas, s);
+    if (dkdv) {
+        cudaError_t e = launch(dkdv_tc_kernel<D, kBF16, Tg, false, kWindow>, BCfg<D>::kDkdvSmem, a, num_ctas, s);
+        if constexpr (kWindow) {
+            if (e != cudaSuccess || !a.p.sink_chunk) return e;
+            const dim3 grid(a.p.Hkv, kSinkLanes * (a.p.sink_tiles < 64 ? a.p.sink_tiles : 64), BT / sink_rows(D));
+            e = launch_pdl(sink_sum_kernel<Tg, D>, grid, dim3(256), 0, s, a.p);
+            count_launch();
+        }
+        return e;
+    }
     return launch(dq_tc_kernel<D, kBF16, Tg, kWindow>, BCfg<D>::kDqSmem, a, num_ctas, s);
 }
 

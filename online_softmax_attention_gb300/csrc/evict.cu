@@ -5,7 +5,7 @@
 // behind.  The list is done as a whole or not at all: every entry leaves a mark, and the
 // second kernel does nothing unless all of them are good.
 //
-// Choice.  A token's weight, summed over the layers in f64 and rounded to f32, becomes a whole
+// Choice.  A token's weight, summed over the layers and rounded to f32, becomes a whole
 // number in the same order; three passes over 11, 11 and 10 bits, a histogram a pass, find the
 // smallest number that is kept and how many of the tokens that have it are (the first ones).
 // A thread then numbers a run of tokens, behind two scans over the block.  Every result is a
@@ -19,6 +19,8 @@
 // rows move in place, many at once, without a copy.
 //
 // Bound: HBM, the moved rows read and written once; few rows: the chain of the two kernels.
+#include <cfloat>
+
 #include "../../include/attn.h"
 #include "common.cuh"
 #include "pages.h"
@@ -91,14 +93,41 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
     const int sinks = p.sinks, last = len - p.recent;  // the tokens [sinks, last) are chosen from
     const int want = budget - sinks - p.recent, n = last - sinks;
     const float *w = p.weights + (int64_t)s * p.w_seq + sinks;
-    auto sum_of = [&](int t) {
-        double x = w[t];
-#pragma unroll 8
-        for (int y = 1; y < p.w_layers; ++y) x += (double)w[(int64_t)y * p.w_layer + t];
-        return order_of((float)x);
+    // kTokens tokens' sums over the layers, t + kPlanThreads k (those below n): each with the
+    // additions' errors beside it, twice f32's precision.  (The GPU adds few f64 numbers at a time:
+    // 25 us of them for 32 sequences of 6000 tokens in 8 layers.)
+    constexpr int kTokens = 4;
+    auto sums_of = [&](int t, uint32_t (&r)[kTokens]) {
+        float hi[kTokens], lo[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) hi[k] = lo[k] = 0.f;
+#pragma unroll 4
+        for (int y = 0; y < p.w_layers; ++y)
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                const float x = t + kPlanThreads * k < n ? w[(int64_t)y * p.w_layer + t + kPlanThreads * k] : 0.f;
+                const float sum = __fadd_rn(hi[k], x), was = __fsub_rn(sum, x);
+                lo[k] = __fadd_rn(lo[k], __fadd_rn(__fsub_rn(hi[k], was), __fsub_rn(x, __fsub_rn(sum, was))));
+                hi[k] = sum;
+            }
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            float x = __fadd_rn(hi[k], lo[k]);
+            if (!(fabsf(x) <= FLT_MAX) && t + kPlanThreads * k < n) {  // infinities, NaN, or a sum on the way past f32
+                double s = 0.;
+                for (int y = 0; y < p.w_layers; ++y) s += (double)w[(int64_t)y * p.w_layer + t + kPlanThreads * k];
+                x = (float)s;
+            }
+            r[k] = order_of(x);
+        }
     };
     const bool keep = n <= kHeld;
-    auto number_of = [&](int t) { return keep ? held[t] : sum_of(t); };
+    auto number_of = [&](int t) -> uint32_t {
+        if (keep) return held[t];
+        uint32_t r[kTokens];
+        sums_of(t, r);
+        return r[0];
+    };
 
     // the smallest number that is kept: its digits from the top; `left` of those that share them so far
     uint32_t found = 0;
@@ -108,16 +137,19 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 0 : pass == 1 ? 21 : 10;
         for (int b = tid; b < kBins; b += kPlanThreads) bins[b] = 0;
         __syncthreads();
-        for (int t = tid; t < n; t += kPlanThreads) {
-            uint32_t x;
-            if (pass == 0) {
-                x = sum_of(t);
-                if (keep) held[t] = x;
-            } else {
-                x = number_of(t);
-                if (x >> above != found >> above) continue;
+        const bool sums = pass == 0 || !keep;
+        for (int t = tid; t < n; t += kTokens * kPlanThreads) {
+            uint32_t x[kTokens];
+            if (sums) sums_of(t, x);
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                const int at = t + kPlanThreads * k;
+                if (at >= n) break;
+                if (!sums) x[k] = held[at];
+                else if (keep) held[at] = x[k];
+                if (pass == 0 || x[k] >> above == found >> above)
+                    atomicAdd(&bins[(x[k] >> shift) & (pass == 2 ? 1023u : 2047u)], 1);
             }
-            atomicAdd(&bins[(x >> shift) & (pass == 2 ? 1023u : 2047u)], 1);
         }
         __syncthreads();
         // the largest digit with at least `left` numbers from it on; a thread has two digits, the largest first

@@ -92,6 +92,8 @@ struct PlainSeg {
 struct WindowSeg : PlainSeg {
     TileList list;    // of the unit: its j-th key tile is tile list.at(j)
     int T;            // tokens of the entry
+    int sinks;
+    int from[NQT];    // first key of the window of each tile's first row
 };
 template <bool kWindow>
 using Seg = std::conditional_t<kWindow, WindowSeg, PlainSeg>;
@@ -99,6 +101,21 @@ using Seg = std::conditional_t<kWindow, WindowSeg, PlainSeg>;
 // First key of key tile j of the part's unit.
 __device__ __forceinline__ int key_of(const PlainSeg &, int j) { return BN * j; }
 __device__ __forceinline__ int key_of(const WindowSeg &g, int j) { return BN * g.list.at(j); }
+
+// Of key tile j of the unit, the 16-key MMA steps that hold a key which query tile t may see: up to
+// this one (one at least: an entry without keys) ...
+__device__ __forceinline__ int key_steps(int left) { return min(BN / 16, max(1, (left + 15) >> 4)); }
+__device__ __forceinline__ int steps_of(const PlainSeg &g, int t, int j) { return key_steps(g.end[t] - BN * j); }
+__device__ __forceinline__ int steps_of(const WindowSeg &g, int t, int j) {
+    // (tiles before the window hold sinks, and nothing else that is seen)
+    return key_steps((j < g.list.sinks ? min(g.end[t], g.sinks) : g.end[t]) - key_of(g, j));
+}
+// ... from this one on.
+__device__ __forceinline__ int first_step(const PlainSeg &, int, int) { return 0; }
+__device__ __forceinline__ int first_step(const WindowSeg &g, int t, int j) {
+    const int key0 = key_of(g, j);
+    return j < g.list.sinks || key0 < g.sinks ? 0 : max(0, min(BN / 16 - 1, (g.from[t] - key0) >> 4));
+}
 
 struct __align__(8) Bars {
     uint64_t q_full[NQT], q_empty[NQT];
@@ -294,6 +311,10 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
         if constexpr (kWindow) {
             g.list = list;
             g.T = e.T;
+            g.sinks = p.sinks;
+#pragma unroll
+            for (int t = 0; t < NQT; ++t)
+                g.from[t] = e.ctx + (ordered ? unit * per + t * tok_tile + 1 : 0) - p.window;
         }
         g.q0 = e.q0;
         g.hk = hk;
@@ -385,10 +406,6 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
     }
 }
 
-// Of a key tile whose first `left` keys a query tile may see, the 16-key MMA steps
-// that hold them (one at least: an entry without keys).
-__device__ __forceinline__ int key_steps(int left) { return min(BN / 16, max(1, (left + 15) >> 4)); }
-
 // ---- warp 1: MMA issuer (the whole warp, one elected lane issuing) ----------------------
 
 template <int D, bool kBF16, bool kWindow>
@@ -407,30 +424,33 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
     const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(sK, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sV, C::kBoxBytes, 1024);
-    auto issue_s = [&](int t, uint32_t kslot, int steps) {  // S_t = Q_t K^T over 16 * steps keys
-        const uint32_t id = steps == BN / 16 ? idS : idS_of(steps);
+    // S_t = Q_t K^T over keys [16 from, 16 steps)
+    auto issue_s = [&](int t, uint32_t kslot, int from, int steps) {
+        const uint32_t id = steps - from == BN / 16 ? idS : idS_of(steps - from);
         const uint64_t qa = q_desc + sdesc_step(t * C::kTileBytes);
-        const uint64_t ka = k_desc + sdesc_step(kslot * C::kTileBytes);
+        const uint64_t ka = k_desc + sdesc_step(kslot * C::kTileBytes + (kWindow ? from * 2048 : 0));
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = sdesc_step((kk >> 2) * C::kBoxBytes + (kk & 3) * 32);
-                mma_ss(tmem + BN * t, qa + off, ka + off, id, kk > 0);
+                mma_ss(tmem + BN * t + (kWindow ? 16 * from : 0), qa + off, ka + off, id, kk > 0);
             }
             tc_commit(smem_u32(&bars.s_full[t]));
         }
         __syncwarp();
     };
-    auto issue_pv = [&](int t, uint32_t vslot, bool acc, int steps) {  // U_t (+)= P_t V over 16 * steps keys
+    // U_t (+)= P_t V over keys [16 from, 16 steps)
+    auto issue_pv = [&](int t, uint32_t vslot, bool acc, int from, int steps) {
         const uint64_t va = v_desc + sdesc_step(vslot * C::kTileBytes);
         if (elect_one()) {
-            if (steps == BN / 16) {
+            if (steps - (kWindow ? from : 0) == BN / 16) {
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
                     mma_ts(tmem + 256 + D * t, tmem + BN * t + 8 * kk, va + sdesc_step(kk * 2048), idO, acc || kk > 0);
             } else {
-                for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tmem + 256 + D * t, tmem + BN * t + 8 * kk, va + sdesc_step(kk * 2048), idO, acc || kk > 0);
+                for (int kk = kWindow ? from : 0; kk < steps; ++kk)
+                    mma_ts(tmem + 256 + D * t, tmem + BN * t + 8 * kk, va + sdesc_step(kk * 2048), idO,
+                           acc || kk > (kWindow ? from : 0));
             }
         }
         __syncwarp();
@@ -446,12 +466,24 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         const int slot = i % kSegs;
         if (!wait(bars.seg_full[slot], (i / kSegs) & 1)) return;
         const int n0 = segs[slot].n[0], n1 = segs[slot].n[1], nkv = segs[slot].nkv;
-        const int j0 = segs[slot].j0, key0 = kWindow ? 0 : BN * j0;
-        const int left0 = segs[slot].end[0] - key0, left1 = segs[slot].end[1] - key0;
-        TileList list = {0, 0};
-        if constexpr (kWindow) list = segs[slot].list;
-        // keys from the part's j-th tile on that query tile t may see
-        auto left_of = [&](int t, int j) { return (t ? left1 : left0) - BN * (kWindow ? list.at(j0 + j) : j); };
+        const int j0 = segs[slot].j0, key0 = BN * j0, left0 = segs[slot].end[0] - key0, left1 = segs[slot].end[1] - key0;
+        WindowSeg win;  // with a window, what the steps need of the part
+        if constexpr (kWindow) {
+            win.list = segs[slot].list;
+            win.sinks = segs[slot].sinks;
+#pragma unroll
+            for (int t = 0; t < NQT; ++t) {
+                win.end[t] = segs[slot].end[t];
+                win.from[t] = segs[slot].from[t];
+            }
+        }
+        // the steps of query tile t and the part's j-th key tile
+        auto steps_at = [&](int t, int j) {
+            return kWindow ? t ? steps_of(win, 1, j0 + j) : steps_of(win, 0, j0 + j) : key_steps((t ? left1 : left0) - BN * j);
+        };
+        auto first_at = [&](int t, int j) {
+            return kWindow ? t ? first_step(win, 1, j0 + j) : first_step(win, 0, j0 + j) : 0;
+        };
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
         if (nkv < 0) return;
@@ -464,7 +496,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             q_ph ^= 1u << t;
             if (!wait(bars.k_full[ks], kr.phase())) return;
             tc_fence_after();
-            issue_s(t, ks, key_steps(left_of(t, 0)));
+            issue_s(t, ks, first_at(t, 0), steps_at(t, 0));
             if (n == 1) commit(bars.q_empty[t]);
         }
         ++kr.i;
@@ -475,9 +507,9 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             bool have_next_k = false;
 #pragma unroll 1
             for (int t = 0; t < NQT; ++t) {
-                const int n = t ? n1 : n0, left = left_of(t, j);
+                const int n = t ? n1 : n0;
                 if (j >= n) continue;
-                const int steps = key_steps(left), next_steps = key_steps(kWindow ? left_of(t, j + 1) : left - BN);
+                const int steps = steps_at(t, j), next_steps = steps_at(t, j + 1);
                 if (!wait(bars.p_full[t], (p_ph >> t) & 1)) return;
                 p_ph ^= 1u << t;
                 if (j == 0) {
@@ -486,7 +518,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                     of_ph ^= 1u << t;
                 }
                 tc_fence_after();
-                issue_pv(t, vs, j > 0, steps);
+                issue_pv(t, vs, j > 0, first_at(t, j), steps);
                 if (j == n - 1) commit(bars.o_done[t]);
                 if (j + 1 < n) {
                     if (!have_next_k) {
@@ -494,7 +526,7 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                         have_next_k = true;
                         tc_fence_after();
                     }
-                    issue_s(t, nks, next_steps);
+                    issue_s(t, nks, first_at(t, j + 1), next_steps);
                     if (j + 1 == n - 1) commit(bars.q_empty[t]);
                 }
             }
@@ -707,7 +739,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             // unit's few masked tiles, which costs more than it computes (48 packed prompts of 9 to
             // 420 tokens 63 -> 85 us, long prompts the same)
             const int key0 = key_of(sg, sg.j0 + j), left = sg.L - key0;
-            const int steps = key_steps(sg.end[t] - key0);
+            const int steps = steps_of(sg, t, sg.j0 + j);
             const int token = sg.tok[t] + my_tok;
             const int lim = min(left, ordered ? sg.ctx + token + 1 - key0 : BN);  // keys [0, lim) admitted, but for the mask
             const unsigned long long *mrow =
@@ -722,7 +754,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return false;
             tc_fence_after();
-            if (left < 16 * steps && (t == 0 || j >= sg.n[0] || left >= 16 * key_steps(sg.end[0] - key0))) {
+            if (left < 16 * steps && (t == 0 || j >= sg.n[0] || left >= 16 * steps_of(sg, 0, sg.j0 + j))) {
                 // V rows of the last MMA step behind the entry's end (another sequence's, stale
                 // slots; NaN times p = 0 would be NaN): zeroed, by the query tile whose value
                 // contraction comes first.  (V landed with K, before the scores waited for.)
@@ -733,10 +765,10 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                     if (lrow < chunks) st_shared_v4(base + b * C::kBoxBytes + 16 * lrow, 0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-            const int chunks = (steps + 1) >> 1;
+            const int chunks = (steps + 1) >> 1, chunk0 = first_step(sg, t, sg.j0 + j) >> 1;
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = chunk0; c < chunks; ++c) {
                 uint32_t r[32];
                 tmem_ld_x32(s_addr + 32 * c, r);
                 const uint32_t bits = visible(c);
@@ -751,7 +783,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             const float m_use = m == -INFINITY ? 0.f : m;
             float sum = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = chunk0; c < chunks; ++c) {
                 uint32_t r[32], pk[16];
                 tmem_ld_x32(s_addr + 32 * c, r);
                 const uint32_t bits = visible(c);

@@ -285,6 +285,10 @@ struct BwdParams {
     int *status;
     long long watchdog_cycles;
     int window, sinks;  // sliding window (window.h); window 0: none
+    // key blocks with a sink, whose query blocks are cut into items of sink_chunk (bwd_tc.cuh);
+    // sink_chunk 0: none
+    int sink_tiles, sink_chunk;
+    float *sink_parts;  // their partial sums, in the workspace
 };
 
 // Schedule preparation: validates cu_seqlens on the device and writes the
@@ -294,6 +298,7 @@ struct BwdParams {
 struct PrepJob {
     int H, block, rows_are_keys, splits;
     Sched sched;
+    int sink_tiles, sink_chunk;  // BwdParams
 };
 struct PrepJobs {
     PrepJob job[2];

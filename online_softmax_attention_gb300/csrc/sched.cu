@@ -8,6 +8,7 @@
 // work and reads nothing out of bounds.
 #include "../../include/attn.h"
 #include "common.cuh"
+#include "window.h"
 
 namespace attn {
 
@@ -73,7 +74,12 @@ prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, 
         int cnt = 0;
         if (b < n_seq && !bad) {
             const int len = order ? s_len[s_order[b]] : length(b);
-            cnt = (len + block - 1) / block * H * splits;
+            int tiles = (len + block - 1) / block;
+            if (job.sink_chunk) {
+                const SinkItems sink = sink_items(tiles, job.sink_tiles, job.sink_chunk);
+                tiles += sink.tiles * (sink.chunks - 1);
+            }
+            cnt = tiles * H * splits;
         }
         // inclusive scan across the block
         int x = cnt;

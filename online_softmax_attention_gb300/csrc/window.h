@@ -36,6 +36,22 @@ ATTN_HD long long skipped_tiles(int window, int sinks, int ctx, int per, int n) 
     return i0 < n ? floor_sum((int)(n - i0), per, (int)(b + i0 * per)) : 0;
 }
 
+// dK / dV items of a head of a sequence of `blocks` key (and query) blocks.  A block with a sink
+// is seen by all queries behind it; where those are more than `chunk` blocks they are cut into
+// chunks, an item each, so that no item is much longer than those of a window.
+struct SinkItems {
+    int tiles;   // blocks with a sink
+    int chunks;  // items of each
+};
+ATTN_HD SinkItems sink_items(int blocks, int sink_tiles, int chunk) {
+    return {sink_tiles < blocks ? sink_tiles : blocks, chunk > 0 && blocks > chunk ? (blocks - 1) / chunk + 1 : 1};
+}
+// Slots of partial sums of a head, and the first one of a sequence whose blocks are cut: it has more
+// than chunk blocks, so rows / (128 chunk), at most doubled, holds its chunks.
+ATTN_HD long long sink_slot(long long row, int sink_tiles, int chunk) {
+    return 2ll * sink_tiles * (row / (128ll * chunk));
+}
+
 // The keys that a row of a tree sees: below `hi`, or from `lo` on, of the ctx keys before the
 // new tokens and the new tokens u < T whose bits are set in `mask`.
 struct RowWindow {
