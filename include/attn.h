@@ -383,6 +383,8 @@ typedef struct attn_weigh_args {
     const int32_t *seqs;    /* device, n sequences */
     const int32_t *cu;      /* device, n + 1 offsets from 0 */
     const int32_t *fresh;   /* device, n: last tokens whose weight starts anew; NULL: the new ones */
+    void *workspace;        /* attn_weigh_workspace_bytes() bytes, 256-byte aligned; NULL where that is 0 */
+    size_t workspace_bytes;
 } attn_weigh_args;
 
 /* The weights by which attn_cache_evict chooses: (n_layers, max_seqs, cols) f32. */
@@ -554,9 +556,11 @@ ATTN_API int attn_cache_compact(const attn_cache *c, int32_t *remap, void *works
                                 size_t workspace_bytes, void *stream);
 
 /* Adds the attention that cached tokens get from new ones to their weights (see
- * attn_weigh_args).  One kernel on `stream`; no workspace.  Calls on the same rows of
- * weights must be ordered by the caller. */
+ * attn_weigh_args).  Calls on the same rows of weights must be ordered by the caller, and
+ * calls that may overlap need a workspace each; its size depends on sizes only (0 for few
+ * query rows an entry, f32, windows, pages below 8 rows, and arguments that are refused). */
 ATTN_API int attn_cache_weigh(const attn_weigh_args *a, void *stream);
+ATTN_API size_t attn_weigh_workspace_bytes(const attn_weigh_args *a);
 
 /* Cuts every listed sequence of more than budgets[i] tokens to that many: its first `sinks`,
  * its last `recent`, and the heaviest of the others by the sum of their weights over the

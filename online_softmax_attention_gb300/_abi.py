@@ -37,7 +37,7 @@ EXPORTS = (
     "attn_cache_workspace_bytes", "attn_cache_extend", "attn_cache_write", "attn_cache_fork",
     "attn_cache_keep", "attn_cache_free", "attn_cache_compact",
     "attn_weigh_args_size", "attn_weights_size", "attn_cache_weigh", "attn_cache_evict",
-    "attn_cache_evict_workspace_bytes",
+    "attn_cache_evict_workspace_bytes", "attn_weigh_workspace_bytes",
 )
 
 
@@ -111,6 +111,7 @@ class WeighArgs(ctypes.Structure):
         ("cols", ctypes.c_int32), ("n", ctypes.c_int32), ("n_q", ctypes.c_int32),
         ("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
         ("seqs", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("fresh", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -195,6 +196,7 @@ def load() -> ctypes.CDLL:
         "attn_weigh_args_size": (sz, []),
         "attn_weights_size": (sz, []),
         "attn_cache_weigh": (ctypes.c_int, [wa, vp]),
+        "attn_weigh_workspace_bytes": (sz, [wa]),
         "attn_cache_evict": (ctypes.c_int, [cc, vp, vp, i32, wt, i32, i32, vp, sz, vp]),
         "attn_cache_evict_workspace_bytes": (sz, [cc, i32, i32]),
         "attn_launch_count": (ctypes.c_uint64, []),

@@ -29,7 +29,7 @@ FWD = struct.Struct("@" + _TENSOR * 4 + "P" + "iiii" + "f" + "iiii" + "PP" + "PN
 BWD = struct.Struct("@" + _TENSOR * 5 + "P" + _TENSOR * 3 + "iiii" + "f" + "iiiii" + "PP" + "PN" + "ii" + "f" + "iiii" + "0P")
 CACHE = struct.Struct("@" + "PP" + "qqqq" + "PPP" + "q" + "iiiiiiii" + "0P")
 TREE = struct.Struct("@" + "%ds" % CACHE.size + "ii" + _TENSOR * 2 + "PPPP" + "iii" + "f" + "i" + "PN" + "ii" + "0P")
-WEIGH = struct.Struct("@" + "%ds" % CACHE.size + "ii" + _TENSOR + "PP" + "q" + "iii" + "f" + "ii" + "PPP" + "0P")
+WEIGH = struct.Struct("@" + "%ds" % CACHE.size + "ii" + _TENSOR + "PP" + "q" + "iii" + "f" + "ii" + "PPP" + "PN" + "0P")
 WEIGHTS = struct.Struct("@" + "Pqq" + "ii" + "0P")
 VIEW = struct.Struct("@" + _TENSOR)
 for _s, _c in ((FWD, _abi.FwdArgs), (BWD, _abi.BwdArgs), (CACHE, _abi.Cache), (TREE, _abi.TreeArgs),

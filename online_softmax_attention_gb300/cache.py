@@ -233,11 +233,13 @@ class Cache:
         T, H, _ = q.shape
         if tuple(lse.shape) != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
             raise ValueError(f"lse must be contiguous float32 {(H, T)} on the cache's device")
-        self._call_packed("attn_cache_weigh", _host.WEIGH.pack(
-            self.args, int(layer), H, *q_fields, lse.data_ptr(), w[int(layer)].data_ptr(),
-            w.stride(1) if self.max_seqs > 1 else w.shape[2], w.shape[2], n, T,
-            _host.f32(scale) if scale is not None else D ** -0.5, *_host.window(window, sinks), seqs.data_ptr(),
-            cu.data_ptr(), fresh.data_ptr() if fresh is not None else 0))
+        head = (self.args, int(layer), H, *q_fields, lse.data_ptr(), w[int(layer)].data_ptr(),
+                w.stride(1) if self.max_seqs > 1 else w.shape[2], w.shape[2], n, T,
+                _host.f32(scale) if scale is not None else D ** -0.5, *_host.window(window, sinks), seqs.data_ptr(),
+                cu.data_ptr(), fresh.data_ptr() if fresh is not None else 0)
+        need = _host.call(dev.index, _host.entry("attn_weigh_workspace_bytes"), None, _host.WEIGH.pack(*head, 0, 0))
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        self._call_packed("attn_cache_weigh", _host.WEIGH.pack(*head, ws.data_ptr() if need else 0, need))
 
     def evict(self, seqs, budgets, weights: torch.Tensor, *, sinks: int = 0, recent: int = 0) -> None:
         """Cuts every sequence ``seqs[i]`` of more than ``budgets[i]`` tokens to that many: the first

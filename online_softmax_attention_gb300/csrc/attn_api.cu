@@ -585,7 +585,7 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
 }
 
 // Validates the arguments of the accumulation of attention weights.
-int plan_weigh(const attn_weigh_args *a, WeighParams &p) {
+int plan_weigh(const attn_weigh_args *a, WeighParams &p, bool check_views = true) {
     if (!a) return ATTN_EINVAL;
     std::memset(&p, 0, sizeof(p));
     const int rc = plan_cache(&a->cache, p.c);
@@ -596,7 +596,7 @@ int plan_weigh(const attn_weigh_args *a, WeighParams &p) {
     if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return ATTN_EINVAL;
     if ((int64_t)a->n_q * a->H > kMostTokens || a->cols > kMostTokens) return ATTN_EUNSUPPORTED;
     if (check_window(a->window, a->sinks, ATTN_CAUSAL)) return ATTN_EINVAL;
-    if (a->n > 0 && (!aligned4(a->seqs) || !aligned4(a->cu) || (reinterpret_cast<uintptr_t>(a->fresh) & 3) ||
+    if (check_views && a->n > 0 && (!aligned4(a->seqs) || !aligned4(a->cu) || (reinterpret_cast<uintptr_t>(a->fresh) & 3) ||
                      (a->cols > 0 && !aligned4(a->weights)) || !valid_view(a->q, a->cache.dtype, a->n_q > 0) ||
                      (a->n_q > 0 && !aligned4(a->lse))))
         return ATTN_EINVAL;
@@ -1091,9 +1091,20 @@ int attn_cache_weigh(const attn_weigh_args *a, void *stream) {
     WeighParams p;
     const int rc = plan_weigh(a, p);
     if (rc || a->n == 0) return rc;
+    const bool tc = weigh_on_tc(p);
+    if (tc && (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255) ||
+               a->workspace_bytes < weigh_tc_bytes(a->workspace, p)))
+        return ATTN_EWORKSPACE;
     if (!(p.c.status = status_ptr())) return ATTN_ECUDA;
-    const cudaError_t e = launch_cache_weigh(p, static_cast<cudaStream_t>(stream));
+    p.watchdog_cycles = watchdog_cycles();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = tc ? launch_weigh_tc(p, s) : launch_cache_weigh(p, s);
     return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+}
+
+size_t attn_weigh_workspace_bytes(const attn_weigh_args *a) {
+    WeighParams p;
+    return plan_weigh(a, p, false) == ATTN_OK && weigh_on_tc(p) ? weigh_tc_bytes(nullptr, p) : 0;
 }
 
 size_t attn_cache_evict_workspace_bytes(const attn_cache *c, int32_t n, int32_t cols) {

@@ -229,7 +229,20 @@ struct WeighParams {
     unsigned long long group_inv;  // group_inverse(group)
     int window, sinks;
     float scale_log2;
+    // on the tensor cores (weigh_tc.cu): parts of units cut between blocks, two slots of 256 sums a
+    // block, and the blocks' notes for the merge
+    float *slots;
+    struct WeighCut *cut;
+    long long watchdog_cycles;
 };
+struct WeighCut {
+    int last;           // block that holds the unit's last part; <= the writing block: nothing to merge
+    int s, key0;        // sequence, first key
+    int L, fresh;       // of the entry
+};
+bool weigh_on_tc(const WeighParams &p);
+size_t weigh_tc_bytes(void *workspace, WeighParams &p);  // lays the workspace out; its bytes
+cudaError_t launch_weigh_tc(const WeighParams &p, cudaStream_t s);
 cudaError_t launch_cache_weigh(const WeighParams &p, cudaStream_t s);
 
 // Eviction: the weights, and what the plan hands to the kernel that moves the rows.

@@ -139,3 +139,61 @@ def test_arguments_that_are_refused():
         cache.weigh(seqs, [0, 1], q.float(), lse, w)
     cache.weigh(seqs, [0, 0], q[:0], lse[:, :0].contiguous(), w)  # no rows: nothing to add
     assert (w == 0).all() and attn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float16, 64)])
+@pytest.mark.parametrize("lens,news,page,heads,group", [
+    ([1500], [1500], 16, 2, 4), ([900, 3, 700, 128], [300, 3, 0, 128], 8, 1, 3), ([2000, 1300], [64, 200], 64, 8, 4),
+    ([127, 128, 129], [127, 128, 129], 128, 3, 1), ([300] * 40, [20] * 40, 32, 2, 5), ([5000], [77], 1024, 1, 128),
+    ([600, 600], [1, 599], 16, 4, 16)])
+def test_many_rows(lens, news, page, heads, group, d, dtype):
+    """Tensor-core units: tiles of rows that the group does not fill, new tokens over several key tiles,
+    units cut between blocks, entries without new tokens beside others."""
+    cache, model, seqs, g = make(lens, page, heads, d, dtype, 88)
+    q = torch.randn(sum(news), heads * group, d, generator=g).to(dtype)
+    first = check(cache, model, seqs, news, q, what=f"{lens}")
+    again = check(cache, model, seqs, news, q)
+    assert torch.equal(first[..., :-1], again[..., :-1])
+    check(cache, model, seqs, news, q, fresh=lens, what=f"{lens} fresh")
+    check(cache, model, seqs, news, q, scale=-0.1, what=f"{lens} scaled")
+
+
+def test_other_rows_and_stale_slots_may_hold_anything():
+    """Query rows of no entry, and cached slots behind the sequences, with NaN in them."""
+    cache, model, seqs, g = make([300, 70], 16, 2, 64, torch.bfloat16, 89)
+    q = torch.randn(150, 8, 64, generator=g).bfloat16().cuda()
+    lse = attn.tree_fwd(q[:110], cache, seqs, [0, 50, 110])[1]
+    w, want = cache.new_weights(), cache.new_weights()
+    cache.weigh(seqs, [0, 50, 110], q[:110], lse, want)
+    q[110:] = float("nan")
+    more = torch.full((8, 150), float("nan"), device="cuda")
+    more[:, :110] = lse
+    cache.weigh(seqs, [0, 50, 110], q, more, w)
+    assert torch.equal(w, want) and torch.isfinite(w).all() and attn.device_status() == 0
+
+
+def test_workspaces_streams_and_graphs():
+    cache, model, seqs, g = make([700, 300], 16, 2, 64, torch.bfloat16, 90)
+    q = torch.randn(200, 8, 64, generator=g).bfloat16().cuda()
+    lse = attn.tree_fwd(q, cache, seqs, [0, 120, 200])[1]
+    want = cache.new_weights()
+    ids, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (seqs, [0, 120, 200]))
+    cache.weigh(ids, cu, q, lse, want)
+    torch.cuda.synchronize()
+    outs = [cache.new_weights() for _ in range(3)]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, w in zip(side, outs):
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                w.zero_()
+                cache.weigh(ids, cu, q, lse, w)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        outs[2].zero_()
+        cache.weigh(ids, cu, q, lse, outs[2])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, want) for w in outs)
