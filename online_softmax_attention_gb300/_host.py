@@ -88,7 +88,8 @@ _NATIVE = os.path.join(os.path.dirname(_abi.LIB_PATH), "_native.so")
 # the entry points that csrc/binding.cpp calls, in its order
 _NATIVE_CALLS = ("attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_workspace_bytes", "attn_tree_fwd",
                  "attn_tree_workspace_bytes", "attn_cache_workspace_bytes", "attn_cache_extend", "attn_cache_fork",
-                 "attn_cache_keep", "attn_cache_free", "attn_cache_write")
+                 "attn_cache_keep", "attn_cache_free", "attn_cache_write", "attn_cache_weigh", "attn_weigh_workspace_bytes",
+                 "attn_cache_evict", "attn_cache_evict_workspace_bytes")
 _native = None
 
 

@@ -219,6 +219,9 @@ class Cache:
 
         The arguments are those of ``tree_fwd`` (without a mask), ``lse`` what it returned.  The
         last ``fresh[i]`` tokens' weights start anew (None: the new tokens', ``cu[i + 1] - cu[i]``)."""
+        if self._done("attn_cache_weigh", self._native.weigh(self.args, self._index, seqs, cu_seqlens_q, q, lse, weights, layer,
+                                                             scale, window, sinks, fresh)):
+            return
         dev, D = self.device, self.head_dim
         seqs, cu = _ints(seqs, dev, "seqs"), _ints(cu_seqlens_q, dev, "cu_seqlens_q")
         n = seqs.numel()
@@ -245,6 +248,8 @@ class Cache:
         """Cuts every sequence ``seqs[i]`` of more than ``budgets[i]`` tokens to that many: the first
         ``sinks``, the last ``recent`` and the heaviest others by ``weights`` summed over its
         layers (equal ones: the first).  Rows and weights move down; a whole list or nothing."""
+        if self._done("attn_cache_evict", self._native.evict(self.args, self._index, seqs, budgets, weights, sinks, recent)):
+            return
         seqs, budgets = self._lists(None, seqs=seqs, budgets=budgets)
         w = self._weights(weights)
         for x, name in ((sinks, "sinks"), (recent, "recent")):

@@ -40,6 +40,10 @@ struct Api {
     decltype(&attn_cache_keep) keep;
     decltype(&attn_cache_free) free;
     decltype(&attn_cache_write) write;
+    decltype(&attn_cache_weigh) weigh;
+    decltype(&attn_weigh_workspace_bytes) weigh_bytes;
+    decltype(&attn_cache_evict) evict;
+    decltype(&attn_cache_evict_workspace_bytes) evict_bytes;
 } api;
 
 // A call's conditions: the first that does not hold ends it with None.
@@ -346,6 +350,77 @@ PyObject *py_free(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return status(api.free(&c, int_ptr(s), (int32_t)s->size(0), stream_of(dev)));
 }
 
+// Weights of a cache's sequences: float32 (layers, sequences, tokens), rows of their own.
+bool weights_of(const Tensor *t, int device, const attn_cache &c, attn_weights &w) {
+    if (!on(t, device) || t->dim() != 3 || t->scalar_type() != at::kFloat || t->size(0) < 1 || t->size(1) != c.max_seqs ||
+        !fits(t->size(0)) || !fits(t->size(2)) || (t->size(2) > 1 && t->stride(2) != 1))
+        return false;
+    w.stride_seq = t->size(1) > 1 ? t->stride(1) : t->size(2);
+    w.stride_layer = t->size(0) > 1 ? t->stride(0) : t->size(1) * t->size(2);
+    if (w.stride_seq < t->size(2) || (t->size(0) > 1 && w.stride_layer < w.stride_seq * (t->size(1) - 1) + t->size(2)))
+        return false;
+    w.ptr = static_cast<float *>(t->data_ptr());
+    w.n_layers = (int32_t)t->size(0);
+    w.cols = (int32_t)t->size(2);
+    return true;
+}
+
+// weigh(cache, device, seqs, cu, q, lse, weights, layer, scale, window, sinks, fresh) -> status | None
+PyObject *py_weigh(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    attn_weigh_args a;
+    std::memset(&a, 0, sizeof(a));
+    attn_weights w;
+    int dev;
+    NEED(n == 12 && cache_of(args[0], args[1], a.cache, dev) && windowed(args[9], args[10], a.window, a.sinks));
+    const Tensor *seqs = tensor(args[2]), *cu = tensor(args[3]), *q = tensor(args[4]), *lse = tensor(args[5]);
+    long layer;
+    NEED(ints(seqs, dev) && ints(cu, dev) && cu->size(0) == seqs->size(0) + 1 && fits(seqs->size(0)));
+    NEED(q && rows(q, dev, a.cache.D, a.q) && dtype_code(*q) == a.cache.dtype && weights_of(tensor(args[6]), dev, a.cache, w) &&
+         as_long(args[7], layer) && layer >= 0 && layer < a.cache.n_layers && layer < w.n_layers);
+    const int64_t T = q->size(0), H = q->size(1);
+    NEED(T > 0 && fits(T * H) && as_scale(args[8], a.cache.D, a.scale) && on(lse, dev) && lse->scalar_type() == at::kFloat &&
+         lse->dim() == 2 && lse->size(0) == H && lse->size(1) == T && lse->is_contiguous());
+    if (args[11] != Py_None) {
+        const Tensor *fresh = tensor(args[11]);
+        NEED(ints(fresh, dev) && fresh->size(0) == seqs->size(0));
+        a.fresh = int_ptr(fresh);
+    }
+    a.layer = (int32_t)layer;
+    a.H = (int32_t)H;
+    a.lse = static_cast<const float *>(lse->data_ptr());
+    a.weights = w.ptr + layer * w.stride_layer;
+    a.weights_stride = w.stride_seq;
+    a.cols = w.cols;
+    a.n = (int32_t)seqs->size(0);
+    a.n_q = (int32_t)T;
+    a.seqs = int_ptr(seqs);
+    a.cu = int_ptr(cu);
+    const size_t bytes = api.weigh_bytes(&a);
+    Tensor ws;
+    if (bytes) {
+        ws = scratch(bytes, dev);
+        a.workspace = ws.data_ptr();
+        a.workspace_bytes = (size_t)ws.size(0);
+    }
+    return status(api.weigh(&a, stream_of(dev)));
+}
+
+// evict(cache, device, seqs, budgets, weights, sinks, recent) -> status | None
+PyObject *py_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    attn_cache c;
+    attn_weights w;
+    int dev;
+    NEED(n == 7 && cache_of(args[0], args[1], c, dev));
+    const Tensor *s = tensor(args[2]), *b = tensor(args[3]);
+    long sinks, recent;
+    NEED(ints(s, dev) && ints(b, dev) && b->size(0) == s->size(0) && fits(s->size(0)) && weights_of(tensor(args[4]), dev, c, w));
+    NEED(!PyBool_Check(args[5]) && !PyBool_Check(args[6]) && as_long(args[5], sinks) && as_long(args[6], recent) && sinks >= 0 &&
+         recent >= 0);
+    const Tensor ws = scratch(api.evict_bytes(&c, (int32_t)s->size(0), w.cols), dev);
+    return status(api.evict(&c, int_ptr(s), int_ptr(b), (int32_t)s->size(0), &w, (int32_t)sinks, (int32_t)recent,
+                            ws.data_ptr(), (size_t)ws.size(0), stream_of(dev)));
+}
+
 // init(addresses): the entry points, in Api's order
 PyObject *py_init(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 1 || !PyTuple_Check(args[0]) || (size_t)PyTuple_GET_SIZE(args[0]) * sizeof(void *) != sizeof(api)) {
@@ -385,7 +460,8 @@ PyMethodDef methods[] = {
     ENTRY("bwd", py_bwd),            ENTRY("tree", py_tree),
     ENTRY("write", py_write),        ENTRY("extend", py_alloc<false>),
     ENTRY("fork", py_alloc<true>),   ENTRY("keep", py_keep),
-    ENTRY("free", py_free),          {nullptr, nullptr, 0, nullptr},
+    ENTRY("free", py_free),          ENTRY("weigh", py_weigh),
+    ENTRY("evict", py_evict),        {nullptr, nullptr, 0, nullptr},
 };
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
