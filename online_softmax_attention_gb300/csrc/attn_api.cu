@@ -991,7 +991,7 @@ size_t attn_tree_args_size(void) { return sizeof(attn_tree_args); }
 size_t attn_tree_workspace_bytes(const attn_tree_args *a) {
     TreeParams p;
     if (plan_tree(a, p, false) != ATTN_OK) return 0;
-    return parts_layout(tree_blocks(), tree_rows(p), p.D, nullptr, p.parts);
+    return parts_layout(tree_blocks(p), tree_rows(p), p.D, nullptr, p.parts);
 }
 
 int attn_tree_fwd(const attn_tree_args *a, void *stream) {
@@ -1000,7 +1000,7 @@ int attn_tree_fwd(const attn_tree_args *a, void *stream) {
     if (rc) return rc;
     if (p.n == 0 || p.n_q == 0) return ATTN_OK;
     if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255) ||
-        a->workspace_bytes < parts_layout(tree_blocks(), tree_rows(p), p.D, a->workspace, p.parts))
+        a->workspace_bytes < parts_layout(tree_blocks(p), tree_rows(p), p.D, a->workspace, p.parts))
         return ATTN_EWORKSPACE;
     if (!(p.c.status = status_ptr())) return ATTN_ECUDA;
     p.watchdog_cycles = watchdog_cycles();

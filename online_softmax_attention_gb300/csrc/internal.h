@@ -180,7 +180,7 @@ struct TreeParams {
 // Query rows (token, head of the group) of a work unit (kGroupRows: the
 // tensor-core kernel of group_tc.cuh), and the grid.
 int tree_rows(const TreeParams &p);
-int tree_blocks();
+int tree_blocks(const TreeParams &p);
 
 // Grouped attention on the tensor cores with packed query rows (group_tc.cuh):
 // over contiguous keys (prompts) or a cache.

@@ -38,15 +38,16 @@ struct Stretch {
         const long long last = (u0 + lead + n - 1) / share;
         return (int)(tile(last * share, u0, n) == n ? last - 1 : last);
     }
-    // Block b's part of a line of that much work, cut for `blocks` blocks (see find_stretch);
-    // false: nothing.
-    ATTN_HD bool take(Work total, unsigned blocks, unsigned b, int turn, int unit_lead, int lead_share) {
+    // Block b's part of a line of that much work, cut for `blocks` blocks (see find_stretch), parts of
+    // `least` positions and more; false: nothing.
+    ATTN_HD bool take(Work total, unsigned blocks, unsigned b, int turn, int unit_lead, int lead_share, int least = 1) {
         const bool long_enough = total.tiles >= (long long)lead_share * blocks;
         lead = long_enough ? unit_lead : 0;
         snap = long_enough && unit_lead ? 2 : 0;
         const long long all = length(total);
         share = all < 0x7fffffff - (long long)blocks ? (long long)(((unsigned)all + blocks - 1) / blocks)
                                                      : (all + blocks - 1) / blocks;
+        if (share < least) share = least;
         if (share > turn) share = (share + turn - 1) / turn * turn;
         at = b * share;
         end = at + share < all ? at + share : all;

@@ -49,10 +49,10 @@ __device__ __forceinline__ Work block_prefix(Work x, Work &total) {
 // The block's stretch; work(i, report): the Work of entry i.  A unit counts kLead more
 // positions than tiles where blocks have `kLeadShare` tiles and more (units are counted
 // only then: kLead = 0 leaves them out); the share is a multiple of `turn` where it is
-// longer than that.  False: no work.
+// longer than that, and `least` at least.  False: no work.
 constexpr int kLeadShare = 12;
 template <int kWarps, int kLead, typename F>
-__device__ __forceinline__ bool find_stretch(int n, int turn, F work, Stretch &s) {
+__device__ __forceinline__ bool find_stretch(int n, int turn, F work, Stretch &s, int least = 1) {
     __shared__ int s_entry;
     __shared__ long long s_before;
     __shared__ Work s_work;
@@ -80,7 +80,7 @@ __device__ __forceinline__ bool find_stretch(int n, int turn, F work, Stretch &s
             if (n > 32 * kWarps && s.at < s.length(carry)) break;  // the same for every thread
         }
         if (pass == 1) break;
-        if (!s.take(carry, gridDim.x, blockIdx.x, turn, kLead, kLeadShare)) return false;
+        if (!s.take(carry, gridDim.x, blockIdx.x, turn, kLead, kLeadShare, least)) return false;
     }
     __syncthreads();
     s.entry = s_entry;

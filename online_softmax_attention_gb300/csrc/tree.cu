@@ -35,11 +35,16 @@ namespace attn {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+// Warps of a block; with as many warps an SM, blocks of an SM.
+#ifndef ATTN_WINDOW_WARPS
+#define ATTN_WINDOW_WARPS 2
+#endif
+constexpr int warps_of(bool window, bool f32) { return window && !f32 ? ATTN_WINDOW_WARPS : 4; }
+constexpr int per_sm(bool window, bool f32) { return 4 / warps_of(window, f32); }
 
-template <typename T, int D>
+template <typename T, int D, bool kWindow>
 struct Cfg {
+    static constexpr int kWarps = warps_of(kWindow, sizeof(T) == 4), kThreads = 32 * kWarps;
     static constexpr int kRows = 16;
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kKeys = kRowBytes > 256 ? 16 : 32;  // keys of a tile
@@ -53,7 +58,7 @@ struct Cfg {
     static_assert(kMergeBytes <= kRingBytes, "the rings hold the warps' sums at a unit's end");
     static constexpr int kQBytes = kRows * kRowBytes;
     static constexpr int kSmem = kRingBytes + kQBytes + kWarps * kRows * 8;
-    static_assert(kSmem + 1024 <= 232448, "shared memory budget");
+    static_assert((kSmem + 1024 + 256) * per_sm(kWindow, sizeof(T) == 4) <= 233472, "shared memory budget");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -138,8 +143,9 @@ __device__ __forceinline__ void store_out(const TreeParams &p, int token, int he
 }
 
 template <typename T, typename Tout, int D, bool kWindow>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
-    using C = Cfg<T, D>;
+__global__ void __launch_bounds__(32 * warps_of(kWindow, sizeof(T) == 4), per_sm(kWindow, sizeof(T) == 4)) tree_kernel(const TreeParams p) {
+    using C = Cfg<T, D, kWindow>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int kRows = C::kRows, kKeys = C::kKeys;
     constexpr bool kMma = sizeof(T) == 2;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -154,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
 
     Stretch st;
     const bool any = find_stretch<kWarps, 0>(
-        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at<kWindow>(p, i, kRows, kKeys, report).tiles}; }, st);
+        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at<kWindow>(p, i, kRows, kKeys, report).tiles}; }, st,
+        kWindow ? kWarps : 1);  // (a tile a warp at least: one sequence, window 1024: 14.5 us, 20.5 with a tile a block)
     if (!any) {
         if (tid == 0) p.parts.cut[blockIdx.x].last = -1;
         return;
@@ -481,14 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeParams p) {
     }
 }
 
-template <typename T, typename Tout, int D>
+template <typename T, typename Tout, int D, bool kWindow>
 cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
-    using C = Cfg<T, D>;
-    auto kern = p.window ? tree_kernel<T, Tout, D, true> : tree_kernel<T, Tout, D, false>;
+    using C = Cfg<T, D, kWindow>;
+    auto kern = tree_kernel<T, Tout, D, kWindow>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int blocks = tree_blocks();
-    e = launch_pdl(kern, dim3(blocks), dim3(kThreads), C::kSmem, s, p);
+    const int blocks = tree_blocks(p);
+    e = launch_pdl(kern, dim3(blocks), dim3(C::kThreads), C::kSmem, s, p);
     count_launch();
     if (e != cudaSuccess) return e;
     PartsMergeParams m;
@@ -506,9 +513,14 @@ cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
     return launch_parts_merge(m, s);
 }
 
+template <typename T, typename Tout, int D>
+cudaError_t launch_window(const TreeParams &p, cudaStream_t s) {
+    return p.window ? launch_typed<T, Tout, D, true>(p, s) : launch_typed<T, Tout, D, false>(p, s);
+}
+
 template <typename T, typename Tout>
 cudaError_t launch_d(const TreeParams &p, cudaStream_t s) {
-    return p.D == 64 ? launch_typed<T, Tout, 64>(p, s) : launch_typed<T, Tout, 128>(p, s);
+    return p.D == 64 ? launch_window<T, Tout, 64>(p, s) : launch_window<T, Tout, 128>(p, s);
 }
 
 template <typename T>
@@ -519,7 +531,7 @@ cudaError_t launch_out(const TreeParams &p, cudaStream_t s) {
 
 }  // namespace
 
-int tree_blocks() { return sm_count(); }
+int tree_blocks(const TreeParams &p) { return tree_rows(p) == kGroupRows ? sm_count() : sm_count() * per_sm(p.window > 0, p.dtype == ATTN_F32); }
 
 // Entries of more than 16 rows on average take the tensor-core kernel's units: the
 // keys are read once for up to 256 rows (32 sequences of 2000-4000 tokens, 32 key heads'
