@@ -42,6 +42,8 @@
 // their code.
 #pragma once
 
+#include <cfloat>
+
 #include "sm100.cuh"
 #include "tc.h"
 #include "window.h"
@@ -183,6 +185,24 @@ __device__ __forceinline__ void zero_cols(T *dst, int n) {
 }
 
 // =============================== dK, dV =======================================
+
+// Bits of the columns [u, u + 32) that are below `lim`.
+__device__ __forceinline__ uint32_t bits_below(int lim, int u) {
+    const int n = lim - u;
+    return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
+}
+
+// Scores of the columns whose bit is not set: -inf, whose exponential is 0 and with it P and dS.
+// (Ahead of the exponentials: zeroing P, its 16-bit form and dS behind them takes three times the
+// instructions, and a window masks most of the blocks.)
+__device__ __forceinline__ void hide(uint32_t (&s)[2][32], const uint32_t (&bits)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (__all_sync(0xffffffffu, bits[h] == 0xffffffffu)) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[h][e] = (bits[h] >> e) & 1 ? s[h][e] : 0xff800000u;
+    }
+}
 
 struct DkdvInfo {
     int q_start, Lq, k_start, Lk, h, key0, qb0, t;
@@ -594,7 +614,8 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
     const int quarter = warp & 3;
     const int kl = 32 * quarter + lane;    // key row inside the tile = TMEM lane
     const uint32_t lane_base = tmem_addr(tmem, 32 * quarter, 0);
-    const float sl2 = fabsf(p.scale_log2);  // the score MMA negated S for a negative scale
+    // the score MMA negated S for a negative scale; with a window never 0, so that -inf stays -inf
+    const float sl2 = kWindow ? fmaxf(fabsf(p.scale_log2), FLT_MIN) : fabsf(p.scale_log2);
     uint32_t st_cnt = 0, dp_cnt = 0, ad_cnt = 0, stat_i = 0;
 
     for (int i = 0;; ++i) {
@@ -629,9 +650,14 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
         int qh = 0;  // block x of the item is block qh of its query head
         for (int x = 0; x < f.nq; ++x) {
             const bool diag = p.causal && (f.qb0 + qh == f.t);  // query block == key block
-            // queries of the block, from this one on, that no longer see the lane's key
-            int q_end = BT;
-            if (kWindow && key >= p.sinks) q_end = (int)min((long long)BT, (long long)key + p.window - BT * (f.qb0 + qh));
+            uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // of the warpgroup's queries: those that see the lane's key
+            if constexpr (kWindow) {
+                const int q_begin = diag ? kl : 0;
+                const int q_end = key < p.sinks ? BT : (int)min((long long)BT, (long long)key + p.window - BT * (f.qb0 + qh));
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    seen[h] = bits_below(q_end, 64 * wg + 32 * h) & ~bits_below(q_begin, 64 * wg + 32 * h);
+            }
             if (++qh == f.nqh) {  // the next block is the first of the group's next query head
                 qh = 0;
                 stat_src += p.n_q;
@@ -655,6 +681,7 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
             tmem_ld_x32(lane_base + 64 * wg + 32, r[1]);
             tmem_ld_wait(r[0]);
             tmem_ld_wait(r[1]);
+            if constexpr (kWindow) hide(r, seen);
             float2 pr[32];
             const float2 sc2 = make_float2(sl2, sl2);
             uint32_t pk[32];
@@ -667,7 +694,7 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
                 pr[c] = pv;
                 pk[c] = pack2(pv.x, pv.y, kBF16);
             }
-            if (diag) {
+            if (!kWindow && diag) {
                 // queries before the key: P^T = 0 (whatever their discarded exponentials
                 // gave); kept out of the loop above, which every block runs
 #pragma unroll
@@ -679,19 +706,6 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
                     } else if (kl > q) {
                         pr[c].x = 0.f;
                         pk[c] &= 0xFFFF0000u;  // the pair's first value
-                    }
-                }
-            }
-            if (kWindow && __any_sync(0xffffffffu, q_end < BT)) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const int q = 64 * wg + 2 * c;
-                    if (q >= q_end) {
-                        pr[c] = make_float2(0.f, 0.f);
-                        pk[c] = 0u;
-                    } else if (q + 1 >= q_end) {
-                        pr[c].y = 0.f;
-                        pk[c] &= 0xFFFFu;  // the pair's second value
                     }
                 }
             }
@@ -1075,6 +1089,11 @@ using DqInfoOf = std::conditional_t<kWindow, WindowDqInfo, DqInfo>;
 // Key block j of the item.
 __device__ __forceinline__ int block_of(const DqInfo &, int j) { return j; }
 __device__ __forceinline__ int block_of(const WindowDqInfo &f, int j) { return f.list.at(j); }
+// MMA steps of 16 keys that hold one which is seen: blocks ahead of the window hold sinks, and no more.
+__device__ __forceinline__ int steps_of(const DqInfo &, int, int) { return BT / 16; }
+__device__ __forceinline__ int steps_of(const WindowDqInfo &f, int j, int sinks) {
+    return j < f.list.sinks ? min(BT / 16, (sinks - BT * j + 15) >> 4) : BT / 16;
+}
 
 template <bool kWindow>
 __device__ __forceinline__ DqInfoOf<kWindow> dq_info(const BwdParams &p, int w) {
@@ -1179,6 +1198,8 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
     // S with a negative scale: negate Q (the A operand) so P uses |scale|
     const uint32_t idS = idSS | (p.scale_log2 < 0.f ? (1u << 13) : 0u);
     constexpr uint32_t idTS = idesc_f16(kBF16, BT, D, 1);
+    // the same over fewer keys
+    auto of_steps = [&](uint32_t id, int steps) { return kWindow ? (id & ~(63u << 17)) | ((uint32_t)(2 * steps) << 17) : id; };
     uint32_t q_cnt = 0, af_cnt = 0;
     // key blocks taken before this item: block g uses K / V slots g % KS, g % VS,
     // and is the g-th phase of s_free, dp_free and (alternating) ds_ready
@@ -1212,9 +1233,9 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
         if (!wait(bars.k_full[g0 % KS], (g0 / KS) & 1)) return;
         tc_fence_after();
         if (elect_one()) {
-            issue_ss(0, dq_desc, sK + (g0 % KS) * C::kTileBytes, idS);  // S = Q K^T
+            issue_ss(0, dq_desc, sK + (g0 % KS) * C::kTileBytes, of_steps(idS, steps_of(f, 0, p.sinks)));  // S = Q K^T
             tc_commit(smem_u32(&bars.s_full));
-            issue_ss(BT, ddo_desc, sV + (g0 % VS) * C::kTileBytes, idSS);  // dP = dO V^T
+            issue_ss(BT, ddo_desc, sV + (g0 % VS) * C::kTileBytes, of_steps(idSS, steps_of(f, 0, p.sinks)));  // dP = dO V^T
             tc_commit(smem_u32(&bars.dp_full));
             tc_commit(smem_u32(&bars.v_empty[g0 % VS]));
         }
@@ -1249,13 +1270,13 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
                     tc_fence_after();
                     if (step == 0) {
                         if (more) {
-                            issue_ss(0, dq_desc, sK + ((g + 1) % KS) * C::kTileBytes, idS);
+                            issue_ss(0, dq_desc, sK + ((g + 1) % KS) * C::kTileBytes, of_steps(idS, steps_of(f, j + 1, p.sinks)));
                             tc_commit(smem_u32(&bars.s_full));
                         }
                         step = 1;
                     } else if (step == 1) {
                         if (more) {
-                            issue_ss(BT, ddo_desc, sV + ((g + 1) % VS) * C::kTileBytes, idSS);
+                            issue_ss(BT, ddo_desc, sV + ((g + 1) % VS) * C::kTileBytes, of_steps(idSS, steps_of(f, j + 1, p.sinks)));
                             tc_commit(smem_u32(&bars.dp_full));
                             tc_commit(smem_u32(&bars.v_empty[(g + 1) % VS]));
                         }
@@ -1263,9 +1284,15 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
                     } else {
                         const uint64_t kd = nmaj + sdesc_step(sK + (g % KS) * C::kTileBytes);
                         const uint32_t ds_col = tmem + 256 + 64 * (j & 1);
+                        const int steps = steps_of(f, j, p.sinks);
+                        if (steps == BT / 16) {
 #pragma unroll
-                        for (int kk = 0; kk < BT / 16; ++kk)  // dQ += dS K
-                            mma_ts(tmem + 384, ds_col + 8 * kk, sdesc_add(kd, kk * 2048), idTS, j > 0 || kk > 0);
+                            for (int kk = 0; kk < BT / 16; ++kk)  // dQ += dS K
+                                mma_ts(tmem + 384, ds_col + 8 * kk, sdesc_add(kd, kk * 2048), idTS, j > 0 || kk > 0);
+                        } else {
+                            for (int kk = 0; kk < steps; ++kk)
+                                mma_ts(tmem + 384, ds_col + 8 * kk, sdesc_add(kd, kk * 2048), idTS, j > 0 || kk > 0);
+                        }
                         tc_commit(smem_u32(&bars.k_empty[g % KS]));
                         ++j;
                         step = 0;
@@ -1298,7 +1325,8 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
     const int quarter = warp & 3;
     const int rl = 32 * quarter + lane;
     const uint32_t lane_base = tmem_addr(tmem, 32 * quarter, 0);
-    const float sl2 = fabsf(p.scale_log2);  // the score MMA negated S for a negative scale
+    // (as in dK / dV)
+    const float sl2 = kWindow ? fmaxf(fabsf(p.scale_log2), FLT_MIN) : fabsf(p.scale_log2);
     uint32_t s_cnt = 0, dp_cnt = 0, ad_cnt = 0, step = 0;
 
     for (int i = 0;; ++i) {
@@ -1329,6 +1357,16 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
             tmem_ld_wait(rs[1]);
             tc_fence_before();
             mbar_arrive_warp(smem_u32(&bars.s_free));  // the S buffer may be overwritten
+            if constexpr (kWindow) {
+                // keys up to the row and the sequence's end, from the row's window on or among the sinks
+                const int key0 = BT * block_of(f, j), c0 = 64 * wg;
+                const int lim = min(f.Lk, row + 1) - key0, from = row + 1 - p.window - key0, sink = p.sinks - key0;
+                uint32_t seen[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    seen[h] = bits_below(lim, c0 + 32 * h) & (~bits_below(from, c0 + 32 * h) | bits_below(sink, c0 + 32 * h));
+                hide(rs, seen);
+            }
 
             // P = 2^(S scale log2e - lse2), in place of S, while dP may still be in flight
             const float2 sc2 = make_float2(sl2, sl2), nl2 = make_float2(-lse2, -lse2);
@@ -1363,7 +1401,7 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
                 lim = min(f.Lk - key0, p.causal ? row - key0 + 1 : BT);
             const int c0 = 64 * wg;
             const float2 ndr2 = make_float2(-drr, -drr);
-            const bool masked = lim < BT;
+            const bool masked = !kWindow && lim < BT;
             uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
@@ -1383,18 +1421,6 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
                     const int col = c0 + 2 * c;
                     if (col >= lim) pk[c] = 0u;
                     else if (col + 1 >= lim) pk[c] &= 0xFFFFu;  // the pair's second value
-                }
-            }
-            if constexpr (kWindow) {
-                // keys before the row's window, but for the sinks
-                const int from = row + 1 - p.window - key0, sink = p.sinks - key0;  // in the tile
-                if (__any_sync(0xffffffffu, from > 0 && sink < BT)) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int col = c0 + 2 * c;
-                        if (col < from && col >= sink) pk[c] &= 0xFFFF0000u;  // the pair's first value
-                        if (col + 1 < from && col + 1 >= sink) pk[c] &= 0xFFFFu;
-                    }
                 }
             }
             tmem_st_x32(lane_base + 256 + 64 * (j & 1) + 32 * wg, pk);

@@ -26,11 +26,13 @@
 // head (4 * 128 operations per 2-byte key element pair), the tensor pipe beyond.
 // Every wait is bounded, as in fwd_tc.cu.
 //
-// kWindow: a sliding window with sinks (window.h).  A unit's key tiles are then a list with
-// a gap, of the tiles that hold a sink and those from its first row's window on; places
-// in the line and a part's [j0, j0 + nkv) count the list's tiles.  Masked tiles stand at
-// both ends of the window, so that a loop takes either kind; the kernels without a window
-// (group_tc.cu) are apart from those with one (group_tc_window.cu) and keep their two loops.
+// kWindow: a sliding window with sinks (window.h).  A unit's keys are then a list, the sinks and those
+// from its first row's window on, and its tiles 128 places of that list each: the sinks share
+// the window's first tile, which is put together from boxes of 16 rows (2 prompts of 14000 to 16384
+// tokens, window 2048: OLD us with whole tiles of keys, the sinks' apart, NEW so).  Behind the
+// loading warp everything counts places: a part's L, ctx and ends are given less the list's shift.
+// Masked tiles stand at both ends of the window, so that a loop takes either kind; the kernels without
+// a window (group_tc.cu) are apart from those with one (group_tc_window.cu) and keep their two loops.
 #pragma once
 
 #include <cfloat>
@@ -58,6 +60,10 @@ constexpr float kRescaleThreshold = 8.f;  // log2 units, as fwd_tc.cu
 // 73.6 / 194.6 / 960 / 120.2 us with 0, 61.6 / 182.4 / 924 / 118.8 with 1,
 // 63.1 / 183.1 / 940 / 119.0 with 2, 63.4 / 184.9 / 947 / 117.4 with 3.)
 constexpr int kLead = 1;
+// With a window, whose units are short and begin and end with masked tiles (2 prompts of 14000 to 16384
+// tokens take 9 us a unit more than its window's tiles).  (Trees of 63 drafts, window 4096; 48 packed
+// prompts, window 128: 65.6 / 76.6 us with 1, 62.1 / 78.1 with 3, 62.0 / 77.3 with 6.)
+constexpr int kWindowLead = 6;
 
 template <int D>
 struct Cfg {
@@ -70,12 +76,19 @@ struct Cfg {
     static constexpr int kRegsProducer = D == 128 ? 88 : 72;
     static constexpr int kRegsSoftmax = D == 128 ? 208 : 216;
     static_assert(128 * kRegsProducer + 256 * kRegsSoftmax <= kThreads * 168, "register split");
+    static constexpr int kRegsWindowProducer = 88, kRegsWindowSoftmax = 208;
+    static_assert(128 * kRegsWindowProducer + 256 * kRegsWindowSoftmax <= kThreads * 168, "register split");
 };
 
 struct GroupArgs {
     CUtensorMap tq, tk, tv;
     GroupParams p;
 };
+struct WindowGroupArgs : GroupArgs {
+    CUtensorMap tk16, tv16;  // contiguous keys: boxes of 16 rows
+};
+template <bool kWindow>
+using GroupArgsOf = std::conditional_t<kWindow, WindowGroupArgs, GroupArgs>;
 
 // A part of a unit: key tiles [j0, j0 + nkv) for its two query tiles.
 struct PlainSeg {
@@ -90,32 +103,23 @@ struct PlainSeg {
     int slot;         // workspace slot of a cut unit; -1: the whole unit
 };
 struct WindowSeg : PlainSeg {
-    TileList list;    // of the unit: its j-th key tile is tile list.at(j)
     int T;            // tokens of the entry
     int sinks;
-    int from[NQT];    // first key of the window of each tile's first row
+    int from[NQT];    // first place of the window of each tile's first row
 };
 template <bool kWindow>
 using Seg = std::conditional_t<kWindow, WindowSeg, PlainSeg>;
-
-// First key of key tile j of the part's unit.
-__device__ __forceinline__ int key_of(const PlainSeg &, int j) { return BN * j; }
-__device__ __forceinline__ int key_of(const WindowSeg &g, int j) { return BN * g.list.at(j); }
 
 // Of key tile j of the unit, the 16-key MMA steps that hold a key which query tile t may see: up to
 // this one (one at least: an entry without keys) ...
 __device__ __forceinline__ int key_steps(int left) { return min(BN / 16, max(1, (left + 15) >> 4)); }
 __device__ __forceinline__ int steps_of(const PlainSeg &g, int t, int j) { return key_steps(g.end[t] - BN * j); }
-__device__ __forceinline__ int steps_of(const WindowSeg &g, int t, int j) {
-    // (tiles before the window hold sinks, and nothing else that is seen)
-    return key_steps((j < g.list.sinks ? min(g.end[t], g.sinks) : g.end[t]) - key_of(g, j));
-}
 // ... from this one on.
-__device__ __forceinline__ int first_step(const PlainSeg &, int, int) { return 0; }
-__device__ __forceinline__ int first_step(const WindowSeg &g, int t, int j) {
-    const int key0 = key_of(g, j);
-    return j < g.list.sinks || key0 < g.sinks ? 0 : max(0, min(BN / 16 - 1, (g.from[t] - key0) >> 4));
+__device__ __forceinline__ int first_step(int from, int sinks, int j) {
+    return BN * j < sinks ? 0 : max(0, min(BN / 16 - 1, (from - BN * j) >> 4));
 }
+__device__ __forceinline__ int first_step(const PlainSeg &, int, int) { return 0; }
+__device__ __forceinline__ int first_step(const WindowSeg &g, int t, int j) { return first_step(g.from[t], g.sinks, j); }
 
 struct __align__(8) Bars {
     uint64_t q_full[NQT], q_empty[NQT];
@@ -142,19 +146,15 @@ __device__ __forceinline__ int tiles_to(const GroupParams &p, const Entry &e, in
     return attn::tiles_to(is_ordered(p), e.L, e.ctx, e.T, tok);
 }
 
-// The key tiles of the unit that begins at a token of the entry.  (A row of a tree may see none
-// of the new tokens.)
-__device__ __forceinline__ TileList list_of(const GroupParams &p, const Entry &e, int tok) {
-    return tile_list(p.window, p.sinks, is_ordered(p) ? e.ctx + tok + 1 : e.ctx, BN);
+__device__ __forceinline__ WindowUnits window_units(const GroupParams &p, const Entry &e, int per) {
+    return {is_ordered(p), e.L, e.ctx, e.T, e.units, per, p.window, p.sinks, p.paged ? min(1 << p.c.page_shift, BN) : 0};
 }
 
 // key tiles of the first n units of a key head
 template <bool kWindow>
 __device__ __forceinline__ long long unit_tiles(const GroupParams &p, const Entry &e, int per, int n) {
-    const long long all = attn::unit_tiles(is_ordered(p), e.L, e.ctx, e.T, e.units, per, n);
-    if constexpr (!kWindow) return all;
-    else if (is_ordered(p)) return all - skipped_tiles(p.window, p.sinks, e.ctx, per, n);
-    else return all - (long long)n * list_of(p, e, 0).skip;
+    if constexpr (kWindow) return window_units(p, e, per).before(n);
+    else return attn::unit_tiles(is_ordered(p), e.L, e.ctx, e.T, e.units, per, n);
 }
 
 __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, bool report) {
@@ -212,7 +212,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, long l
 // ---- warp 0: walks the stretch, loads ------------------------------------------------
 
 template <int D, bool kWindow>
-__device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, const Stretch &st, uint32_t sQ, uint32_t sK,
+__device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow> *segs, const Stretch &st, uint32_t sQ, uint32_t sK,
                          uint32_t sV, const Watchdog &wd) {
     using C = Cfg<D>;
     const GroupParams &p = a.p;
@@ -230,8 +230,10 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
     // pages: this lane's piece of a key tile
     const int psz = p.paged ? min(1 << p.c.page_shift, BN) : BN, pieces = BN / psz;
     Entry e = {};
-    auto page_at = [&](int key0) -> int {
-        const int pos = key0 + lane * psz;
+    KeyList list = {0, 0};  // with a window, of the unit
+    auto key_at = [&](int place) { return kWindow ? list.at(place) : place; };
+    auto page_at = [&](int j) -> int {
+        const int pos = key_at(BN * j + lane * psz);
         if (!p.paged || lane >= pieces || pos >= e.L) return 0;
         const int id = p.c.table[(int64_t)e.s * p.c.table_stride + (pos >> p.c.page_shift)];
         if ((unsigned)id < (unsigned)p.c.n_pages) return id;
@@ -299,9 +301,12 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
     while (u0 < st.end) {
         if (!entered) enter();
         entered = true;
-        TileList list = {0, 0};
-        if constexpr (kWindow) list = list_of(p, e, unit * per);
-        const int n_unit = tiles_to(p, e, (unit + 1) * per) - list.skip;
+        auto tiles_of = [&](int tok) {  // key tiles that tokens [0, tok) of the entry need of the unit's
+            if constexpr (kWindow) return window_units(p, e, per).tiles_to(list, tok);
+            else return tiles_to(p, e, tok);
+        };
+        if constexpr (kWindow) list = window_units(p, e, per).list(unit);
+        const int n_unit = tiles_of((unit + 1) * per);
         const int t0 = st.tile(st.at, u0, n_unit), t1 = st.tile(st.end, u0, n_unit);
         if (t0 >= t1) {
             next_unit(n_unit);
@@ -309,25 +314,24 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
         }
         Seg<kWindow> g;
         if constexpr (kWindow) {
-            g.list = list;
             g.T = e.T;
             g.sinks = p.sinks;
 #pragma unroll
             for (int t = 0; t < NQT; ++t)
-                g.from[t] = e.ctx + (ordered ? unit * per + t * tok_tile + 1 : 0) - p.window;
+                g.from[t] = e.ctx + (ordered ? unit * per + t * tok_tile + 1 : 0) - p.window - list.shift;
         }
         g.q0 = e.q0;
         g.hk = hk;
-        g.L = e.L;
-        g.ctx = e.ctx;
+        g.L = e.L - list.shift;
+        g.ctx = e.ctx - list.shift;
         g.j0 = t0;
         g.nkv = t1 - t0;
 #pragma unroll
         for (int t = 0; t < NQT; ++t) {
             g.tok[t] = unit * per + t * tok_tile;
             g.live[t] = max(0, min(tok_tile, e.T - g.tok[t])) * p.group;
-            g.n[t] = g.live[t] > 0 ? max(0, min(tiles_to(p, e, g.tok[t] + tok_tile) - list.skip, t1) - t0) : 0;
-            g.end[t] = ordered ? min(e.L, e.ctx + min(g.tok[t] + tok_tile, e.T)) : e.L;
+            g.n[t] = g.live[t] > 0 ? max(0, min(tiles_of(g.tok[t] + tok_tile), t1) - t0) : 0;
+            g.end[t] = ordered ? min(g.L, g.ctx + min(g.tok[t] + tok_tile, e.T)) : g.L;
         }
         g.slot = t1 - t0 == n_unit ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
         if (t0 == 0 && t1 < n_unit && lane == 0) {  // begins here and goes on behind the stretch: for the merge
@@ -352,14 +356,31 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
             ++q_uses[t];
             q_pending[t] = true;
         }
-        int page = page_at(key_of(g, t0));
+        int page = page_at(t0);
         for (int j = t0; j < t1 && ok; ++j) {
             const uint32_t ks = kr.slot(), vs = vr.slot();
             ok = wait(bars.k_empty[ks], kr.phase() ^ 1) && wait(bars.v_empty[vs], vr.phase() ^ 1);
             if (!ok) break;
             const uint32_t bar = smem_u32(&bars.k_full[ks]);
-            const int key0 = key_of(g, j);
-            if (!p.paged) {
+            const int place0 = BN * j;
+            bool mixed = false;  // contiguous keys: sinks and keys of the window
+            if constexpr (kWindow) mixed = !p.paged && place0 < list.held && place0 + BN > list.held;
+            if (mixed) {
+                if constexpr (kWindow) {
+                    if (lane == 0) mbar_expect_tx(bar, 2 * C::kTileBytes);
+                    __syncwarp();
+                    if (lane < BN / 16) {
+                        const int row = e.k0 + list.at(place0 + 16 * lane);
+                        const uint32_t off = lane * 16 * 128;
+#pragma unroll
+                        for (int b = 0; b < C::kBoxes; ++b) {
+                            tma_load_3d(sK + ks * C::kTileBytes + b * C::kBoxBytes + off, &a.tk16, 64 * b, row, hk, bar);
+                            tma_load_3d(sV + vs * C::kTileBytes + b * C::kBoxBytes + off, &a.tv16, 64 * b, row, hk, bar);
+                        }
+                    }
+                }
+            } else if (!p.paged) {
+                const int key0 = key_at(place0);
                 if (elect_one()) {
                     mbar_expect_tx(bar, 2 * C::kTileBytes);
 #pragma unroll
@@ -370,11 +391,11 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
                 }
             } else {
                 // the pieces that hold keys, one a lane
-                const int there = min(pieces, cdiv(e.L - key0, psz));
+                const int there = min(pieces, cdiv(g.L - place0, psz));
                 if (lane == 0) mbar_expect_tx(bar, there * psz * 128 * C::kBoxes * 2);
                 __syncwarp();
                 if (lane < there) {
-                    const int row = (key0 + lane * psz) & ((1 << p.c.page_shift) - 1);
+                    const int row = key_at(place0 + lane * psz) & ((1 << p.c.page_shift) - 1);
                     const uint32_t off = lane * psz * 128;
 #pragma unroll
                     for (int b = 0; b < C::kBoxes; ++b) {
@@ -386,7 +407,7 @@ __device__ void producer(const GroupArgs &a, Bars &bars, Seg<kWindow> *segs, con
             __syncwarp();
             ++kr.i;
             ++vr.i;
-            if (j + 1 < t1) page = page_at(key_of(g, j + 1));
+            if (j + 1 < t1) page = page_at(j + 1);
         }
         if (!ok) break;
         next_unit(n_unit);
@@ -467,23 +488,15 @@ __device__ void mma_issuer(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         if (!wait(bars.seg_full[slot], (i / kSegs) & 1)) return;
         const int n0 = segs[slot].n[0], n1 = segs[slot].n[1], nkv = segs[slot].nkv;
         const int j0 = segs[slot].j0, key0 = BN * j0, left0 = segs[slot].end[0] - key0, left1 = segs[slot].end[1] - key0;
-        WindowSeg win;  // with a window, what the steps need of the part
+        int from0 = 0, from1 = 0, sinks = 0;
         if constexpr (kWindow) {
-            win.list = segs[slot].list;
-            win.sinks = segs[slot].sinks;
-#pragma unroll
-            for (int t = 0; t < NQT; ++t) {
-                win.end[t] = segs[slot].end[t];
-                win.from[t] = segs[slot].from[t];
-            }
+            from0 = segs[slot].from[0];
+            from1 = segs[slot].from[1];
+            sinks = segs[slot].sinks;
         }
         // the steps of query tile t and the part's j-th key tile
-        auto steps_at = [&](int t, int j) {
-            return kWindow ? t ? steps_of(win, 1, j0 + j) : steps_of(win, 0, j0 + j) : key_steps((t ? left1 : left0) - BN * j);
-        };
-        auto first_at = [&](int t, int j) {
-            return kWindow ? t ? first_step(win, 1, j0 + j) : first_step(win, 0, j0 + j) : 0;
-        };
+        auto steps_at = [&](int t, int j) { return key_steps((t ? left1 : left0) - BN * j); };
+        auto first_at = [&](int t, int j) { return kWindow ? first_step(t ? from1 : from0, sinks, j0 + j) : 0; };
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bars.seg_empty[slot]));
         if (nkv < 0) return;
@@ -738,7 +751,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             // and the only masked code: unrolled over the 128 columns it is fetched anew for each
             // unit's few masked tiles, which costs more than it computes (48 packed prompts of 9 to
             // 420 tokens 63 -> 85 us, long prompts the same)
-            const int key0 = key_of(sg, sg.j0 + j), left = sg.L - key0;
+            const int key0 = BN * (sg.j0 + j), left = sg.L - key0;
             const int steps = steps_of(sg, t, sg.j0 + j);
             const int token = sg.tok[t] + my_tok;
             const int lim = min(left, ordered ? sg.ctx + token + 1 - key0 : BN);  // keys [0, lim) admitted, but for the mask
@@ -812,7 +825,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         };
         if constexpr (kWindow) {
             for (int j = 0; j < n; ++j) {
-                const int key0 = key_of(sg, sg.j0 + j);
+                const int key0 = BN * (sg.j0 + j);
                 const bool whole = key0 + BN <= all_end && (key0 >= all_from || key0 + BN <= p.sinks);
                 if (!(whole ? plain_tile(j) : masked_tile(j))) return;
             }
@@ -874,7 +887,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
 }
 
 template <int D, bool kBF16, typename Tout, bool kWindow>
-__global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ GroupArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ GroupArgsOf<kWindow> a) {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
@@ -926,14 +939,14 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     pdl_wait();
     const int per = NQT * (BM / a.p.group);
     Stretch st;
-    const bool any = find_stretch<kThreads / 32, kLead>(
+    const bool any = find_stretch<kThreads / 32, kWindow ? kWindowLead : kLead>(
         a.p.n, 1, [&](int i, bool report) { return entry_work<kWindow>(a.p, entry_at(a.p, i, per, report), per); }, st);
     if (!any) st.end = st.at;
     if (threadIdx.x == 0) a.p.parts.cut[blockIdx.x].last = -1;  // the loading warp may put a unit there
     __syncthreads();
 
     if (warp < 4) {
-        regs_dec<C::kRegsProducer>();
+        regs_dec<kWindow ? C::kRegsWindowProducer : C::kRegsProducer>();
         if (warp == 0) {
             producer<D, kWindow>(a, bars, segs, st, sQ, sK, sV, wd);  // the whole warp
         } else if (warp == 1) {
@@ -944,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             }
         }
     } else {
-        regs_inc<C::kRegsSoftmax>();
+        regs_inc<kWindow ? C::kRegsWindowSoftmax : C::kRegsSoftmax>();
         softmax_wg<D, kBF16, Tout, kWindow>(a, bars, segs, sV, tmem, wd);
     }
     tc_fence_before();
@@ -956,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
 }
 
 template <int D, bool kBF16, typename Tout, bool kWindow>
-cudaError_t launch_typed(const GroupArgs &args, cudaStream_t s) {
+cudaError_t launch_typed(const GroupArgsOf<kWindow> &args, cudaStream_t s) {
     auto kern = group_tc_kernel<D, kBF16, Tout, kWindow>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -966,7 +979,7 @@ cudaError_t launch_typed(const GroupArgs &args, cudaStream_t s) {
 }
 
 template <int D, bool kWindow>
-cudaError_t launch_d(const GroupArgs &a, cudaStream_t s) {
+cudaError_t launch_d(const GroupArgsOf<kWindow> &a, cudaStream_t s) {
     const bool f32 = a.p.o_dtype == ATTN_F32;
     if (a.p.dtype == ATTN_BF16)
         return f32 ? launch_typed<D, true, float, kWindow>(a, s) : launch_typed<D, true, __nv_bfloat16, kWindow>(a, s);
@@ -976,7 +989,7 @@ cudaError_t launch_d(const GroupArgs &a, cudaStream_t s) {
 // The attention kernel, and the merge of cut units.
 template <bool kWindow>
 cudaError_t launch_group_of(const GroupParams &p, cudaStream_t s) {
-    GroupArgs a;
+    GroupArgsOf<kWindow> a;
     a.p = p;
     const uint64_t D = (uint64_t)p.D;
     const int tok = BM / p.group;
@@ -996,6 +1009,9 @@ cudaError_t launch_group_of(const GroupParams &p, cudaStream_t s) {
     } else {
         ok = ok && make_tile_map(&a.tk, p.k, p.dtype, p.D, p.n_k, p.Hkv, p.k_st, p.k_sh) &&
              make_tile_map(&a.tv, p.v, p.dtype, p.D, p.n_k, p.Hkv, p.v_st, p.v_sh);
+        if constexpr (kWindow)
+            ok = ok && make_tile_map(&a.tk16, p.k, p.dtype, p.D, p.n_k, p.Hkv, p.k_st, p.k_sh, 16) &&
+                 make_tile_map(&a.tv16, p.v, p.dtype, p.D, p.n_k, p.Hkv, p.v_st, p.v_sh, 16);
     }
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t e = p.D == 64 ? launch_d<64, kWindow>(a, s) : launch_d<128, kWindow>(a, s);

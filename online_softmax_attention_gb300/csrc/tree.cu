@@ -21,9 +21,10 @@
 // zero-filled by cp.async and never read from memory, so stale slots (NaN
 // included) do not matter.
 //
-// kWindow: a sliding window with sinks (window.h).  An entry's key tiles are those that hold
-// a sink and those from the first new token's window on, the same for all its units (its
-// new tokens are few here; a chunk of T reads T keys more than its last row needs).
+// kWindow: a sliding window with sinks (window.h).  An entry's keys are a list, the sinks and those from
+// the first new token's window on, and its tiles count the list's places; the list is the same for
+// all its units (its new tokens are few here; a chunk of T reads T keys more than its last row
+// needs).
 #include "../../include/attn.h"
 #include <type_traits>
 
@@ -97,7 +98,7 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 struct Entry {
     int s, L, T, q0;   // sequence, cached tokens, new tokens, first query row
     int row_tiles, key_tiles;
-    TileList list;     // the key tiles
+    KeyList list;      // the keys
     long long tiles;   // of all its units
 };
 
@@ -120,8 +121,8 @@ __device__ __forceinline__ Entry entry_at(const TreeParams &p, int i, int rows, 
     e.list = {0, 0};
     if (kWindow && e.T > 0) {
         // (a row of a tree may see none of the new tokens)
-        e.list = tile_list(p.window, p.sinks, e.L - e.T + (p.mask ? 0 : 1), keys);
-        e.key_tiles -= e.list.skip;
+        e.list = key_list(p.window, p.sinks, e.L - e.T + (p.mask ? 0 : 1), 1, 1);
+        e.key_tiles = (e.L - e.list.shift + keys - 1) / keys;
     }
     e.tiles = (long long)p.c.H * e.row_tiles * e.key_tiles;
     return e;
@@ -207,21 +208,21 @@ __global__ void __launch_bounds__(32 * warps_of(kWindow, sizeof(T) == 4), per_sm
             s_window[tid] = p.mask ? tree_window(p.mask + (int64_t)(e.q0 + t) * p.mask_words, e.T, ctx, p.window, p.sinks)
                                    : RowWindow{ctx + t + 1 - p.window, p.sinks};
         }
-        // whether some row of the entry does not see every key of a tile before the new tokens
-        auto outside = [&](int key0) { return key0 < ctx + e.T - p.window && key0 + kKeys > p.sinks; };
+        // places [hidden0, hidden1) of the list are hidden from some row of the entry
+        const int hidden0 = e.list.shift ? e.list.held : p.sinks, hidden1 = ctx + e.T - p.window - e.list.shift;
         auto hidden = [&](int row, int key) { return key < s_window[row].lo && key >= s_window[row].hi; };
-        auto key_of = [&](int tile) { return (kWindow ? e.list.at(tile) : tile) * kKeys; };
+        auto key_of = [&](int place) { return kWindow ? e.list.at(place) : place; };
 
         // this warp's tiles: t0 + warp, t0 + warp + kWarps, ...
         const int *table = p.c.table + (int64_t)e.s * p.c.table_stride;
         const int page_mask = (1 << p.c.page_shift) - 1;
         const char *kh = p.c.k + hk * p.c.b_head, *vh = p.c.v + hk * p.c.b_head;
         auto page_at = [&](int tile) -> int {  // the page of this lane's key of the tile
-            const int key = key_of(tile) + lane;
+            const int key = key_of(tile * kKeys + lane);
             return lane < kKeys && tile < t1 && key < e.L ? table[key >> p.c.page_shift] : -1;
         };
         auto load = [&](int tile, int page, int stage) {
-            const int key = key_of(tile) + lane;
+            const int key = key_of(tile * kKeys + lane);
             const bool live = (unsigned)page < (unsigned)p.c.n_pages;
             if (!live && lane < kKeys && tile < t1 && key < e.L) report_status(p.c.status, ATTN_EINVAL);
             const long long off = live ? page * p.c.b_page + (key & page_mask) * p.c.b_tok : -1;
@@ -286,9 +287,10 @@ __global__ void __launch_bounds__(32 * warps_of(kWindow, sizeof(T) == 4), per_sm
                 page = page_at(next);
             }
             const uint32_t k_a = ring_a + stage * 2 * C::kTileBytes, v_a = k_a + C::kTileBytes;
-            const int key0 = key_of(tile);
+            const int key0 = tile * kKeys;  // with a window, the list's place
             // the tile reaches the new tokens or the end
-            const bool masked = key0 + kKeys > ctx || (kWindow && outside(key0));
+            const bool masked = key0 + kKeys > (kWindow ? ctx - e.list.shift : ctx) ||
+                                (kWindow && hidden0 < hidden1 && key0 < hidden1 && key0 + kKeys > hidden0);
             if constexpr (kMma) {
                 float sc[kKeys / 8][4];
 #pragma unroll
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(32 * warps_of(kWindow, sizeof(T) == 4), per_sm
                         for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const int key = key0 + 8 * j + 2 * (lane & 3) + k;
+                                const int key = key_of(key0 + 8 * j + 2 * (lane & 3) + k);
                                 if (key >= e.L || !sees(p, e, t, key - ctx) || (kWindow && hidden(8 * hf + (lane >> 2), key)))
                                     sc[j][2 * hf + k] = -INFINITY;
                             }
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(32 * warps_of(kWindow, sizeof(T) == 4), per_sm
                         sc[r] = fmaf(qv.w, kv.w, sc[r]);
                     }
                 }
-                const int key = key0 + lane;
+                const int key = key_of(key0 + lane);
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
                     const int t = min((row0 + r) / p.group, e.T - 1);

@@ -52,6 +52,67 @@ ATTN_HD long long sink_slot(long long row, int sink_tiles, int chunk) {
     return 2ll * sink_tiles * (row / (128ll * chunk));
 }
 
+// The same list in single keys: places [0, held) are keys 0 .. (the sinks, rounded up to whole pieces
+// of a load), the places behind them the keys from the window's first on.  {0, 0}: no gap.
+struct KeyList {
+    int held;
+    int shift;  // of the places behind
+    ATTN_HD int at(int place) const { return place < held ? place : place + shift; }
+};
+
+// `seen` as in tile_list; the window begins at a multiple of `grain` keys, the sinks take a multiple of
+// `held_grain`.
+ATTN_HD KeyList key_list(int window, int sinks, int seen, int grain, int held_grain) {
+    const int from = seen > window ? (seen - window) / grain * grain : 0;
+    const long long held = ((long long)sinks + held_grain - 1) / held_grain * held_grain;
+    if (held >= from) return {0, 0};
+    return {(int)held, from - (int)held};
+}
+
+// The units of an entry over such lists, in tiles of 128 places; unit i begins at token i per.
+struct WindowUnits {
+    bool ordered;               // tokens see those up to themselves; else what a mask says, of all L keys
+    int L, ctx, T, units, per;  // as in unit_tiles
+    int window, sinks;
+    int piece;                  // rows that a load of the keys takes at once (pages); 0: any
+
+    // Of pages, many units begin at whole tiles, so that their sum has a closed form.
+    ATTN_HD int grain() const { return piece == 0 ? 1 : units <= 8 || !ordered ? piece : 128; }
+    ATTN_HD KeyList list(int i) const {
+        return key_list(window, sinks, ordered ? ctx + i * per + 1 : ctx, grain(), piece == 0 ? 16 : grain());
+    }
+    // tiles of a list that hold the keys which the entry's first `tok` tokens see; one at least
+    ATTN_HD int tiles_to(KeyList l, int tok) const {
+        int end = L;
+        if (ordered) {
+            const int upto = ctx + (tok < T ? tok : T);
+            end = upto < L ? upto : L;
+        }
+        const int n = (end - l.shift + 127) / 128;
+        return n > 1 ? n : 1;
+    }
+    ATTN_HD int tiles(int i) const { return tiles_to(list(i), (i + 1) * per); }
+    // of the first n units
+    ATTN_HD long long before(int n) const {
+        if (!ordered) return (long long)n * tiles(0);
+        if (n <= 8) {
+            long long r = 0;
+            for (int i = 0; i < n; ++i) r += tiles(i);
+            return r;
+        }
+        if (piece) return unit_tiles(true, L, ctx, T, units, per, n) - skipped_tiles(window, sinks, ctx, per, n);
+        // up to the first unit with a gap as without a window; those behind it have per - 1 + window keys
+        // and the sinks each, but for the entry's last one
+        const long long held = ((long long)sinks + 15) / 16 * 16, x = window + held - 1 - ctx;
+        const long long gap = x < 0 ? 0 : x / per + 1;
+        if (gap >= n) return unit_tiles(true, L, ctx, T, units, per, n);
+        const int first = (int)gap, whole = n < units ? n : units - 1;
+        long long r = first ? unit_tiles(true, L, ctx, T, units, per, first) : 0;
+        if (whole > first) r += (whole - first) * ((per - 1 + window + held + 127) / 128);
+        return n == units ? r + tiles(units - 1) : r;
+    }
+};
+
 // The keys that a row of a tree sees: below `hi`, or from `lo` on, of the ctx keys before the
 // new tokens and the new tokens u < T whose bits are set in `mask`.
 struct RowWindow {

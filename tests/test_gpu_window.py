@@ -278,3 +278,27 @@ def test_many_sequences():
     c = cuda(x)
     assert_output(*attn.fwd(c["q"], c["k"], c["v"], causal=True, cu_seqlens_q=cu, window=3, sinks=1),
                   reference(x, lens, 0.125, 3, 1), torch.float16)
+
+
+@pytest.mark.parametrize("scale", [0.3, -0.11])
+@pytest.mark.parametrize("window,sinks", [(100, 3), (260, 300)])
+def test_backward_scaled(scale, window, sinks):
+    lens = [700, 90]
+    x, cu = make(lens, 4, 2, 128, torch.bfloat16, 70, True)
+    c = cuda(x)
+    w = dict(causal=True, cu_seqlens_q=cu, scale=scale, window=window, sinks=sinks)
+    o, lse = attn.fwd(c["q"], c["k"], c["v"], out_dtype=torch.float32, **w)
+    got = attn.bwd(c["q"], c["k"], c["v"], o, lse, c["do"], grad_dtype=torch.float32, **w)
+    for name, g, r in zip(("dq", "dk", "dv"), got, gradients(x, lens, scale, window, sinks)):
+        check_grad(g, r, f"{name} {scale}")
+
+
+def test_backward_of_a_scale_of_zero():
+    """The uniform average of the admitted values: dq = dk = 0, dv as by the formula."""
+    x, cu = make([400], 4, 2, 64, torch.float16, 79, True)
+    c = cuda(x)
+    w = dict(causal=True, cu_seqlens_q=cu, scale=0.0, window=150, sinks=2)
+    o, lse = attn.fwd(c["q"], c["k"], c["v"], out_dtype=torch.float32, **w)
+    dq, dk, dv = attn.bwd(c["q"], c["k"], c["v"], o, lse, c["do"], grad_dtype=torch.float32, **w)
+    assert (dq == 0).all() and (dk == 0).all()
+    check_grad(dv, gradients(x, [400], 0.0, 150, 2)[2], "dv")
