@@ -11,8 +11,8 @@
 // A thread then numbers a run of tokens, behind two scans over the block.  Every result is a
 // function of the inputs.
 //
-// Move.  Kept token number j comes from source[j] >= j, ascending.  A cluster of 8 blocks owns up
-// to 512 bytes of every row of a layer of k or v, and moves 512 rows and more at a time:
+// Move.  Kept token number j comes from source[j] >= j, ascending.  A block, or a cluster of them, owns
+// up to 512 bytes of every row of a layer of k or v, and moves 64 rows a block and more at a time:
 // all of a batch's rows are in shared memory before any is stored (a barrier over the
 // cluster), and the next batch's loads are in flight meanwhile, which the stores cannot meet:
 // their sources lie at or behind their own places, which follow this batch's.  So a sequence's
@@ -207,20 +207,22 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
     }
 }
 
+template <int kCluster>
 __device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if constexpr (kCluster == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Cluster (i, y): entry i; y walks the strips of the layers of k and v, then the layers of weights.
-constexpr int kCluster = 8;
 constexpr int kMoveRows = 8;  // of a warp and batch, in instructions of 32 chunks of 16 bytes
 constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kMoveBytes = kMoveWarps * kMoveRows * 512;  // of a batch
 
+// Cluster (i, y): entry i; y walks the strips of the layers of k and v, then the layers of weights.
+template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
     evict_move_kernel(const CacheParams c, const EvictParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -267,7 +269,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
                 const int j = j0 + warp0 + lane;
                 const long long to = lane < rows && j < count ? offset(j) : 0;
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
-                cluster_barrier();  // the batch is in shared memory
+                cluster_barrier<kCluster>();  // the batch is in shared memory
                 if (j0 + step < count) load(j0 + step, buffer ^ 1);
 #pragma unroll
                 for (int r = 0; r < kMoveRows; ++r) {
@@ -288,7 +290,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
 #pragma unroll
                 for (int r = 0; r < kTokens; ++r)
                     if (j0 + r * kStep < count) v[r] = w[source[j0 + r * kStep]];
-                cluster_barrier();
+                cluster_barrier<kCluster>();
 #pragma unroll
                 for (int r = 0; r < kTokens; ++r)
                     if (j0 + r * kStep < count) w[j0 + r * kStep] = v[r];
@@ -306,6 +308,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
     }
 }
 
+template <int kCluster>
+cudaError_t launch_move(const CacheParams &c, const EvictParams &p, unsigned y, cudaStream_t s) {
+    auto kern = evict_move_kernel<kCluster>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kMoveBytes);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(kCluster * p.n, y), dim3(kMoveThreads), 2 * kMoveBytes, s, c, p);
+    count_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaStream_t s) {
@@ -316,12 +328,13 @@ cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaS
     count_launch();
     if (e != cudaSuccess) return e;
     const int64_t per_tok = (int64_t)c.H * (c.row_bytes >> 4), columns = 2 * c.n_layers * ((per_tok + 31) / 32) + p.w_layers;
-    e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kMoveBytes);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(evict_move_kernel, dim3(kCluster * p.n, (unsigned)(columns < 65535 ? columns : 65535)), dim3(kMoveThreads),
-                   2 * kMoveBytes, s, c, p);
-    count_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
+    // Few clusters are wide ones, which move a strip in few batches; many need no width to fill the GPU, and
+    // single blocks wait for no others.  (Clusters of 8 and of 1: one sequence of 4 layers, 36 clusters:
+    // 24.7 and 36.6 us; 4 sequences of 4000 kept tokens, 144: 122 and 146; 8 sequences, 288: 70 and
+    // 64; 32 sequences of 8 layers, 2304: 413 and 351.)
+    const int64_t clusters = p.n * columns;
+    const unsigned y = (unsigned)(columns < 65535 ? columns : 65535);
+    return clusters < 256 ? launch_move<8>(c, p, y, s) : launch_move<1>(c, p, y, s);
 }
 
 }  // namespace attn

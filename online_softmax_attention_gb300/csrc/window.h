@@ -32,8 +32,9 @@ ATTN_HD TileList tile_list(int window, int sinks, int seen, int tile) {
 ATTN_HD long long skipped_tiles(int window, int sinks, int ctx, int per, int n) {
     const long long held = sinks / 128 + (sinks % 128 != 0);
     const long long b = (long long)ctx + 1 - window - 128 * held;  // of unit 0; the first terms may be below 0
-    const long long i0 = b >= 0 ? 0 : (per - 1 - b) / per;
-    return i0 < n ? floor_sum((int)(n - i0), per, (int)(b + i0 * per)) : 0;
+    if (b + (n - 1ll) * per < 0) return 0;
+    const int i0 = b >= 0 ? 0 : (per - 1 - (int)b) / per;
+    return floor_sum(n - i0, per, (int)(b + (long long)i0 * per));
 }
 
 // dK / dV items of a head of a sequence of `blocks` key (and query) blocks.  A block with a sink
@@ -61,11 +62,11 @@ struct KeyList {
 };
 
 // `seen` as in tile_list; the window begins at a multiple of `grain` keys, the sinks take a multiple of
-// `held_grain`.
+// `held_grain` (powers of two).
 ATTN_HD KeyList key_list(int window, int sinks, int seen, int grain, int held_grain) {
-    const int from = seen > window ? (seen - window) / grain * grain : 0;
-    const long long held = ((long long)sinks + held_grain - 1) / held_grain * held_grain;
-    if (held >= from) return {0, 0};
+    const int from = seen > window ? (seen - window) & ~(grain - 1) : 0;
+    const unsigned held = ((unsigned)sinks + held_grain - 1) & ~(unsigned)(held_grain - 1);
+    if (held >= (unsigned)from) return {0, 0};
     return {(int)held, from - (int)held};
 }
 
@@ -103,12 +104,11 @@ struct WindowUnits {
         if (piece) return unit_tiles(true, L, ctx, T, units, per, n) - skipped_tiles(window, sinks, ctx, per, n);
         // up to the first unit with a gap as without a window; those behind it have per - 1 + window keys
         // and the sinks each, but for the entry's last one
-        const long long held = ((long long)sinks + 15) / 16 * 16, x = window + held - 1 - ctx;
-        const long long gap = x < 0 ? 0 : x / per + 1;
-        if (gap >= n) return unit_tiles(true, L, ctx, T, units, per, n);
-        const int first = (int)gap, whole = n < units ? n : units - 1;
+        const long long held = (long long)(((unsigned)sinks + 15) & ~15u), x = window + held - 1 - ctx;
+        if (x >= (long long)(n - 1) * per) return unit_tiles(true, L, ctx, T, units, per, n);
+        const int first = x < 0 ? 0 : (int)x / per + 1, whole = n < units ? n : units - 1;
         long long r = first ? unit_tiles(true, L, ctx, T, units, per, first) : 0;
-        if (whole > first) r += (whole - first) * ((per - 1 + window + held + 127) / 128);
+        if (whole > first) r += (whole - first) * ((per - 1 + window + held + 127) >> 7);
         return n == units ? r + tiles(units - 1) : r;
     }
 };
