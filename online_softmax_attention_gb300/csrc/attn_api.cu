@@ -351,25 +351,24 @@ struct BwdLayout {
     size_t kv, q, dr, lse2, dqa, sinks, total;
 };
 
-// Chunks of the sinks' key blocks on the tensor cores: twice the query blocks that see a block of a
-// window, more where half a CTA's share of all blocks is more or the partial sums would pass 256
-// slots a head; none where no row is longer.  (24 rows of 30 to 1000 tokens, window 200: 82 us for dK
-// and dV with chunks as long as a window's items, 81 uncut.)
-void sink_cut(const attn_bwd_args *a, int &tiles, int &chunk) {
+// Chunks of the sinks' key blocks, of blocks of `block` rows: as long as a window's items where those are
+// few, so that all run at once (an f32 row of 2000 tokens, 8 query heads of one key head, window 100: 778 us
+// with twice that, 471 so), else twice that, more where half a CTA's share of all blocks (152 CTAs) is
+// more or the partial sums would pass 256 slots a head; none where no row is longer.
+void sink_cut(const attn_bwd_args *a, int block, int &tiles, int &chunk) {
     tiles = chunk = 0;
     if (a->window <= 0 || a->window >= a->n_k || a->sinks <= 0) return;
-    const int64_t blocks = a->n_q / 128 + 1, held = ((int64_t)a->sinks + 127) / 128;
-    const int64_t n = held < blocks ? held : blocks;
-    const int64_t seen = (254 + (int64_t)a->window) / 128, heads = a->H_kv > 0 ? a->H_kv : a->H;
-    int64_t c = 2 * seen;
-    if (c < heads * blocks * seen / (2 * sm_count())) c = heads * blocks * seen / (2 * sm_count());
+    const int64_t blocks = a->n_q / block + 1, held = ((int64_t)a->sinks + block - 1) / block;
+    const int64_t n = held < blocks ? held : blocks, heads = a->H_kv > 0 ? a->H_kv : a->H;
+    const int64_t seen = (2 * block - 2 + (int64_t)a->window) / block;
+    int64_t c = heads * blocks < 2 * 152 ? seen : 2 * seen;
+    if (c < heads * blocks * seen / (2 * 152)) c = heads * blocks * seen / (2 * 152);
     if (c < (n * blocks + 127) / 128) c = (n * blocks + 127) / 128;
     if (blocks <= c) return;
     tiles = (int)n;
     chunk = (int)c;
 }
 
-// fused: room for the dq partial sums (n_q * H * D f32) after the row statistics
 BwdLayout bwd_layout(int n_seq, int H, int n_q, int D, bool fused, size_t sink_floats) {
     BwdLayout L;
     const size_t rows = align256(sizeof(float) * (size_t)H * (size_t)(n_q > 0 ? n_q : 1));
@@ -401,12 +400,16 @@ bool bwd_on_tc(const attn_bwd_args *a) {
 // resolves to the separate dq kernel).
 bool bwd_fused(const attn_bwd_args *a) { return a->dq_mode == ATTN_DQ_FUSED && bwd_on_tc(a); }
 
-// Floats of the sinks' partial sums: two of 128 rows a slot.
+// Rows of a backward's blocks.
+int bwd_block(const attn_bwd_args *a) { return bwd_on_tc(a) ? 128 : kSimtBlock; }
+
+// Floats of the sinks' partial sums: dV and dK of a block a slot.
 size_t sink_floats(const attn_bwd_args *a) {
     int tiles, chunk;
-    sink_cut(a, tiles, chunk);
-    if (!chunk || !bwd_on_tc(a)) return 0;
-    return (size_t)(a->H_kv > 0 ? a->H_kv : a->H) * (size_t)sink_slot(a->n_q, tiles, chunk) * 2 * 128 * (size_t)a->D;
+    const int block = bwd_block(a);
+    sink_cut(a, block, tiles, chunk);
+    if (!chunk) return 0;
+    return (size_t)(a->H_kv > 0 ? a->H_kv : a->H) * (size_t)sink_slot(a->n_q, block, tiles, chunk) * 2 * block * (size_t)a->D;
 }
 
 int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
@@ -464,7 +467,7 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     p.lse2 = reinterpret_cast<float *>(ws + L.lse2);
     p.dq_accum = fused ? reinterpret_cast<float *>(ws + L.dqa) : nullptr;
     if (sink_floats(a)) {
-        sink_cut(a, p.sink_tiles, p.sink_chunk);
+        sink_cut(a, bwd_block(a), p.sink_tiles, p.sink_chunk);
         p.sink_parts = reinterpret_cast<float *>(ws + L.sinks);
     }
     p.status = status_ptr();

@@ -214,7 +214,9 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
         int q_start, Lq, k_start, Lk;
         seq_bounds(p.cu_q, p.n_q, it.b, q_start, Lq);
         seq_bounds(p.cu_k, p.n_k, it.b, k_start, Lk);
-        const int key0 = it.t * B, h = it.h;
+        SinkItem item = {it.t, 0, 0, -1};
+        if constexpr (kWindow) item = sink_item(it.t, (Lq + B - 1) / B, p.sink_tiles, p.sink_chunk);
+        const int key0 = item.tile * B, h = it.h;
 
         stage_tile<Tin, D>(sK, gk + (int64_t)k_start * p.k_st + (int64_t)h * p.k_sh, p.k_st, key0, Lk);
         stage_tile<Tin, D>(sV, gv + (int64_t)k_start * p.v_st + (int64_t)h * p.v_sh, p.v_st, key0, Lk);
@@ -225,10 +227,14 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
 #pragma unroll
             for (int e = 0; e < NG * 4; ++e) dk[r][e] = dv[r][e] = 0.f;
 
-        const int qb_first = p.causal ? key0 / B : 0;
+        const int qb_first = kWindow ? item.first : p.causal ? key0 / B : 0;
         // with a window, up to the last query that still sees the block's last key (the sinks': every one)
         const int q_end = kWindow && key0 >= p.sinks ? (int)min((long long)Lq, (long long)key0 + B - 1 + p.window) : Lq;
-        const int qb_end = (q_end + B - 1) / B;
+        int qb_end = (q_end + B - 1) / B;
+        if constexpr (kWindow) {  // (a block's items of chunks: key blocks with a sink)
+            if (item.part >= 0) qb_end = min(qb_end, qb_first + item.most);
+            if (qb_first >= qb_end) continue;  // a chunk behind the last query block: not read
+        }
 
         // the query blocks of every query head that shares this key / value head
         for (int hq = h * p.group; hq < (h + 1) * p.group; ++hq) {
@@ -292,6 +298,22 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
             }
         }
 
+        if constexpr (kWindow) {
+            if (item.part >= 0) {  // unscaled, for the sum over the key block's items
+                const long long slot = h * sink_slot(p.n_q, B, p.sink_tiles, p.sink_chunk) +
+                                       sink_slot(q_start, B, p.sink_tiles, p.sink_chunk) + item.part;
+                float *part = p.sink_parts + slot * 2 * (B * D);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const int at = (ty + 16 * r) * D + 64 * g + 4 * tx;
+                        store4(part + at, make_float4(dv[r][4 * g], dv[r][4 * g + 1], dv[r][4 * g + 2], dv[r][4 * g + 3]));
+                        store4(part + B * D + at, make_float4(dk[r][4 * g], dk[r][4 * g + 1], dk[r][4 * g + 2], dk[r][4 * g + 3]));
+                    }
+                continue;
+            }
+        }
         Tg *gdk = static_cast<Tg *>(p.dk);
         Tg *gdv = static_cast<Tg *>(p.dv);
 #pragma unroll
@@ -454,9 +476,11 @@ cudaError_t launch_persistent(K kern, size_t smem, int num_ctas, const BwdParams
 
 template <typename Tin, typename Tg, int D>
 cudaError_t bwd_typed(const BwdParams &p, int num_ctas, cudaStream_t s, bool dkdv) {
-    if (dkdv)
-        return launch_persistent(p.window ? dkdv_simt_kernel<Tin, Tg, D, true> : dkdv_simt_kernel<Tin, Tg, D, false>,
-                                 dkdv_smem_bytes<D>(), num_ctas, p, s);
+    if (dkdv) {
+        const cudaError_t e = launch_persistent(p.window ? dkdv_simt_kernel<Tin, Tg, D, true> : dkdv_simt_kernel<Tin, Tg, D, false>,
+                                                dkdv_smem_bytes<D>(), num_ctas, p, s);
+        return e != cudaSuccess || !p.sink_chunk ? e : launch_sink_sum(p, B, s);
+    }
     return launch_persistent(p.window ? dq_simt_kernel<Tin, Tg, D, true> : dq_simt_kernel<Tin, Tg, D, false>,
                              dq_smem_bytes<D>(), num_ctas, p, s);
 }

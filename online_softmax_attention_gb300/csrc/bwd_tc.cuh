@@ -37,7 +37,7 @@
 // blocks up to its last key's window, a block with a sink by all behind it: those are cut into
 // chunks, an item each, whose partial sums a small kernel adds up in order (2 rows of 8192 tokens,
 // 32 / 8 heads, window 1024: one item took as long as the other ones of a CTA together, 676 us
-// instead of SINK_US).  A query block scans the key blocks that hold a sink or a key of its window; pairs outside are
+// instead of 453).  A query block scans the key blocks that hold a sink or a key of its window; pairs outside are
 // zeroed in P^T and dS.  Kernels of their own (bwd_tc_window.cu), so that the others keep
 // their code.
 #pragma once
@@ -228,21 +228,13 @@ __device__ __forceinline__ DkdvInfoOf<kWindow> dkdv_info(const BwdParams &p, int
     f.nqh = max(0, cdiv(f.Lq, BT) - f.qb0);
     if constexpr (kWindow) {
         const int blocks = cdiv(f.Lq, BT);
-        const SinkItems sink = sink_items(blocks, p.sink_tiles, p.sink_chunk);
-        f.part = -1;
-        if (sink.chunks > 1) {
-            const int cut = sink.tiles * sink.chunks;  // the first items
-            f.t = it.t < cut ? it.t / sink.chunks : it.t - cut + sink.tiles;
-            f.key0 = f.t * BT;
-            f.qb0 = f.t;
-            if (it.t < cut) {
-                f.qb0 += (it.t - f.t * sink.chunks) * p.sink_chunk;
-                f.part = it.h * sink_slot(p.n_q, p.sink_tiles, p.sink_chunk) +
-                         sink_slot(f.q_start, p.sink_tiles, p.sink_chunk) + it.t;
-            }
-            f.nqh = max(0, blocks - f.qb0);
-            if (it.t < cut) f.nqh = min(f.nqh, p.sink_chunk);
-        }
+        const SinkItem item = sink_item(it.t, blocks, p.sink_tiles, p.sink_chunk);
+        f.t = item.tile;
+        f.key0 = f.t * BT;
+        f.qb0 = item.first;
+        f.nqh = max(0, min(blocks - f.qb0, item.most));
+        f.part = item.part < 0 ? -1 : it.h * sink_slot(p.n_q, BT, p.sink_tiles, p.sink_chunk) +
+                                          sink_slot(f.q_start, BT, p.sink_tiles, p.sink_chunk) + item.part;
         // the last query that sees the block's last key: key0 + BT - 1 + window - 1
         if (f.key0 >= p.sinks) f.nqh = min(f.nqh, (int)(((long long)BT + BT - 2 + p.window) / BT));
     }
@@ -1031,49 +1023,6 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
     }
 }
 
-// The sums of the sinks' key blocks over their items, in the items' order.  Block (head, block and
-// sequences, rows): a thread has four columns of one row of dV or dK.
-constexpr int kSinkLanes = 32;  // sequences at a time
-constexpr int sink_rows(int D) { return 128 / (D / 4); }
-
-template <typename Tg, int D>
-__global__ void __launch_bounds__(256) sink_sum_kernel(const BwdParams p) {
-    pdl_trigger();
-    pdl_wait();
-    if (p.sched_kv.hdr[1] == 0) return;  // offsets that do not fit
-    const int h = blockIdx.x, which = threadIdx.x >> 7, x = threadIdx.x & 127;
-    const int r = blockIdx.z * sink_rows(D) + x / (D / 4), d = x % (D / 4) * 4;
-    const int lane = blockIdx.y % kSinkLanes;
-    for (int b = lane; b < p.n_seq; b += kSinkLanes) {
-        int start, len;
-        seq_bounds(p.cu_q, p.n_q, b, start, len);
-        const int blocks = cdiv(len, BT);
-        const SinkItems sink = sink_items(blocks, p.sink_tiles, p.sink_chunk);
-        if (sink.chunks == 1) continue;
-        for (int t = blockIdx.y / kSinkLanes; t < sink.tiles; t += gridDim.y / kSinkLanes) {
-            const int used = cdiv(blocks - t, p.sink_chunk);  // chunks that hold a query block
-            const int key = t * BT + r;
-            if (key >= len) continue;
-            const long long slot = h * sink_slot(p.n_q, p.sink_tiles, p.sink_chunk) +
-                                   sink_slot(start, p.sink_tiles, p.sink_chunk) + t * sink.chunks;
-            const float *at = p.sink_parts + (slot * 2 + which) * (BT * D) + r * D + d;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int c = 0; c < used; ++c) {
-                const float4 v = *reinterpret_cast<const float4 *>(at + (int64_t)c * 2 * BT * D);
-                sum.x += v.x;
-                sum.y += v.y;
-                sum.z += v.z;
-                sum.w += v.w;
-            }
-            const float mul = which ? p.scale : 1.f;
-            store4(static_cast<Tg *>(which ? p.dk : p.dv) + (int64_t)(start + key) * (which ? p.dk_st : p.dv_st) +
-                       (int64_t)h * (which ? p.dk_sh : p.dv_sh) + d,
-                   make_float4(sum.x * mul, sum.y * mul, sum.z * mul, sum.w * mul));
-        }
-    }
-}
-
 // ================================= dQ =========================================
 
 struct DqInfo {
@@ -1549,9 +1498,7 @@ cudaError_t launch_typed(const TcBwdArgs &a, int num_ctas, cudaStream_t s, bool 
         cudaError_t e = launch(dkdv_tc_kernel<D, kBF16, Tg, false, kWindow>, BCfg<D>::kDkdvSmem, a, num_ctas, s);
         if constexpr (kWindow) {
             if (e != cudaSuccess || !a.p.sink_chunk) return e;
-            const dim3 grid(a.p.Hkv, kSinkLanes * (a.p.sink_tiles < 64 ? a.p.sink_tiles : 64), BT / sink_rows(D));
-            e = launch_pdl(sink_sum_kernel<Tg, D>, grid, dim3(256), 0, s, a.p);
-            count_launch();
+            return launch_sink_sum(a.p, BT, s);
         }
         return e;
     }

@@ -29,7 +29,7 @@
 // kWindow: a sliding window with sinks (window.h).  A unit's keys are then a list, the sinks and those
 // from its first row's window on, and its tiles 128 places of that list each: the sinks share
 // the window's first tile, which is put together from boxes of 16 rows (2 prompts of 14000 to 16384
-// tokens, window 2048: OLD us with whole tiles of keys, the sinks' apart, NEW so).  Behind the
+// tokens, window 2048: 876 us with whole tiles of keys, the sinks' apart, 840 so).  Behind the
 // loading warp everything counts places: a part's L, ctx and ends are given less the list's shift.
 // Masked tiles stand at both ends of the window, so that a loop takes either kind; the kernels without
 // a window (group_tc.cu) are apart from those with one (group_tc_window.cu) and keep their two loops.

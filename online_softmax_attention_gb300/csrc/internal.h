@@ -298,7 +298,7 @@ struct BwdParams {
     int *status;
     long long watchdog_cycles;
     int window, sinks;  // sliding window (window.h); window 0: none
-    // key blocks with a sink, whose query blocks are cut into items of sink_chunk (bwd_tc.cuh);
+    // key blocks with a sink, whose query blocks are cut into items of sink_chunk (window.h);
     // sink_chunk 0: none
     int sink_tiles, sink_chunk;
     float *sink_parts;  // their partial sums, in the workspace
@@ -326,6 +326,8 @@ cudaError_t launch_merge(const MergeParams &p, cudaStream_t s);
 constexpr int kSimtBlock = 64;
 cudaError_t launch_fwd_simt(const FwdParams &p, int num_ctas, cudaStream_t s);
 int fwd_simt_ctas_per_sm(const FwdParams &p);  // resident CTAs per SM of the kernel p selects
+// dk, dv of the key blocks that were cut (sink_sum.cu), of blocks of `block` rows
+cudaError_t launch_sink_sum(const BwdParams &p, int block, cudaStream_t s);
 cudaError_t launch_bwd_preprocess(const BwdParams &p, cudaStream_t s);
 cudaError_t launch_bwd_dkdv_simt(const BwdParams &p, int num_ctas, cudaStream_t s);
 cudaError_t launch_bwd_dq_simt(const BwdParams &p, int num_ctas, cudaStream_t s);

@@ -47,10 +47,24 @@ struct SinkItems {
 ATTN_HD SinkItems sink_items(int blocks, int sink_tiles, int chunk) {
     return {sink_tiles < blocks ? sink_tiles : blocks, chunk > 0 && blocks > chunk ? (blocks - 1) / chunk + 1 : 1};
 }
-// Slots of partial sums of a head, and the first one of a sequence whose blocks are cut: it has more
-// than chunk blocks, so rows / (128 chunk), at most doubled, holds its chunks.
-ATTN_HD long long sink_slot(long long row, int sink_tiles, int chunk) {
-    return 2ll * sink_tiles * (row / (128ll * chunk));
+// Item t of a head: those of blocks with a sink come first, where they are cut.
+struct SinkItem {
+    int tile;         // key block
+    int first, most;  // first query block; as many at most
+    int part;         // its slot of partial sums, among the sequence's; -1: it has all its query blocks
+};
+ATTN_HD SinkItem sink_item(int t, int blocks, int sink_tiles, int chunk) {
+    const SinkItems sink = sink_items(blocks, sink_tiles, chunk);
+    if (sink.chunks == 1) return {t, t, blocks, -1};
+    const int cut = sink.tiles * sink.chunks;
+    if (t >= cut) return {t - cut + sink.tiles, t - cut + sink.tiles, blocks, -1};
+    const int tile = t / sink.chunks;
+    return {tile, tile + (t - tile * sink.chunks) * chunk, chunk, t};
+}
+// Slots of partial sums of a head before row `row` (all of them: of n_q): a sequence whose blocks of
+// `block` rows are cut has more than chunk of them, so rows / (block chunk), doubled, holds its chunks.
+ATTN_HD long long sink_slot(long long row, int block, int sink_tiles, int chunk) {
+    return 2ll * sink_tiles * (row / ((long long)block * chunk));
 }
 
 // The same list in single keys: places [0, held) are keys 0 .. (the sinks, rounded up to whole pieces

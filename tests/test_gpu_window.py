@@ -302,3 +302,25 @@ def test_backward_of_a_scale_of_zero():
     dq, dk, dv = attn.bwd(c["q"], c["k"], c["v"], o, lse, c["do"], grad_dtype=torch.float32, **w)
     assert (dq == 0).all() and (dk == 0).all()
     check_grad(dv, gradients(x, [400], 0.0, 150, 2)[2], "dv")
+
+
+@pytest.mark.parametrize("kernel,dtype,d", [("simt", torch.float32, 64), ("simt", torch.float32, 128), ("tc", torch.bfloat16, 128),
+                                            ("tc", torch.float16, 64)])
+@pytest.mark.parametrize("window,sinks", [(5, 1), (60, 200), (130, 4), (3, 900)])
+def test_backward_of_sinks_that_many_queries_see(kernel, dtype, d, window, sinks):
+    """Key blocks with a sink cut into several items: rows that are cut beside ones that are not, more
+    than one block of sinks, chunks behind the last query."""
+    lens = [90, 1100, 300, 700] if kernel == "tc" else [90, 600, 270, 300]
+    x, cu = make(lens, 4, 2, d, dtype, 80, True)
+    c = cuda(x)
+    w = dict(causal=True, cu_seqlens_q=cu, kernel=kernel, window=window, sinks=sinks)
+    o, lse = attn.fwd(c["q"], c["k"], c["v"], out_dtype=torch.float32, **w)
+    call = attn.BwdCall(c["q"], c["k"], c["v"], o, lse, c["do"], grad_dtype=torch.float32, **w)
+    plain = attn.BwdCall(c["q"], c["k"], c["v"], o, lse, c["do"], grad_dtype=torch.float32, **{**w, "sinks": 0})
+    assert call.workspace.numel() > plain.workspace.numel()
+    call.workspace.fill_(255)  # (NaN, where a slot is read that was not written)
+    for t in (call.dq, call.dk, call.dv):
+        t.fill_(float("nan"))
+    for name, g, r in zip(("dq", "dk", "dv"), call.run(), gradients(x, lens, d ** -0.5, window, sinks)):
+        check_grad(g, r, f"{name} {window}+{sinks}")
+    assert attn.device_status() == 0
