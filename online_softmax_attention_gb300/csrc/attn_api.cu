@@ -1,6 +1,7 @@
 // C ABI of the attention library: argument validation, workspace layout,
 // schedule preparation and kernel dispatch.  See include/attn.h for the
 // contract of each entry point.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -188,7 +189,8 @@ size_t parts_layout(int blocks, int rows, int D, void *workspace, Parts &w) {
 // microseconds for this many); batches of more sequences take the prepared schedule.
 constexpr int kPackedMaxSeqs = 2048;
 
-// A sliding window's arguments: 0 and 0, or window > 0 and the causal relation.
+// A sliding window's arguments: 0 and 0, or window > 0 and the causal relation.  (Kernels get no more sinks
+// than there can be keys, so that sums with them stay below 2^31.)
 int check_window(int window, int sinks, int relation) {
     if (window < 0 || sinks < 0 || (window == 0 && sinks > 0)) return ATTN_EINVAL;
     return window > 0 && relation != ATTN_CAUSAL ? ATTN_EUNSUPPORTED : ATTN_OK;
@@ -282,7 +284,7 @@ int plan_fwd(const attn_fwd_args *a, FwdParams &p, bool &use_tc, bool check_view
     p.pruned_tiles = reinterpret_cast<unsigned long long *>(a->pruned_tiles);
     if (a->window < a->n_k) {  // (a longer one leaves nothing out)
         p.window = a->window;
-        p.sinks = a->sinks;
+        p.sinks = std::min(a->sinks, a->n_k);
     }
     rc = choose_tc(a->kernel, p.window ? group_supported(p.dtype, p.D, p.group) : tc_fwd_supported(p), use_tc);
     if (rc) return rc;
@@ -458,7 +460,7 @@ int build_bwd(const attn_bwd_args *a, BwdParams &p, bool &use_tc) {
     p.cu_q = a->cu_seqlens_q; p.cu_k = a->cu_seqlens_k;
     if (a->window < a->n_k) {  // (a longer one leaves nothing out)
         p.window = a->window;
-        p.sinks = a->sinks;
+        p.sinks = std::min(a->sinks, a->n_k);
     }
     const bool fused = bwd_fused(a);
     const BwdLayout L = bwd_layout(a->n_seq, a->H, a->n_q, a->D, fused, sink_floats(a));
@@ -582,7 +584,7 @@ int plan_tree(const attn_tree_args *a, TreeParams &p, bool check_views = true) {
     p.dtype = a->cache.dtype; p.o_dtype = a->o_dtype;
     if (a->window < a->cache.max_pages * a->cache.page_size) {  // (a longer one leaves nothing out)
         p.window = a->window;
-        p.sinks = a->sinks;
+        p.sinks = std::min(a->sinks, a->cache.max_pages * a->cache.page_size);
     }
     return ATTN_OK;
 }
@@ -616,7 +618,7 @@ int plan_weigh(const attn_weigh_args *a, WeighParams &p, bool check_views = true
     p.scale_log2 = a->scale * 1.4426950408889634f;
     if (a->window < a->cache.max_pages * a->cache.page_size) {
         p.window = a->window;
-        p.sinks = a->sinks;
+        p.sinks = std::min(a->sinks, a->cache.max_pages * a->cache.page_size);
     }
     return ATTN_OK;
 }
@@ -1125,6 +1127,8 @@ int attn_cache_evict(const attn_cache *c, const int32_t *seqs, const int32_t *bu
     if (!w || n < 0 || sinks < 0 || recent < 0 || w->n_layers < 1 || w->cols < 0 || w->stride_seq < w->cols ||
         w->stride_layer < 0)
         return ATTN_EINVAL;
+    // (the layers' rows are moved at the same time)
+    if (w->n_layers > 1 && w->stride_layer < (int64_t)(c->max_seqs - 1) * w->stride_seq + w->cols) return ATTN_EINVAL;
     if (w->cols > kMostTokens) return ATTN_EUNSUPPORTED;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
         workspace_bytes < evict_plan(n, w->cols, workspace, e))

@@ -324,3 +324,49 @@ def test_backward_of_sinks_that_many_queries_see(kernel, dtype, d, window, sinks
     for name, g, r in zip(("dq", "dk", "dv"), call.run(), gradients(x, lens, d ** -0.5, window, sinks)):
         check_grad(g, r, f"{name} {window}+{sinks}")
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float16, 64)])
+def test_values_that_a_window_hides_stay_out_of_the_units_behind(dtype, d):
+    """A value of infinity beside the sinks reaches the rows that see it and their tiles, no others."""
+    x, _ = make([1500], 8, 2, d, dtype, 60)
+    c = cuda(x)
+    want = attn.fwd(c["q"], c["k"], c["v"], causal=True, window=100, sinks=5)
+    c["v"][6:12] = torch.inf
+    got = attn.fwd(c["q"], c["k"], c["v"], causal=True, window=100, sinks=5)
+    assert torch.equal(got[0][256:], want[0][256:]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype,kernel", [(torch.bfloat16, "tc"), (torch.float32, "simt")])
+def test_a_step_with_more_sinks_than_keys(dtype, kernel):
+    x, cu = make([500, 90], 4, 2, 64, dtype, 61, True)
+    c = cuda(x)
+    w = dict(causal=True, cu_seqlens_q=cu, kernel=kernel, window=5, sinks=2 ** 31 - 1)
+    o, lse = attn.fwd(c["q"], c["k"], c["v"], out_dtype=torch.float32, **w)
+    assert_output(o, lse, reference(x, [500, 90], 0.125, None, 0), dtype)
+    got = attn.bwd(c["q"], c["k"], c["v"], o, lse, c["do"], grad_dtype=torch.float32, **w)
+    for name, g, r in zip(("dq", "dk", "dv"), got, gradients(x, [500, 90], 0.125, None, 0)):
+        check_grad(g, r, name)
+    assert attn.device_status() == 0
+
+
+def test_two_steps_at_once():
+    x, cu = make([900, 300], 8, 2, 64, torch.float16, 62, True)
+    c = cuda(x)
+    calls, want = [], []
+    for window, sinks in ((100, 4), (300, 0)):
+        f = attn.FwdCall(c["q"], c["k"], c["v"], causal=True, cu_seqlens_q=cu, window=window, sinks=sinks)
+        o, lse = f.run()
+        b = attn.BwdCall(c["q"], c["k"], c["v"], o, lse, c["do"], causal=True, cu_seqlens_q=cu, window=window, sinks=sinks)
+        want.append([t.clone() for t in (o, lse, *b.run())])
+        calls.append((f, b))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [None] * 2
+    for _ in range(5):
+        for i, (s, (f, b)) in enumerate(zip(streams, calls)):
+            with torch.cuda.stream(s):
+                got[i] = [*f.run(), *b.run()]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(y, z) for y, z in zip(a, b))

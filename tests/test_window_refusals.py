@@ -149,3 +149,11 @@ def test_windows_as_python_gives_them():
     for bad in ((4.0, 0), (True, 0), (4, None), (4, 1.5), ("4", 0)):
         with pytest.raises(TypeError, match="whole number"):
             _host.window(*bad)
+
+
+@pytest.mark.parametrize("layer,seq", [(0, 128), (511, 128), (600, 200)])
+def test_weights_whose_layers_overlap_are_refused(layer, seq):
+    """4 sequences' rows a layer, moved at the same time as the other layer's."""
+    assert _cache().max_seqs == 4
+    assert _evict(w=_abi.Weights(A, layer, seq, 2, 128)) == _abi.ATTN_EINVAL
+    assert _evict(w=_abi.Weights(A, layer, seq, 1, 128), n=0) == _abi.ATTN_OK
