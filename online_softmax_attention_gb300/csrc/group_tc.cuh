@@ -767,16 +767,28 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return false;
             tc_fence_after();
-            if (left < 16 * steps && (t == 0 || j >= sg.n[0] || left >= 16 * steps_of(sg, 0, sg.j0 + j))) {
-                // V rows of the last MMA step behind the entry's end (another sequence's, stale
-                // slots; NaN times p = 0 would be NaN): zeroed, by the query tile whose value
-                // contraction comes first.  (V landed with K, before the scores waited for.)
-                const int first = max(0, left), chunks = (16 * steps - first) * 8;  // 16-byte chunks of a box
-                const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + first * 128;
+            auto zero_rows = [&](int from, int to) {  // of V
+                const int chunks = (to - from) * 8;   // 16-byte chunks of a box
+                const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + from * 128;
 #pragma unroll
-                for (int b = 0; b < C::kBoxes; ++b)
-                    if (lrow < chunks) st_shared_v4(base + b * C::kBoxBytes + 16 * lrow, 0, 0, 0, 0);
+                for (int b = 0; b < C::kBoxes; ++b) {
+                    if constexpr (kWindow) {
+#pragma unroll 1
+                        for (int x = lrow; x < chunks; x += BM) st_shared_v4(base + b * C::kBoxBytes + 16 * x, 0, 0, 0, 0);
+                    } else {
+                        if (lrow < chunks) st_shared_v4(base + b * C::kBoxBytes + 16 * lrow, 0, 0, 0, 0);
+                    }
+                }
                 fence_proxy_async_smem();
+            };
+            // V rows of the last MMA step behind the entry's end (another sequence's, stale
+            // slots; NaN times p = 0 would be NaN): zeroed, by the query tile whose value
+            // contraction comes first.  (V landed with K, before the scores waited for.)
+            if (left < 16 * steps && (t == 0 || j >= sg.n[0] || left >= 16 * steps_of(sg, 0, sg.j0 + j)))
+                zero_rows(max(0, left), 16 * steps);
+            if constexpr (kWindow) {  // so are those that the window hides from all the unit's rows
+                const int from = max(p.sinks - key0, 16 * first_step(sg, t, sg.j0 + j)), to = min(sg.from[0] - key0, 16 * steps);
+                if (max(0, from) < to && (t == 0 || j >= sg.n[0])) zero_rows(max(0, from), to);
             }
             const int chunks = (steps + 1) >> 1, chunk0 = first_step(sg, t, sg.j0 + j) >> 1;
             float mx = -INFINITY;

@@ -37,10 +37,7 @@ namespace attn {
 namespace {
 
 // Warps of a block; with as many warps an SM, blocks of an SM.
-#ifndef ATTN_WINDOW_WARPS
-#define ATTN_WINDOW_WARPS 2
-#endif
-constexpr int warps_of(bool window, bool f32) { return window && !f32 ? ATTN_WINDOW_WARPS : 4; }
+constexpr int warps_of(bool window, bool f32) { return window && !f32 ? 2 : 4; }
 constexpr int per_sm(bool window, bool f32) { return 4 / warps_of(window, f32); }
 
 template <typename T, int D, bool kWindow>

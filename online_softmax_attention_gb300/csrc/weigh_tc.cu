@@ -310,8 +310,9 @@ __device__ void mma_issuer(const WeighParams &p, Bars &bars, const Seg *segs, ui
         for (int j = 0; j < n; ++j) {
             const uint32_t qs = qr.slot();
             const bool first = j == 0 || tile == 0, last = tile + 1 == g.tiles || j + 1 == n;  // of the key tiles
-            // whole MMA steps of 16 rows
-            const uint32_t id = idesc_f16(kBF16, BM, 0, 0) | ((uint32_t)(2 * max(1, cdiv(rows_of(g, tile, tok, p.group), 16))) << 17);
+            // whole MMA steps of 16 rows; a full tile's 128 columns, whatever G is: all of them are read
+            const int rows = rows_of(g, tile, tok, p.group);
+            const uint32_t id = idesc_f16(kBF16, BM, 0, 0) | ((uint32_t)(rows == tok * p.group ? BN / 8 : 2 * max(1, cdiv(rows, 16))) << 17);
             if (!wait(bars.q_full[qs], qr.phase())) return;
 #pragma unroll
             for (int t = 0; t < NKT; ++t) {

@@ -197,3 +197,32 @@ def test_workspaces_streams_and_graphs():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(w, want) for w in outs)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [11, 22, 28, 37, 48, 65, 100, 128])
+def test_groups_that_leave_a_part_of_a_query_tile(group, d):
+    """The rows of whole tokens are fewer than a tile's; calls before leave infinite scores behind."""
+    cache, model, seqs, g = make([300, 129], 16, 1, d, torch.bfloat16, 91)
+    big, _, ids, _ = make([700], 16, 1, d, torch.bfloat16, 92)
+    big.k.fill_(2.0 ** 120)
+    q = torch.full((600, 8, d), 2.0 ** 100).bfloat16().cuda()
+    for _ in range(2):
+        big.weigh(ids, [0, 600], q, torch.zeros(8, 600, device="cuda"), big.new_weights())
+    q = torch.randn(50, group, d, generator=g).bfloat16()
+    check(cache, model, seqs, [20, 30], q, what=f"{group}")
+
+
+@pytest.mark.parametrize("dtype,t", [(torch.bfloat16, 1), (torch.float16, 30), (torch.float32, 4)])
+def test_tokens_that_a_window_hides_may_hold_anything(dtype, t):
+    cache, _, seqs, g = make([700, 300], 16, 2, 64, dtype, 93)
+    q = torch.randn(2 * t, 8, 64, generator=g).to(dtype).cuda()
+    kw = dict(window=90, sinks=3)
+    lse = attn.tree_fwd(q, cache, seqs, [0, t, 2 * t], **kw)[1]
+    w, want = cache.new_weights(), cache.new_weights()
+    cache.weigh(seqs, [0, t, 2 * t], q, lse, want, **kw)
+    for s, n in zip(seqs, (700, 300)):
+        hidden = torch.arange(3, n - t + 1 - 90, device="cuda")
+        cache.k[:, cache.table[s].long()[hidden // 16], hidden % 16] = float("nan")
+    cache.weigh(seqs, [0, t, 2 * t], q, lse, w, **kw)
+    assert torch.equal(w, want) and torch.isfinite(w).all() and attn.device_status() == 0

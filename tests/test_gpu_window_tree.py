@@ -125,3 +125,50 @@ def test_a_prompt_and_its_decoding_are_one_attention(dtype, d):
     step = 2 * (2.0 ** -8 if dtype == torch.bfloat16 else 1e-5)
     assert (o - whole[0]).abs().max() <= step * (1 + whole[0].abs().max()) and (lse - whole[1]).abs().max() <= 2e-3
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float16, 64), (torch.float32, 64)])
+@pytest.mark.parametrize("lens,news,page,heads,group", [([700, 95], [1, 1], 16, 2, 4), ([700, 400], [3, 2], 32, 2, 2),
+                                                        ([900, 600], [40, 20], 64, 2, 4), ([700], [30], 8, 1, 2),
+                                                        ([2000], [1100], 16, 1, 2), ([2100, 1700], [1100, 70], 128, 1, 3)])
+@pytest.mark.parametrize("window,sinks", [(50, 0), (33, 5), (200, 130)])
+def test_tokens_that_no_row_sees_may_hold_anything(lens, news, page, heads, group, window, sinks, dtype, d):
+    cache, _, seqs, g = make(lens, page, heads, d, dtype, 78)
+    q = torch.randn(sum(news), heads * group, d, generator=g).to(dtype).cuda()
+    cu = [0] + [int(x) for x in np.cumsum(news)]
+    mask = torch.from_numpy(random_mask(news, -(-max(news) // 64), np.random.default_rng(79)).view(np.int64)).cuda()
+    calls = [dict(mask=m, window=window, sinks=sinks) for m in (None, mask)]
+    want = [attn.tree_fwd(q, cache, seqs, cu, **kw) for kw in calls]
+    for s, n, t in zip(seqs, lens, news):
+        hidden = torch.arange(sinks, max(sinks, n - t - window), device="cuda")
+        pages = cache.table[s].long()[hidden // page]
+        cache.k[:, pages, hidden % page] = float("nan")
+        cache.v[:, pages, hidden % page] = torch.inf
+    for kw, w in zip(calls, want):
+        got = attn.tree_fwd(q, cache, seqs, cu, **kw)
+        assert torch.isfinite(got[0]).all()
+        assert all(torch.equal(a, b) for a, b in zip(got, w)), kw["mask"] is None
+    assert attn.device_status() == 0
+
+
+def test_two_streams_at_once():
+    """Prepared calls of both kernels, on two streams over one cache."""
+    cache, _, seqs, g = make([3000, 1700, 900], 16, 2, 128, torch.bfloat16, 80)
+    calls = []
+    for t in (1, 40):
+        q = torch.randn(3 * t, 8, 128, generator=g).bfloat16().cuda()
+        calls += [attn.TreeCall(q, cache, seqs, [0, t, 2 * t, 3 * t], window=w, sinks=4) for w in (600, 90)]
+    want = []
+    for c in calls:
+        c.run()
+        want.append((c.o.clone(), c.lse.clone()))
+        c.o.fill_(9)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for s, c in zip(streams, calls):
+            with torch.cuda.stream(s):
+                c.run()
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(calls, want):
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
