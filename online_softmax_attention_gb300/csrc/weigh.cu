@@ -175,14 +175,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
             return key <= ctx + t && (!p.window || key > ctx + t - p.window || key < p.sinks);
         };
         auto token_of = [&](int r) { return key_head(r, p.group_inv); };  // of row r of a head
-        // minus the lse in log2 units of row r of the head whose rows begin at lh; one that does not exist, or
-        // saw nothing, adds 2^-inf
+        // the lse of row r of the head whose rows begin at lh
         auto lse_of = [&](const float *lh, int r) -> float {
             if (r >= rows) return -INFINITY;
             const int t = token_of(r);
-            const float x = __ldg(lh + (int64_t)(r - t * p.group) * p.n_q + t);
-            return x == -INFINITY ? -INFINITY : -x * kLog2e;
+            return __ldg(lh + (int64_t)(r - t * p.group) * p.n_q + t);
         };
+        // minus that in log2 units; a row that does not exist, or saw nothing, adds 2^-inf
+        auto added = [](float x) -> float { return x == -INFINITY ? -INFINITY : -x * kLog2e; };
         // the key that this lane writes, and its weight so far
         const int mine = key0 + (kMma ? g + 8 * c : lane);
         float *const w = p.weights + (int64_t)e.s * p.weights_stride + mine;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
                 if (none) continue;
                 for (int r0 = 0; r0 < rows; r0 += kRows) {
                     float x[2][4];
-                    const float n0 = l0, n1 = l1;
+                    const float n0 = added(l0), n1 = added(l1);  // (here, where the loads have landed)
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
                     }
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        const float pv = exp2_approx(fmaf(x[r], p.scale_log2, lse_of(lh, r0 + r)));
+                        const float pv = exp2_approx(fmaf(x[r], p.scale_log2, added(lse_of(lh, r0 + r))));
                         if (whole || sees(token_of(r0 + r), mine)) sum += pv;
                     }
                 }

@@ -15,7 +15,9 @@
 // MMAs into two TMEM buffers a key tile, 4-7 and 8-11 take the exponentials of a key tile each.
 // Every wait is bounded, as in fwd_tc.cu.
 //
-// Bound: the exponentials (the SFU) and the tensor pipe alike: 128 operations of 2 D a key and row.
+// Bound: the L2's reads.  A step takes 32 KiB of queries and, where a head has two tiles of them, 32 KiB of
+// keys (D = 128) into every SM: about 0.95 us a step at the 10 TB/s that all SMs draw so, of which the
+// exponentials and sums of a key tile take 0.55.  A third stage of queries does not fit the shared memory.
 #include "sm100.cuh"
 #include "stretch.cuh"
 #include "tc.h"
@@ -29,7 +31,8 @@ using namespace sm100;
 constexpr int BM = 128, BN = 128;  // keys; query rows
 constexpr int kThreads = 384;
 constexpr int kSegs = 4;
-constexpr int kSegConsumers = 2 + 8;
+constexpr int kSumWarps = 8;
+constexpr int kSegConsumers = 2 + kSumWarps;
 constexpr int NKT = 2, kUnit = NKT * BM;  // key tiles of a unit; keys
 constexpr int kBuffers = 2;  // TMEM, of a key tile
 
@@ -40,7 +43,7 @@ struct Cfg {
     static constexpr int kTileBytes = 128 * D * 2;
     static constexpr int kKStages = D == 128 ? 4 : 8, kQStages = D == 128 ? 2 : 4;
     static constexpr int kSmemBytes = (kKStages + kQStages) * kTileBytes + 1024;
-    static_assert(kSmemBytes + 6144 <= 232448, "shared memory budget (dynamic + static)");
+    static_assert(kSmemBytes + 4 * kSumWarps * 2 * BN + 6144 <= 232448, "shared memory budget (dynamic + static)");
     static constexpr int kRegsProducer = 88, kRegsSum = 208;
     static_assert(128 * kRegsProducer + 256 * kRegsSum <= kThreads * 168, "register split");
 };
@@ -68,7 +71,6 @@ struct __align__(8) Bars {
     uint64_t q_full[4], q_empty[4], k_full[8], k_empty[8];
     uint64_t s_full[NKT][kBuffers], s_empty[NKT][kBuffers];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
-    uint64_t stats_ready[2][2];          // a step's lse, by warpgroup and buffer
     uint64_t mma_drain;
 };
 
@@ -347,10 +349,21 @@ __device__ void mma_issuer(const WeighParams &p, Bars &bars, const Seg *segs, ui
 __device__ void sum_wg(const WeighArgs &a, Bars &bars, const Seg *segs, float *stats, uint32_t tmem, const Watchdog &wd) {
     const WeighParams &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wg = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;  // key row; also the query row whose lse it stages
-    const int tok = BN / p.group, my_tok = row / p.group, my_head = row - my_tok * p.group;
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;  // key row
+    const int tok = BN / p.group;
+    // the query rows whose lse this lane puts into its warp's copy: tokens within a tile, offsets of their heads
+    // (every warp has a copy, so that none waits for another)
+    constexpr int kPer = BN / 32;
+    int my_tok[kPer], my_head[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int r = lane + 32 * k;
+        my_tok[k] = r / p.group;
+        my_head[k] = r - my_tok[k] * p.group;
+        if (my_tok[k] >= tok) my_tok[k] = -1;  // (G does not divide 128)
+    }
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    stats += wg * 2 * BN;
+    stats += (warp - 4) * 2 * BN;
     uint32_t step = 0;  // of this warpgroup
     for (int i = 0;; ++i) {
         const int slot = i % kSegs;
@@ -368,28 +381,28 @@ __device__ void sum_wg(const WeighArgs &a, Bars &bars, const Seg *segs, float *s
         const float old = writes && key < g.L - g.fresh ? *w : 0.f;
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         int hk = g.j0 / g.tiles, tile = g.j0 - hk * g.tiles;
-        // minus the lse, in log2 units, of this thread's row of a step; a row that does not exist, or saw nothing,
-        // adds 2^-inf
-        auto fetch = [&](int hk, int tile) -> float {
-            const int t = (g.tile0 + tile) * tok + my_tok;
-            if (my_tok >= tok || t >= g.T) return -INFINITY;
-            const float x = __ldg(p.lse + (int64_t)(hk * p.group + my_head) * p.n_q + g.q0 + t);
-            return x == -INFINITY ? -INFINITY : -x * kLog2e;
+        // the lse of this lane's rows of a step, as it is: nothing waits for the loads before the next step
+        auto fetch = [&](int hk, int tile, float (&x)[kPer]) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int t = (g.tile0 + tile) * tok + my_tok[k];
+                x[k] = my_tok[k] >= 0 && t < g.T ? __ldg(p.lse + (int64_t)(hk * p.group + my_head[k]) * p.n_q + g.q0 + t) : -INFINITY;
+            }
         };
-        float next = fetch(hk, tile);
+        float next[kPer];
+        fetch(hk, tile, next);
         for (int j = 0; j < g.n; ++j, ++step) {
+            // minus the lse in log2 units; a row that does not exist, or saw nothing, adds 2^-inf
             float *sb = stats + (step & 1) * BN;
-            sb[row] = next;
-            uint64_t &ready = bars.stats_ready[wg][step & 1];
-            mbar_arrive_warp(smem_u32(&ready));
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) sb[lane + 32 * k] = next[k] == -INFINITY ? -INFINITY : -next[k] * kLog2e;
+            __syncwarp();
             const int t0 = (g.tile0 + tile) * tok, rows = rows_of(g, tile, tok, p.group);
             if (++tile == g.tiles) {
                 tile = 0;
                 ++hk;
             }
-            if (j + 1 < g.n) next = fetch(hk, tile);  // in flight during this step
-            ok = mbar_wait_small(smem_u32(&ready), (step >> 1) & 1, wd);
-            if (!__all_sync(0xffffffffu, ok)) return;
+            if (j + 1 < g.n) fetch(hk, tile, next);  // in flight during this step
             const uint32_t buffer = step % kBuffers, at = tmem_addr(tmem, 32 * quarter, BN * (kBuffers * wg + buffer));
             ok = mbar_wait_small(smem_u32(&bars.s_full[wg][buffer]), (step / kBuffers) & 1, wd);
             if (!__all_sync(0xffffffffu, ok)) return;
@@ -444,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     __shared__ Seg segs[kSegs];
-    __shared__ __align__(16) float stats[2 * 2 * BN];
+    __shared__ __align__(16) float stats[kSumWarps * 2 * BN];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const uint32_t raw = smem_u32(smem_raw), sK = (raw + 1023u) & ~1023u, sQ = sK + C::kKStages * C::kTileBytes;
@@ -469,10 +482,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         for (int s = 0; s < kSegs; ++s) {
             mbar_init(smem_u32(&bars.seg_full[s]), 1);
             mbar_init(smem_u32(&bars.seg_empty[s]), kSegConsumers);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars.stats_ready[0][s]), 4);
-            mbar_init(smem_u32(&bars.stats_ready[1][s]), 4);
         }
         mbar_init(smem_u32(&bars.mma_drain), 1);
         fence_mbar_init();
@@ -582,8 +591,8 @@ cudaError_t launch_typed(const WeighArgs &a, cudaStream_t s) {
 }  // namespace
 
 // More than 8 query rows a key head: on the tensor cores.  (64 sequences of 3000 tokens, 32 / 8 heads,
-// D = 128; weigh.cu and this kernel: 8 rows 68 us and about 70, 16 rows 87 and 70, 32 rows 148 and 68, 256
-// rows 1138 and 136.)
+// D = 128; weigh.cu and this kernel: 8 rows 67 us and about 70, 16 rows 80 and 70, 32 rows 141 and 70, 256
+// rows 1138 and 111.)
 bool weigh_on_tc(const WeighParams &p) {
     return p.dtype != ATTN_F32 && !p.window && p.n_q > 0 && p.group <= BN && p.c.page_shift >= 3 &&
            (int64_t)p.n_q * p.group > (int64_t)8 * p.n && tc_device_ok();
