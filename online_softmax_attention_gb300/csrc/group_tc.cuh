@@ -878,8 +878,9 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                 p.lse[(int64_t)(hk * p.group + lrow - my_tok * p.group) * p.n_q + q0 + token] =
                     l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
         } else {
-            // (at most two parts a block: a row a lane, in little code)
-            float *row = p.parts.o + (part_row + lrow) * D;
+            // as parts_merge.cu reads them: four columns of a warp's 32 rows after the other, so that a store
+            // writes whole lines (a row after the other: 6200 cycles for the two query tiles' 128 KiB)
+            float *at = p.parts.o + (part_row + 32 * quarter) * D + 4 * lane;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t u[32];
@@ -888,7 +889,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                 if (lrow < live) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(row + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                        *reinterpret_cast<uint4 *>(at + 32 * (c + e)) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
                 }
             }
             if (lrow < live) p.parts.ml[part_row + lrow] = make_float2(m, l);

@@ -143,7 +143,7 @@ struct CutUnit {
     int pad[3];
 };
 struct Parts {
-    float *o;       // (2 blocks, rows, D) f32 sums relative to the row's max
+    float *o;       // (2 blocks, rows, D) f32 sums relative to the row's max; more than 16 rows: (2 blocks, rows / 32, D / 4, 32, 4)
     float2 *ml;     // (2 blocks, rows): max in log2 units, sum
     CutUnit *cut;   // (blocks)
 };
