@@ -403,6 +403,8 @@ __device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars<kWindow> &bars, uint32_t s
             tc_commit(smem_u32(&bars.st_full));
             issue_ss(BT, sV, sDO + qslot(0) * C::kTileBytes, idSS);  // dP^T = V dO^T
             tc_commit(smem_u32(&bars.dp_full));
+            // the item's last dP^T: the next item's K and V land during the rest of it
+            if (f.nq == 1) tc_commit(smem_u32(&bars.kv_empty));
         }
         __syncwarp();
         // Per query block qb three issue steps, each behind one barrier:
@@ -444,6 +446,7 @@ __device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars<kWindow> &bars, uint32_t s
                         if (qb + 1 < f.nq) {
                             issue_ss(BT, sV, sDO + qslot(qb + 1) * C::kTileBytes, idSS);  // dP^T of the next block
                             tc_commit(smem_u32(&bars.dp_full));
+                            if (qb + 2 == f.nq) tc_commit(smem_u32(&bars.kv_empty));
                         }
                         ++qb;
                         step = 0;
@@ -463,10 +466,7 @@ __device__ void dkdv_mma(const TcBwdArgs &a, DkdvBars<kWindow> &bars, uint32_t s
         }
         ++af_cnt;
         q0 += f.nq;
-        if (elect_one()) {
-            tc_commit(smem_u32(&bars.acc_done));
-            tc_commit(smem_u32(&bars.kv_empty));
-        }
+        if (elect_one()) tc_commit(smem_u32(&bars.acc_done));
         __syncwarp();
     }
 }
@@ -1187,6 +1187,8 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
             issue_ss(BT, ddo_desc, sV + (g0 % VS) * C::kTileBytes, of_steps(idSS, steps_of(f, 0, p.sinks)));  // dP = dO V^T
             tc_commit(smem_u32(&bars.dp_full));
             tc_commit(smem_u32(&bars.v_empty[g0 % VS]));
+            // the item's last dP: the next item's Q and dO land during the rest of it
+            if (f.nk == 1) tc_commit(smem_u32(&bars.q_empty));
         }
         __syncwarp();
         // Per key block j (global g = g0 + j) three issue steps, each behind its barriers:
@@ -1228,6 +1230,7 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
                             issue_ss(BT, ddo_desc, sV + ((g + 1) % VS) * C::kTileBytes, of_steps(idSS, steps_of(f, j + 1, p.sinks)));
                             tc_commit(smem_u32(&bars.dp_full));
                             tc_commit(smem_u32(&bars.v_empty[(g + 1) % VS]));
+                            if (j + 2 == f.nk) tc_commit(smem_u32(&bars.q_empty));
                         }
                         step = 2;
                     } else {
@@ -1257,10 +1260,7 @@ __device__ void dq_mma(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32_t sQ, u
         }
         ++af_cnt;
         g0 += f.nk;
-        if (elect_one()) {
-            tc_commit(smem_u32(&bars.acc_done));
-            tc_commit(smem_u32(&bars.q_empty));
-        }
+        if (elect_one()) tc_commit(smem_u32(&bars.acc_done));
         __syncwarp();
     }
 }
