@@ -558,7 +558,7 @@ ATTN_API int attn_cache_compact(const attn_cache *c, int32_t *remap, void *works
 /* Adds the attention that cached tokens get from new ones to their weights (see
  * attn_weigh_args).  Calls on the same rows of weights must be ordered by the caller, and
  * calls that may overlap need a workspace each; its size depends on sizes only (0 for few
- * query rows an entry, f32, windows, pages below 8 rows, and arguments that are refused). */
+ * query rows an entry, f32, pages below 8 rows, and arguments that are refused). */
 ATTN_API int attn_cache_weigh(const attn_weigh_args *a, void *stream);
 ATTN_API size_t attn_weigh_workspace_bytes(const attn_weigh_args *a);
 

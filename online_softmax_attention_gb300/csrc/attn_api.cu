@@ -626,12 +626,14 @@ int plan_weigh(const attn_weigh_args *a, WeighParams &p, bool check_views = true
 // Lays the eviction's plan out in the workspace; returns its bytes.
 size_t evict_plan(int n, int cols, void *workspace, EvictParams &p) {
     const size_t list = align256(sizeof(int) * ((size_t)n + 1)), rows = align256(sizeof(int) * (size_t)n * (size_t)cols);
+    const bool numbers = evict_needs_numbers(cols);
     char *at = static_cast<char *>(workspace);
     p.good = reinterpret_cast<int *>(at);
     p.len = reinterpret_cast<int *>(at + list);
     p.first = reinterpret_cast<int *>(at + 2 * list);
     p.source = reinterpret_cast<int *>(at + 3 * list);
-    return 3 * list + rows;
+    p.numbers = numbers ? reinterpret_cast<uint32_t *>(at + 3 * list + rows) : nullptr;
+    return 3 * list + (numbers ? 2 : 1) * rows;
 }
 
 int build_cache(const attn_cache *c, int n, void *workspace, size_t workspace_bytes, CacheParams &p, CachePlan &w) {

@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kHeld = 40960;  // tokens whose numbers fit shared memory; more are summed anew each pass
+constexpr int kHeld = 40960;  // tokens whose numbers fit shared memory; more have them in the workspace
 
 __device__ __forceinline__ bool in_range(int x, int n) { return (unsigned)x < (unsigned)n; }
 
@@ -72,7 +72,7 @@ __device__ __forceinline__ int block_prefix(int x, int *s_warp, int &total) {
 constexpr int kBins = 2048;
 
 __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheParams c, const EvictParams p) {
-    extern __shared__ uint32_t held[];
+    extern __shared__ uint32_t s_held[];
     __shared__ int bins[kBins], s_warp[32], s_first, s_digit, s_above;
     pdl_trigger();
     pdl_wait();
@@ -121,13 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
             r[k] = order_of(x);
         }
     };
-    const bool keep = n <= kHeld;
-    auto number_of = [&](int t) -> uint32_t {
-        if (keep) return held[t];
-        uint32_t r[kTokens];
-        sums_of(t, r);
-        return r[0];
-    };
+    uint32_t *const held = n <= kHeld ? s_held : p.numbers + (int64_t)i * p.cols;
 
     // the smallest number that is kept: its digits from the top; `left` of those that share them so far
     uint32_t found = 0;
@@ -137,16 +131,15 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 0 : pass == 1 ? 21 : 10;
         for (int b = tid; b < kBins; b += kPlanThreads) bins[b] = 0;
         __syncthreads();
-        const bool sums = pass == 0 || !keep;
         for (int t = tid; t < n; t += kTokens * kPlanThreads) {
             uint32_t x[kTokens];
-            if (sums) sums_of(t, x);
+            if (pass == 0) sums_of(t, x);
 #pragma unroll
             for (int k = 0; k < kTokens; ++k) {
                 const int at = t + kPlanThreads * k;
                 if (at >= n) break;
-                if (!sums) x[k] = held[at];
-                else if (keep) held[at] = x[k];
+                if (pass > 0) x[k] = held[at];
+                else held[at] = x[k];
                 if (pass == 0 || x[k] >> above == found >> above)
                     atomicAdd(&bins[(x[k] >> shift) & (pass == 2 ? 1023u : 2047u)], 1);
             }
@@ -175,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
     int more = 0, equal = 0;
     if (want > 0)
         for (int t = t0; t < t1; ++t) {
-            const uint32_t x = number_of(t);
+            const uint32_t x = held[t];
             more += x > found;
             equal += x == found;
         }
@@ -183,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
     const int ties = max(0, min(equal, left - block_prefix(equal, s_warp, all)));  // of this run that are kept
     int to = sinks + block_prefix(more + ties, s_warp, all), taken = 0, first = len;
     for (int t = t0; t < t1; ++t) {
-        const uint32_t x = want > 0 ? number_of(t) : 0u;
+        const uint32_t x = want > 0 ? held[t] : 0u;
         if (want > 0 && (x > found || (x == found && taken < ties))) {
             taken += x == found;
             source[to++] = sinks + t;
@@ -320,8 +313,10 @@ cudaError_t launch_move(const CacheParams &c, const EvictParams &p, unsigned y, 
 
 }  // namespace
 
+bool evict_needs_numbers(int cols) { return cols > kHeld; }
+
 cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaStream_t s) {
-    const int held = 4 * (p.cols < kHeld ? p.cols : kHeld);
+    const int held = 4 * (p.cols < kHeld ? p.cols : kHeld);  // bytes
     cudaError_t e = cudaFuncSetAttribute(evict_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, held);
     if (e != cudaSuccess) return e;
     e = launch_pdl(evict_choose_kernel, dim3(p.n), dim3(kPlanThreads), held, s, c, p);

@@ -239,6 +239,7 @@ struct WeighCut {
     int last;           // block that holds the unit's last part; <= the writing block: nothing to merge
     int s, key0;        // sequence, first key
     int L, fresh;       // of the entry
+    int refused;        // the list is
 };
 bool weigh_on_tc(const WeighParams &p);
 size_t weigh_tc_bytes(void *workspace, WeighParams &p);  // lays the workspace out; its bytes
@@ -257,7 +258,9 @@ struct EvictParams {
     int *len;     // n: length before the call
     int *first;   // n, of those that are cut: tokens that stay where they are, before the first that goes
     int *source;  // (n, cols): the kept tokens, in order
+    uint32_t *numbers;  // (n, cols) where evict_needs_numbers: the tokens' weights as numbers
 };
+bool evict_needs_numbers(int cols);
 cudaError_t launch_cache_evict(const CacheParams &c, const EvictParams &p, cudaStream_t s);
 
 cudaError_t launch_cache_extend(const CacheParams &c, const CachePlan &w, const int *seqs, const int *counts, int n,

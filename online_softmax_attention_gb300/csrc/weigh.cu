@@ -3,8 +3,8 @@
 // exp(scale <q_th, k_j> - lse_th), where t sees j.  The rows' lse is known, so there is no
 // running maximum, values are not read, and nothing is joined between blocks.
 //
-// Decomposition.  A unit is 32 keys of one entry with all its heads and rows, and one warp has
-// all of it, so that a token's sum is in one place: no atomics, no joining, a fixed order.
+// Decomposition.  A unit is 32 keys of one entry with all its heads and rows, and one warp (of f32: a
+// block, mostly) has all of it, so that a token's sum is in one place: no atomics, a fixed order.
 // Blocks take equal stretches of all units (stretch.cuh), their warps a unit each in turn.
 //
 // 16-bit caches.  A warp's K rows, a key head at a time, come through a ring of cp.async stages
@@ -16,7 +16,8 @@
 // exponentials of four keys over its columns, and lanes are joined once a unit.  f32 caches use
 // FFMA, a key a lane.
 //
-// Bound: HBM, the K rows read once, for few rows; the mma.sync rate for many.
+// Bound: HBM, the K rows read once.  (More than eight rows a key head run weigh_tc.cu, but for f32, pages below
+// 8 rows and groups of more than 128.)
 #include "../../include/attn.h"
 #include "mma.cuh"
 #include "stretch.cuh"
@@ -75,11 +76,15 @@ struct Cursor {
     Entry e;
 };
 
-template <typename T, int D>
+// kWide (f32): a block's warps share a unit, its rows eight at a time, and add their sums up in order.
+template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kernel(const WeighParams p) {
     using C = Cfg<T, D>;
     constexpr bool kMma = C::kMma;
     constexpr int kSteps = D / 32;  // 16-byte chunks of a row a lane
+    constexpr int kTurn = kWide ? 1 : kWarps;  // units at a time
+    static_assert(!kMma || !kWide);
+    __shared__ float s_sum[kWide ? kWarps : 1][kKeys];
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -105,9 +110,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
     }
     Stretch st;
     const bool any = find_stretch<kWarps, 0>(
-        p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at(p, i, report).units}; }, st);
+        p.n, kTurn, [&](int i, bool report) { return Work{0, entry_at(p, i, report).units}; }, st);
     if (!any) return;
-    Cursor now{st.at + warp, st.before, st.entry, entry_at(p, st.entry, false)};
+    Cursor now{st.at + (kWide ? 0 : warp), st.before, st.entry, entry_at(p, st.entry, false)};
     // to the entry of unit cur.at, which is one of the stretch's
     auto seek = [&](Cursor &cur) {
         while (cur.at >= cur.before + cur.e.units) {
@@ -123,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
     // offset of this lane's key's row; -1: no such key, or none that is seen
     auto row_of = [&](const Entry &e, int key0) -> long long {
         const int key = key0 + lane;
-        if (key >= e.L || e.T == 0 || hidden(e, key0)) return -1;
+        if (key >= e.L || e.T == 0 || (p.window && key >= p.sinks && key < e.L - e.T + 1 - p.window)) return -1;
         const int page = p.c.table[(int64_t)e.s * p.c.table_stride + (key >> p.c.page_shift)];
         if ((unsigned)page < (unsigned)p.c.n_pages)
             return page * p.c.b_page + (key & ((1 << p.c.page_shift) - 1)) * p.c.b_tok;
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
     for (int s = 0; s < C::kStages - 1; ++s) load_next(s);
 
     int stage = 0;
-    for (; now.at < st.end; now.at += kWarps) {
+    for (; now.at < st.end; now.at += kTurn) {
         seek(now);
         const Entry &e = now.e;
         const int key0 = (int)(now.at - now.before) * kKeys, ctx = e.L - e.T, rows = e.T * p.group;
@@ -256,46 +261,59 @@ __global__ void __launch_bounds__(kThreads, Cfg<T, D>::kMma ? 1 : 2) weigh_kerne
             sum = c == 0 ? acc[0] : c == 1 ? acc[1] : c == 2 ? acc[2] : acc[3];
         } else {
             const long long off = row_of(e, key0);
-            for (int hk = 0; hk < p.c.H && __any_sync(0xffffffffu, off >= 0); ++hk) {
+            const int runs = (rows + kRows - 1) / kRows;  // of a head's rows
+            int hk = 0, run = kWide ? warp : 0;
+            for (; __any_sync(0xffffffffu, off >= 0); run += kWide ? kWarps : 1) {
+                while (run >= runs && hk < p.c.H) {
+                    run -= runs;
+                    ++hk;
+                }
+                if (hk == p.c.H) break;
+                const int r0 = run * kRows;
                 const float4 *kr = reinterpret_cast<const float4 *>(p.c.k + hk * p.c.b_head + (off < 0 ? 0 : off));
                 const T *qh = static_cast<const T *>(p.q) + (int64_t)e.q0 * p.q_st + (int64_t)hk * p.group * p.q_sh;
                 const float *lh = p.lse + (int64_t)hk * p.group * p.n_q + e.q0;
-                for (int r0 = 0; r0 < rows; r0 += kRows) {
-                    float x[kRows];
-                    const float4 *qr[kRows];
+                float x[kRows];
+                const float4 *qr[kRows];
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
-                        const int row = min(r0 + r, rows - 1), t = token_of(row);
-                        qr[r] = reinterpret_cast<const float4 *>(qh + (int64_t)t * p.q_st + (row - t * p.group) * p.q_sh);
-                        x[r] = 0.f;
-                    }
+                for (int r = 0; r < kRows; ++r) {
+                    const int row = min(r0 + r, rows - 1), t = token_of(row);
+                    qr[r] = reinterpret_cast<const float4 *>(qh + (int64_t)t * p.q_st + (row - t * p.group) * p.q_sh);
+                    x[r] = 0.f;
+                }
 #pragma unroll 4
-                    for (int d = 0; d < D / 4; ++d) {
-                        const float4 kv = off >= 0 ? __ldg(kr + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int r = 0; r < kRows; ++r) {
-                            const float4 qv = __ldg(qr[r] + d);
-                            x[r] = fmaf(qv.x, kv.x, x[r]);
-                            x[r] = fmaf(qv.y, kv.y, x[r]);
-                            x[r] = fmaf(qv.z, kv.z, x[r]);
-                            x[r] = fmaf(qv.w, kv.w, x[r]);
-                        }
-                    }
+                for (int d = 0; d < D / 4; ++d) {
+                    const float4 kv = off >= 0 ? __ldg(kr + d) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        const float pv = exp2_approx(fmaf(x[r], p.scale_log2, added(lse_of(lh, r0 + r))));
-                        if (whole || sees(token_of(r0 + r), mine)) sum += pv;
+                        const float4 qv = __ldg(qr[r] + d);
+                        x[r] = fmaf(qv.x, kv.x, x[r]);
+                        x[r] = fmaf(qv.y, kv.y, x[r]);
+                        x[r] = fmaf(qv.z, kv.z, x[r]);
+                        x[r] = fmaf(qv.w, kv.w, x[r]);
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float pv = exp2_approx(fmaf(x[r], p.scale_log2, added(lse_of(lh, r0 + r))));
+                    if (whole || sees(token_of(r0 + r), mine)) sum += pv;
+                }
+            }
+            if constexpr (kWide) {
+                s_sum[warp][lane] = sum;
+                __syncthreads();
+                sum = 0.f;
+                for (int x = 0; x < kWarps; ++x) sum += s_sum[x][lane];
+                __syncthreads();  // (before the next unit's)
             }
         }
-        if (mine < e.L) *w = old + sum;
+        if (mine < e.L && (!kWide || warp == 0)) *w = old + sum;
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_typed(const WeighParams &p, cudaStream_t s) {
-    auto kern = weigh_kernel<T, D>;
+template <typename T, int D, bool kWide>
+cudaError_t launch_kernel(const WeighParams &p, cudaStream_t s) {
+    auto kern = weigh_kernel<T, D, kWide>;
     using C = Cfg<T, D>;
     const size_t bits = p.n > 1 ? sizeof(uint32_t) * (size_t)((p.c.max_seqs + 31) / 32) : 0;
     const size_t smem = C::kRingBytes > bits ? C::kRingBytes : bits;
@@ -304,6 +322,16 @@ cudaError_t launch_typed(const WeighParams &p, cudaStream_t s) {
     e = launch_pdl(kern, dim3((C::kMma ? 1 : 2) * sm_count()), dim3(kThreads), smem, s, p);
     count_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// f32: a block a unit where that gives all its warps rows, eight of a key head's to each.  (A chunk of 128 of
+// 5000 tokens, window 1000, 32 / 8 heads: 3907 us with a warp a unit, 665 so; 64 sequences of 3000, a new
+// token each: 439 and 397.)
+template <typename T, int D>
+cudaError_t launch_typed(const WeighParams &p, cudaStream_t s) {
+    if constexpr (!Cfg<T, D>::kMma)
+        if (p.c.H * ((int64_t)p.n_q * p.group / p.n / kRows + 1) >= kWarps) return launch_kernel<T, D, true>(p, s);
+    return launch_kernel<T, D, false>(p, s);
 }
 
 template <typename T>

@@ -8,7 +8,9 @@
 // Schedule.  A unit is two 128-key tiles of an entry, which share every query tile that is loaded;
 // its steps are its (key head, tile of query rows) pairs that have a row which sees one of its
 // keys.  Every block takes an equal stretch of all units' steps (stretch.cuh).  A unit that is cut
-// leaves its parts' 256 sums in two slots a block, and a small kernel adds them up in block order.
+// leaves its parts' 256 sums in two slots a block, and a small kernel adds them up in block order.  With a
+// window, units that it hides from every new token are left out, and a unit's steps end with the last token
+// that sees one of its keys.
 //
 // Warp roles: 0 walks the stretch and loads key tiles (TMA; pages as in group_tc.cuh), several heads
 // ahead, since they come from HBM; 2 loads the query tiles, which the L2 holds; 1 issues tcgen05
@@ -55,8 +57,10 @@ struct WeighArgs {
 
 struct Entry {
     int s, L, T, q0, fresh;
-    int units;  // runs of kUnit keys
-    int tiles;  // of query rows
+    int units;       // runs of kUnit keys, without those that a window hides from every new token:
+    int held, gap;   // the first `held` runs, and those behind the next `gap`
+    int tiles;       // of query rows
+    __device__ int unit(int i) const { return i < held ? i : i + gap; }
 };
 
 // A part of a unit: steps [j0, j0 + n), of `tiles` tiles of query rows a key head, from tile `tile0` on.
@@ -91,20 +95,38 @@ __device__ __forceinline__ Entry entry_at(const WeighParams &p, int i, int tok, 
         e.L = e.T = e.fresh = 0;
     }
     e.units = e.T > 0 || e.fresh > 0 ? cdiv(e.L, kUnit) : 0;
+    e.held = e.gap = 0;
+    if (p.window) {
+        // (without new tokens all are hidden)
+        const int from = e.T > 0 ? max(0, e.L - e.T + 1 - p.window) / kUnit : e.units;
+        e.held = min(e.units, e.T > 0 ? cdiv(p.sinks, kUnit) : 0);
+        e.gap = max(0, from - e.held);
+        e.units -= e.gap;
+    }
     e.tiles = max(1, cdiv(e.T, tok));  // (without new tokens: a tile of no rows)
     return e;
 }
 
-// First tile of query rows that sees a key of unit u: token key0 - ctx does.
+// First tile of query rows that sees a key of run u: token key0 - ctx does.
 __device__ __forceinline__ int first_tile(const Entry &e, int u, int tok) {
     return max(0, kUnit * u - (e.L - e.T)) / tok;
 }
 
-// Steps of the first n units, of one key head.
-__device__ __forceinline__ long long head_steps(const Entry &e, int n, int tok) {
-    const int full = min(n, (e.L - e.T) / kUnit + 1);  // units that every tile sees a key of
+// Tiles of query rows that see a key of run u; its last key is the last one to leave a window.
+__device__ __forceinline__ int tiles_of(const WeighParams &p, const Entry &e, int u, int tok) {
+    int last = e.tiles;
+    if (p.window && kUnit * u >= p.sinks) {
+        const long long behind = (long long)kUnit * u + kUnit - 1 + p.window - (e.L - e.T);
+        if (behind < e.T) last = cdiv((int)behind, tok);
+    }
+    return last - first_tile(e, u, tok);
+}
+
+// Steps of the entry's units, of one key head.
+__device__ __forceinline__ long long head_steps(const WeighParams &p, const Entry &e, int tok) {
+    const int full = p.window ? 0 : min(e.units, (e.L - e.T) / kUnit + 1);  // units that every tile sees a key of
     long long r = (long long)full * e.tiles;
-    for (int u = full; u < n; ++u) r += e.tiles - first_tile(e, u, tok);
+    for (int i = full; i < e.units; ++i) r += tiles_of(p, e, e.unit(i), tok);
     return r;
 }
 
@@ -201,11 +223,11 @@ __device__ void producer(const WeighArgs &a, Bars &bars, Seg *segs, const Stretc
             if (fresh) {  // the unit that the stretch begins in
                 fresh = false;
                 const long long off = st.at - st.before;
-                const int full = min(e.units, (e.L - e.T) / kUnit + 1);
+                const int full = p.window ? 0 : min(e.units, (e.L - e.T) / kUnit + 1);
                 unit = (int)min((long long)full, off / ((long long)p.c.H * e.tiles));
                 u0 += (long long)unit * p.c.H * e.tiles;
                 while (unit >= full && unit < e.units) {
-                    const int n = p.c.H * (e.tiles - first_tile(e, unit, tok));
+                    const int n = p.c.H * tiles_of(p, e, e.unit(unit), tok);
                     if (u0 + n > st.at) break;
                     u0 += n;
                     ++unit;
@@ -213,11 +235,11 @@ __device__ void producer(const WeighArgs &a, Bars &bars, Seg *segs, const Stretc
             }
         }
         Seg g;
-        g.tile0 = first_tile(e, unit, tok);
-        g.tiles = e.tiles - g.tile0;
+        g.tile0 = first_tile(e, e.unit(unit), tok);
+        g.tiles = tiles_of(p, e, e.unit(unit), tok);
         const int n_unit = p.c.H * g.tiles, t0 = st.tile(st.at, u0, n_unit), t1 = st.tile(st.end, u0, n_unit);
         if (t0 < t1) {
-            g.key0 = kUnit * unit;
+            g.key0 = kUnit * e.unit(unit);
             g.L = e.L;
             g.T = e.T;
             g.q0 = e.q0;
@@ -227,7 +249,7 @@ __device__ void producer(const WeighArgs &a, Bars &bars, Seg *segs, const Stretc
             g.n = t1 - t0;
             g.slot = t1 - t0 == n_unit ? -1 : 2 * (int)blockIdx.x + (t0 == 0);
             if (t0 == 0 && t1 < n_unit && lane == 0)  // begins here and goes on behind the stretch: for the merge
-                p.cut[blockIdx.x] = WeighCut{st.last_block(u0, n_unit), e.s, g.key0, e.L, e.fresh};
+                p.cut[blockIdx.x] = WeighCut{st.last_block(u0, n_unit), e.s, g.key0, e.L, e.fresh, 0};
             ok = publish(g);
             if (!ok) break;
             // this lane's piece of the key tiles
@@ -235,7 +257,9 @@ __device__ void producer(const WeighArgs &a, Bars &bars, Seg *segs, const Stretc
             const int my_tile = lane / pieces;
             int page = 0;
             if (lane < there) {
-                page = p.c.table[(int64_t)e.s * p.c.table_stride + (pos >> p.c.page_shift)];
+                // (a piece that a window hides from every new token may be gone)
+                const bool gone = p.window && pos >= p.sinks && pos + psz <= e.L - e.T + 1 - p.window;
+                if (!gone) page = p.c.table[(int64_t)e.s * p.c.table_stride + (pos >> p.c.page_shift)];
                 if ((unsigned)page >= (unsigned)p.c.n_pages) {
                     report_status(p.c.status, ATTN_EINVAL);
                     page = 0;  // any page that exists: the entry's weights are reported as invalid
@@ -409,7 +433,8 @@ __device__ void sum_wg(const WeighArgs &a, Bars &bars, const Seg *segs, float *s
             tc_fence_after();
             // a step all of whose columns see every key of the warp.  (Columns behind the tile's rows hold
             // zeros, and their lse is infinite.)
-            if (t0 + tok <= g.T && key0 + 32 * quarter + 31 - ctx <= t0) {
+            const int first = key0 + 32 * quarter, last = first + 31;
+            if (t0 + tok <= g.T && last - ctx <= t0 && (!p.window || ctx + t0 + tok - p.window <= first || last < p.sinks)) {
                 uint32_t r[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld_x32(at + 32 * c, r[c]);
@@ -427,8 +452,12 @@ __device__ void sum_wg(const WeighArgs &a, Bars &bars, const Seg *segs, float *s
                     acc[(2 * c + 1) & 3] = __fadd2_rn(acc[(2 * c + 1) & 3], make_float2(exp2_approx(y.x), exp2_approx(y.y)));
                 }
             } else {
-                // columns [lo, rows) see the key, the tile's tokens from key - ctx on; 32 columns at a time
+                // columns [lo, hi) see the key, the tile's tokens from key - ctx on, up to the last one whose window
+                // it is in; 32 columns at a time
                 const int lo = max(0, min(tok, key - ctx - t0)) * p.group;
+                const int hi = p.window && key >= p.sinks
+                                   ? min(rows, (int)max(0ll, min((long long)tok, (long long)key + p.window - ctx - t0)) * p.group)
+                                   : rows;
 #pragma unroll 1
                 for (int c0 = 0; c0 < rows; c0 += 32) {
                     uint32_t r[32];
@@ -437,7 +466,7 @@ __device__ void sum_wg(const WeighArgs &a, Bars &bars, const Seg *segs, float *s
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
                         const float x = exp2_approx(fmaf(__uint_as_float(r[c]), p.scale_log2, sb[c0 + c]));
-                        acc[c & 3].x += c0 + c >= lo && c0 + c < rows ? x : 0.f;
+                        acc[c & 3].x += c0 + c >= lo && c0 + c < hi ? x : 0.f;
                     }
                 }
                 tc_fence_before();
@@ -527,13 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     const bool any = !refused && find_stretch<kThreads / 32, 0>(
         a.p.n, 1, [&](int i, bool report) {
             const Entry e = entry_at(a.p, i, tok, report);
-            return Work{0, a.p.c.H * head_steps(e, e.units, tok)};
+            return Work{0, a.p.c.H * head_steps(a.p, e, tok)};
         }, st);
     if (!any) {
         st.at = st.end = st.before = 0;
         st.entry = 0;
     }
-    if (threadIdx.x == 0) a.p.cut[blockIdx.x].last = -1;  // the loading warp may put a unit there
+    if (threadIdx.x == 0) {  // (the loading warp may put a unit there)
+        a.p.cut[blockIdx.x].last = -1;
+        a.p.cut[blockIdx.x].refused = refused;
+    }
     __syncthreads();
 
     if (warp < 4) {
@@ -561,11 +593,19 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     }
 }
 
-// Adds the parts of the unit that block b of the kernel above noted as begun and cut, in block order.
+// Adds the parts of the unit that block b of the kernel above noted as begun and cut, in block order.  The
+// weights that start anew of tokens in the runs that a window hides from every new token are zeroed here.
 __global__ void __launch_bounds__(kUnit) weigh_merge_kernel(const WeighParams p) {
     pdl_trigger();
     pdl_wait();
     const int first = blockIdx.x;
+    if (p.window && !p.cut[first].refused)
+        for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
+            const Entry e = entry_at(p, i, BN / p.group, false);
+            const int end = min(e.L, kUnit * (e.held + e.gap));
+            for (int t = max(kUnit * e.held, e.L - e.fresh) + (int)threadIdx.x; t < end; t += kUnit)
+                p.weights[(int64_t)e.s * p.weights_stride + t] = 0.f;
+        }
     const WeighCut u = p.cut[first];
     if (u.last <= first) return;
     const int key = u.key0 + threadIdx.x;
@@ -594,7 +634,7 @@ cudaError_t launch_typed(const WeighArgs &a, cudaStream_t s) {
 // D = 128; weigh.cu and this kernel: 8 rows 67 us and about 70, 16 rows 80 and 70, 32 rows 141 and 70, 256
 // rows 1138 and 111.)
 bool weigh_on_tc(const WeighParams &p) {
-    return p.dtype != ATTN_F32 && !p.window && p.n_q > 0 && p.group <= BN && p.c.page_shift >= 3 &&
+    return p.dtype != ATTN_F32 && p.n_q > 0 && p.group <= BN && p.c.page_shift >= 3 &&
            (int64_t)p.n_q * p.group > (int64_t)8 * p.n && tc_device_ok();
 }
 

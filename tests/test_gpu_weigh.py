@@ -226,3 +226,35 @@ def test_tokens_that_a_window_hides_may_hold_anything(dtype, t):
         cache.k[:, cache.table[s].long()[hidden // 16], hidden % 16] = float("nan")
     cache.weigh(seqs, [0, t, 2 * t], q, lse, w, **kw)
     assert torch.equal(w, want) and torch.isfinite(w).all() and attn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float16, 64)])
+@pytest.mark.parametrize("lens,news,page,heads,group", [
+    ([700], [700], 16, 2, 4), ([900, 3, 700, 128], [300, 3, 0, 128], 8, 1, 3), ([2000, 1300], [64, 20], 64, 2, 4),
+    ([300] * 40, [5] * 40, 32, 2, 5), ([5000], [7], 1024, 1, 128), ([1300, 600], [1299, 1], 16, 1, 2)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 3), (256, 0), (300, 300), (700, 2 ** 31 - 1), (900, 40)])
+def test_many_rows_over_windows(lens, news, page, heads, group, d, dtype, window, sinks):
+    """Units that a window hides, wholly or from the last rows; the sinks' ones; weights that start anew there."""
+    cache, model, seqs, g = make(lens, page, heads, d, dtype, 94)
+    q = torch.randn(sum(news), heads * group, d, generator=g).to(dtype)
+    first = check(cache, model, seqs, news, q, window, sinks, what=f"{lens}")
+    again = check(cache, model, seqs, news, q, window, sinks)
+    assert torch.equal(first[..., :-1], again[..., :-1])
+    check(cache, model, seqs, news, q, window, sinks, fresh=lens, what=f"{lens} fresh")
+    check(cache, model, seqs, news, q, window, sinks, fresh=[(n + 1) // 2 for n in lens], what=f"{lens} half fresh")
+
+
+@pytest.mark.parametrize("dtype,t", [(torch.bfloat16, 1), (torch.float16, 40), (torch.float32, 9)])
+def test_pages_that_a_window_hides_may_be_gone(dtype, t):
+    cache, _, seqs, g = make([3000, 1700], 64, 2, 64, dtype, 95)
+    q = torch.randn(2 * t, 8, 64, generator=g).to(dtype).cuda()
+    kw = dict(window=500, sinks=70)
+    lse = attn.tree_fwd(q, cache, seqs, [0, t, 2 * t], **kw)[1]
+    w, want = cache.new_weights(), cache.new_weights()
+    cache.weigh(seqs, [0, t, 2 * t], q, lse, want, **kw)
+    for s, n in zip(seqs, (3000, 1700)):
+        cache.table[s, 2:(n - t + 1 - 500) // 64] = -1
+    cache.weigh(seqs, [0, t, 2 * t], q, lse, w, **kw)
+    assert torch.equal(w, want) and attn.device_status() == 0
+    cache.weigh([seqs[0]] * 2, [0, t, 2 * t], q, lse, w, fresh=[3000, 3000], **kw)  # twice: nothing is touched
+    assert torch.equal(w, want) and attn.device_status() == _abi.ATTN_EINVAL
