@@ -57,15 +57,16 @@ __device__ __forceinline__ int block_prefix(int x, int *s_warp, int &total) {
     }
     if (lane == 31) s_warp[warp] = y;
     __syncthreads();
-    int before = 0;
-    total = 0;
+    int sums = s_warp[lane];  // (every warp adds them up: there are as many as lanes)
+    __syncthreads();          // s_warp may be reused
 #pragma unroll
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before += s_warp[w];
-        total += s_warp[w];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += z;
     }
-    __syncthreads();  // s_warp may be reused
-    return before + y - x;
+    total = __shfl_sync(0xffffffffu, sums, 31);
+    const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + y - x;
 }
 
 // The number of digit places of the passes, and the bits below a pass's digit.
@@ -90,6 +91,9 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
         if (bad) report_status(c.status, ATTN_EINVAL);
     }
     if (bad || len <= budget) return;
+    // this thread's page of the sequence, for the check at the end
+    const int pages = pages_of(len, c.page_shift), my_page = tid < pages ? table_at(c, s, tid) : 0;
+    const int my_refs = in_range(my_page, c.n_pages) ? c.refs[my_page] : 0;
     const int sinks = p.sinks, last = len - p.recent;  // the tokens [sinks, last) are chosen from
     const int want = budget - sinks - p.recent, n = last - sinks;
     const float *w = p.weights + (int64_t)s * p.w_seq + sinks;
@@ -190,7 +194,8 @@ __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheP
     if (tid == 0) p.first[i] = first;
     // every page from the first row that moves on exists, and those that rows move into are the sequence's own
     const int end = first < budget ? pages_of(budget, c.page_shift) : 0;
-    for (int k = (first >> c.page_shift) + tid; k < pages_of(len, c.page_shift); k += kPlanThreads) {
+    if (tid >= first >> c.page_shift && tid < pages) bad = !in_range(my_page, c.n_pages) || (tid < end && my_refs > 1);
+    for (int k = max(first >> c.page_shift, kPlanThreads) + tid; k < pages; k += kPlanThreads) {
         const int page = table_at(c, s, k);
         bad = bad || !in_range(page, c.n_pages) || (k < end && c.refs[page] > 1);
     }
@@ -221,13 +226,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kMoveThreads)
     extern __shared__ __align__(128) uint8_t smem[];
     pdl_trigger();
     pdl_wait();
+    const int i = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // (one round of loads; `first` is there for those that are cut)
+    const int s = p.seqs[i], count = p.budgets[i], len = p.len[i], first = p.first[i];
     bool good = true;
     for (int j = threadIdx.x; j < p.n; j += kMoveThreads) good = good && p.good[j];
-    if (!__syncthreads_and(good)) return;
-    const int i = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = p.seqs[i], count = p.budgets[i], len = p.len[i];
-    if (len <= count) return;  // (the whole cluster)
-    const int first = p.first[i];
+    if (!__syncthreads_and(good) || len <= count) return;  // (the whole cluster)
     const int *source = p.source + (int64_t)i * p.cols;
     const int per_row = c.row_bytes >> 4, per_tok = c.H * per_row, strips = (per_tok + 31) / 32;
     const int mask = (1 << c.page_shift) - 1, pools = 2 * c.n_layers * strips;
