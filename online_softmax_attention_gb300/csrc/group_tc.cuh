@@ -64,6 +64,8 @@ constexpr int kLead = 1;
 // tokens take 9 us a unit more than its window's tiles).  (Trees of 63 drafts, window 4096; 48 packed
 // prompts, window 128: 65.6 / 76.6 us with 1, 62.1 / 78.1 with 3, 62.0 / 77.3 with 6.)
 constexpr int kWindowLead = 6;
+// Uncut units over a window, by a line of tiles and leads as the cut ones', or of units.
+constexpr int kTileLine = 1, kUnitLine = 2;
 
 template <int D>
 struct Cfg {
@@ -197,6 +199,7 @@ __device__ __forceinline__ Entry entry_at(const GroupParams &p, int i, int per, 
 
 template <bool kWindow>
 __device__ __forceinline__ Work entry_work(const GroupParams &p, const Entry &e, int per) {
+    if (kWindow && p.whole == kUnitLine) return Work{0, (long long)p.Hkv * e.units};
     return e.T > 0 ? Work{(long long)p.Hkv * e.units, p.Hkv * unit_tiles<kWindow>(p, e, per, e.units)} : Work{0, 0};
 }
 
@@ -227,6 +230,7 @@ __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow>
         return __all_sync(0xffffffffu, mbar_wait_small(smem_u32(&bar), parity, wd));
     };
     const bool ordered = is_ordered(p);
+    const bool whole = kWindow && p.whole;  // a unit is the block's in whose stretch it begins
     // pages: this lane's piece of a key tile
     const int psz = p.paged ? min(1 << p.c.page_shift, BN) : BN, pieces = BN / psz;
     Entry e = {};
@@ -251,6 +255,13 @@ __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow>
         }
         if (!fresh) return;
         fresh = false;
+        if (kWindow && p.whole == kUnitLine) {
+            unit = (int)(st.at - st.before);
+            hk = unit / e.units;
+            unit -= hk * e.units;
+            u0 = st.at;
+            return;
+        }
         const long long per_head = st.length(st.work) / p.Hkv;
         long long off = st.at - st.before;
         hk = (int)(off / per_head);
@@ -289,7 +300,7 @@ __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow>
     // the next unit of the line
     bool entered = false;
     auto next_unit = [&](int n_unit) {
-        u0 += st.lead + n_unit;
+        u0 += kWindow && p.whole == kUnitLine ? 1 : st.lead + n_unit;
         if (++unit < e.units) return;
         unit = 0;
         if (++hk < p.Hkv) return;
@@ -307,7 +318,8 @@ __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow>
         };
         if constexpr (kWindow) list = window_units(p, e, per).list(unit);
         const int n_unit = tiles_of((unit + 1) * per);
-        const int t0 = st.tile(st.at, u0, n_unit), t1 = st.tile(st.end, u0, n_unit);
+        const int t0 = whole ? (u0 < st.at ? n_unit : 0) : st.tile(st.at, u0, n_unit);
+        const int t1 = whole ? n_unit : st.tile(st.end, u0, n_unit);
         if (t0 >= t1) {
             next_unit(n_unit);
             continue;
@@ -999,11 +1011,26 @@ cudaError_t launch_d(const GroupArgsOf<kWindow> &a, cudaStream_t s) {
     return f32 ? launch_typed<D, false, float, kWindow>(a, s) : launch_typed<D, false, __half, kWindow>(a, s);
 }
 
+// Units of few tiles are not cut, so that no merge follows: a block's are those that begin in its stretch, or, where
+// there are no more units than blocks, the unit of its number.  (Cut and whole: one prompt of 100 tokens, 32 / 8
+// heads, D = 128, 13.2 and 10.0 us; of 700, window 256, 23.2 and 15.8; 4 of 1000 tokens, window 500, 53.2 and 51.8;
+// 48 of 9 to 420, window 128, 72.5 and 70.7; 2 x 8192, window 1024, of 10 tiles, the same; 64 units of 33
+// tiles 59 and 75.)
+int whole_units(const GroupParams &p) {
+    const int64_t per = NQT * (BM / p.group), units = p.Hkv * (p.n_q / per + p.n);
+    int64_t keys = (p.mask ? 64 * (int64_t)p.mask_words : per - 1) + p.window + p.sinks + (p.paged ? 2 * (BN - 1) : 15);
+    const int64_t there = p.paged ? (int64_t)p.c.max_pages << p.c.page_shift : p.n_k;
+    if (keys > there) keys = there;
+    if (keys > 6 * BN) return 0;
+    return units <= sm_count() ? kUnitLine : kTileLine;
+}
+
 // The attention kernel, and the merge of cut units.
 template <bool kWindow>
 cudaError_t launch_group_of(const GroupParams &p, cudaStream_t s) {
     GroupArgsOf<kWindow> a;
     a.p = p;
+    if constexpr (kWindow) a.p.whole = whole_units(p);
     const uint64_t D = (uint64_t)p.D;
     const int tok = BM / p.group;
     bool ok;
@@ -1028,7 +1055,7 @@ cudaError_t launch_group_of(const GroupParams &p, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t e = p.D == 64 ? launch_d<64, kWindow>(a, s) : launch_d<128, kWindow>(a, s);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || (kWindow && a.p.whole)) return e;
     PartsMergeParams m;
     m.parts = p.parts;
     m.o = p.o;

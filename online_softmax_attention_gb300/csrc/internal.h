@@ -209,6 +209,7 @@ struct GroupParams {
     int *status;
     long long watchdog_cycles;
     int window, sinks;               // window 0: none
+    int whole;  // with a window: how uncut units are dealt out (group_tc.cuh); 0: they are cut
 };
 constexpr int kGroupRows = 256;  // query rows of a unit (two 128-row tiles)
 bool group_supported(int dtype, int D, int group);
