@@ -158,7 +158,13 @@ typedef struct attn_fwd_args {
  * is none.  f16 / bf16 inputs run the kernel that packs grouped heads' rows (for ungrouped
  * heads too, and any number of sequences), which takes neither num_splits > 1 nor
  * num_ctas > 0 (ATTN_EUNSUPPORTED) and whose workspace attn_fwd_noalloc does not have;
- * with ATTN_KERNEL_SIMT, groups of more than 128 or f32 inputs, the CUDA-core kernels. */
+ * with ATTN_KERNEL_SIMT, groups of more than 128 or f32 inputs, the CUDA-core kernels.
+ * With sinks the backward's workspace holds partial sums of dk and dv (the sinks' key
+ * blocks are seen by all queries behind them and cut into items; at most 256 blocks a
+ * key head), which are added in a fixed order.  Over a cache, tokens that the window hides
+ * from every new token of an entry may hold anything, NaN included, and the table's
+ * entries are not followed for pages in a run of 256 tokens, from a multiple of 256 on,
+ * that it hides whole. */
 
 /* Grouped heads (H_kv in the forward and the backward; no counterpart on the
  * pages): k and v hold H_kv heads, each shared by a group of G = H / H_kv
@@ -390,7 +396,7 @@ typedef struct attn_weigh_args {
 /* The weights by which attn_cache_evict chooses: (n_layers, max_seqs, cols) f32. */
 typedef struct attn_weights {
     float *ptr;
-    int64_t stride_layer, stride_seq; /* elements; tokens are contiguous */
+    int64_t stride_layer, stride_seq; /* elements; tokens are contiguous, layers do not overlap */
     int32_t n_layers;                 /* >= 1; need not be the cache's */
     int32_t cols;
 } attn_weights;
@@ -410,7 +416,8 @@ ATTN_API size_t attn_weights_size(void);
 /* Bytes of device workspace the call needs (depends on n_seq, H, n_q, and
  * for the forward on the number of key splits: n_splits > 1 adds the partial
  * results, n_splits * n_q * H * (D + 1) * 4 bytes; for the backward on the dq
- * mode: ATTN_DQ_FUSED adds the dq partial sums, n_q * H * D * 4 bytes).
+ * mode: ATTN_DQ_FUSED adds the dq partial sums, n_q * H * D * 4 bytes; a window
+ * with sinks adds the sinks' partial sums).
  * Only sizes, dtypes, the relation, the kernel choice, num_splits and whether
  * cu_seqlens are given are read: the tensor and workspace pointers may still
  * be unset.  Arguments the call would reject give the unsplit size. */

@@ -647,7 +647,7 @@ int64_t most_units(const TreeParams &p) {
 template <typename C>
 int cluster_of(const TreeParams &p, bool f32) {
     constexpr int kMost = 8;
-    if (most_units(p) >= 1 << 27) return 0;
+    if (p.n > 512 || most_units(p) >= 1 << 27) return 0;  // (every cluster counts the entries: 300 of them cost 3 us)
     const int64_t keys = std::min<int64_t>((int64_t)p.window + p.sinks, (int64_t)p.c.max_pages << p.c.page_shift);
     const int64_t units = most_units(p), places = f32 ? sm_count() / 2 : 2 * sm_count(), each = C::kWarps * C::kKeys;
     int size = kMost;

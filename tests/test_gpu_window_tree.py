@@ -5,6 +5,7 @@ import torch
 
 import online_softmax_attention_gb300 as attn
 from cache_model import assert_output, attention, seen_tree
+from online_softmax_attention_gb300 import _abi
 from test_gpu_tree import make, random_mask
 from window_model import windowed
 
@@ -172,3 +173,26 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for c, (o, lse) in zip(calls, want):
         assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+
+
+def test_offsets_that_go_back():
+    """Entries that fit are carried out, more units than offsets in order can have among them; the others are reported."""
+    cache, _, seqs, g = make([700, 90], 16, 2, 64, torch.bfloat16, 96)
+    a, b = seqs
+    q = torch.randn(3, 32, 64, generator=g).bfloat16().cuda()
+    want = attn.tree_fwd(q, cache, [a], [0, 3], window=100, sinks=3)
+    assert attn.device_status() == 0
+    got = attn.tree_fwd(q, cache, [a, b, a, b, a], [0, 3, 0, 3, 0, 3], window=100, sinks=3)
+    assert attn.device_status() == _abi.ATTN_EINVAL
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("n,heads,group", [(600, 2, 4), (512, 1, 4), (40, 1, 20), (33, 2, 2)])
+def test_many_entries(n, heads, group):
+    """Some without new tokens, some with several, more than a cluster counts at once."""
+    r = np.random.default_rng(97)
+    lens = [int(x) for x in r.integers(1, 90, n)]
+    news = [int(min(x, y)) for x, y in zip(r.choice([0, 1, 1, 1, 2, 5], n), lens)]
+    cache, model, seqs, g = make(lens, 16, heads, 64, torch.float16, 98)
+    q = torch.randn(sum(news), heads * group, 64, generator=g).half()
+    run(cache, model, seqs, news, q, 20, 2, what=f"{n}")
