@@ -37,7 +37,7 @@
 // blocks up to its last key's window, a block with a sink by all behind it: those are cut into
 // chunks, an item each, whose partial sums a small kernel adds up in order (2 rows of 8192 tokens,
 // 32 / 8 heads, window 1024: one item took as long as the other ones of a CTA together, 676 us
-// instead of 453).  A query block scans the key blocks that hold a sink or a key of its window; pairs outside are
+// instead of 415).  A query block scans the key blocks that hold a sink or a key of its window; pairs outside are
 // zeroed in P^T and dS.  Kernels of their own (bwd_tc_window.cu), so that the others keep
 // their code.
 #pragma once

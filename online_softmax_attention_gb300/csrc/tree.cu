@@ -6,7 +6,8 @@
 //
 // Decomposition.  A unit is (entry, key head, tile of kRows query rows); its
 // keys are cut in tiles of 32 (16 for rows over 256 bytes), and every block (one
-// per SM) takes an equal stretch of all units' tiles (stretch.cuh).
+// per SM; two of half the warps with a window) takes an equal stretch of all
+// units' tiles (stretch.cuh).
 //
 // Inside a block the four warps take the stretch's tiles in turn, each with a
 // ring of cp.async stages of its own (no block-wide barrier in the loop), and
@@ -24,7 +25,7 @@
 // kWindow: a sliding window with sinks (window.h).  An entry's keys are a list, the sinks and those from
 // the first new token's window on, and its tiles count the list's places; the list is the same for
 // all its units (its new tokens are few here; a chunk of T reads T keys more than its last row
-// needs).
+// needs).  Mostly clusters of blocks take the units (cluster_of), which leaves no merge.
 #include "../../include/attn.h"
 #include <algorithm>
 #include <climits>
@@ -124,8 +125,8 @@ __device__ __forceinline__ Entry entry_of(const TreeParams &p, int from, int to,
         // (a row of a tree may see none of the new tokens)
         e.list = key_list(p.window, p.sinks, e.L - e.T + (p.mask ? 0 : 1), 1, 1);
         e.key_tiles = (e.L - e.list.shift + keys - 1) / keys;
-        // whole turns of a block's warps, so that short stretches (of one turn) do not meet two units, one
-        // after the other (one sequence, window 1024: 16.5 -> 14.3 us); the tiles behind the list's end load nothing
+        // whole turns of a block's warps, so that short stretches (of one turn) do not meet two units, one after
+        // the other (one sequence of window 1024 in stretches: 16.5 -> 14.3 us); the tiles behind the list's end load nothing
         if (turn > 1) e.key_tiles = (e.key_tiles + turn - 1) & ~(turn - 1);
     }
     e.tiles = (long long)p.c.H * e.row_tiles * e.key_tiles;
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(32 * warps_of(kWindow, sizeof(T) == 4), per_sm
     Stretch st;
     const bool any = find_stretch<kWarps, 0>(
         p.n, kWarps, [&](int i, bool report) { return Work{0, entry_at<kWindow>(p, i, kRows, kKeys, kTurn, report).tiles}; }, st,
-        kWindow ? kWarps : 1);  // (a tile a warp at least: one sequence, window 1024: 14.5 us, 20.5 with a tile a block)
+        kWindow ? kWarps : 1);  // (a tile a warp at least: the same sequence 14.5 us, 20.5 with a tile a block)
     if (!any) {
         if (tid == 0) p.parts.cut[blockIdx.x].last = -1;
         return;
