@@ -844,6 +844,15 @@ int attn_bwd(const attn_bwd_args *a, void *stream) {
     }
     int rc = attn_bwd_preprocess(a, stream);
     if (rc) return rc;
+    BwdParams p;
+    bool use_tc = false;
+    rc = build_bwd(a, p, use_tc);
+    if (rc) return rc;
+    if (use_tc && p.window) {  // both in one: dq fills the SMs that dK / dV leaves
+        p.dq_beside = 1;
+        const cudaError_t e = launch_bwd_dkdv_tc(p, a->num_ctas, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? ATTN_OK : set_cuda_error(e);
+    }
     rc = attn_bwd_dkdv(a, stream);
     if (rc) return rc;
     return attn_bwd_dq(a, stream);

@@ -992,9 +992,11 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    // set-up above overlaps the previous kernel on the stream; inputs are read after this
-    pdl_trigger();
+    // set-up above overlaps the previous kernel on the stream; inputs are read after this.  (With a window the dq
+    // kernel that follows may run beside this one's last blocks: it starts when what it reads is there.)
+    if constexpr (!kWindow) pdl_trigger();
     pdl_wait();
+    if constexpr (kWindow) pdl_trigger();
     if (warp < 4) {
         regs_dec<kFused ? C::kRegsProducerFused : C::kRegsProducer>();
         if (warp == 0 || warp == 2) dkdv_producer<D, kWindow>(a, bars, sK, sV, sQ, sDO, warp == 2, wd);  // whole warps
@@ -1444,9 +1446,12 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    // set-up above overlaps the previous kernel on the stream; inputs are read after this
+    // set-up above overlaps the previous kernel on the stream; inputs are read after this.  Beside dK / dV: that
+    // kernel's blocks have all waited for the ones before it, whose statistics and schedule are what is read here;
+    // each has an SM, so that this kernel's blocks take the SMs that it leaves.
+    const bool beside = kWindow && a.p.dq_beside;
     pdl_trigger();
-    pdl_wait();
+    if (!beside) pdl_wait();
     if (warp < 4) {
         regs_dec<C::kRegsProducer>();
         if (warp == 0 && lane == 0) dq_producer<D, kWindow>(a, bars, sQ, sDO, sK, sV, wd);
@@ -1467,6 +1472,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (beside) pdl_wait();  // what waits for this grid waits for dK / dV too
 }
 
 // ================================ host ========================================
@@ -1497,6 +1503,7 @@ cudaError_t launch_typed(const TcBwdArgs &a, int num_ctas, cudaStream_t s, bool 
     if (dkdv) {
         cudaError_t e = launch(dkdv_tc_kernel<D, kBF16, Tg, false, kWindow>, BCfg<D>::kDkdvSmem, a, num_ctas, s);
         if constexpr (kWindow) {
+            if (e == cudaSuccess && a.p.dq_beside) e = launch(dq_tc_kernel<D, kBF16, Tg, kWindow>, BCfg<D>::kDqSmem, a, num_ctas, s);
             if (e != cudaSuccess || !a.p.sink_chunk) return e;
             return launch_sink_sum(a.p, BT, s);
         }

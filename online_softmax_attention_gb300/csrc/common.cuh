@@ -20,7 +20,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // start once every CTA of this grid has executed it.  pdl_wait: returns once
 // the previous grid on the stream has completed and its writes are visible
 // (at once when this kernel was launched the ordinary way); a kernel reads no
-// global memory before it.
+// global memory before it, but for the windowed dq (bwd_tc.cuh), which starts
+// when the grid before the previous one is known to have completed.
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

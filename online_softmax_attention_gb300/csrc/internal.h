@@ -306,6 +306,7 @@ struct BwdParams {
     // sink_chunk 0: none
     int sink_tiles, sink_chunk;
     float *sink_parts;  // their partial sums, in the workspace
+    int dq_beside;      // with a window: the dq kernel is launched with dK / dV, and may run beside it
 };
 
 // Schedule preparation: validates cu_seqlens on the device and writes the
