@@ -996,7 +996,12 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
     // kernel that follows may run beside this one's last blocks: it starts when what it reads is there.)
     if constexpr (!kWindow) pdl_trigger();
     pdl_wait();
-    if constexpr (kWindow) pdl_trigger();
+    if constexpr (kWindow) {
+        if (a.p.dq_beside && blockIdx.x == 0 && threadIdx.x == 0)
+            asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(a.p.sched_q.hdr + 2) : "memory");
+        __syncthreads();
+        pdl_trigger();
+    }
     if (warp < 4) {
         regs_dec<kFused ? C::kRegsProducerFused : C::kRegsProducer>();
         if (warp == 0 || warp == 2) dkdv_producer<D, kWindow>(a, bars, sK, sV, sQ, sDO, warp == 2, wd);  // whole warps
@@ -1447,11 +1452,17 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     // set-up above overlaps the previous kernel on the stream; inputs are read after this.  Beside dK / dV: that
-    // kernel's blocks have all waited for the ones before it, whose statistics and schedule are what is read here;
-    // each has an SM, so that this kernel's blocks take the SMs that it leaves.
+    // kernel's blocks have all waited for the ones before it, whose statistics and schedule are what is read here,
+    // and one has said so in the schedule's header since it was prepared.
     const bool beside = kWindow && a.p.dq_beside;
     pdl_trigger();
-    if (!beside) pdl_wait();
+    if (beside) {
+        int there;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(a.p.sched_q.hdr + 2) : "memory");
+        if (!__syncthreads_and(there == 1)) pdl_wait();
+    } else {
+        pdl_wait();
+    }
     if (warp < 4) {
         regs_dec<C::kRegsProducer>();
         if (warp == 0 && lane == 0) dq_producer<D, kWindow>(a, bars, sQ, sDO, sK, sV, wd);

@@ -19,7 +19,7 @@ constexpr int kSchedHeaderInts = 16;
 constexpr int kSortedSeqs = 1024;
 
 struct Sched {
-    int *hdr;          // counter, total
+    int *hdr;          // counter, total, windowed dq: whether it may run beside dK / dV
     const int *prefix; // n_seq + 1 entries
     int *order;        // n_seq entries, or null: sequences as they are
 };

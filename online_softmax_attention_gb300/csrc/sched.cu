@@ -111,6 +111,7 @@ prep_kernel(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, 
         prefix[n_seq] = (int)s_carry;
         hdr[0] = 0;
         hdr[1] = (int)s_carry;
+        hdr[2] = 0;
         if (bad) report_status(status, ATTN_EINVAL);
     }
 }
