@@ -36,6 +36,7 @@
 #pragma once
 
 #include <cfloat>
+#include <climits>
 
 #include "sm100.cuh"
 #include "stretch.cuh"
@@ -583,6 +584,19 @@ __device__ __forceinline__ uint32_t bits_below(int lim, int u) {
     return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
 }
 
+// Of the places [first, first + 32), those whose keys none of `tokens` new tokens sees, a token a lane; `ctx` places before
+// the new ones'.  (Apart from the loops over tiles, whose code few calls of masks need it for.)
+__device__ __noinline__ uint32_t unseen_keys(const unsigned long long *mask, int words, int tokens, int T, int ctx, int window,
+                                             int sinks, int first) {
+    uint32_t seen = 0;
+    for (int x = threadIdx.x & 31; x < tokens; x += 32) {
+        const unsigned long long *row = mask + (int64_t)x * words;
+        const RowWindow w = tree_window(row, T, ctx, window, sinks);
+        seen |= mask_bits(row, words, first - ctx) & (~bits_below(w.lo, first) | bits_below(w.hi, first));
+    }
+    return ~__reduce_or_sync(0xffffffffu, seen);
+}
+
 // As store_rows_chunk (sm100.cuh) for rows at any addresses: at[k] is the address
 // of row (lane & ~3) + k of the warp's 32 (null: not written); `col` the chunk's
 // first column.
@@ -661,6 +675,27 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         }
     };
 
+    // With a window and a mask: the place up to which no row of a part's unit sees a key behind the sinks, by the least
+    // number of drafts that one of its tokens sees, a token a lane.  -1: these may not be all the keys that may hold
+    // anything (a window of fewer keys than there are new tokens, sinks among these, a new token that is in no row's
+    // mask), or there are more than 64 new tokens.
+    [[maybe_unused]] auto unseen_until = [&](const auto &g) -> int {
+        if (g.T > 64 || p.window < g.T || p.sinks > g.ctx) return -1;
+        const unsigned long long exist = ~0ull >> (64 - g.T), *mask = p.mask + (int64_t)g.q0 * p.mask_words;
+        unsigned long long any = 0;
+        int least = 64;
+#pragma unroll 2
+        for (int x = lane; x < g.T; x += 32) {
+            const unsigned long long drafts = mask[(int64_t)x * p.mask_words] & exist;
+            if (x >= g.tok[0] && x < g.tok[0] + NQT * (BM / p.group)) least = min(least, __popcll(drafts));
+            any |= drafts;
+        }
+        const bool all = __reduce_or_sync(0xffffffffu, (uint32_t)any) == (uint32_t)exist &&
+                         __reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) == (uint32_t)(exist >> 32);
+        least = __reduce_min_sync(0xffffffffu, least);
+        return all ? max(0, g.ctx - p.window + least) : -1;
+    };
+
     for (int i = 0;; ++i) {
         const int slot = i % kSegs;
         bool ok = mbar_wait_small(smem_u32(&bars.seg_full[slot]), (i / kSegs) & 1, wd);
@@ -686,7 +721,11 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         const int plain = max(0, min(n, (all_end >> 7) - sg.j0));
         int all_from = 0;
         RowWindow mine = {0, 0};  // of this row
+        // With a mask: no row of the unit sees the keys [sinks, unit_from), and the first query tile, which takes every key
+        // tile that the other one takes, zeroes their V; below 0: what is not seen is looked for in each masked tile.
+        int unit_from = 0;
         if constexpr (kWindow) {
+            if (p.mask && t == 0) unit_from = unseen_until(sg);
             const int token = sg.tok[t] + my_tok;
             if (!p.mask) {
                 all_from = sg.ctx + sg.tok[t] + BM / p.group - p.window;
@@ -775,6 +814,12 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                 if (kWindow) bits &= ~bits_below(mine.lo - key0, 32 * c) | bits_below(mine.hi - key0, 32 * c);
                 return bits;
             };
+            uint32_t unseen = 0;
+            if constexpr (kWindow)
+                if (unit_from < 0)
+                    unseen = unseen_keys(p.mask + (int64_t)(sg.q0 + sg.tok[0]) * p.mask_words, p.mask_words,
+                                         min(NQT * (BM / p.group), sg.T - sg.tok[0]), sg.T, sg.ctx, p.window, p.sinks, key0 + 32 * quarter) &
+                             bits_below(left, 32 * quarter);
             ok = mbar_wait_small(smem_u32(&bars.s_full[t]), s_cnt & 1, wd);
             ++s_cnt;
             if (!__all_sync(0xffffffffu, ok)) return false;
@@ -798,9 +843,19 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
             // contraction comes first.  (V landed with K, before the scores waited for.)
             if (left < 16 * steps && (t == 0 || j >= sg.n[0] || left >= 16 * steps_of(sg, 0, sg.j0 + j)))
                 zero_rows(max(0, left), 16 * steps);
-            if constexpr (kWindow) {  // so are those that the window hides from all the unit's rows
-                const int from = max(p.sinks - key0, 16 * first_step(sg, t, sg.j0 + j)), to = min(sg.from[0] - key0, 16 * steps);
+            if constexpr (kWindow) {  // so are those that no row of the unit sees, but for drafts that other units' do
+                const int from = max(p.sinks - key0, 16 * first_step(sg, t, sg.j0 + j));
+                const int to = min((p.mask ? unit_from : sg.from[0]) - key0, 16 * steps);
                 if (max(0, from) < to && (t == 0 || j >= sg.n[0])) zero_rows(max(0, from), to);
+                if (unseen) {
+                    const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + 32 * quarter * 128;
+                    for (int x = lane; x < 32 * 8; x += 32) {  // 16-byte chunks of a box
+                        if (!((unseen >> (x >> 3)) & 1)) continue;
+#pragma unroll
+                        for (int b = 0; b < C::kBoxes; ++b) st_shared_v4(base + b * C::kBoxBytes + 16 * x, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
             }
             const int chunks = (steps + 1) >> 1, chunk0 = first_step(sg, t, sg.j0 + j) >> 1;
             float mx = -INFINITY;

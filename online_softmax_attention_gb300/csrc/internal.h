@@ -216,6 +216,7 @@ bool group_supported(int dtype, int D, int group);
 cudaError_t launch_group(const GroupParams &p, cudaStream_t s);
 cudaError_t launch_group_window(const GroupParams &p, cudaStream_t s);  // the same, window > 0 (causal)
 cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s);
+cudaError_t launch_tree_masks(const TreeParams &p, cudaStream_t s);  // masks over a window, of few rows (tree.cuh)
 
 // Attention weight of cached tokens (attn_weigh_args; c.k: the layer's).
 struct WeighParams {
