@@ -8,6 +8,6 @@ bool group_supported(int dtype, int D, int group) {
            tc_device_ok();
 }
 
-cudaError_t launch_group(const GroupParams &p, cudaStream_t s) { return launch_group_of<false>(p, s); }
+cudaError_t launch_group(const GroupParams &p, cudaStream_t s) { return launch_group_of<false, false>(p, s); }
 
 }  // namespace attn

@@ -32,7 +32,9 @@
 // tokens, window 2048: 876 us with whole tiles of keys, the sinks' apart, 840 so).  Behind the
 // loading warp everything counts places: a part's L, ctx and ends are given less the list's shift.
 // Masked tiles stand at both ends of the window, so that a loop takes either kind; the kernels without
-// a window (group_tc.cu) are apart from those with one (group_tc_window.cu) and keep their two loops.
+// a window (group_tc.cu) are apart from those with one (group_tc_window.cu) and keep their two loops.  So are those with a
+// window and a mask (kMask, group_tc_masks.cu), which look for tokens that no row sees: with that code in one kernel, which
+// short units fetch anew, 48 packed prompts took 76.5 us, 72.8 without.
 #pragma once
 
 #include <cfloat>
@@ -639,7 +641,7 @@ __device__ __forceinline__ void store_rows_at(uint32_t (&u)[32], float mul, T *c
     }
 }
 
-template <int D, bool kBF16, typename Tout, bool kWindow>
+template <int D, bool kBF16, typename Tout, bool kWindow, bool kMask>
 __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *segs, uint32_t sV, uint32_t tmem,
                            const Watchdog &wd) {
     using C = Cfg<D>;
@@ -675,7 +677,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         }
     };
 
-    // With a window and a mask: the place up to which no row of a part's unit sees a key behind the sinks, by the least
+    // kMask: the place up to which no row of a part's unit sees a key behind the sinks, by the least
     // number of drafts that one of its tokens sees, a token a lane.  -1: these may not be all the keys that may hold
     // anything (a window of fewer keys than there are new tokens, sinks among these, a new token that is in no row's
     // mask), or there are more than 64 new tokens.
@@ -721,11 +723,12 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
         const int plain = max(0, min(n, (all_end >> 7) - sg.j0));
         int all_from = 0;
         RowWindow mine = {0, 0};  // of this row
-        // With a mask: no row of the unit sees the keys [sinks, unit_from), and the first query tile, which takes every key
+        // kMask: no row of the unit sees the keys [sinks, unit_from), and the first query tile, which takes every key
         // tile that the other one takes, zeroes their V; below 0: what is not seen is looked for in each masked tile.
         int unit_from = 0;
         if constexpr (kWindow) {
-            if (p.mask && t == 0) unit_from = unseen_until(sg);
+            if constexpr (kMask)
+                if (t == 0) unit_from = unseen_until(sg);
             const int token = sg.tok[t] + my_tok;
             if (!p.mask) {
                 all_from = sg.ctx + sg.tok[t] + BM / p.group - p.window;
@@ -815,7 +818,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                 return bits;
             };
             uint32_t unseen = 0;
-            if constexpr (kWindow)
+            if constexpr (kMask)
                 if (unit_from < 0)
                     unseen = unseen_keys(p.mask + (int64_t)(sg.q0 + sg.tok[0]) * p.mask_words, p.mask_words,
                                          min(NQT * (BM / p.group), sg.T - sg.tok[0]), sg.T, sg.ctx, p.window, p.sinks, key0 + 32 * quarter) &
@@ -845,9 +848,9 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
                 zero_rows(max(0, left), 16 * steps);
             if constexpr (kWindow) {  // so are those that no row of the unit sees, but for drafts that other units' do
                 const int from = max(p.sinks - key0, 16 * first_step(sg, t, sg.j0 + j));
-                const int to = min((p.mask ? unit_from : sg.from[0]) - key0, 16 * steps);
+                const int to = min((kMask ? unit_from : sg.from[0]) - key0, 16 * steps);
                 if (max(0, from) < to && (t == 0 || j >= sg.n[0])) zero_rows(max(0, from), to);
-                if (unseen) {
+                if (kMask && unseen) {
                     const uint32_t base = sV + ((kv0 + j) % C::kVStages) * C::kTileBytes + 32 * quarter * 128;
                     for (int x = lane; x < 32 * 8; x += 32) {  // 16-byte chunks of a box
                         if (!((unseen >> (x >> 3)) & 1)) continue;
@@ -966,7 +969,7 @@ __device__ void softmax_wg(const GroupArgs &a, Bars &bars, const Seg<kWindow> *s
     }
 }
 
-template <int D, bool kBF16, typename Tout, bool kWindow>
+template <int D, bool kBF16, typename Tout, bool kWindow, bool kMask>
 __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ GroupArgsOf<kWindow> a) {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -1038,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         }
     } else {
         regs_inc<kWindow ? C::kRegsWindowSoftmax : C::kRegsSoftmax>();
-        softmax_wg<D, kBF16, Tout, kWindow>(a, bars, segs, sV, tmem, wd);
+        softmax_wg<D, kBF16, Tout, kWindow, kMask>(a, bars, segs, sV, tmem, wd);
     }
     tc_fence_before();
     __syncthreads();
@@ -1048,9 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     }
 }
 
-template <int D, bool kBF16, typename Tout, bool kWindow>
+template <int D, bool kBF16, typename Tout, bool kWindow, bool kMask>
 cudaError_t launch_typed(const GroupArgsOf<kWindow> &args, cudaStream_t s) {
-    auto kern = group_tc_kernel<D, kBF16, Tout, kWindow>;
+    auto kern = group_tc_kernel<D, kBF16, Tout, kWindow, kMask>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(sm_count()), dim3(kThreads), Cfg<D>::kSmemBytes, s, args);
@@ -1058,12 +1061,12 @@ cudaError_t launch_typed(const GroupArgsOf<kWindow> &args, cudaStream_t s) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D, bool kWindow>
+template <int D, bool kWindow, bool kMask>
 cudaError_t launch_d(const GroupArgsOf<kWindow> &a, cudaStream_t s) {
     const bool f32 = a.p.o_dtype == ATTN_F32;
     if (a.p.dtype == ATTN_BF16)
-        return f32 ? launch_typed<D, true, float, kWindow>(a, s) : launch_typed<D, true, __nv_bfloat16, kWindow>(a, s);
-    return f32 ? launch_typed<D, false, float, kWindow>(a, s) : launch_typed<D, false, __half, kWindow>(a, s);
+        return f32 ? launch_typed<D, true, float, kWindow, kMask>(a, s) : launch_typed<D, true, __nv_bfloat16, kWindow, kMask>(a, s);
+    return f32 ? launch_typed<D, false, float, kWindow, kMask>(a, s) : launch_typed<D, false, __half, kWindow, kMask>(a, s);
 }
 
 // Units of few tiles are not cut, so that no merge follows: a block's are those that begin in its stretch, or, where
@@ -1081,7 +1084,7 @@ int whole_units(const GroupParams &p) {
 }
 
 // The attention kernel, and the merge of cut units.
-template <bool kWindow>
+template <bool kWindow, bool kMask>
 cudaError_t launch_group_of(const GroupParams &p, cudaStream_t s) {
     GroupArgsOf<kWindow> a;
     a.p = p;
@@ -1109,7 +1112,7 @@ cudaError_t launch_group_of(const GroupParams &p, cudaStream_t s) {
                  make_tile_map(&a.tv16, p.v, p.dtype, p.D, p.n_k, p.Hkv, p.v_st, p.v_sh, 16);
     }
     if (!ok) return cudaErrorInvalidValue;
-    cudaError_t e = p.D == 64 ? launch_d<64, kWindow>(a, s) : launch_d<128, kWindow>(a, s);
+    cudaError_t e = p.D == 64 ? launch_d<64, kWindow, kMask>(a, s) : launch_d<128, kWindow, kMask>(a, s);
     if (e != cudaSuccess || (kWindow && a.p.whole)) return e;
     PartsMergeParams m;
     m.parts = p.parts;

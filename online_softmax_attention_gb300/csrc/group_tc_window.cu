@@ -3,6 +3,8 @@
 
 namespace attn {
 
-cudaError_t launch_group_window(const GroupParams &p, cudaStream_t s) { return launch_group_of<true>(p, s); }
+cudaError_t launch_group_window(const GroupParams &p, cudaStream_t s) {
+    return p.mask ? launch_group_masks(p, s) : launch_group_of<true, false>(p, s);
+}
 
 }  // namespace attn

@@ -215,6 +215,7 @@ constexpr int kGroupRows = 256;  // query rows of a unit (two 128-row tiles)
 bool group_supported(int dtype, int D, int group);
 cudaError_t launch_group(const GroupParams &p, cudaStream_t s);
 cudaError_t launch_group_window(const GroupParams &p, cudaStream_t s);  // the same, window > 0 (causal)
+cudaError_t launch_group_masks(const GroupParams &p, cudaStream_t s);   // those of a window that have a mask
 cudaError_t launch_tree_fwd(const TreeParams &p, cudaStream_t s);
 cudaError_t launch_tree_masks(const TreeParams &p, cudaStream_t s);  // masks over a window, of few rows (tree.cuh)
 
