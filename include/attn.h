@@ -162,9 +162,9 @@ typedef struct attn_fwd_args {
  * With sinks the backward's workspace holds partial sums of dk and dv (the sinks' key
  * blocks are seen by all queries behind them and cut into items; at most 256 blocks a
  * key head), which are added in a fixed order.  Over a cache, tokens that the window hides
- * from every new token of an entry may hold anything, NaN included, and the table's
- * entries are not followed for pages in a run of 256 tokens, from a multiple of 256 on,
- * that it hides whole. */
+ * from every new token of an entry may hold anything, NaN included (with a mask, so may new
+ * tokens that none of them sees), and the table's entries may be missing for pages in a run
+ * of 256 tokens before the new ones, from a multiple of 256 on, that it hides whole. */
 
 /* Grouped heads (H_kv in the forward and the backward; no counterpart on the
  * pages): k and v hold H_kv heads, each shared by a group of G = H / H_kv

@@ -206,6 +206,23 @@ __device__ __forceinline__ Work entry_work(const GroupParams &p, const Entry &e,
     return e.T > 0 ? Work{(long long)p.Hkv * e.units, p.Hkv * unit_tiles<kWindow>(p, e, per, e.units)} : Work{0, 0};
 }
 
+// Reports the missing pages from key lost[0] to lost[1] if one of `tokens` new tokens, row q0 on, sees a key between them.
+__device__ __noinline__ void check_lost(const GroupParams &p, int q0, int tokens, int T, int ctx, int *lost) {
+    const int lane = threadIdx.x & 31, from = lost[0], to = lost[1];
+    bool seen = to > ctx;
+    for (int x = lane; x < tokens; x += 32) {
+        const RowWindow w = tree_window(p.mask + (int64_t)(q0 + x) * p.mask_words, T, ctx, p.window, p.sinks);
+        seen = seen || from < w.hi || to > w.lo;
+    }
+    if (seen) report_status(p.status, ATTN_EINVAL);
+    __syncwarp();
+    if (lane == 0) {
+        lost[0] = INT_MAX;
+        lost[1] = 0;
+    }
+    __syncwarp();
+}
+
 // Bounded wait for outstanding TMA writes before the CTA exits after an abort.
 constexpr long long kDrainCycles = 1ll << 31;
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, long long budget) {
@@ -217,7 +234,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, long l
 
 // ---- warp 0: walks the stretch, loads ------------------------------------------------
 
-template <int D, bool kWindow>
+template <int D, bool kWindow, bool kMask>
 __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow> *segs, const Stretch &st, uint32_t sQ, uint32_t sK,
                          uint32_t sV, const Watchdog &wd) {
     using C = Cfg<D>;
@@ -238,12 +255,27 @@ __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow>
     const int psz = p.paged ? min(1 << p.c.page_shift, BN) : BN, pieces = BN / psz;
     Entry e = {};
     KeyList list = {0, 0};  // with a window, of the unit
+    // kMask: from the first to the last key of the unit's missing pages.  (Its list begins as for a row that sees no draft; a
+    // page that none of its rows sees may be gone.)
+    __shared__ int lost[2];
+    if constexpr (kMask) {
+        if (lane == 0) {
+            lost[0] = INT_MAX;
+            lost[1] = 0;
+        }
+        __syncwarp();
+    }
     auto key_at = [&](int place) { return kWindow ? list.at(place) : place; };
     auto page_at = [&](int j) -> int {
         const int pos = key_at(BN * j + lane * psz);
         if (!p.paged || lane >= pieces || pos >= e.L) return 0;
         const int id = p.c.table[(int64_t)e.s * p.c.table_stride + (pos >> p.c.page_shift)];
         if ((unsigned)id < (unsigned)p.c.n_pages) return id;
+        if constexpr (kMask) {  // (looked at behind the unit)
+            atomicMin(&lost[0], pos);
+            atomicMax(&lost[1], pos + psz);
+            return 0;
+        }
         report_status(p.status, ATTN_EINVAL);
         return 0;  // any page that exists: the entry's result is reported as invalid
     };
@@ -425,6 +457,10 @@ __device__ void producer(const GroupArgsOf<kWindow> &a, Bars &bars, Seg<kWindow>
             if (j + 1 < t1) page = page_at(j + 1);
         }
         if (!ok) break;
+        if constexpr (kMask) {
+            __syncwarp();
+            if (lost[1] > 0) check_lost(p, e.q0 + unit * per, min(per, e.T - unit * per), e.T, e.ctx, lost);
+        }
         next_unit(n_unit);
     }
     if (ok) {
@@ -1031,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     if (warp < 4) {
         regs_dec<kWindow ? C::kRegsWindowProducer : C::kRegsProducer>();
         if (warp == 0) {
-            producer<D, kWindow>(a, bars, segs, st, sQ, sK, sV, wd);  // the whole warp
+            producer<D, kWindow, kMask>(a, bars, segs, st, sQ, sK, sV, wd);  // the whole warp
         } else if (warp == 1) {
             mma_issuer<D, kBF16, kWindow>(a, bars, segs, sQ, sK, sV, tmem, wd);
             if (lane == 0 && aborting(wd)) {  // let issued MMAs finish before TMEM is freed

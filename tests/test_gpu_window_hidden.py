@@ -71,3 +71,41 @@ def test_tokens_that_no_row_sees(lens, news, page, heads, group, kind, dtype, d)
         got = attn.tree_fwd(q.cuda(), cache, seqs, cu, **call)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), (kind, window, sinks)
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float32, 64)])
+@pytest.mark.parametrize("lens,news,page,heads,group,window,sinks", [
+    # the first token that a row of a chain sees is one of a multiple of 256, or the one behind it
+    ([2000], [4], 16, 2, 2, 205, 0), ([2000], [4], 16, 2, 2, 204, 3), ([2000, 1400], [4, 1], 256, 2, 2, 205, 4), ([2000], [40], 128, 2, 4, 169, 4),
+    ([2000], [40], 8, 2, 4, 168, 0), ([3000, 900], [400, 300], 64, 1, 2, 41, 300), ([9800], [5], 64, 1, 1, 9028, 300),
+    ([1500], [20], 4, 1, 4, 201, 2), ([4500], [30], 1024, 1, 4, 375, 2)])
+@pytest.mark.parametrize("kind", ["causal", "chain", "tree", "bits"])
+def test_pages_that_no_row_sees_may_be_gone(lens, news, page, heads, group, window, sinks, kind, dtype, d):
+    """Table entries of pages in runs of 256 tokens before the new ones that hold none which is seen."""
+    cache, model, seqs, q, cu, call, seen = setup(lens, news, page, heads, group, d, dtype, kind, window, sinks, 111)
+    gone = 0
+    for s, rows, n, t in zip(seqs, seen, lens, news):
+        live = rows.any(0)
+        live[n - t:] = True
+        table = cache.table[s].cpu()
+        for i in range(-(-n // page)):
+            a, b = i * page // 256 * 256, -(-(i + 1) * page // 256) * 256
+            if not live[a:b].any():
+                table[i] = -1
+                gone += 1
+        cache.table[s] = table.cuda()
+    assert gone > 0
+    o, lse = attn.tree_fwd(q.cuda(), cache, seqs, cu, **call)
+    assert attn.device_status() == 0
+    check(o, lse, model, seqs, q, cu, seen, dtype, f"{kind} {window}+{sinks}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t,page", [(4, 16), (40, 16), (40, 256)])
+def test_pages_that_a_row_sees_are_missed(t, page, dtype):
+    """The page of the first token that a row of a chain sees."""
+    cache, _, seqs, q, cu, call, seen = setup([2000], [t], page, 2, 2, 64, dtype, "chain", 300, 2, 112)
+    first = int(np.flatnonzero(seen[0].any(0) & (np.arange(2000) >= 2))[0])
+    cache.table[seqs[0], first // page] = -1
+    attn.tree_fwd(q.cuda(), cache, seqs, cu, **call)
+    assert attn.device_status() == attn._abi.ATTN_EINVAL
