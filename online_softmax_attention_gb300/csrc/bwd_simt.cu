@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(NT) dkdv_simt_kernel(const BwdParams p) {
                         if (kWindow) ok = ok && (row - key < p.window || key < p.sinks);
                         const float pr = ok ? exp2_approx(s[r][c] * p.scale_log2 - l2) : 0.f;
                         sP[rl * LDP + tx + 16 * c] = pr;
-                        sdS[rl * LDP + tx + 16 * c] = pr * (dp[r][c] - drr);
+                        // (with a window, whatever dp is where a pair is not seen)
+                        sdS[rl * LDP + tx + 16 * c] = !kWindow || ok ? pr * (dp[r][c] - drr) : 0.f;
                     }
                 }
                 __syncthreads();
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(NT) dq_simt_kernel(const BwdParams p) {
                     bool ok = key < Lk && (!p.causal || key <= row);
                     if (kWindow) ok = ok && (row - key < p.window || key < p.sinks);
                     const float pr = ok ? exp2_approx(s[r][c] * p.scale_log2 - l2) : 0.f;
-                    sdS[rl * LDP + tx + 16 * c] = pr * (dp[r][c] - drr);
+                    sdS[rl * LDP + tx + 16 * c] = !kWindow || ok ? pr * (dp[r][c] - drr) : 0.f;
                 }
             }
             __syncthreads();

@@ -192,15 +192,36 @@ __device__ __forceinline__ uint32_t bits_below(int lim, int u) {
     return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
 }
 
-// Scores of the columns whose bit is not set: -inf, whose exponential is 0 and with it P and dS.
-// (Ahead of the exponentials: zeroing P, its 16-bit form and dS behind them takes three times the
-// instructions, and a window masks most of the blocks.)
+// Bytes of a and b picked by the four-bit fields of `sel`; a field's top bit: eight times the byte's top bit.
+__device__ __forceinline__ uint32_t pick_bytes(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+// Scores of the columns whose bit is not set: -inf, whose exponential is 0, unless the row's lse is NaN or -inf.  (Ahead
+// of the exponentials: dK / dV's elementwise warps need fewer instructions so than to zero P^T and dS^T behind them.)
 __device__ __forceinline__ void hide(uint32_t (&s)[2][32], const uint32_t (&bits)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (__all_sync(0xffffffffu, bits[h] == 0xffffffffu)) continue;
 #pragma unroll
         for (int e = 0; e < 32; ++e) s[h][e] = (bits[h] >> e) & 1 ? s[h][e] : 0xff800000u;
+    }
+}
+
+// Zeroes the 16-bit values of 64 columns whose bit is not set, whatever they are.  (Behind the exponentials and products,
+// which may be infinite or NaN there; two instructions for two values, by the bits moved to the tops of bytes.)
+__device__ __forceinline__ void keep_seen(uint32_t (&pk)[32], const uint32_t (&bits)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (__all_sync(0xffffffffu, bits[h] == 0xffffffffu)) continue;
+        uint32_t top[8];  // top[i]: bit 8 k + i is the top bit of byte k
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = bits[h] << (7 - i);
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            pk[16 * h + c] &= pick_bytes(top[2 * (c & 3)], top[2 * (c & 3) + 1], 0xcc88u + (c >> 2) * 0x1111u);
     }
 }
 
@@ -656,6 +677,14 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
             }
             float *sb = stats + (stat_i & 1) * 2 * BT;
             sb[e] = stat_valid ? -stat_next : (e < BT ? -INFINITY : 0.f);
+            // with a window, whether one of the warp's lse is not a number or -inf, behind the statistics
+            [[maybe_unused]] int *sbad = reinterpret_cast<int *>(stats + 4 * BT) + 4 * (stat_i & 1);
+            if constexpr (kWindow) {
+                if (wg == 0) {
+                    const int bad = __any_sync(0xffffffffu, stat_valid && !(stat_next > -INFINITY));
+                    if (lane == 0) sbad[quarter] = bad;
+                }
+            }
             mbar_arrive_warp(smem_u32(&bars.stats_ready[stat_i & 1]));
             bool ok = mbar_wait(smem_u32(&bars.stats_ready[stat_i & 1]), (stat_i >> 1) & 1, wd);
             if (!__all_sync(0xffffffffu, ok)) return;
@@ -698,6 +727,18 @@ __device__ void dkdv_elementwise(const TcBwdArgs &a, DkdvBars<kWindow> &bars, fl
                     } else if (kl > q) {
                         pr[c].x = 0.f;
                         pk[c] &= 0xFFFF0000u;  // the pair's first value
+                    }
+                }
+            }
+            if constexpr (kWindow) {
+                // a row whose lse is NaN or -inf (its scores were NaN) has such a P, and none where it does not see the key
+                const int4 bad = *reinterpret_cast<const int4 *>(sbad);
+                if (bad.x | bad.y | bad.z | bad.w) {
+                    keep_seen(pk, seen);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (!((seen[c >> 4] >> (2 * c & 31)) & 1)) pr[c].x = 0.f;
+                        if (!((seen[c >> 4] >> (2 * c + 1 & 31)) & 1)) pr[c].y = 0.f;
                     }
                 }
             }
@@ -943,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkdv_tc_kernel(const __grid_const
     using C = BCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ DkdvBars<kWindow> bars;
-    __shared__ __align__(16) float stats[2 * 2 * BT];
+    __shared__ __align__(16) float stats[2 * 2 * BT + (kWindow ? 2 * 4 : 0)];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -1281,8 +1322,7 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
     const int quarter = warp & 3;
     const int rl = 32 * quarter + lane;
     const uint32_t lane_base = tmem_addr(tmem, 32 * quarter, 0);
-    // (as in dK / dV)
-    const float sl2 = kWindow ? fmaxf(fabsf(p.scale_log2), FLT_MIN) : fabsf(p.scale_log2);
+    const float sl2 = fabsf(p.scale_log2);  // the score MMA negated S for a negative scale
     uint32_t s_cnt = 0, dp_cnt = 0, ad_cnt = 0, step = 0;
 
     for (int i = 0;; ++i) {
@@ -1313,16 +1353,6 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
             tmem_ld_wait(rs[1]);
             tc_fence_before();
             mbar_arrive_warp(smem_u32(&bars.s_free));  // the S buffer may be overwritten
-            if constexpr (kWindow) {
-                // keys up to the row and the sequence's end, from the row's window on or among the sinks
-                const int key0 = BT * block_of(f, j), c0 = 64 * wg;
-                const int lim = min(f.Lk, row + 1) - key0, from = row + 1 - p.window - key0, sink = p.sinks - key0;
-                uint32_t seen[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    seen[h] = bits_below(lim, c0 + 32 * h) & (~bits_below(from, c0 + 32 * h) | bits_below(sink, c0 + 32 * h));
-                hide(rs, seen);
-            }
 
             // P = 2^(S scale log2e - lse2), in place of S, while dP may still be in flight
             const float2 sc2 = make_float2(sl2, sl2), nl2 = make_float2(-lse2, -lse2);
@@ -1367,6 +1397,15 @@ __device__ void dq_elementwise(const TcBwdArgs &a, DqBars<kWindow> &bars, uint32
                                               __uint_as_float(rp[(2 * c + 1) >> 5][(2 * c + 1) & 31]));
                 const float2 d = __fmul2_rn(pv, __fadd2_rn(dp, ndr2));
                 pk[c] = pack2(d.x, d.y, kBF16);
+            }
+            if constexpr (kWindow) {
+                // keys up to the row and the sequence's end, from the row's window on or among the sinks
+                const int end = min(f.Lk, row + 1) - key0, from = row + 1 - p.window - key0, sink = p.sinks - key0;
+                uint32_t seen[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    seen[h] = bits_below(end, c0 + 32 * h) & (~bits_below(from, c0 + 32 * h) | bits_below(sink, c0 + 32 * h));
+                keep_seen(pk, seen);
             }
             if (masked) {
                 // keys at or past lim: dS = 0 (whatever their discarded exponentials
