@@ -355,16 +355,17 @@ struct BwdLayout {
 
 // Chunks of the sinks' key blocks, of blocks of `block` rows: as long as a window's items where those are
 // few, so that all run at once (an f32 row of 2000 tokens, 8 query heads of one key head, window 100: 778 us
-// with twice that, 471 so), else twice that, more where half a CTA's share of all blocks (152 CTAs) is
+// with twice that, 471 so), else twice that, more where half a CTA's share of all blocks (a CTA an SM) is
 // more or the partial sums would pass 256 slots a head; none where no row is longer.
 void sink_cut(const attn_bwd_args *a, int block, int &tiles, int &chunk) {
     tiles = chunk = 0;
     if (a->window <= 0 || a->window >= a->n_k || a->sinks <= 0) return;
     const int64_t blocks = a->n_q / block + 1, held = ((int64_t)a->sinks + block - 1) / block;
     const int64_t n = held < blocks ? held : blocks, heads = a->H_kv > 0 ? a->H_kv : a->H;
-    const int64_t seen = (2 * block - 2 + (int64_t)a->window) / block;
-    int64_t c = heads * blocks < 2 * 152 ? seen : 2 * seen;
-    if (c < heads * blocks * seen / (2 * 152)) c = heads * blocks * seen / (2 * 152);
+    const int64_t seen = (2 * block - 2 + (int64_t)a->window) / block, two_each = 2 * (int64_t)sm_count();
+    const int64_t share = heads * blocks * seen / two_each;
+    int64_t c = heads * blocks < two_each ? seen : 2 * seen;
+    if (c < share) c = share;
     if (c < (n * blocks + 127) / 128) c = (n * blocks + 127) / 128;
     if (blocks <= c) return;
     tiles = (int)n;
