@@ -226,8 +226,6 @@ __device__ __forceinline__ void take_unit(const TreeParams &p, const Entry &e, i
                       __reduce_or_sync(0xffffffffu, (uint32_t)drafts);
         if (tid < kRows) s_window[tid] = w;
         if (e.T > 64) __syncthreads();  // more new tokens: seen_draft reads the rows' windows
-    } else if (kWindow && tid < kRows) {
-        s_window[tid] = RowWindow{ctx + min((row0 + tid) / p.group, e.T - 1) + 1 - p.window, p.sinks};
     }
     // query rows: (token, head of the group), row-major; 16-byte chunks swizzled
     // by the row's low bits so that ldmatrix reads are conflict-free
@@ -242,6 +240,10 @@ __device__ __forceinline__ void take_unit(const TreeParams &p, const Entry &e, i
         *reinterpret_cast<uint4 *>(sQ + r * C::kRowBytes + 16 * (ch ^ (r & 7))) = v;
     }
 
+    if (kWindow && !kMask && tid < kRows) {
+        const int t = min((row0 + tid) / p.group, e.T - 1);
+        s_window[tid] = RowWindow{ctx + t + 1 - p.window, p.sinks};
+    }
     // places [hidden0, hidden1) of the list are hidden from some row of the entry
     const int hidden0 = e.list.shift ? e.list.held : p.sinks, hidden1 = ctx + e.T - p.window - e.list.shift;
     auto hidden = [&](int row, int key) { return key < s_window[row].lo && key >= s_window[row].hi; };
