@@ -153,7 +153,8 @@ typedef struct attn_fwd_args {
  * window, in order, it sees the first `sinks` and the last `window` (all of them where
  * they are no more than both together).  So query i of a sequence sees key j <= i if
  * i - j < window or j < sinks, and work and reads go with window + sinks, not with
- * the sequence.  Causal relation only; window > 0 (or none: both 0, ATTN_EINVAL else); no
+ * the sequence (attn_cache_weigh of few query rows passes over all of a sequence's weights,
+ * though not over the hidden keys).  Causal relation only; window > 0 (or none: both 0, ATTN_EINVAL else); no
  * fp8, no pruning, no ATTN_DQ_FUSED (ATTN_EUNSUPPORTED).  A window as long as all the keys
  * is none.  f16 / bf16 inputs run the kernel that packs grouped heads' rows (for ungrouped
  * heads too, and any number of sequences), which takes neither num_splits > 1 nor

@@ -69,7 +69,7 @@ __device__ __forceinline__ int block_prefix(int x, int *s_warp, int &total) {
     return (warp > 0 ? before : 0) + y - x;
 }
 
-// The number of digit places of the passes, and the bits below a pass's digit.
+// Bins of a pass's histogram: 11 bits of the weights' numbers (the last pass has 10).
 constexpr int kBins = 2048;
 
 __global__ void __launch_bounds__(kPlanThreads) evict_choose_kernel(const CacheParams c, const EvictParams p) {

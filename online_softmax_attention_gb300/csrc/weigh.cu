@@ -17,7 +17,8 @@
 // FFMA, a key a lane.
 //
 // Bound: HBM, the K rows read once.  (More than eight rows a key head run weigh_tc.cu, but for f32, pages below
-// 8 rows and groups of more than 128.)
+// 8 rows and groups of more than 128.)  With a window K rows that it hides from every new token are not read, but
+// their units are counted and their weights pass through, so that the time goes with the sequence's length.
 #include "../../include/attn.h"
 #include "mma.cuh"
 #include "stretch.cuh"

@@ -109,3 +109,40 @@ def test_pages_that_a_row_sees_are_missed(t, page, dtype):
     cache.table[seqs[0], first // page] = -1
     attn.tree_fwd(q.cuda(), cache, seqs, cu, **call)
     assert attn.device_status() == attn._abi.ATTN_EINVAL
+
+
+def test_trees_in_a_graph_and_on_streams_at_once():
+    """Prepared calls of both kernels over one cache whose hidden tokens are NaN, replayed for other lengths and masks."""
+    lens, streams = [3000, 1700, 900], []
+    calls = []
+    for t, window in ((4, 600), (40, 600), (70, 30)):
+        cache, _, seqs, q, cu, call, seen = setup(lens, [t] * 3, 16, 2, 4, 128, torch.bfloat16, "tree", window, 4, 113)
+        for s, rows in zip(seqs, seen):
+            hidden = torch.from_numpy(np.flatnonzero(~rows.any(0))).cuda()
+            cache.v[:, cache.table[s].long()[hidden // 16], hidden % 16] = float("nan")
+        c = attn.TreeCall(q.cuda(), cache, seqs, cu, **call)
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.isfinite(c.o).all()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run()
+        calls.append((c, graph, c.o.clone(), c.lse.clone(), cache, seqs, q, cu, call))
+        streams.append(torch.cuda.Stream())
+    for c, *_ in calls:
+        c.o.fill_(9)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (c, graph, *_) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for c, graph, o, lse, cache, seqs, q, cu, call in calls:
+        assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+        # every draft now sees the ones before it, of shorter sequences
+        call["mask"].copy_(torch.from_numpy(masks("chain", [int(n) for n in np.diff(cu)], call["mask"].shape[1], None).view(np.int64)))
+        cache.lens[seqs[0]], cache.v[...] = 500, torch.randn(cache.v.shape, device="cuda").bfloat16()
+        graph.replay()
+        want = attn.tree_fwd(q.cuda(), cache, seqs, cu, **call)
+        assert torch.equal(c.o, want[0]) and torch.equal(c.lse, want[1])
+    assert attn.device_status() == 0
