@@ -162,10 +162,11 @@ typedef struct attn_fwd_args {
  * with ATTN_KERNEL_SIMT, groups of more than 128 or f32 inputs, the CUDA-core kernels.
  * With sinks the backward's workspace holds partial sums of dk and dv (the sinks' key
  * blocks are seen by all queries behind them and cut into items; at most 256 blocks a
- * key head), which are added in a fixed order.  Over a cache, tokens that the window hides
- * from every new token of an entry may hold anything, NaN included (with a mask, so may new
- * tokens that none of them sees), and the table's entries may be missing for pages in a run
- * of 256 tokens before the new ones, from a multiple of 256 on, that it hides whole. */
+ * key head), which are added in a fixed order.  Over a cache whose sequences can be longer
+ * than the window, tokens that it hides from every new token of an entry may hold anything,
+ * NaN included (with a mask, so may new tokens that none of them sees), and the table's
+ * entries may be missing for pages in a run of 256 tokens before the new ones, from a
+ * multiple of 256 on, that it hides whole. */
 
 /* Grouped heads (H_kv in the forward and the backward; no counterpart on the
  * pages): k and v hold H_kv heads, each shared by a group of G = H / H_kv
